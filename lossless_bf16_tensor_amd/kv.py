@@ -1,0 +1,374 @@
+"""KV-cache operators (C-ABI: include/uzip_kv.h) over torch tensors.
+
+What a serving step does to a cache before it is encoded for its transfer and
+after it is decoded: :func:`rope`, :func:`append`, :func:`attend` and
+:func:`evict`. Every step runs in the library's HIP kernels; this module checks
+shapes, which the library cannot see, and passes pointers on.
+
+Caches. ``k`` and ``v`` are [sequences, tokens, kv heads, head dim], or with a
+page ``table`` (int32 [sequences, entries]) pools [pages, page, kv heads, head
+dim]; page is a power of two, at least 16. They may be any views whose last dim
+is contiguous and whose other strides are multiples of 8, so a cache kept
+[sequences, kv heads, tokens, head dim] is passed transposed. Element types:
+bfloat16, float16, or float8_e5m2 beside queries of either. The head dim is a
+multiple of 8 up to 256.
+
+``length`` (int32 [sequences], on the device) counts the tokens each sequence
+has; ``drafted`` (int32, optional) the new ones, when they are fewer than the
+tensors hold. Values on the device are not checked, and none of them makes a
+kernel read or write outside the tensors: lengths are clamped, table entries
+outside the pool are absent pages.
+
+Calls run on the current stream of the tensors' device, or on ``stream=``, and
+can be captured. A workspace passed as ``ws=`` must not be shared by calls that
+may overlap.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+import math
+import struct
+
+import torch
+
+from .uzip import UzipError, lib as _codec_lib
+
+# every symbol include/uzip_kv.h declares
+EXPORTS = ("uzip_kv_rope", "uzip_kv_append", "uzip_kv_attend", "uzip_kv_attend_workspace_bytes", "uzip_kv_evict",
+           "uzip_kv_evict_workspace_bytes")
+
+_DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e5m2: 2}
+_INTERLEAVED, _INVERSE = 1, 2
+
+# uzip_kv_cache_t, uzip_kv_rope_t, uzip_kv_append_args_t, uzip_kv_attend_args_t, uzip_kv_evict_args_t
+_CACHE = struct.Struct("=3Q7q8I")
+_ROPE = struct.Struct("=2Qq2IfI")
+_TENSOR = struct.Struct("=Q3q")
+_APPEND = struct.Struct("=16q2Q4I")
+_ATTEND = struct.Struct("=8q2Q2q3Q2q3If")
+_EVICT = struct.Struct("=Q2q4Q4I")
+
+_lib = None
+
+
+def lib():
+    """The library with the signatures of uzip_kv.h."""
+    global _lib
+    if _lib is None:
+        L = _codec_lib()
+        vp, u64, u32, st = ctypes.c_void_p, ctypes.c_uint64, ctypes.c_uint32, ctypes.c_char_p
+        sig = {
+            "uzip_kv_rope": (ctypes.c_int, [st, st, u32, u32, u32, u32, u32, st, vp]),
+            "uzip_kv_append": (ctypes.c_int, [st, st, st, vp]),
+            "uzip_kv_attend": (ctypes.c_int, [st, st, vp, u64, vp]),
+            "uzip_kv_attend_workspace_bytes": (u64, [u32] * 6),
+            "uzip_kv_evict": (ctypes.c_int, [st, st, st, vp, u64, vp]),
+            "uzip_kv_evict_workspace_bytes": (u64, [u32] * 3),
+        }
+        for name, (res, args) in sig.items():
+            f = getattr(L, name)
+            f.restype = res
+            f.argtypes = args
+        _lib = L
+    return _lib
+
+
+def _check(rc: int, what: str):
+    if rc != 0:
+        raise UzipError(rc, f"{what}: {lib().uzip_strerror(rc).decode()}")
+
+
+def _need(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+class _On:
+    """The device of a call made current, and the call's stream."""
+    __slots__ = ("device", "stream", "guards")
+
+    def __init__(self, device: torch.device, stream):
+        _need(device.type == "cuda", "expected device tensors")
+        self.device = device
+        self.guards = ()
+        if stream is None:
+            if device.index == torch.cuda.current_device():
+                self.stream = torch.cuda.current_stream().cuda_stream
+                return
+            guard = torch.cuda.device(device)
+            guard.__enter__()
+            self.guards = (guard,)
+            self.stream = torch.cuda.current_stream().cuda_stream
+        else:
+            _need(stream.device == device, "the stream belongs to another device than the tensors")
+            guard = torch.cuda.stream(stream)      # makes its device current too; new tensors belong to it
+            guard.__enter__()
+            self.guards = (guard,)
+            self.stream = stream.cuda_stream
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *e):
+        for guard in self.guards:
+            guard.__exit__(*e)
+
+
+def _strides(t: torch.Tensor):
+    """Strides of the first three dims, 0 where a dim has one element; the last dim is contiguous."""
+    shape, st = t.shape, t.stride()
+    _need(len(shape) == 4, f"expected four dims, got {len(shape)}")
+    _need(st[3] == 1 or shape[3] == 1, "the head dim is not contiguous")
+    return tuple(0 if shape[i] == 1 else st[i] for i in range(3))
+
+
+def _written(t: torch.Tensor, what: str):
+    for n, s in zip(t.shape, t.stride()):
+        _need(n == 1 or s != 0, f"{what} has elements that share memory")
+
+
+def _counts(t, seqs: int, device, what: str) -> int:
+    """Address of an int32 tensor with one value a sequence; 0 for None."""
+    if t is None:
+        return 0
+    _need(t.dtype == torch.int32 and t.shape == (seqs,) and t.is_contiguous() and t.device == device,
+          f"{what}: expected a contiguous int32 tensor of {seqs} on {device}")
+    return t.data_ptr()
+
+
+def _cache(k: torch.Tensor, v: torch.Tensor, table, seqs: int):
+    """(packed uzip_kv_cache_t, kv heads, head dim, tokens a sequence)"""
+    _need(k.shape == v.shape and k.dtype == v.dtype and k.device == v.device, "k and v caches differ in shape, type or device")
+    dtype = _DTYPE.get(k.dtype)
+    _need(dtype is not None, f"caches are bfloat16, float16 or float8_e5m2, got {k.dtype}")
+    ks, vs = _strides(k), _strides(v)
+    first, second, heads, dim = k.shape
+    if table is None:
+        _need(first == seqs, f"the cache holds {first} sequences, expected {seqs}")
+        return _CACHE.pack(k.data_ptr(), v.data_ptr(), 0, *ks, *vs, 0, dtype, seqs, heads, dim, second, 0, 0, 0), heads, dim, second
+    _need(table.dtype == torch.int32 and table.dim() == 2 and table.shape[0] == seqs and table.device == k.device
+          and table.shape[1] >= 1 and (table.stride(1) == 1 or table.shape[1] == 1),
+          f"table: expected int32 [{seqs}, entries] with contiguous rows on {k.device}")
+    tokens = table.shape[1] * second
+    return (_CACHE.pack(k.data_ptr(), v.data_ptr(), table.data_ptr(), *ks, *vs, table.stride(0) if seqs > 1 else 0, dtype,
+                        seqs, heads, dim, tokens, second, first, 0), heads, dim, tokens)
+
+
+def _types(new: torch.Tensor, cache: torch.Tensor):
+    _need(new.dtype in (torch.bfloat16, torch.float16), f"expected bfloat16 or float16, got {new.dtype}")
+    _need(cache.dtype in (new.dtype, torch.float8_e5m2), f"{new.dtype} does not go with a {cache.dtype} cache")
+
+
+def _rope(freq, pos, amplitude: float, flags: int, seqs: int, tokens: int, dim: int, device):
+    """Packed uzip_kv_rope_t."""
+    _need(freq.dtype == torch.float64 and freq.dim() == 1 and freq.is_contiguous() and freq.device == device,
+          f"freq: expected a contiguous float64 vector on {device}")
+    _need(2 * freq.numel() <= dim, f"freq turns {2 * freq.numel()} of {dim} elements")
+    at = stride = 0
+    if pos is not None:
+        _need(pos.dtype == torch.int32 and pos.device == device and pos.shape in ((seqs, tokens), (tokens,))
+              and (pos.stride(-1) == 1 or tokens == 1), f"pos: expected int32 [{seqs}, {tokens}] or [{tokens}] with contiguous rows on {device}")
+        at, stride = pos.data_ptr(), pos.stride(0) if pos.dim() == 2 and seqs > 1 else 0
+    return _ROPE.pack(freq.data_ptr(), at, stride, 2 * freq.numel(), flags, amplitude, 0)
+
+
+def rope_freq(rot: int, base: float = 10000.0, *, linear: float = 1.0, ntk: float = 1.0, bands=None,
+              device=None) -> torch.Tensor:
+    """Turns per position of the rot / 2 pairs of a rotary embedding, float64:
+    base ** (-2 i / rot) / (2 pi), scaled for contexts longer than trained on.
+
+    linear: all positions divided by this factor.
+    ntk:    base times factor ** (rot / (rot - 2)), which slows the slowest
+            pair by the factor and leaves the fastest.
+    bands:  (factor, trained, low, high): pairs that turn at most `low` times
+            over the `trained` positions are slowed by the factor, those that
+            turn at least `high` times are kept, and between them the two
+            frequencies are mixed in proportion.
+    """
+    _need(rot >= 2 and rot % 2 == 0, f"rot is even and positive, got {rot}")
+    _need(base > 0 and linear > 0 and ntk > 0, "base and factors are positive")
+    if ntk != 1.0:
+        _need(rot > 2, "ntk scaling needs more than one pair")
+        base = base * ntk ** (rot / (rot - 2))
+    i = torch.arange(rot // 2, dtype=torch.float64)
+    f = base ** (-2.0 * i / rot) / (2.0 * math.pi) / linear
+    if bands is not None:
+        factor, trained, low, high = bands
+        _need(factor > 0 and high > low, "bands: expected a positive factor and low < high")
+        keep = ((f * trained - low) / (high - low)).clamp(0.0, 1.0)
+        f = f * (keep + (1.0 - keep) / factor)
+    return f if device is None else f.to(device)
+
+
+def rope(x: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, *, amplitude: float = 1.0, interleaved: bool = False,
+         inverse: bool = False, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Rotary positions of x [sequences, tokens, heads, dim], bfloat16 or
+    float16. pos: int32 [sequences, tokens] or [tokens]. freq: turns per
+    position of each pair (:func:`rope_freq`); the first 2 * len(freq) elements
+    turn, as halves (i, i + len(freq)) or interleaved (2i, 2i + 1). inverse
+    turns back: the gradient, and what moves kept keys to other positions. out
+    may be x."""
+    _need(x.dtype in (torch.bfloat16, torch.float16), f"expected bfloat16 or float16, got {x.dtype}")
+    xs = _strides(x)
+    B, T, H, D = x.shape
+    packed = _rope(freq, pos, amplitude, interleaved * _INTERLEAVED | inverse * _INVERSE, B, T, D, x.device)
+    with _On(x.device, stream) as on:
+        if out is None:
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        else:
+            _need(out.shape == x.shape and out.dtype == x.dtype and out.device == x.device, "out differs from x in shape, type or device")
+            _written(out, "out")
+        _check(lib().uzip_kv_rope(_TENSOR.pack(x.data_ptr(), *xs), _TENSOR.pack(out.data_ptr(), *_strides(out)),
+                                  _DTYPE[x.dtype], B, T, H, D, packed, on.stream), "rope")
+    return out
+
+
+def append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+           length: torch.Tensor, freq: torch.Tensor | None = None, *, pos: torch.Tensor | None = None,
+           table: torch.Tensor | None = None, drafted: torch.Tensor | None = None, amplitude: float = 1.0,
+           interleaved: bool = False, out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """Writes new tokens' keys k (turned to their positions) and values v
+    [sequences, tokens, kv heads, dim] into the cache behind each sequence's
+    length tokens, and returns the turned queries q [sequences, tokens, heads,
+    dim]; q may be None. pos defaults to length + 0, 1, ...; without freq
+    nothing turns. length is not changed. Tokens from drafted on, past the
+    cache's end or in an absent page are not written."""
+    B, T, H, D = k.shape
+    _need(v.shape == k.shape and v.dtype == k.dtype and v.device == k.device, "k and v differ in shape, type or device")
+    _types(k, k_cache)
+    cache, heads, dim, _ = _cache(k_cache, v_cache, table, B)
+    _written(k_cache, "the key cache")
+    _written(v_cache, "the value cache")
+    dev = k.device
+    _need(k_cache.device == dev, "the cache is on another device")
+    _need(heads == H and dim == D, f"the cache has {heads} heads of {dim}, the new keys {H} of {D}")
+    packed = None
+    if freq is not None:
+        packed = _rope(freq, pos, amplitude, interleaved * _INTERLEAVED, B, T, D, dev)
+    with _On(dev, stream) as on:
+        if q is None:
+            qs = (0,) * 8
+            hq = 0
+        else:
+            _need(q.dim() == 4 and q.shape[0] == B and q.shape[1] == T and q.shape[3] == D and q.dtype == k.dtype
+                  and q.device == dev, "q does not go with k")
+            hq = q.shape[2]
+            if out is None:
+                out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+            else:
+                _need(out.shape == q.shape and out.dtype == q.dtype and out.device == dev, "out differs from q in shape, type or device")
+                _written(out, "out")
+            qs = (q.data_ptr(), *_strides(q), out.data_ptr(), *_strides(out))
+        args = _APPEND.pack(*qs, k.data_ptr(), *_strides(k), v.data_ptr(), *_strides(v), _counts(length, B, dev, "length"),
+                            _counts(drafted, B, dev, "drafted"), _DTYPE[k.dtype], T, hq, 0)
+        _check(lib().uzip_kv_append(cache, args, packed, on.stream), "append")
+    return out if q is not None else None
+
+
+@functools.lru_cache(maxsize=4096)
+def attend_workspace_bytes(seqs: int, kv_heads: int, dim: int, cache_tokens: int, tokens: int, heads: int) -> int:
+    """Workspace that :func:`attend` needs for these shapes; 0 when they are invalid."""
+    return int(lib().uzip_kv_attend_workspace_bytes(seqs, kv_heads, dim, cache_tokens, tokens, heads))
+
+
+def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, length: torch.Tensor, *,
+           table: torch.Tensor | None = None, tree: torch.Tensor | None = None, drafted: torch.Tensor | None = None,
+           scale: float | None = None, score: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+           out: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of the drafted tokens q [sequences, tokens, heads, dim] over a
+    cache that holds length earlier tokens and, behind them, the drafted ones'
+    keys and values (:func:`append`). A drafted token sees every earlier token
+    and those drafted ones that its row of tree (bool [tokens, tokens], or one
+    such per sequence) names; without a tree, those up to itself. heads is a
+    multiple of the cache's. scale defaults to 1 / sqrt(dim).
+
+    score (float32 [sequences, kv heads, cache tokens]) has the weight that each
+    cached token received from the drafted tokens and the heads that share it
+    added. lse (float32 [sequences, tokens, heads], contiguous) receives the log
+    of each query's sum of exponentials. A query that sees nothing gives zeros
+    and -inf, as do those from drafted on. Masked keys and values have no
+    effect, whatever they hold."""
+    _types(q, k_cache)
+    qs = _strides(q)
+    B, T, hq, D = q.shape
+    dev = q.device
+    cache, heads, dim, tokens = _cache(k_cache, v_cache, table, B)
+    _need(k_cache.device == dev, "the cache is on another device")
+    _need(dim == D and hq >= heads and hq % heads == 0, f"{hq} query heads of {D} do not go with {heads} heads of {dim}")
+    ts = (0, 0)
+    if tree is not None:
+        _need(tree.dtype in (torch.bool, torch.uint8) and tree.device == dev and tree.shape in ((T, T), (B, T, T))
+              and (tree.stride(-1) == 1 or T == 1), f"tree: expected bool [{T}, {T}] or [{B}, {T}, {T}] with contiguous rows on {dev}")
+        ts = (tree.stride(0) if tree.dim() == 3 else 0, tree.stride(-2))
+    ss = (0, 0)
+    if score is not None:
+        _need(score.dtype == torch.float32 and score.shape == (B, heads, tokens) and score.device == dev
+              and (score.stride(2) == 1 or tokens == 1), f"score: expected float32 [{B}, {heads}, {tokens}] with contiguous rows on {dev}")
+        _written(score, "score")
+        ss = score.stride()[:2]
+    if lse is not None:
+        _need(lse.dtype == torch.float32 and lse.shape == (B, T, hq) and lse.is_contiguous() and lse.device == dev,
+              f"lse: expected contiguous float32 [{B}, {T}, {hq}] on {dev}")
+    with _On(dev, stream) as on:
+        if out is None:
+            out = torch.empty((B, T, hq, D), dtype=q.dtype, device=dev)
+        else:
+            _need(out.shape == q.shape and out.dtype == q.dtype and out.device == dev, "out differs from q in shape, type or device")
+            _written(out, "out")
+        if ws is None:
+            ws = torch.empty(attend_workspace_bytes(B, heads, D, tokens, T, hq), dtype=torch.uint8, device=dev)
+        else:
+            _need(ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev, "ws: expected contiguous uint8")
+        args = _ATTEND.pack(q.data_ptr(), *qs, out.data_ptr(), *_strides(out), lse.data_ptr() if lse is not None else 0,
+                            score.data_ptr() if score is not None else 0, *ss, _counts(length, B, dev, "length"),
+                            _counts(drafted, B, dev, "drafted"), tree.data_ptr() if tree is not None else 0, *ts,
+                            _DTYPE[q.dtype], T, hq, 1.0 / math.sqrt(D) if scale is None else scale)
+        _check(lib().uzip_kv_attend(cache, args, ws.data_ptr(), ws.numel(), on.stream), "attend")
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def evict_workspace_bytes(seqs: int, kv_heads: int, cache_tokens: int) -> int:
+    """Workspace that :func:`evict` needs; 0 when the shapes are invalid."""
+    return int(lib().uzip_kv_evict_workspace_bytes(seqs, kv_heads, cache_tokens))
+
+
+def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, score: torch.Tensor, length: torch.Tensor, keep: int, *,
+          sink: int = 0, recent: int = 0, table: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+          v_out: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """Cuts a cache to keep tokens per sequence and head: the first `sink`, the
+    last `recent`, and the others with the largest score (float32 [sequences, kv
+    heads, cache tokens], as :func:`attend` adds it up), ties to the lower
+    token, NaN last. Returns (k, v, score, length, index): caches [sequences,
+    keep, kv heads, dim] with the kept tokens in order and zeros behind them,
+    ready for ``uzip.encode``; their scores [sequences, kv heads, keep]; min(length,
+    keep); and where each came from, int32 [sequences, kv heads, keep], -1
+    behind the last. Keys keep the positions they were turned to."""
+    B = length.numel()
+    cache, heads, dim, tokens = _cache(k_cache, v_cache, table, B)
+    dev = k_cache.device
+    _need(score.dtype == torch.float32 and score.shape == (B, heads, tokens) and score.device == dev
+          and (score.stride(2) == 1 or tokens == 1), f"score: expected float32 [{B}, {heads}, {tokens}] with contiguous rows on {dev}")
+    _need(1 <= keep <= 1 << 30 and sink >= 0 and recent >= 0 and sink + recent <= keep,
+          f"keep {keep}, sink {sink}, recent {recent}: expected 1 <= keep and sink + recent <= keep")
+    with _On(dev, stream) as on:
+        made = []
+        for t in (k_out, v_out):
+            if t is None:
+                t = torch.empty((B, keep, heads, dim), dtype=k_cache.dtype, device=dev)
+            else:
+                _need(t.shape == (B, keep, heads, dim) and t.dtype == k_cache.dtype and t.device == dev,
+                      f"k_out, v_out: expected {k_cache.dtype} [{B}, {keep}, {heads}, {dim}] on {dev}")
+                _written(t, "k_out or v_out")
+            made.append(t)
+        kept, index = torch.empty((B, heads, keep), device=dev), torch.empty((B, heads, keep), dtype=torch.int32, device=dev)
+        left = torch.empty(B, dtype=torch.int32, device=dev)
+        if ws is None:
+            ws = torch.empty(evict_workspace_bytes(B, heads, tokens), dtype=torch.uint8, device=dev)
+        else:
+            _need(ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev, "ws: expected contiguous uint8")
+        args = _EVICT.pack(score.data_ptr(), score.stride(0), score.stride(1), _counts(length, B, dev, "length"),
+                           index.data_ptr(), kept.data_ptr(), left.data_ptr(), keep, sink, recent, 0)
+        _check(lib().uzip_kv_evict(cache, _cache(*made, None, B)[0], args, ws.data_ptr(), ws.numel(), on.stream), "evict")
+    return made[0], made[1], kept, left, index
