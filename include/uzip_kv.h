@@ -141,7 +141,7 @@ typedef struct uzip_kv_attend_args {
     uzip_kv_tensor_t q, out;
     float           *lse;       /* [seqs, tokens, heads], contiguous; 4-byte aligned */
     float           *score;     /* 4-byte aligned */
-    int64_t          score_stride[2];  /* sequence, kv head; keys are contiguous, cache->tokens of them */
+    int64_t          score_stride[2];  /* sequence, kv head; keys are contiguous */
     const int32_t   *length;
     const int32_t   *drafted;   /* NULL: all */
     const uint8_t   *tree;      /* NULL: a chain */
@@ -150,6 +150,8 @@ typedef struct uzip_kv_attend_args {
     uint32_t         tokens;
     uint32_t         heads;     /* query heads: a multiple of the cache's */
     float            scale;
+    uint32_t         score_tokens;     /* keys a row of score holds, at most cache->tokens: later ones are not added */
+    uint32_t         reserved;  /* 0 */
 } uzip_kv_attend_args_t;
 int uzip_kv_attend(const uzip_kv_cache_t *cache, const uzip_kv_attend_args_t *a, void *d_ws, uint64_t ws_bytes,
                    hipStream_t s);
@@ -159,7 +161,7 @@ uint64_t uzip_kv_attend_workspace_bytes(uint32_t seqs, uint32_t kv_heads, uint32
                                         uint32_t tokens, uint32_t heads);
 
 /* async. Cuts a cache to `keep` tokens per sequence and head. With n =
- * length[b] (clamped to [0, cache->tokens]), head h keeps min(n, keep) of its
+ * length[b] (clamped to [0, score_tokens]), head h keeps min(n, keep) of its
  * tokens: the first min(sink, n), the last min(recent, n), and of the others
  * those with the largest score, ties to the lower token; NaN ranks with -inf.
  * Kept tokens stay in order: slot j of out holds token index[b, h, j]; slots
@@ -177,7 +179,7 @@ typedef struct uzip_kv_evict_args {
     uint32_t       keep;
     uint32_t       sink;
     uint32_t       recent;
-    uint32_t       reserved;    /* 0 */
+    uint32_t       score_tokens;       /* scores a row holds, at most cache->tokens: the cache is taken to end there */
 } uzip_kv_evict_args_t;
 int uzip_kv_evict(const uzip_kv_cache_t *cache, const uzip_kv_cache_t *out, const uzip_kv_evict_args_t *a,
                   void *d_ws, uint64_t ws_bytes, hipStream_t s);

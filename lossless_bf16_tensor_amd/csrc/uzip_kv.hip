@@ -511,7 +511,8 @@ int uzip_kv_evict(const uzip_kv_cache_t *cache, const uzip_kv_cache_t *out, cons
                   void *d_ws, uint64_t ws_bytes, hipStream_t s)
 {
     using namespace uzip_kv;
-    if (!a || a->reserved || !valid_cache(cache) || !valid_cache(out) || out->table) return UZIP_EINVAL;
+    if (!a || !valid_cache(cache) || !valid_cache(out) || out->table) return UZIP_EINVAL;
+    if (a->score_tokens < 1 || a->score_tokens > cache->tokens) return UZIP_EINVAL;
     if (out->seqs != cache->seqs || out->heads != cache->heads || out->dim != cache->dim || out->dtype != cache->dtype) return UZIP_EINVAL;
     if (a->keep < 1 || out->tokens != a->keep || a->sink > a->keep || a->recent > a->keep - a->sink) return UZIP_EINVAL;
     if (!a->score || !aligned(a->score, 4) || a->score_stride[0] < 0 || a->score_stride[1] < 0) return UZIP_EINVAL;
@@ -522,6 +523,7 @@ int uzip_kv_evict(const uzip_kv_cache_t *cache, const uzip_kv_cache_t *out, cons
     EvictParams p;
     memset(&p, 0, sizeof p);
     p.c = view_of(cache);
+    p.c.tokens = a->score_tokens;
     p.o = view_of(out);
     p.score = a->score;
     p.sc0 = a->score_stride[0], p.sc1 = a->score_stride[1];

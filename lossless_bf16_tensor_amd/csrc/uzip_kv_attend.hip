@@ -37,6 +37,7 @@ struct AttendParams {
     const uint8_t *tree;
     int64_t qs0, qs1, qs2, os0, os1, os2;     // bytes
     int64_t sc0, sc1, tr0, tr1;               // elements
+    int score_tokens;
     float *part_o;                            // [row][split][DP], when nsplit > 1
     float2 *part_ml;                          // [row][split]: maximum (times c), sum
     int T, G, R, D, heads;                    // heads: key/value heads
@@ -612,7 +613,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attend_weigh(AttendParams p)
             float v = sum[hf][k];
             for (int y = 1; y < 16; y <<= 1) v += __shfl_xor(v, y);
             const int key = t.key + 16 * hf + 4 * g + k;
-            if (x == 0 && t.there[hf] && key < end) p.score[b * p.sc0 + h * p.sc1 + key] += v;
+            if (x == 0 && t.there[hf] && key < min(end, p.score_tokens)) p.score[b * p.sc0 + h * p.sc1 + key] += v;
         }
 }
 
@@ -716,7 +717,7 @@ int uzip_kv_attend(const uzip_kv_cache_t *cache, const uzip_kv_attend_args_t *a,
     if (a->dtype > UZIP_KV_F16 || (cache->dtype != UZIP_KV_E5M2 && cache->dtype != a->dtype)) return UZIP_EINVAL;
     if (!a->length || !aligned(a->length, 4) || !aligned(a->drafted, 4) || !aligned(a->lse, 4) || !aligned(a->score, 4)) return UZIP_EINVAL;
     if (!(a->scale >= 0x1p-60f) || !(a->scale <= 0x1p60f)) return UZIP_EINVAL;
-    if (a->score && (a->score_stride[0] < 0 || a->score_stride[1] < 0)) return UZIP_EINVAL;
+    if (a->reserved || (a->score && (a->score_stride[0] < 0 || a->score_stride[1] < 0 || a->score_tokens > cache->tokens))) return UZIP_EINVAL;
     if (a->tree && (a->tree_stride[0] < 0 || a->tree_stride[1] < 0)) return UZIP_EINVAL;
     if (!d_ws || !aligned(d_ws, 16)) return UZIP_EINVAL;
     const Plan plan = make_plan(cache->seqs, cache->heads, cache->dim, cache->tokens, a->tokens, a->heads);
@@ -735,6 +736,7 @@ int uzip_kv_attend(const uzip_kv_cache_t *cache, const uzip_kv_attend_args_t *a,
     p.lse = a->lse ? a->lse : a->score ? reinterpret_cast<float *>(ws + plan.off_lse) : nullptr;
     p.score = a->score;
     p.sc0 = a->score_stride[0], p.sc1 = a->score_stride[1];
+    p.score_tokens = (int)a->score_tokens;
     p.length = a->length;
     p.drafted = a->drafted;
     p.tree = a->tree;

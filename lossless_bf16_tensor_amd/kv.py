@@ -46,7 +46,7 @@ _CACHE = struct.Struct("=3Q7q8I")
 _ROPE = struct.Struct("=2Qq2IfI")
 _TENSOR = struct.Struct("=Q3q")
 _APPEND = struct.Struct("=16q2Q4I")
-_ATTEND = struct.Struct("=8q2Q2q3Q2q3If")
+_ATTEND = struct.Struct("=8q2Q2q3Q2q3If2I")
 _EVICT = struct.Struct("=Q2q4Q4I")
 
 _lib = None
@@ -153,6 +153,15 @@ def _cache(k: torch.Tensor, v: torch.Tensor, table, seqs: int):
     tokens = table.shape[1] * second
     return (_CACHE.pack(k.data_ptr(), v.data_ptr(), table.data_ptr(), *ks, *vs, table.stride(0) if seqs > 1 else 0, dtype,
                         seqs, heads, dim, tokens, second, first, 0), heads, dim, tokens)
+
+
+def _score(score, seqs: int, heads: int, tokens: int, table, device):
+    """((sequence, head) strides, tokens) of accumulated weights: as many tokens as the cache, or fewer when it is in pages."""
+    n = score.shape[-1]
+    _need(score.dtype == torch.float32 and score.shape == (seqs, heads, n) and score.device == device
+          and (n == tokens or (table is not None and 1 <= n < tokens)) and (score.stride(2) == 1 or n == 1),
+          f"score: expected float32 [{seqs}, {heads}, {tokens}] with contiguous rows on {device}")
+    return score.stride()[:2], n
 
 
 def _types(new: torch.Tensor, cache: torch.Tensor):
@@ -285,7 +294,8 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, length
 
     score (float32 [sequences, kv heads, cache tokens]) has the weight that each
     cached token received from the drafted tokens and the heads that share it
-    added. lse (float32 [sequences, tokens, heads], contiguous) receives the log
+    added. A cache in pages may end behind the last token of score: what is
+    there is not added. lse (float32 [sequences, tokens, heads], contiguous) receives the log
     of each query's sum of exponentials. A query that sees nothing gives zeros
     and -inf, as do those from drafted on. Masked keys and values have no
     effect, whatever they hold."""
@@ -301,12 +311,10 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, length
         _need(tree.dtype in (torch.bool, torch.uint8) and tree.device == dev and tree.shape in ((T, T), (B, T, T))
               and (tree.stride(-1) == 1 or T == 1), f"tree: expected bool [{T}, {T}] or [{B}, {T}, {T}] with contiguous rows on {dev}")
         ts = (tree.stride(0) if tree.dim() == 3 else 0, tree.stride(-2))
-    ss = (0, 0)
+    ss, seen = (0, 0), 0
     if score is not None:
-        _need(score.dtype == torch.float32 and score.shape == (B, heads, tokens) and score.device == dev
-              and (score.stride(2) == 1 or tokens == 1), f"score: expected float32 [{B}, {heads}, {tokens}] with contiguous rows on {dev}")
+        ss, seen = _score(score, B, heads, tokens, table, dev)
         _written(score, "score")
-        ss = score.stride()[:2]
     if lse is not None:
         _need(lse.dtype == torch.float32 and lse.shape == (B, T, hq) and lse.is_contiguous() and lse.device == dev,
               f"lse: expected contiguous float32 [{B}, {T}, {hq}] on {dev}")
@@ -323,7 +331,7 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, length
         args = _ATTEND.pack(q.data_ptr(), *qs, out.data_ptr(), *_strides(out), lse.data_ptr() if lse is not None else 0,
                             score.data_ptr() if score is not None else 0, *ss, _counts(length, B, dev, "length"),
                             _counts(drafted, B, dev, "drafted"), tree.data_ptr() if tree is not None else 0, *ts,
-                            _DTYPE[q.dtype], T, hq, 1.0 / math.sqrt(D) if scale is None else scale)
+                            _DTYPE[q.dtype], T, hq, 1.0 / math.sqrt(D) if scale is None else scale, seen, 0)
         _check(lib().uzip_kv_attend(cache, args, ws.data_ptr(), ws.numel(), on.stream), "attend")
     return out
 
@@ -340,7 +348,8 @@ def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, score: torch.Tensor, len
     """Cuts a cache to keep tokens per sequence and head: the first `sink`, the
     last `recent`, and the others with the largest score (float32 [sequences, kv
     heads, cache tokens], as :func:`attend` adds it up), ties to the lower
-    token, NaN last. Returns (k, v, score, length, index): caches [sequences,
+    token, NaN last. A cache in pages may have more tokens than score: it is taken to
+    end with it. Returns (k, v, score, length, index): caches [sequences,
     keep, kv heads, dim] with the kept tokens in order and zeros behind them,
     ready for ``uzip.encode``; their scores [sequences, kv heads, keep]; min(length,
     keep); and where each came from, int32 [sequences, kv heads, keep], -1
@@ -348,8 +357,7 @@ def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, score: torch.Tensor, len
     B = length.numel()
     cache, heads, dim, tokens = _cache(k_cache, v_cache, table, B)
     dev = k_cache.device
-    _need(score.dtype == torch.float32 and score.shape == (B, heads, tokens) and score.device == dev
-          and (score.stride(2) == 1 or tokens == 1), f"score: expected float32 [{B}, {heads}, {tokens}] with contiguous rows on {dev}")
+    ss, seen = _score(score, B, heads, tokens, table, dev)
     _need(1 <= keep <= 1 << 30 and sink >= 0 and recent >= 0 and sink + recent <= keep,
           f"keep {keep}, sink {sink}, recent {recent}: expected 1 <= keep and sink + recent <= keep")
     with _On(dev, stream) as on:
@@ -368,7 +376,7 @@ def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, score: torch.Tensor, len
             ws = torch.empty(evict_workspace_bytes(B, heads, tokens), dtype=torch.uint8, device=dev)
         else:
             _need(ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev, "ws: expected contiguous uint8")
-        args = _EVICT.pack(score.data_ptr(), score.stride(0), score.stride(1), _counts(length, B, dev, "length"),
-                           index.data_ptr(), kept.data_ptr(), left.data_ptr(), keep, sink, recent, 0)
+        args = _EVICT.pack(score.data_ptr(), *ss, _counts(length, B, dev, "length"),
+                           index.data_ptr(), kept.data_ptr(), left.data_ptr(), keep, sink, recent, seen)
         _check(lib().uzip_kv_evict(cache, _cache(*made, None, B)[0], args, ws.data_ptr(), ws.numel(), on.stream), "evict")
     return made[0], made[1], kept, left, index

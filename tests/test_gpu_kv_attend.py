@@ -169,6 +169,17 @@ def test_absent_pages():
     check(q, k, v, [190, 190], table=table)
 
 
+def test_score_shorter_than_the_pages():
+    q, k, v, table = make(2, 5, 4, 2, 64, 75, layout="paged32", seed=8)
+    n = torch.tensor([70, 20], dtype=torch.int32)
+    want = ref.attend(q, k, v, n, table=table)
+    whole = torch.zeros(2, 2, 80, device=DEV)
+    out = kv.attend(put(q), put(k), put(v), n.to(DEV), table=put(table), score=whole[..., :73])
+    ref.within(out, want["out"], want["out_bound"])
+    ref.within(whole[..., :73], want["weight"][..., :73], want["weight_bound"][..., :73])
+    assert not whole[..., 73:].any()
+
+
 def test_lengths_outside_the_cache_are_clamped():
     q, k, v, _ = make(4, 3, 4, 2, 64, 50, seed=2)
     check(q, k, v, [-5, 49, 50, 2 ** 31 - 1], drafted=[3, 3, 2, 9])

@@ -48,7 +48,6 @@ def run(B, H, S, D, lens, keep, sink, recent, kind="plain", cache=BF16, layout="
         per = -(-S // page)
         k, v = mk(B * per + 1, page, H, D), mk(B * per + 1, page, H, D)
         table = torch.randperm(B * per + 1, generator=g)[:B * per].view(B, per).to(torch.int32)
-        S = per * page
     else:
         k, v = mk(B, S, H, D), mk(B, S, H, D)
     score = scores(kind, B, H, S, seed)

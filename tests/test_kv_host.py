@@ -47,9 +47,9 @@ BAD_CACHES = [dict(k=0), dict(v=0), dict(k=(1 << 20) + 8), dict(ks=(0, 512, 100)
 
 
 def attend(c=None, q=None, out=None, lse=0, score=0, ss=(256, 64), length=1 << 24, drafted=0, tree=0, ts=(0, 4), dtype=0, T=4,
-           heads=8, scale=0.1, ws=1 << 25, ws_bytes=1 << 40):
+           heads=8, scale=0.1, seen=64, reserved=0, ws=1 << 25, ws_bytes=1 << 40):
     args = kv._ATTEND.pack(*struct.unpack("=Q3q", q or tensor()), *struct.unpack("=Q3q", out or tensor()), lse, score, *ss, length,
-                           drafted, tree, *ts, dtype, T, heads, scale)
+                           drafted, tree, *ts, dtype, T, heads, scale, seen, reserved)
     return kv.lib().uzip_kv_attend(c or cache(), args, ws, ws_bytes, None)
 
 
@@ -65,7 +65,8 @@ def test_bad_caches_are_refused(bad):
     dict(q=tensor(0)), dict(q=tensor(8)), dict(q=tensor(stride=(0, 4, 8))), dict(out=tensor(0)), dict(out=tensor(stride=(0, -8, 8))),
     dict(length=0), dict(length=2), dict(drafted=2), dict(lse=1), dict(score=3), dict(score=1 << 20, ss=(-1, 64)),
     dict(tree=1 << 20, ts=(-4, 4)), dict(dtype=1), dict(dtype=2), dict(T=0), dict(T=(1 << 20) + 1), dict(heads=0), dict(heads=6),
-    dict(heads=3), dict(scale=0.0), dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan), dict(scale=2.0 ** -61), dict(ws=0), dict(ws=8)])
+    dict(heads=3), dict(scale=0.0), dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan), dict(scale=2.0 ** -61), dict(ws=0), dict(ws=8),
+    dict(score=1 << 20, seen=65), dict(reserved=1)])
 def test_attend_refuses(bad):
     assert attend(**bad) == EINVAL
 
@@ -128,8 +129,8 @@ def test_rope_refuses(args):
 
 
 def evict(c=None, out=None, score=1 << 24, ss=(256, 64), length=1 << 24, index=1 << 24, score_out=0, length_out=0, keep=16, sink=2,
-          recent=4, reserved=0, ws=1 << 25, ws_bytes=1 << 40):
-    args = kv._EVICT.pack(score, *ss, length, index, score_out, length_out, keep, sink, recent, reserved)
+          recent=4, seen=64, ws=1 << 25, ws_bytes=1 << 40):
+    args = kv._EVICT.pack(score, *ss, length, index, score_out, length_out, keep, sink, recent, seen)
     return kv.lib().uzip_kv_evict(c or cache(), out or cache(k=1 << 26, v=1 << 27, tokens=16), args, ws, ws_bytes, None)
 
 
@@ -139,7 +140,7 @@ def evict(c=None, out=None, score=1 << 24, ss=(256, 64), length=1 << 24, index=1
     dict(out=cache(k=1 << 26, v=1 << 27, tokens=16, seqs=2)), dict(out=cache(tokens=16)),
     dict(out=cache(k=1 << 26, v=1 << 27, tokens=16, table=1 << 24, page=16, pages=4)), dict(score=0), dict(score=2), dict(ss=(-1, 0)),
     dict(length=0), dict(index=0), dict(index=2), dict(score_out=2), dict(length_out=1), dict(keep=0), dict(sink=17), dict(sink=10, recent=7),
-    dict(reserved=1), dict(ws=0), dict(ws=4)])
+    dict(seen=0), dict(seen=65), dict(ws=0), dict(ws=4)])
 def test_evict_refuses(bad):
     assert evict(**bad) == EINVAL
 
