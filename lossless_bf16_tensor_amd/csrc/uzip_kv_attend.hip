@@ -27,6 +27,7 @@ namespace {
 
 constexpr int kWaves = 4;                     // per workgroup
 constexpr int kTileKeys = 32;
+constexpr float kSlack = 8.f;
 
 struct AttendParams {
     CacheView c;
@@ -91,14 +92,6 @@ __device__ inline uint32_t not_finite(uint32_t w)
         const uint32_t t = ((w & (e | e << 16)) + (one | one << 16)) & 0x80008000u;
         return (t << 1) - (t >> 15);
     }
-}
-
-template <int CT>
-__device__ inline float load_value(const char *p)
-{
-    if constexpr (CT == kE5M2) return f16_to_f32((uint16_t)(*reinterpret_cast<const uint8_t *>(p) << 8));
-    if constexpr (CT == kBF16) return bf16_to_f32(*reinterpret_cast<const uint16_t *>(p));
-    return f16_to_f32(*reinterpret_cast<const uint16_t *>(p));
 }
 
 // A row's 16-byte fragments of Q for the matrix cores (8 dims at 32 ks + 8 g).
@@ -184,6 +177,34 @@ struct TileFinder {
     }
 };
 
+// What a lane's row sees of its eight keys, a bit each: keys 4 g .. 4 g + 3 of
+// both halves of a tile.
+// ... those before place `left` behind the lane's first key
+__device__ inline uint32_t leading_bits(int left)
+{
+    const int a = min(max(left, 0), 4), c = min(max(left - 16, 0), 4);
+    return ((1u << a) - 1) | ((1u << c) - 1) << 4;
+}
+
+// ... those whose page is there
+__device__ inline uint32_t there_bits(const Tile &t) { return (t.there[0] ? 0x0fu : 0) | (t.there[1] ? 0xf0u : 0); }
+
+// ... those of the drafted tokens, the first of them drafted token j0, that
+// the mask names. Its bytes are read at places held inside it, all at once.
+__device__ inline uint32_t tree_bits(const AttendParams &p, int b, int tok, int j0, int nd)
+{
+    const uint8_t *row = p.tree + b * p.tr0 + min(tok, nd - 1) * p.tr1;
+    uint32_t bits = 0, named[8];
+#pragma unroll
+    for (int k = 0; k < 8; k++) named[k] = row[min(max(j0 + 16 * (k >> 2) + (k & 3), 0), nd - 1)];
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+        const int j = j0 + 16 * (k >> 2) + (k & 3);
+        bits |= named[k] && j >= 0 && j < nd ? 1u << k : 0;
+    }
+    return bits;
+}
+
 // 8 dims (32 ks + 8 g ..) of key x in each half
 template <int CT, int KS, bool PAD, bool MASKED>
 __device__ inline void load_keys(const AttendParams &p, const Tile &t, int end, int x, int g, uint32_t off, Raw<CT> (&r)[2][KS])
@@ -247,99 +268,35 @@ __global__ __launch_bounds__(kWaves * 64, RB == 4 || DP == 256 ? 1 : 2) void k_a
     if (!p.tree) lim = min(end, n + min((min(row0 + RB * 16, p.R) - 1) / p.G, p.T - 1) + 1);
 
     f32x4 acc[RB][NV] = {};
-    float m[RB], l[RB];
+    float m[RB], l[RB];                           // l: of this lane's keys
 #pragma unroll
     for (int rb = 0; rb < RB; rb++) m[rb] = -INFINITY, l[rb] = 0.f;
 
     const uint32_t koff = (uint32_t)(x * p.c.ks1) + g * 8 * es;
     const uint32_t voff = (uint32_t)(g * 4 * p.c.vs1) + x * VE * es;
-    TileFinder finder;
-    Tile nxt;
-    Raw<CT> kr[2][KS];
-    const int first = t0 + wkey;
-    if (first < t1 && row0 < p.R) {
-        nxt = finder.at(p, b, h, 0, first, n, lim);
-        if (nxt.fast) load_keys<CT, KS, PAD, false>(p, nxt, lim, x, g, koff, kr);
-    }
-    for (int i = 0; row0 < p.R && first + i * p.wk < t1; i++) {
-        const Tile t = nxt;
-        typedef uint32_t vraw __attribute__((ext_vector_type(VW)));
-        vraw vr[VC][8];
-        if (t.fast) {
-#pragma unroll
-            for (int c = 0; c < VC; c++)
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    if (PAD) vr[c][j] = vraw{};
-                    if (!PAD || c * 128 + x * VE < p.D)
-                        vr[c][j] = *reinterpret_cast<const vraw *>(t.v[j >> 2] + (j & 3) * p.c.vs1 + (voff + c * 128 * es));
-                }
-        } else {
-            load_keys<CT, KS, PAD, true>(p, t, lim, x, g, koff, kr);
-#pragma unroll
-            for (int c = 0; c < VC; c++)
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    vr[c][j] = vraw{};
-                    if ((!PAD || c * 128 + x * VE < p.D) && t.there[j >> 2] && t.key + 16 * (j >> 2) + 4 * g + (j & 3) < lim)
-                        vr[c][j] = *reinterpret_cast<const vraw *>(t.v[j >> 2] + (j & 3) * p.c.vs1 + (voff + c * 128 * es));
-                }
-        }
+    typedef uint32_t vraw __attribute__((ext_vector_type(VW)));
 
-        f32x4 s[RB][2] = {};
+    const auto score_tile = [&](const Raw<CT> (&kr)[2][KS], f32x4 (&s)[RB][2]) {
 #pragma unroll
         for (int hf = 0; hf < 2; hf++)
 #pragma unroll
             for (int ks = 0; ks < KS; ks++) {
                 const u32x4 a = widen<CT>(kr[hf][ks]);
 #pragma unroll
-                for (int rb = 0; rb < RB; rb++) s[rb][hf] = mfma<CT>(a, q[rb][ks], s[rb][hf]);
+                for (int rb = 0; rb < RB; rb++) s[rb][hf] = mfma<CT>(a, q[rb][ks], ks ? s[rb][hf] : f32x4{0.f, 0.f, 0.f, 0.f});
             }
-        // the next tile's keys are on their way while this one is finished
-        if (first + (i + 1) * p.wk < t1) {
-            nxt = finder.at(p, b, h, i + 1, first, n, lim);
-            if (nxt.fast) load_keys<CT, KS, PAD, false>(p, nxt, lim, x, g, koff, kr);
-        }
-
-        uint32_t seen[RB];
-        bool odd = false;                         // values that are not finite, in a tile that not all rows see
-        if (!t.fast) {
-#pragma unroll
-            for (int rb = 0; rb < RB; rb++) {
-                seen[rb] = 0;
-#pragma unroll
-                for (int hf = 0; hf < 2; hf++)
-#pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        const int key = t.key + 16 * hf + 4 * g + k;
-                        bool see = t.there[hf] && key < lim;
-                        if (see && key >= n)
-                            see = p.tree ? tok[rb] < nd && p.tree[b * p.tr0 + tok[rb] * p.tr1 + (key - n)] != 0 : key - n <= tok[rb];
-                        if (see) seen[rb] |= 1u << (hf * 4 + k);
-                        else s[rb][hf][k] = -INFINITY;
-                    }
-            }
-            uint32_t any = 0;
-#pragma unroll
-            for (int c = 0; c < VC; c++)
-#pragma unroll
-                for (int j = 0; j < 8; j++)
-#pragma unroll
-                    for (int w = 0; w < VW; w++) {
-                        const uint32_t bad = not_finite<CT>(vr[c][j][w]);
-                        any |= bad;
-                        vr[c][j][w] &= ~bad;
-                    }
-            odd = __builtin_amdgcn_ballot_w64(any != 0) != 0;
-        }
-
-        u32x4 pw[RB];
+    };
+    // Scores to weights. m need not be the maximum so far, only near it: the
+    // weights stay below 2^kSlack and nothing is lost in binary32, while the
+    // output is scaled anew in the first tile and then hardly ever.
+    const auto weigh_tile = [&](f32x4 (&s)[RB][2], u32x4 (&pw)[RB]) {
 #pragma unroll
         for (int rb = 0; rb < RB; rb++) {
             float top = fmaxf(fmaxf(fmaxf(s[rb][0][0], s[rb][0][1]), fmaxf(s[rb][0][2], s[rb][0][3])),
                               fmaxf(fmaxf(s[rb][1][0], s[rb][1][1]), fmaxf(s[rb][1][2], s[rb][1][3])));
-            top = fmaxf(quad_max(top), m[rb]);
-            if (__builtin_amdgcn_ballot_w64(top > m[rb])) {
+            top = quad_max(top);
+            if (__builtin_amdgcn_ballot_w64((top - m[rb]) * c2[rb] > kSlack)) {
+                top = fmaxf(top, m[rb]);
                 const float a = __builtin_amdgcn_exp2f((m[rb] - (top == -INFINITY ? 0.f : top)) * c2[rb]);
                 m[rb] = top;
                 l[rb] *= a;
@@ -354,64 +311,163 @@ __global__ __launch_bounds__(kWaves * 64, RB == 4 || DP == 256 ? 1 : 2) void k_a
                     s[rb][hf][k] = __builtin_amdgcn_exp2f(fmaf(s[rb][hf][k], c2[rb], -base));
                     l[rb] += s[rb][hf][k];
                 }
-            // the one rounding of the weights: half a step of the values' own type
+            // The one rounding of the weights, half a step of the products'
+            // type. Their sum is taken before it: lse keeps binary32.
             pw[rb] = u32x4{pack2<f16>(s[rb][0][0], s[rb][0][1]), pack2<f16>(s[rb][0][2], s[rb][0][3]),
                            pack2<f16>(s[rb][1][0], s[rb][1][1]), pack2<f16>(s[rb][1][2], s[rb][1][3])};
         }
-
+    };
+    // element (c, e) of the lane's dims for its eight keys
+    const auto value_fragment = [&](const vraw (&vr)[VC][8], int c, int e) {
+        u32x4 a;
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            if constexpr (CT == kE5M2) {
+                const uint32_t sel = ((4u + e % 4) << 24) | (0x0cu << 16) | ((uint32_t)(e % 4) << 8) | 0x0cu;
+                a[k] = __builtin_amdgcn_perm(vr[c][2 * k + 1][e / 4], vr[c][2 * k][e / 4], sel);
+            } else {
+                a[k] = __builtin_amdgcn_perm(vr[c][2 * k + 1][e / 2], vr[c][2 * k][e / 2], e % 2 ? 0x07060302u : 0x05040100u);
+            }
+        }
+        return a;
+    };
+    const auto add_tile = [&](const vraw (&vr)[VC][8], const u32x4 (&pw)[RB]) {
 #pragma unroll
         for (int c = 0; c < VC; c++)
 #pragma unroll
             for (int e = 0; e < VE; e++) {
-                u32x4 a;
-#pragma unroll
-                for (int k = 0; k < 4; k++) {     // keys 2k, 2k + 1 of the lane's eight
-                    if constexpr (CT == kE5M2) {
-                        const uint32_t sel = ((4u + e % 4) << 24) | (0x0cu << 16) | ((uint32_t)(e % 4) << 8) | 0x0cu;
-                        a[k] = __builtin_amdgcn_perm(vr[c][2 * k + 1][e / 4], vr[c][2 * k][e / 4], sel);
-                    } else {
-                        a[k] = __builtin_amdgcn_perm(vr[c][2 * k + 1][e / 2], vr[c][2 * k][e / 2], e % 2 ? 0x07060302u : 0x05040100u);
-                    }
-                }
+                const u32x4 a = value_fragment(vr, c, e);
 #pragma unroll
                 for (int rb = 0; rb < RB; rb++) acc[rb][c * VE + e] = mfma<CT>(a, pw[rb], acc[rb][c * VE + e]);
             }
+    };
 
-        if (odd) {
-            // Values that are not finite were left out above; add them for the
-            // rows that see their key (0 * inf is NaN there, as it should be).
-            // Rare: weights go through LDS, -1 where a row does not see the key.
-            float *w = smem + wave * RB * 16 * 32;
+    // Tiles that every row sees: keys one tile ahead in registers, values
+    // loaded while the scores are worked out.
+    const int first = t0 + wkey, count = row0 < p.R ? (t1 - first + p.wk - 1) / p.wk : 0;
+    int i = 0;
+    if (count > 0) {
+        TileFinder finder;
+        Tile t = finder.at(p, b, h, 0, first, n, lim);
+        Raw<CT> kr[2][KS];
+        if (t.fast) load_keys<CT, KS, PAD, false>(p, t, lim, x, g, koff, kr);
+        while (t.fast) {
+            Tile nxt = t;
+            nxt.fast = false;
+            if (++i < count) {
+                const Tile f = finder.at(p, b, h, i, first, n, lim);
+                if (f.fast) nxt = f;
+            }
+            vraw vr[VC][8];
+#pragma unroll
+            for (int c = 0; c < VC; c++)
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    if (PAD) vr[c][j] = vraw{};
+                    if (!PAD || c * 128 + x * VE < p.D)
+                        vr[c][j] = *reinterpret_cast<const vraw *>(t.v[j >> 2] + (j & 3) * p.c.vs1 + (voff + c * 128 * es));
+                }
+            f32x4 s[RB][2];
+            u32x4 pw[RB];
+            score_tile(kr, s);
+            load_keys<CT, KS, PAD, false>(p, nxt, lim, x, g, koff, kr);   // the same ones again after the last
+            weigh_tile(s, pw);
+            add_tile(vr, pw);
+            t = nxt;
+        }
+    }
+    // The others: the drafted tokens' own tiles, the last one, absent pages.
+    TileFinder finder;
+    for (; i < count; i++) {
+        const Tile t = finder.at(p, b, h, i, first, n, lim);
+        if (t.key >= lim) break;
+        Raw<CT> kr[2][KS];
+        vraw vr[VC][8];
+        load_keys<CT, KS, PAD, true>(p, t, lim, x, g, koff, kr);
+#pragma unroll
+        for (int c = 0; c < VC; c++)
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                vr[c][j] = vraw{};
+                if ((!PAD || c * 128 + x * VE < p.D) && t.there[j >> 2] && t.key + 16 * (j >> 2) + 4 * g + (j & 3) < lim)
+                    vr[c][j] = *reinterpret_cast<const vraw *>(t.v[j >> 2] + (j & 3) * p.c.vs1 + (voff + c * 128 * es));
+            }
+        f32x4 s[RB][2];
+        u32x4 pw[RB];
+        score_tile(kr, s);
+        uint32_t seen[RB];
+#pragma unroll
+        for (int rb = 0; rb < RB; rb++) seen[rb] = 0;
+        if (p.tree) {
+#pragma unroll
+            for (int rb = 0; rb < RB; rb++) seen[rb] = tree_bits(p, b, tok[rb], t.key + 4 * g - n, nd);
+        }
+#pragma unroll
+        for (int rb = 0; rb < RB; rb++) {
+            seen[rb] |= leading_bits((p.tree ? n : min(lim, n + tok[rb] + 1)) - t.key - 4 * g);
+            seen[rb] &= there_bits(t);
+#pragma unroll
+            for (int k = 0; k < 8; k++) s[rb][k >> 2][k & 3] = seen[rb] >> k & 1 ? s[rb][k >> 2][k & 3] : -INFINITY;
+        }
+        weigh_tile(s, pw);
+        // A value that is not finite must reach only the rows that see its
+        // key, and in a product it would reach all (0 * inf). Rare: count the
+        // seen ones per row and dim with products of zeros and ones, +inf and
+        // NaN in one, -inf and NaN in the other, and leave them out below.
+        uint32_t any = 0;
+#pragma unroll
+        for (int c = 0; c < VC; c++)
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+#pragma unroll
+                for (int w = 0; w < VW; w++) any |= not_finite<CT>(vr[c][j][w]);
+        if (__builtin_amdgcn_ballot_w64(any != 0)) {
+            constexpr uint32_t one = f16 ? 0x3c003c00u : 0x3f803f80u;
+            u32x4 pi[RB];
 #pragma unroll
             for (int rb = 0; rb < RB; rb++)
 #pragma unroll
-                for (int k = 0; k < 8; k++)
-                    w[(rb * 16 + x) * 32 + (k >> 2) * 16 + 4 * g + (k & 3)] = seen[rb] >> k & 1 ? s[rb][k >> 2][k & 3] : -1.f;
-            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            for (int k = 0; k < kTileKeys && t.key + k < lim; k++) {
-                if (!(k < 16 ? t.there[0] : t.there[1])) continue;
-                const char *vrow = (k < 16 ? t.v[0] : t.v[1]) + (k & 15) * p.c.vs1;
+                for (int k = 0; k < 4; k++)
+                    pi[rb][k] = (seen[rb] >> (2 * k) & 1 ? one & 0xffffu : 0) | (seen[rb] >> (2 * k + 1) & 1 ? one & 0xffff0000u : 0);
+            constexpr uint32_t top16 = f16 ? 0x7c00u : 0x7f80u;
 #pragma unroll
-                for (int c = 0; c < VC; c++)
+            for (int c = 0; c < VC; c++)
 #pragma unroll
-                    for (int ii = 0; ii < 4; ii++)
+                for (int e = 0; e < VE; e++) {
+                    const u32x4 a = value_fragment(vr, c, e);
+                    u32x4 up, down;
 #pragma unroll
-                        for (int e = 0; e < VE; e++) {
-                            const int d = c * 128 + (4 * g + ii) * VE + e;
-                            if (PAD && d >= p.D) continue;
-                            const float v = load_value<CT>(vrow + d * es);
-                            if (fabsf(v) < INFINITY) continue;
+                    for (int k = 0; k < 4; k++) {
+                        const uint32_t bad = not_finite<f16 ? kF16 : kBF16>(a[k]);
+                        uint32_t u = 0, d = 0;
 #pragma unroll
-                            for (int rb = 0; rb < RB; rb++) {
-                                const float weight = w[(rb * 16 + x) * 32 + k];
-                                if (!(weight < 0.f)) acc[rb][c * VE + e][ii] += weight * v;
+                        for (int half = 0; half < 2; half++) {
+                            const uint32_t v = a[k] >> (16 * half) & 0xffffu, o = (one & 0xffffu) << (16 * half);
+                            if (bad >> (16 * half) & 1) {
+                                if (v != (top16 | 0x8000u)) u |= o;
+                                if (v != top16) d |= o;
                             }
                         }
-            }
-            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-            __builtin_amdgcn_wave_barrier();
+                        up[k] = u, down[k] = d;
+                    }
+#pragma unroll
+                    for (int rb = 0; rb < RB; rb++) {
+                        const f32x4 nu = mfma<CT>(up, pi[rb], f32x4{0.f, 0.f, 0.f, 0.f}), nn = mfma<CT>(down, pi[rb], f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            if (nu[k] > 0.f) acc[rb][c * VE + e][k] += INFINITY;
+                            if (nn[k] > 0.f) acc[rb][c * VE + e][k] -= INFINITY;
+                        }
+                    }
+                }
+#pragma unroll
+            for (int c = 0; c < VC; c++)
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+#pragma unroll
+                    for (int w = 0; w < VW; w++) vr[c][j][w] &= ~not_finite<CT>(vr[c][j][w]);
         }
+        add_tile(vr, pw);
     }
 
     // join the waves that split the keys
@@ -422,7 +478,6 @@ __global__ __launch_bounds__(kWaves * 64, RB == 4 || DP == 256 ? 1 : 2) void k_a
     }
     if (p.wk > 1) {
         float *ml = smem + 2 * RB * 16 * DP;      // [wave][row][2]
-        __syncthreads();                          // the weights above share this memory
         if (g == 0)
 #pragma unroll
             for (int rb = 0; rb < RB; rb++) {
@@ -512,21 +567,23 @@ __global__ __launch_bounds__(kWaves * 64, RB == 4 || DP == 256 ? 1 : 2) void k_a
     }
 }
 
-// Joins a row's splits; a workgroup a row, its waves taking every fourth split.
-template <int DP>
-__global__ __launch_bounds__(256) void k_attend_join(AttendParams p, int half)
+// Joins a row's splits: W waves a row, each taking every W-th split.
+template <int DP, int W>
+__global__ __launch_bounds__(kWaves * 64) void k_attend_join(AttendParams p, int64_t rows, int half)
 {
-    __shared__ float so[kWaves][DP];
-    constexpr int E = DP / 64;
-    const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
-    const int64_t row = blockIdx.x;                // ((b * heads) + h) * R + r
+    constexpr int E = DP / 64, U = 8;             // dims a lane, splits whose loads are under way together
+    __shared__ float so[W > 1 ? kWaves : 1][DP];
+    const int lane = (int)(threadIdx.x & 63), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int64_t row = (int64_t)blockIdx.x * (kWaves / W) + wave / W;      // ((b * heads) + h) * R + r
+    if (row >= rows) return;                      // W == 1 only: rows are whole workgroups otherwise
+    const int part = wave % W;
     const int r = (int)(row % p.R), h = (int)(row / p.R % p.heads), b = (int)(row / p.R / p.heads);
     const int n = clamp_length(p.length, b, p.c.tokens), nd = clamp_drafted(p.drafted, b, p.T);
     const int end = nd == 0 ? 0 : (uint32_t)nd > p.c.tokens - (uint32_t)n ? (int)p.c.tokens : n + nd;
     const int ntiles = (end + kTileKeys - 1) / kTileKeys, tps = tiles_per_split(ntiles, p);
     const int used = (ntiles + tps - 1) / tps, tok = r / p.G, head = h * p.G + r % p.G;
     const float2 *ml = p.part_ml + row * p.nsplit;
-    const float *po = p.part_o + row * p.nsplit * DP;
+    const float *po = p.part_o + row * p.nsplit * DP + lane * E;
 
     float top = -INFINITY;
     for (int k = lane; k < used; k += 64) top = fmaxf(top, ml[k].x);
@@ -538,23 +595,43 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendParams p, int half)
 
     typedef float fe __attribute__((ext_vector_type(E)));
     fe o = {};
-    for (int k = wave; k < used; k += kWaves) {
-        const float a = __builtin_amdgcn_exp2f(ml[k].x - base);
-        if constexpr (E == 1) o += po[(int64_t)k * DP + lane] * a;
-        else o += *reinterpret_cast<const fe *>(po + (int64_t)k * DP + lane * E) * a;
+    for (int k0 = part; k0 < used; k0 += W * U) {
+        fe v[U];
+        float a[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            const int k = min(k0 + u * W, used - 1);
+            a[u] = ml[k].x;
+            if constexpr (E == 1) v[u][0] = po[(int64_t)k * DP];
+            else v[u] = *reinterpret_cast<const fe *>(po + (int64_t)k * DP);
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++)
+            if (k0 + u * W < used) o += v[u] * __builtin_amdgcn_exp2f(a[u] - base);
     }
-    if constexpr (E == 1) so[wave][lane] = o[0];
-    else *reinterpret_cast<fe *>(&so[wave][lane * E]) = o;
-    __syncthreads();
+    if constexpr (W > 1) {
+        if constexpr (E == 1) so[wave][lane] = o[0];
+        else *reinterpret_cast<fe *>(&so[wave][lane * E]) = o;
+        __syncthreads();
+        if (part) return;
+        for (int w = 1; w < W; w++)
+            if constexpr (E == 1) o[0] += so[wave + w][lane];
+            else o += *reinterpret_cast<const fe *>(&so[wave + w][lane * E]);
+    }
     const bool empty = sum == 0.f || tok >= nd;
-    if (threadIdx.x == 0 && p.lse) p.lse[((int64_t)b * p.T + tok) * (p.heads * p.G) + head] = empty ? -INFINITY : (top + __log2f(sum)) * 0.6931471805599453f;
-    const int d = 2 * (int)threadIdx.x;
-    if (d < p.D) {
-        const float inv = empty ? 0.f : 1.f / sum;
-        float u = so[0][d] + so[1][d] + so[2][d] + so[3][d], v = so[0][d + 1] + so[1][d + 1] + so[2][d + 1] + so[3][d + 1];
-        u = empty ? 0.f : u * inv;
-        v = empty ? 0.f : v * inv;
-        *reinterpret_cast<uint32_t *>(p.out + b * p.os0 + tok * p.os1 + head * p.os2 + d * 2) = half ? pack2<true>(u, v) : pack2<false>(u, v);
+    if (lane == 0 && p.lse) p.lse[((int64_t)b * p.T + tok) * (p.heads * p.G) + head] = empty ? -INFINITY : (top + __log2f(sum)) * 0.6931471805599453f;
+    if (lane * E >= p.D) return;
+    const float inv = 1.f / sum;
+    char *out = p.out + b * p.os0 + tok * p.os1 + head * p.os2 + lane * E * 2;
+    if constexpr (E == 1) {
+        const float u = empty ? 0.f : o[0] * inv;
+        *reinterpret_cast<uint16_t *>(out) = (uint16_t)(half ? pack2<true>(u, 0.f) : pack2<false>(u, 0.f));
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+            const float u = empty ? 0.f : o[e] * inv, v = empty ? 0.f : o[e + 1] * inv;
+            *reinterpret_cast<uint32_t *>(out + e * 2) = half ? pack2<true>(u, v) : pack2<false>(u, v);
+        }
     }
 }
 
@@ -582,39 +659,67 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attend_weigh(AttendParams p)
     const Tile t = finder.at(p, b, h, 0, tile, n, end);
     Raw<CT> kr[2][KS];
     load_keys<CT, KS, PAD, true>(p, t, end, x, g, (uint32_t)(x * p.c.ks1) + g * 8 * es, kr);
+    // the sum this lane will add to, on its way already
+    const int key = t.key + 16 * (x >> 2 & 1) + 4 * g + (x & 3);
+    const bool mine = (x & 4 ? t.there[1] : t.there[0]) && key < min(end, p.score_tokens);
+    float *at = p.score + b * p.sc0 + h * p.sc1 + key;
+    const float old = mine ? *at : 0.f;
     f32x4 sum[2] = {};
-    for (int r0 = 0; r0 < nd * p.G; r0 += 16) {
-        const int r = r0 + x, tok = r / p.G, head = h * p.G + r % p.G;
-        const bool row = r < nd * p.G;
-        u32x4 q[KS];
-        const float c2 = p.c2 * load_q<CT, KS, PAD>(p, p.q + b * p.qs0 + tok * p.qs1 + head * p.qs2, row, g, q);
-        const float lse = row ? p.lse[((int64_t)b * p.T + tok) * (p.heads * p.G) + head] : -INFINITY;
-        const float base = lse * 1.4426950408889634f;
-        f32x4 s[2] = {};
+    const int rows = nd * p.G;
+    u32x4 q[KS];
+    float c2, lse;
+    int tok;
+    const auto load_row = [&](int r0) {
+        const int r = r0 + x;
+        tok = r / p.G;
+        const int head = h * p.G + r % p.G;
+        c2 = p.c2 * load_q<CT, KS, PAD>(p, p.q + b * p.qs0 + tok * p.qs1 + head * p.qs2, r < rows, g, q);
+        lse = r < rows ? p.lse[((int64_t)b * p.T + tok) * (p.heads * p.G) + head] : -INFINITY;
+    };
+    load_row(0);
+    for (int r0 = 0; r0 < rows; r0 += 16) {
+        f32x4 s[2];
 #pragma unroll
         for (int hf = 0; hf < 2; hf++)
 #pragma unroll
-            for (int ks = 0; ks < KS; ks++) s[hf] = mfma<CT>(widen<CT>(kr[hf][ks]), q[ks], s[hf]);
+            for (int ks = 0; ks < KS; ks++) s[hf] = mfma<CT>(widen<CT>(kr[hf][ks]), q[ks], ks ? s[hf] : f32x4{0.f, 0.f, 0.f, 0.f});
+        const float base = lse * 1.4426950408889634f, scale = c2;
+        const bool any = lse != -INFINITY;
+        const int me = tok;
+        if (r0 + 16 < rows) load_row(r0 + 16);
+        if (t.fast) {
 #pragma unroll
-        for (int hf = 0; hf < 2; hf++)
+            for (int hf = 0; hf < 2; hf++)
 #pragma unroll
-            for (int k = 0; k < 4; k++) {
-                const int key = t.key + 16 * hf + 4 * g + k;
-                bool see = row && t.there[hf] && key < end && lse != -INFINITY;
-                if (see && key >= n)
-                    see = p.tree ? p.tree[b * p.tr0 + tok * p.tr1 + (key - n)] != 0 : key - n <= tok;
-                if (see) sum[hf][k] += __builtin_amdgcn_exp2f(fmaf(s[hf][k], c2, -base));
-            }
-    }
-#pragma unroll
-    for (int hf = 0; hf < 2; hf++)
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-            float v = sum[hf][k];
-            for (int y = 1; y < 16; y <<= 1) v += __shfl_xor(v, y);
-            const int key = t.key + 16 * hf + 4 * g + k;
-            if (x == 0 && t.there[hf] && key < min(end, p.score_tokens)) p.score[b * p.sc0 + h * p.sc1 + key] += v;
+                for (int k = 0; k < 4; k++) {
+                    const float w = __builtin_amdgcn_exp2f(fmaf(s[hf][k], scale, -base));
+                    sum[hf][k] += any ? w : 0.f;
+                }
+            continue;
         }
+        uint32_t seen = p.tree ? tree_bits(p, b, me, t.key + 4 * g - n, nd) : 0;
+        seen |= leading_bits((p.tree ? n : min(end, n + me + 1)) - t.key - 4 * g);
+        seen = any ? seen & there_bits(t) : 0;
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const float w = __builtin_amdgcn_exp2f(fmaf(s[k >> 2][k & 3], scale, -base));
+            sum[k >> 2][k & 3] += seen >> k & 1 ? w : 0.f;
+        }
+    }
+    // Sums over the 16 lanes of a row of lanes, halving the keys a lane holds
+    // with each step: lane x ends with key x % 8 of the eight.
+    float v[8] = {sum[0][0], sum[0][1], sum[0][2], sum[0][3], sum[1][0], sum[1][1], sum[1][2], sum[1][3]};
+#pragma unroll
+    for (int half = 4; half; half >>= 1) {
+        const bool up = x & half;
+#pragma unroll
+        for (int k = 0; k < half; k++) {
+            const float give = up ? v[k] : v[k + half], keep = up ? v[k + half] : v[k];
+            v[k] = keep + __shfl_xor(give, half);
+        }
+    }
+    v[0] += __shfl_xor(v[0], 8);
+    if (x < 8 && mine) *at = old + v[0];
 }
 
 // ------------------------------------------------------------------- host --
@@ -639,7 +744,7 @@ Plan make_plan(uint32_t seqs, uint32_t kv_heads, uint32_t dim, uint32_t cache_to
     a.min_tiles = 2 * a.wk;
     const uint64_t base = (uint64_t)seqs * kv_heads * a.nrg;
     const uint64_t tiles = ((uint64_t)cache_tokens + kTileKeys - 1) / kTileKeys;
-    const uint64_t want = a.RB == 1 ? 8 * kCUs : 4 * kCUs;
+    const uint64_t want = a.RB == 1 ? 8 * kCUs : a.RB == 2 ? 4 * kCUs : 2 * kCUs;
     uint64_t split = (want + base - 1) / base;
     const uint64_t most = (tiles + a.min_tiles - 1) / a.min_tiles;
     split = split > most ? most : split;
@@ -677,7 +782,9 @@ int run(const AttendParams &p, const Plan &plan, int seqs, int half, hipStream_t
     else rc = UZIP_EINVAL;
     if (rc) return rc;
     if (p.nsplit > 1) {
-        k_attend_join<DP><<<(unsigned)plan.rows, 256, 0, s>>>(p, half);
+        // a wave a row while it can have all its splits' loads under way at once
+        if (p.nsplit <= 16) k_attend_join<DP, 1><<<(unsigned)((plan.rows + kWaves - 1) / kWaves), kWaves * 64, 0, s>>>(p, (int64_t)plan.rows, half);
+        else k_attend_join<DP, kWaves><<<(unsigned)plan.rows, kWaves * 64, 0, s>>>(p, (int64_t)plan.rows, half);
         UZIP_KV_LAUNCH_CHECK("k_attend_join");
     }
     if (p.score) {

@@ -79,77 +79,82 @@ def _check(rc: int, what: str):
         raise UzipError(rc, f"{what}: {lib().uzip_strerror(rc).decode()}")
 
 
-def _need(ok: bool, what: str):
-    if not ok:
-        raise ValueError(what)
-
-
-class _On:
-    """The device of a call made current, and the call's stream."""
-    __slots__ = ("device", "stream", "guards")
-
-    def __init__(self, device: torch.device, stream):
-        _need(device.type == "cuda", "expected device tensors")
-        self.device = device
-        self.guards = ()
-        if stream is None:
-            if device.index == torch.cuda.current_device():
-                self.stream = torch.cuda.current_stream().cuda_stream
-                return
-            guard = torch.cuda.device(device)
-            guard.__enter__()
-            self.guards = (guard,)
-            self.stream = torch.cuda.current_stream().cuda_stream
-        else:
-            _need(stream.device == device, "the stream belongs to another device than the tensors")
-            guard = torch.cuda.stream(stream)      # makes its device current too; new tensors belong to it
-            guard.__enter__()
-            self.guards = (guard,)
-            self.stream = stream.cuda_stream
+class _Here:
+    """The current device and stream."""
 
     def __enter__(self):
         return self
 
     def __exit__(self, *e):
-        for guard in self.guards:
-            guard.__exit__(*e)
+        return None
+
+
+_HERE = _Here()
+
+
+def _on(device: torch.device, stream):
+    """A context that makes the tensors' device and `stream` (None: that
+    device's current one) current, so that new tensors belong to it. The usual
+    call, on the current device and stream, changes nothing: switching takes
+    longer than the smallest kernels here."""
+    if device.type != "cuda":
+        raise ValueError("expected device tensors")
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError("the stream belongs to another device than the tensors")
+        return torch.cuda.stream(stream)
+    return _HERE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
+
+
+def _stream(device: torch.device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _strides(t: torch.Tensor):
-    """Strides of the first three dims, 0 where a dim has one element; the last dim is contiguous."""
-    shape, st = t.shape, t.stride()
-    _need(len(shape) == 4, f"expected four dims, got {len(shape)}")
-    _need(st[3] == 1 or shape[3] == 1, "the head dim is not contiguous")
-    return tuple(0 if shape[i] == 1 else st[i] for i in range(3))
+    """Strides of the first three dims; 0 for a dim of one element where its own does not fit the library's rules."""
+    st = t.stride()
+    if len(st) != 4:
+        raise ValueError(f"expected four dims, got {len(st)}")
+    s0, s1, s2, s3 = st
+    if s3 != 1 and t.shape[3] != 1:
+        raise ValueError("the head dim is not contiguous")
+    if (s0 | s1 | s2) & 7 or s1 >= 1 << 26:
+        return tuple(0 if t.shape[i] == 1 else st[i] for i in range(3))
+    return s0, s1, s2
 
 
 def _written(t: torch.Tensor, what: str):
-    for n, s in zip(t.shape, t.stride()):
-        _need(n == 1 or s != 0, f"{what} has elements that share memory")
+    if 0 in t.stride():
+        for n, s in zip(t.shape, t.stride()):
+            if n != 1 and s == 0:
+                raise ValueError(f"{what} has elements that share memory")
 
 
 def _counts(t, seqs: int, device, what: str) -> int:
     """Address of an int32 tensor with one value a sequence; 0 for None."""
     if t is None:
         return 0
-    _need(t.dtype == torch.int32 and t.shape == (seqs,) and t.is_contiguous() and t.device == device,
-          f"{what}: expected a contiguous int32 tensor of {seqs} on {device}")
+    if not (t.dtype == torch.int32 and t.shape == (seqs,) and t.is_contiguous() and t.device == device):
+        raise ValueError(f"{what}: expected a contiguous int32 tensor of {seqs} on {device}")
     return t.data_ptr()
 
 
 def _cache(k: torch.Tensor, v: torch.Tensor, table, seqs: int):
     """(packed uzip_kv_cache_t, kv heads, head dim, tokens a sequence)"""
-    _need(k.shape == v.shape and k.dtype == v.dtype and k.device == v.device, "k and v caches differ in shape, type or device")
+    if not (k.shape == v.shape and k.dtype == v.dtype and k.device == v.device):
+        raise ValueError("k and v caches differ in shape, type or device")
     dtype = _DTYPE.get(k.dtype)
-    _need(dtype is not None, f"caches are bfloat16, float16 or float8_e5m2, got {k.dtype}")
+    if dtype is None:
+        raise ValueError(f"caches are bfloat16, float16 or float8_e5m2, got {k.dtype}")
     ks, vs = _strides(k), _strides(v)
     first, second, heads, dim = k.shape
     if table is None:
-        _need(first == seqs, f"the cache holds {first} sequences, expected {seqs}")
+        if first != seqs:
+            raise ValueError(f"the cache holds {first} sequences, expected {seqs}")
         return _CACHE.pack(k.data_ptr(), v.data_ptr(), 0, *ks, *vs, 0, dtype, seqs, heads, dim, second, 0, 0, 0), heads, dim, second
-    _need(table.dtype == torch.int32 and table.dim() == 2 and table.shape[0] == seqs and table.device == k.device
-          and table.shape[1] >= 1 and (table.stride(1) == 1 or table.shape[1] == 1),
-          f"table: expected int32 [{seqs}, entries] with contiguous rows on {k.device}")
+    if not (table.dtype == torch.int32 and table.dim() == 2 and table.shape[0] == seqs and table.device == k.device
+            and table.shape[1] >= 1 and (table.stride(1) == 1 or table.shape[1] == 1)):
+        raise ValueError(f"table: expected int32 [{seqs}, entries] with contiguous rows on {k.device}")
     tokens = table.shape[1] * second
     return (_CACHE.pack(k.data_ptr(), v.data_ptr(), table.data_ptr(), *ks, *vs, table.stride(0) if seqs > 1 else 0, dtype,
                         seqs, heads, dim, tokens, second, first, 0), heads, dim, tokens)
@@ -158,26 +163,30 @@ def _cache(k: torch.Tensor, v: torch.Tensor, table, seqs: int):
 def _score(score, seqs: int, heads: int, tokens: int, table, device):
     """((sequence, head) strides, tokens) of accumulated weights: as many tokens as the cache, or fewer when it is in pages."""
     n = score.shape[-1]
-    _need(score.dtype == torch.float32 and score.shape == (seqs, heads, n) and score.device == device
-          and (n == tokens or (table is not None and 1 <= n < tokens)) and (score.stride(2) == 1 or n == 1),
-          f"score: expected float32 [{seqs}, {heads}, {tokens}] with contiguous rows on {device}")
+    if not (score.dtype == torch.float32 and score.shape == (seqs, heads, n) and score.device == device
+            and (n == tokens or (table is not None and 1 <= n < tokens)) and (score.stride(2) == 1 or n == 1)):
+        raise ValueError(f"score: expected float32 [{seqs}, {heads}, {tokens}] with contiguous rows on {device}")
     return score.stride()[:2], n
 
 
 def _types(new: torch.Tensor, cache: torch.Tensor):
-    _need(new.dtype in (torch.bfloat16, torch.float16), f"expected bfloat16 or float16, got {new.dtype}")
-    _need(cache.dtype in (new.dtype, torch.float8_e5m2), f"{new.dtype} does not go with a {cache.dtype} cache")
+    if new.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"expected bfloat16 or float16, got {new.dtype}")
+    if cache.dtype not in (new.dtype, torch.float8_e5m2):
+        raise ValueError(f"{new.dtype} does not go with a {cache.dtype} cache")
 
 
 def _rope(freq, pos, amplitude: float, flags: int, seqs: int, tokens: int, dim: int, device):
     """Packed uzip_kv_rope_t."""
-    _need(freq.dtype == torch.float64 and freq.dim() == 1 and freq.is_contiguous() and freq.device == device,
-          f"freq: expected a contiguous float64 vector on {device}")
-    _need(2 * freq.numel() <= dim, f"freq turns {2 * freq.numel()} of {dim} elements")
+    if not (freq.dtype == torch.float64 and freq.dim() == 1 and freq.is_contiguous() and freq.device == device):
+        raise ValueError(f"freq: expected a contiguous float64 vector on {device}")
+    if 2 * freq.numel() > dim:
+        raise ValueError(f"freq turns {2 * freq.numel()} of {dim} elements")
     at = stride = 0
     if pos is not None:
-        _need(pos.dtype == torch.int32 and pos.device == device and pos.shape in ((seqs, tokens), (tokens,))
-              and (pos.stride(-1) == 1 or tokens == 1), f"pos: expected int32 [{seqs}, {tokens}] or [{tokens}] with contiguous rows on {device}")
+        if not (pos.dtype == torch.int32 and pos.device == device and pos.shape in ((seqs, tokens), (tokens,))
+                and (pos.stride(-1) == 1 or tokens == 1)):
+            raise ValueError(f"pos: expected int32 [{seqs}, {tokens}] or [{tokens}] with contiguous rows on {device}")
         at, stride = pos.data_ptr(), pos.stride(0) if pos.dim() == 2 and seqs > 1 else 0
     return _ROPE.pack(freq.data_ptr(), at, stride, 2 * freq.numel(), flags, amplitude, 0)
 
@@ -195,16 +204,20 @@ def rope_freq(rot: int, base: float = 10000.0, *, linear: float = 1.0, ntk: floa
             turn at least `high` times are kept, and between them the two
             frequencies are mixed in proportion.
     """
-    _need(rot >= 2 and rot % 2 == 0, f"rot is even and positive, got {rot}")
-    _need(base > 0 and linear > 0 and ntk > 0, "base and factors are positive")
+    if not (rot >= 2 and rot % 2 == 0):
+        raise ValueError(f"rot is even and positive, got {rot}")
+    if not (base > 0 and linear > 0 and ntk > 0):
+        raise ValueError("base and factors are positive")
     if ntk != 1.0:
-        _need(rot > 2, "ntk scaling needs more than one pair")
+        if rot <= 2:
+            raise ValueError("ntk scaling needs more than one pair")
         base = base * ntk ** (rot / (rot - 2))
     i = torch.arange(rot // 2, dtype=torch.float64)
     f = base ** (-2.0 * i / rot) / (2.0 * math.pi) / linear
     if bands is not None:
         factor, trained, low, high = bands
-        _need(factor > 0 and high > low, "bands: expected a positive factor and low < high")
+        if not (factor > 0 and high > low):
+            raise ValueError("bands: expected a positive factor and low < high")
         keep = ((f * trained - low) / (high - low)).clamp(0.0, 1.0)
         f = f * (keep + (1.0 - keep) / factor)
     return f if device is None else f.to(device)
@@ -218,18 +231,21 @@ def rope(x: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, *, amplitude: f
     turn, as halves (i, i + len(freq)) or interleaved (2i, 2i + 1). inverse
     turns back: the gradient, and what moves kept keys to other positions. out
     may be x."""
-    _need(x.dtype in (torch.bfloat16, torch.float16), f"expected bfloat16 or float16, got {x.dtype}")
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"expected bfloat16 or float16, got {x.dtype}")
     xs = _strides(x)
     B, T, H, D = x.shape
-    packed = _rope(freq, pos, amplitude, interleaved * _INTERLEAVED | inverse * _INVERSE, B, T, D, x.device)
-    with _On(x.device, stream) as on:
+    dev = x.device
+    packed = _rope(freq, pos, amplitude, interleaved * _INTERLEAVED | inverse * _INVERSE, B, T, D, dev)
+    with _on(dev, stream):
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            out = torch.empty((B, T, H, D), dtype=x.dtype, device=dev)
         else:
-            _need(out.shape == x.shape and out.dtype == x.dtype and out.device == x.device, "out differs from x in shape, type or device")
+            if not (out.shape == x.shape and out.dtype == x.dtype and out.device == dev):
+                raise ValueError("out differs from x in shape, type or device")
             _written(out, "out")
         _check(lib().uzip_kv_rope(_TENSOR.pack(x.data_ptr(), *xs), _TENSOR.pack(out.data_ptr(), *_strides(out)),
-                                  _DTYPE[x.dtype], B, T, H, D, packed, on.stream), "rope")
+                                  _DTYPE[x.dtype], B, T, H, D, packed, _stream(dev)), "rope")
     return out
 
 
@@ -244,34 +260,39 @@ def append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, k_cache: to
     nothing turns. length is not changed. Tokens from drafted on, past the
     cache's end or in an absent page are not written."""
     B, T, H, D = k.shape
-    _need(v.shape == k.shape and v.dtype == k.dtype and v.device == k.device, "k and v differ in shape, type or device")
+    if not (v.shape == k.shape and v.dtype == k.dtype and v.device == k.device):
+        raise ValueError("k and v differ in shape, type or device")
     _types(k, k_cache)
     cache, heads, dim, _ = _cache(k_cache, v_cache, table, B)
     _written(k_cache, "the key cache")
     _written(v_cache, "the value cache")
     dev = k.device
-    _need(k_cache.device == dev, "the cache is on another device")
-    _need(heads == H and dim == D, f"the cache has {heads} heads of {dim}, the new keys {H} of {D}")
+    if k_cache.device != dev:
+        raise ValueError("the cache is on another device")
+    if not (heads == H and dim == D):
+        raise ValueError(f"the cache has {heads} heads of {dim}, the new keys {H} of {D}")
     packed = None
     if freq is not None:
         packed = _rope(freq, pos, amplitude, interleaved * _INTERLEAVED, B, T, D, dev)
-    with _On(dev, stream) as on:
+    with _on(dev, stream):
         if q is None:
             qs = (0,) * 8
             hq = 0
         else:
-            _need(q.dim() == 4 and q.shape[0] == B and q.shape[1] == T and q.shape[3] == D and q.dtype == k.dtype
-                  and q.device == dev, "q does not go with k")
+            if not (q.dim() == 4 and q.shape[0] == B and q.shape[1] == T and q.shape[3] == D and q.dtype == k.dtype
+                    and q.device == dev):
+                raise ValueError("q does not go with k")
             hq = q.shape[2]
             if out is None:
                 out = torch.empty(q.shape, dtype=q.dtype, device=dev)
             else:
-                _need(out.shape == q.shape and out.dtype == q.dtype and out.device == dev, "out differs from q in shape, type or device")
+                if not (out.shape == q.shape and out.dtype == q.dtype and out.device == dev):
+                    raise ValueError("out differs from q in shape, type or device")
                 _written(out, "out")
             qs = (q.data_ptr(), *_strides(q), out.data_ptr(), *_strides(out))
         args = _APPEND.pack(*qs, k.data_ptr(), *_strides(k), v.data_ptr(), *_strides(v), _counts(length, B, dev, "length"),
                             _counts(drafted, B, dev, "drafted"), _DTYPE[k.dtype], T, hq, 0)
-        _check(lib().uzip_kv_append(cache, args, packed, on.stream), "append")
+        _check(lib().uzip_kv_append(cache, args, packed, _stream(dev)), "append")
     return out if q is not None else None
 
 
@@ -304,35 +325,40 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, length
     B, T, hq, D = q.shape
     dev = q.device
     cache, heads, dim, tokens = _cache(k_cache, v_cache, table, B)
-    _need(k_cache.device == dev, "the cache is on another device")
-    _need(dim == D and hq >= heads and hq % heads == 0, f"{hq} query heads of {D} do not go with {heads} heads of {dim}")
+    if k_cache.device != dev:
+        raise ValueError("the cache is on another device")
+    if not (dim == D and hq >= heads and hq % heads == 0):
+        raise ValueError(f"{hq} query heads of {D} do not go with {heads} heads of {dim}")
     ts = (0, 0)
     if tree is not None:
-        _need(tree.dtype in (torch.bool, torch.uint8) and tree.device == dev and tree.shape in ((T, T), (B, T, T))
-              and (tree.stride(-1) == 1 or T == 1), f"tree: expected bool [{T}, {T}] or [{B}, {T}, {T}] with contiguous rows on {dev}")
+        if not (tree.dtype in (torch.bool, torch.uint8) and tree.device == dev and tree.shape in ((T, T), (B, T, T))
+                and (tree.stride(-1) == 1 or T == 1)):
+            raise ValueError(f"tree: expected bool [{T}, {T}] or [{B}, {T}, {T}] with contiguous rows on {dev}")
         ts = (tree.stride(0) if tree.dim() == 3 else 0, tree.stride(-2))
     ss, seen = (0, 0), 0
     if score is not None:
         ss, seen = _score(score, B, heads, tokens, table, dev)
         _written(score, "score")
     if lse is not None:
-        _need(lse.dtype == torch.float32 and lse.shape == (B, T, hq) and lse.is_contiguous() and lse.device == dev,
-              f"lse: expected contiguous float32 [{B}, {T}, {hq}] on {dev}")
-    with _On(dev, stream) as on:
+        if not (lse.dtype == torch.float32 and lse.shape == (B, T, hq) and lse.is_contiguous() and lse.device == dev):
+            raise ValueError(f"lse: expected contiguous float32 [{B}, {T}, {hq}] on {dev}")
+    with _on(dev, stream):
         if out is None:
             out = torch.empty((B, T, hq, D), dtype=q.dtype, device=dev)
         else:
-            _need(out.shape == q.shape and out.dtype == q.dtype and out.device == dev, "out differs from q in shape, type or device")
+            if not (out.shape == q.shape and out.dtype == q.dtype and out.device == dev):
+                raise ValueError("out differs from q in shape, type or device")
             _written(out, "out")
         if ws is None:
             ws = torch.empty(attend_workspace_bytes(B, heads, D, tokens, T, hq), dtype=torch.uint8, device=dev)
         else:
-            _need(ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev, "ws: expected contiguous uint8")
+            if not (ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev):
+                raise ValueError("ws: expected contiguous uint8")
         args = _ATTEND.pack(q.data_ptr(), *qs, out.data_ptr(), *_strides(out), lse.data_ptr() if lse is not None else 0,
                             score.data_ptr() if score is not None else 0, *ss, _counts(length, B, dev, "length"),
                             _counts(drafted, B, dev, "drafted"), tree.data_ptr() if tree is not None else 0, *ts,
                             _DTYPE[q.dtype], T, hq, 1.0 / math.sqrt(D) if scale is None else scale, seen, 0)
-        _check(lib().uzip_kv_attend(cache, args, ws.data_ptr(), ws.numel(), on.stream), "attend")
+        _check(lib().uzip_kv_attend(cache, args, ws.data_ptr(), ws.numel(), _stream(dev)), "attend")
     return out
 
 
@@ -358,16 +384,16 @@ def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, score: torch.Tensor, len
     cache, heads, dim, tokens = _cache(k_cache, v_cache, table, B)
     dev = k_cache.device
     ss, seen = _score(score, B, heads, tokens, table, dev)
-    _need(1 <= keep <= 1 << 30 and sink >= 0 and recent >= 0 and sink + recent <= keep,
-          f"keep {keep}, sink {sink}, recent {recent}: expected 1 <= keep and sink + recent <= keep")
-    with _On(dev, stream) as on:
+    if not (1 <= keep <= 1 << 30 and sink >= 0 and recent >= 0 and sink + recent <= keep):
+        raise ValueError(f"keep {keep}, sink {sink}, recent {recent}: expected 1 <= keep and sink + recent <= keep")
+    with _on(dev, stream):
         made = []
         for t in (k_out, v_out):
             if t is None:
                 t = torch.empty((B, keep, heads, dim), dtype=k_cache.dtype, device=dev)
             else:
-                _need(t.shape == (B, keep, heads, dim) and t.dtype == k_cache.dtype and t.device == dev,
-                      f"k_out, v_out: expected {k_cache.dtype} [{B}, {keep}, {heads}, {dim}] on {dev}")
+                if not (t.shape == (B, keep, heads, dim) and t.dtype == k_cache.dtype and t.device == dev):
+                    raise ValueError(f"k_out, v_out: expected {k_cache.dtype} [{B}, {keep}, {heads}, {dim}] on {dev}")
                 _written(t, "k_out or v_out")
             made.append(t)
         kept, index = torch.empty((B, heads, keep), device=dev), torch.empty((B, heads, keep), dtype=torch.int32, device=dev)
@@ -375,8 +401,9 @@ def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, score: torch.Tensor, len
         if ws is None:
             ws = torch.empty(evict_workspace_bytes(B, heads, tokens), dtype=torch.uint8, device=dev)
         else:
-            _need(ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev, "ws: expected contiguous uint8")
+            if not (ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev):
+                raise ValueError("ws: expected contiguous uint8")
         args = _EVICT.pack(score.data_ptr(), *ss, _counts(length, B, dev, "length"),
                            index.data_ptr(), kept.data_ptr(), left.data_ptr(), keep, sink, recent, seen)
-        _check(lib().uzip_kv_evict(cache, _cache(*made, None, B)[0], args, ws.data_ptr(), ws.numel(), on.stream), "evict")
+        _check(lib().uzip_kv_evict(cache, _cache(*made, None, B)[0], args, ws.data_ptr(), ws.numel(), _stream(dev)), "evict")
     return made[0], made[1], kept, left, index
