@@ -42,7 +42,7 @@ struct AttendParams {
     float *part_o;                            // [row][split][DP], when nsplit > 1
     float2 *part_ml;                          // [row][split]: maximum (times c), sum
     int T, G, R, D, heads;                    // heads: key/value heads
-    int nsplit, nrg, min_tiles;
+    int nsplit, nrg, min_tiles, unit;         // unit: tiles that a workgroup takes in one step
     int wk;                                   // waves of a workgroup that share rows and split keys
     float c2;                                 // scale * log2(e)
     int q_f16;
@@ -53,7 +53,7 @@ __device__ inline int tiles_per_split(int ntiles, const AttendParams &p)
 {
     int t = (ntiles + p.nsplit - 1) / p.nsplit;
     t = t < p.min_tiles ? p.min_tiles : t;
-    return (t + p.wk - 1) / p.wk * p.wk;
+    return (t + p.unit - 1) / p.unit * p.unit;
 }
 
 template <int CT>
@@ -146,12 +146,17 @@ struct TileFinder {
 
     __device__ inline Tile at(const AttendParams &p, int b, int h, int i, int first, int n, int end)
     {
+        return find(p, b, h, i, first, p.wk, n, end);
+    }
+
+    __device__ inline Tile find(const AttendParams &p, int b, int h, int i, int first, int step, int n, int end)
+    {
         Tile t;
-        t.key = (first + i * p.wk) * kTileKeys;
+        t.key = (first + i * step) * kTileKeys;
         if (p.c.table && (i >> 5) != batch) {
             batch = i >> 5;
             const int lane = (int)(threadIdx.x & 63);
-            const int64_t key = ((int64_t)first + ((int64_t)batch * 32 + (lane >> 1)) * p.wk) * kTileKeys + (lane & 1) * 16;
+            const int64_t key = ((int64_t)first + ((int64_t)batch * 32 + (lane >> 1)) * step) * kTileKeys + (lane & 1) * 16;
             entry = key < end ? p.c.table[b * p.c.ts + (key >> p.c.shift)] : -1;
         }
 #pragma unroll
@@ -221,180 +226,162 @@ __device__ inline void load_keys(const AttendParams &p, const Tile &t, int end, 
     }
 }
 
-// One wave's rows over its keys. DP: the head dim rounded up to 64, 128 or
-// 256 (PAD: it is smaller than that); RB: row blocks of 16.
+// A wave's RB blocks of 16 query rows and what it holds for them. DP: the head
+// dim rounded up to 64, 128 or 256 (PAD: it is smaller than that).
 template <int CT, int DP, int RB, bool PAD>
-__global__ __launch_bounds__(kWaves * 64, RB == 4 || DP == 256 ? 1 : 2) void k_attend(AttendParams p)
-{
-    constexpr int KS = DP / 32;                   // steps of the product over the head dim
-    constexpr int VE = DP >= 128 ? 8 : 4;         // dims that a lane loads at once
-    constexpr int VC = DP >= 128 ? DP / 128 : 1;  // ... and how often
-    constexpr int NV = VE * VC;                   // output products; dim = c * 128 + (4 g + i) * VE + e
-    constexpr int VW = VE * (CT == kE5M2 ? 1 : 2) / 4;   // dwords of a load
-    constexpr int es = CT == kE5M2 ? 1 : 2;
-    constexpr bool f16 = CT != kBF16;             // type of the products
-    __shared__ float smem[2 * RB * 16 * DP + 2 * kWaves * RB * 16];
+struct Rows {
+    static constexpr int KS = DP / 32;                   // steps of the product over the head dim
+    static constexpr int VE = DP >= 128 ? 8 : 4;         // dims that a lane takes at once
+    static constexpr int VC = DP >= 128 ? DP / 128 : 1;  // ... and how often
+    static constexpr int NV = VE * VC;                   // output products; dim = c * 128 + (4 g + i) * VE + e
+    static constexpr int VW = VE * (CT == kE5M2 ? 1 : 2) / 4;   // dwords of a lane's dims
+    static constexpr int es = CT == kE5M2 ? 1 : 2;
+    static constexpr bool f16 = CT != kBF16;             // type of the products
+    typedef uint32_t Values __attribute__((ext_vector_type(VW)));
 
-    const int lane = (int)(threadIdx.x & 63), x = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    int id = (int)blockIdx.x;
-    const int h = id % p.heads;
-    id /= p.heads;
-    const int rg = id % p.nrg;
-    id /= p.nrg;
-    const int split = id % p.nsplit, b = id / p.nsplit;
-    const int wkey = wave & (p.wk - 1), wrow = wave / p.wk;
-    const int n = __builtin_amdgcn_readfirstlane(clamp_length(p.length, b, p.c.tokens));
-    const int nd = __builtin_amdgcn_readfirstlane(clamp_drafted(p.drafted, b, p.T));
-    const int end = nd == 0 ? 0 : (uint32_t)nd > p.c.tokens - (uint32_t)n ? (int)p.c.tokens : n + nd;
-    const int ntiles = (end + kTileKeys - 1) / kTileKeys;
-    const int tps = tiles_per_split(ntiles, p);
-    const int t0 = split * tps, t1 = min(t0 + tps, ntiles);
-    if (p.nsplit > 1 && t0 >= t1) return;         // the joining kernel knows
-
-    // this wave's rows: their token, and Q
-    const int row0 = (rg * (kWaves / p.wk) + wrow) * RB * 16;
-    int tok[RB];
-    float c2[RB];
+    int x, g, row0, lim;
+    bool odd;                                     // poison() has something to add
+    int tok[RB];                                  // of the lane's rows
+    float c2[RB], m[RB], l[RB];                   // l: of this lane's keys
+    float base[RB];                               // m c2, or 0 while m is -inf
     u32x4 q[RB][KS];
+    f32x4 acc[RB][NV];
+
+    __device__ inline void init(const AttendParams &p, int b, int h, int first_row, int n, int end)
+    {
+        x = (int)(threadIdx.x & 15), g = (int)(threadIdx.x & 63) >> 4;
+        row0 = first_row;
+        odd = false;
 #pragma unroll
-    for (int rb = 0; rb < RB; rb++) {
-        const int r = row0 + rb * 16 + x;
-        tok[rb] = r / p.G;
-        c2[rb] = p.c2 * load_q<CT, KS, PAD>(p, p.q + b * p.qs0 + tok[rb] * p.qs1 + (int64_t)(h * p.G + r % p.G) * p.qs2, r < p.R, g, q[rb]);
+        for (int rb = 0; rb < RB; rb++) {
+            const int r = row0 + rb * 16 + x;
+            tok[rb] = r / p.G;
+            c2[rb] = p.c2 * load_q<CT, KS, PAD>(p, p.q + b * p.qs0 + tok[rb] * p.qs1 + (int64_t)(h * p.G + r % p.G) * p.qs2, r < p.R, g, q[rb]);
+            m[rb] = -INFINITY, l[rb] = 0.f, base[rb] = 0.f;
+#pragma unroll
+            for (int e = 0; e < NV; e++) acc[rb][e] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+        // keys these rows can see: a chain's later tokens are not read for earlier rows
+        lim = end;
+        if (!p.tree) lim = min(end, n + min((min(row0 + RB * 16, p.R) - 1) / p.G, p.T - 1) + 1);
     }
-    // keys this wave can see: a chain's later tokens are not read for earlier rows
-    int lim = end;
-    if (!p.tree) lim = min(end, n + min((min(row0 + RB * 16, p.R) - 1) / p.G, p.T - 1) + 1);
 
-    f32x4 acc[RB][NV] = {};
-    float m[RB], l[RB];                           // l: of this lane's keys
-#pragma unroll
-    for (int rb = 0; rb < RB; rb++) m[rb] = -INFINITY, l[rb] = 0.f;
-
-    const uint32_t koff = (uint32_t)(x * p.c.ks1) + g * 8 * es;
-    const uint32_t voff = (uint32_t)(g * 4 * p.c.vs1) + x * VE * es;
-    typedef uint32_t vraw __attribute__((ext_vector_type(VW)));
-
-    const auto score_tile = [&](const Raw<CT> (&kr)[2][KS], f32x4 (&s)[RB][2]) {
+    __device__ inline void score(const u32x4 (&k)[2][KS], f32x4 *s0, int stride)
+    {
 #pragma unroll
         for (int hf = 0; hf < 2; hf++)
 #pragma unroll
-            for (int ks = 0; ks < KS; ks++) {
-                const u32x4 a = widen<CT>(kr[hf][ks]);
+            for (int ks = 0; ks < KS; ks++)
 #pragma unroll
-                for (int rb = 0; rb < RB; rb++) s[rb][hf] = mfma<CT>(a, q[rb][ks], ks ? s[rb][hf] : f32x4{0.f, 0.f, 0.f, 0.f});
-            }
-    };
-    // Scores to weights. m need not be the maximum so far, only near it: the
-    // weights stay below 2^kSlack and nothing is lost in binary32, while the
-    // output is scaled anew in the first tile and then hardly ever.
-    const auto weigh_tile = [&](f32x4 (&s)[RB][2], u32x4 (&pw)[RB]) {
+                for (int rb = 0; rb < RB; rb++) {
+                    f32x4 &s = s0[rb * stride + hf];
+                    s = mfma<CT>(k[hf][ks], q[rb][ks], ks ? s : f32x4{0.f, 0.f, 0.f, 0.f});
+                }
+    }
+
+    // Scores of N half tiles to weights. m need not be the maximum so far, only
+    // near it: the weights stay below 2^kSlack and nothing is lost in binary32,
+    // while the output is scaled anew in the first tile and then hardly ever.
+    template <int N>
+    __device__ inline void weigh(f32x4 (&s)[RB][N], u32x4 (&pw)[RB][N / 2])
+    {
 #pragma unroll
         for (int rb = 0; rb < RB; rb++) {
-            float top = fmaxf(fmaxf(fmaxf(s[rb][0][0], s[rb][0][1]), fmaxf(s[rb][0][2], s[rb][0][3])),
-                              fmaxf(fmaxf(s[rb][1][0], s[rb][1][1]), fmaxf(s[rb][1][2], s[rb][1][3])));
+            // A row with a NaN is NaN by its sum, whatever the maximum.
+            float part[N];
+#pragma unroll
+            for (int hf = 0; hf < N; hf++) part[hf] = larger(larger(s[rb][hf][0], s[rb][hf][1]), larger(s[rb][hf][2], s[rb][hf][3]));
+            float top = part[0];
+#pragma unroll
+            for (int hf = 1; hf < N; hf++) top = larger(top, part[hf]);
             top = quad_max(top);
             if (__builtin_amdgcn_ballot_w64((top - m[rb]) * c2[rb] > kSlack)) {
                 top = fmaxf(top, m[rb]);
                 const float a = __builtin_amdgcn_exp2f((m[rb] - (top == -INFINITY ? 0.f : top)) * c2[rb]);
                 m[rb] = top;
+                base[rb] = top == -INFINITY ? 0.f : top * c2[rb];
                 l[rb] *= a;
 #pragma unroll
                 for (int e = 0; e < NV; e++) acc[rb][e] *= a;
             }
-            const float base = (m[rb] == -INFINITY ? 0.f : m[rb]) * c2[rb];
+            float sum[2] = {0.f, 0.f};
 #pragma unroll
-            for (int hf = 0; hf < 2; hf++)
+            for (int hf = 0; hf < N; hf++)
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
-                    s[rb][hf][k] = __builtin_amdgcn_exp2f(fmaf(s[rb][hf][k], c2[rb], -base));
-                    l[rb] += s[rb][hf][k];
+                    s[rb][hf][k] = __builtin_amdgcn_exp2f(fmaf(s[rb][hf][k], c2[rb], -base[rb]));
+                    sum[k & 1] += s[rb][hf][k];
                 }
+            l[rb] += sum[0] + sum[1];
             // The one rounding of the weights, half a step of the products'
             // type. Their sum is taken before it: lse keeps binary32.
-            pw[rb] = u32x4{pack2<f16>(s[rb][0][0], s[rb][0][1]), pack2<f16>(s[rb][0][2], s[rb][0][3]),
-                           pack2<f16>(s[rb][1][0], s[rb][1][1]), pack2<f16>(s[rb][1][2], s[rb][1][3])};
+#pragma unroll
+            for (int t = 0; t < N / 2; t++)
+                pw[rb][t] = u32x4{pack2<f16>(s[rb][2 * t][0], s[rb][2 * t][1]), pack2<f16>(s[rb][2 * t][2], s[rb][2 * t][3]),
+                                  pack2<f16>(s[rb][2 * t + 1][0], s[rb][2 * t + 1][1]), pack2<f16>(s[rb][2 * t + 1][2], s[rb][2 * t + 1][3])};
         }
-    };
+    }
+
     // element (c, e) of the lane's dims for its eight keys
-    const auto value_fragment = [&](const vraw (&vr)[VC][8], int c, int e) {
+    __device__ inline static u32x4 fragment(const Values (&v)[VC][8], int c, int e)
+    {
         u32x4 a;
 #pragma unroll
         for (int k = 0; k < 4; k++) {
             if constexpr (CT == kE5M2) {
                 const uint32_t sel = ((4u + e % 4) << 24) | (0x0cu << 16) | ((uint32_t)(e % 4) << 8) | 0x0cu;
-                a[k] = __builtin_amdgcn_perm(vr[c][2 * k + 1][e / 4], vr[c][2 * k][e / 4], sel);
+                a[k] = __builtin_amdgcn_perm(v[c][2 * k + 1][e / 4], v[c][2 * k][e / 4], sel);
             } else {
-                a[k] = __builtin_amdgcn_perm(vr[c][2 * k + 1][e / 2], vr[c][2 * k][e / 2], e % 2 ? 0x07060302u : 0x05040100u);
+                a[k] = __builtin_amdgcn_perm(v[c][2 * k + 1][e / 2], v[c][2 * k][e / 2], e % 2 ? 0x07060302u : 0x05040100u);
             }
         }
         return a;
-    };
-    const auto add_tile = [&](const vraw (&vr)[VC][8], const u32x4 (&pw)[RB]) {
+    }
+
+    template <int N>
+    __device__ inline void add(const Values (&v)[VC][8], const u32x4 (&pw)[RB][N], int t)
+    {
 #pragma unroll
         for (int c = 0; c < VC; c++)
 #pragma unroll
             for (int e = 0; e < VE; e++) {
-                const u32x4 a = value_fragment(vr, c, e);
+                const u32x4 a = fragment(v, c, e);
 #pragma unroll
-                for (int rb = 0; rb < RB; rb++) acc[rb][c * VE + e] = mfma<CT>(a, pw[rb], acc[rb][c * VE + e]);
+                for (int rb = 0; rb < RB; rb++) acc[rb][c * VE + e] = mfma<CT>(a, pw[rb][t], acc[rb][c * VE + e]);
             }
-    };
-
-    // Tiles that every row sees: keys one tile ahead in registers, values
-    // loaded while the scores are worked out.
-    const int first = t0 + wkey, count = row0 < p.R ? (t1 - first + p.wk - 1) / p.wk : 0;
-    int i = 0;
-    if (count > 0) {
-        TileFinder finder;
-        Tile t = finder.at(p, b, h, 0, first, n, lim);
-        Raw<CT> kr[2][KS];
-        if (t.fast) load_keys<CT, KS, PAD, false>(p, t, lim, x, g, koff, kr);
-        while (t.fast) {
-            Tile nxt = t;
-            nxt.fast = false;
-            if (++i < count) {
-                const Tile f = finder.at(p, b, h, i, first, n, lim);
-                if (f.fast) nxt = f;
-            }
-            vraw vr[VC][8];
-#pragma unroll
-            for (int c = 0; c < VC; c++)
-#pragma unroll
-                for (int j = 0; j < 8; j++) {
-                    if (PAD) vr[c][j] = vraw{};
-                    if (!PAD || c * 128 + x * VE < p.D)
-                        vr[c][j] = *reinterpret_cast<const vraw *>(t.v[j >> 2] + (j & 3) * p.c.vs1 + (voff + c * 128 * es));
-                }
-            f32x4 s[RB][2];
-            u32x4 pw[RB];
-            score_tile(kr, s);
-            load_keys<CT, KS, PAD, false>(p, nxt, lim, x, g, koff, kr);   // the same ones again after the last
-            weigh_tile(s, pw);
-            add_tile(vr, pw);
-            t = nxt;
-        }
     }
-    // The others: the drafted tokens' own tiles, the last one, absent pages.
-    TileFinder finder;
-    for (; i < count; i++) {
-        const Tile t = finder.at(p, b, h, i, first, n, lim);
-        if (t.key >= lim) break;
-        Raw<CT> kr[2][KS];
-        vraw vr[VC][8];
-        load_keys<CT, KS, PAD, true>(p, t, lim, x, g, koff, kr);
+
+    // values of the lane's eight keys
+    template <bool MASKED>
+    __device__ inline void load_values(const AttendParams &p, const Tile &t, Values (&v)[VC][8])
+    {
+        const uint32_t off = (uint32_t)(g * 4 * p.c.vs1) + x * VE * es;
 #pragma unroll
         for (int c = 0; c < VC; c++)
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                vr[c][j] = vraw{};
-                if ((!PAD || c * 128 + x * VE < p.D) && t.there[j >> 2] && t.key + 16 * (j >> 2) + 4 * g + (j & 3) < lim)
-                    vr[c][j] = *reinterpret_cast<const vraw *>(t.v[j >> 2] + (j & 3) * p.c.vs1 + (voff + c * 128 * es));
+                if (MASKED || PAD) v[c][j] = Values{};
+                if ((!PAD || c * 128 + x * VE < p.D) && (!MASKED || (t.there[j >> 2] && t.key + 16 * (j >> 2) + 4 * g + (j & 3) < lim)))
+                    v[c][j] = *reinterpret_cast<const Values *>(t.v[j >> 2] + (j & 3) * p.c.vs1 + (off + c * 128 * es));
             }
+    }
+
+    // A tile that not every row sees whole: the drafted tokens' own, the last
+    // one, one with an absent page.
+    __device__ inline void masked_tile(const AttendParams &p, const Tile &t, int b, int n, int nd)
+    {
+        Raw<CT> kr[2][KS];
+        u32x4 k[2][KS];
+        Values v[VC][8];
+        load_keys<CT, KS, PAD, true>(p, t, lim, x, g, (uint32_t)(x * p.c.ks1) + g * 8 * es, kr);
+#pragma unroll
+        for (int hf = 0; hf < 2; hf++)
+#pragma unroll
+            for (int ks = 0; ks < KS; ks++) k[hf][ks] = widen<CT>(kr[hf][ks]);
         f32x4 s[RB][2];
-        u32x4 pw[RB];
-        score_tile(kr, s);
+        u32x4 pw[RB][1];
+        score(k, &s[0][0], 2);
+        load_values<true>(p, t, v);
         uint32_t seen[RB];
 #pragma unroll
         for (int rb = 0; rb < RB; rb++) seen[rb] = 0;
@@ -407,232 +394,539 @@ __global__ __launch_bounds__(kWaves * 64, RB == 4 || DP == 256 ? 1 : 2) void k_a
             seen[rb] |= leading_bits((p.tree ? n : min(lim, n + tok[rb] + 1)) - t.key - 4 * g);
             seen[rb] &= there_bits(t);
 #pragma unroll
-            for (int k = 0; k < 8; k++) s[rb][k >> 2][k & 3] = seen[rb] >> k & 1 ? s[rb][k >> 2][k & 3] : -INFINITY;
+            for (int i = 0; i < 8; i++) s[rb][i >> 2][i & 3] = seen[rb] >> i & 1 ? s[rb][i >> 2][i & 3] : -INFINITY;
         }
-        weigh_tile(s, pw);
-        // A value that is not finite must reach only the rows that see its
-        // key, and in a product it would reach all (0 * inf). Rare: count the
-        // seen ones per row and dim with products of zeros and ones, +inf and
-        // NaN in one, -inf and NaN in the other, and leave them out below.
-        uint32_t any = 0;
-#pragma unroll
-        for (int c = 0; c < VC; c++)
-#pragma unroll
-            for (int j = 0; j < 8; j++)
-#pragma unroll
-                for (int w = 0; w < VW; w++) any |= not_finite<CT>(vr[c][j][w]);
-        if (__builtin_amdgcn_ballot_w64(any != 0)) {
-            constexpr uint32_t one = f16 ? 0x3c003c00u : 0x3f803f80u;
-            u32x4 pi[RB];
-#pragma unroll
-            for (int rb = 0; rb < RB; rb++)
-#pragma unroll
-                for (int k = 0; k < 4; k++)
-                    pi[rb][k] = (seen[rb] >> (2 * k) & 1 ? one & 0xffffu : 0) | (seen[rb] >> (2 * k + 1) & 1 ? one & 0xffff0000u : 0);
-            constexpr uint32_t top16 = f16 ? 0x7c00u : 0x7f80u;
-#pragma unroll
-            for (int c = 0; c < VC; c++)
-#pragma unroll
-                for (int e = 0; e < VE; e++) {
-                    const u32x4 a = value_fragment(vr, c, e);
-                    u32x4 up, down;
-#pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        const uint32_t bad = not_finite<f16 ? kF16 : kBF16>(a[k]);
-                        uint32_t u = 0, d = 0;
-#pragma unroll
-                        for (int half = 0; half < 2; half++) {
-                            const uint32_t v = a[k] >> (16 * half) & 0xffffu, o = (one & 0xffffu) << (16 * half);
-                            if (bad >> (16 * half) & 1) {
-                                if (v != (top16 | 0x8000u)) u |= o;
-                                if (v != top16) d |= o;
-                            }
-                        }
-                        up[k] = u, down[k] = d;
-                    }
-#pragma unroll
-                    for (int rb = 0; rb < RB; rb++) {
-                        const f32x4 nu = mfma<CT>(up, pi[rb], f32x4{0.f, 0.f, 0.f, 0.f}), nn = mfma<CT>(down, pi[rb], f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-                        for (int k = 0; k < 4; k++) {
-                            if (nu[k] > 0.f) acc[rb][c * VE + e][k] += INFINITY;
-                            if (nn[k] > 0.f) acc[rb][c * VE + e][k] -= INFINITY;
-                        }
-                    }
-                }
+        weigh(s, pw);
+        if (t.key + kTileKeys > n) {
+            // A value that is not finite must reach only the rows that see its
+            // key, and in a product it would reach all (0 * inf): poison() adds it.
+            uint32_t any = 0;
 #pragma unroll
             for (int c = 0; c < VC; c++)
 #pragma unroll
                 for (int j = 0; j < 8; j++)
 #pragma unroll
-                    for (int w = 0; w < VW; w++) vr[c][j][w] &= ~not_finite<CT>(vr[c][j][w]);
+                    for (int i = 0; i < VW; i++) {
+                        const uint32_t bad = not_finite<CT>(v[c][j][i]);
+                        any |= bad;
+                        v[c][j][i] &= ~bad;
+                    }
+            odd = odd || __builtin_amdgcn_ballot_w64(any != 0) != 0;
         }
-        add_tile(vr, pw);
+        add(v, pw, 0);
     }
 
-    // join the waves that split the keys
+    // After the last tile: whole sums, and maxima that waves can compare.
+    __device__ inline void close()
+    {
 #pragma unroll
-    for (int rb = 0; rb < RB; rb++) {
-        l[rb] = quad_sum(l[rb]);
-        m[rb] *= c2[rb];                          // comparable between waves; -inf stays
+        for (int rb = 0; rb < RB; rb++) {
+            l[rb] = quad_sum(l[rb]);
+            m[rb] *= c2[rb];
+        }
     }
-    if (p.wk > 1) {
-        float *ml = smem + 2 * RB * 16 * DP;      // [wave][row][2]
+
+    // Joins the wk (2 or 4) waves that split these rows' keys into the one
+    // with wkey 0. wave0: the first of them; buf: join_words(waves) words for
+    // all waves of the workgroup, which all call this; out: wk / 2 blocks of
+    // RB * 16 * DP floats for these waves.
+    static constexpr int join_words(int waves) { return (2 * RB * 16 + 1) * waves; }
+    __device__ inline void join(int waves, int wk, int wkey, int wave0, float *buf, float *out)
+    {
+        const int lane = (int)(threadIdx.x & 63);
         if (g == 0)
 #pragma unroll
             for (int rb = 0; rb < RB; rb++) {
-                ml[(wave * RB * 16 + rb * 16 + x) * 2] = m[rb];
-                ml[(wave * RB * 16 + rb * 16 + x) * 2 + 1] = l[rb];
+                buf[((wave0 + wkey) * RB * 16 + rb * 16 + x) * 2] = m[rb];
+                buf[((wave0 + wkey) * RB * 16 + rb * 16 + x) * 2 + 1] = l[rb];
             }
+        int *flags = reinterpret_cast<int *>(buf + 2 * waves * RB * 16);
+        if (lane == 0) flags[wave0 + wkey] = odd;
         __syncthreads();
-        const int w0 = wave - wkey;
+        for (int k = 0; k < wk; k++) odd = odd || flags[wave0 + k];
 #pragma unroll
         for (int rb = 0; rb < RB; rb++) {
+            const float *ml = buf + (wave0 * RB * 16 + rb * 16 + x) * 2;
             float top = -INFINITY, sum = 0.f;
-            for (int k = 0; k < p.wk; k++) top = fmaxf(top, ml[((w0 + k) * RB * 16 + rb * 16 + x) * 2]);
+            for (int k = 0; k < wk; k++) top = fmaxf(top, ml[k * RB * 32]);
             const float base = top == -INFINITY ? 0.f : top;
-            for (int k = 0; k < p.wk; k++)
-                sum += ml[((w0 + k) * RB * 16 + rb * 16 + x) * 2 + 1] * __builtin_amdgcn_exp2f(ml[((w0 + k) * RB * 16 + rb * 16 + x) * 2] - base);
+            for (int k = 0; k < wk; k++) sum += ml[k * RB * 32 + 1] * __builtin_amdgcn_exp2f(ml[k * RB * 32] - base);
             const float a = __builtin_amdgcn_exp2f(m[rb] - base);
             m[rb] = top;
             l[rb] = sum;
 #pragma unroll
             for (int e = 0; e < NV; e++) acc[rb][e] *= a;
         }
-        for (int step = p.wk >> 1; step; step >>= 1) {
-            // 4 waves: waves 2, 3 hand over to 0, 1, then 1 to 0; 2 + 2 waves: 1 to 0 and 3 to 2
-            const int slot = p.wk == 4 ? wkey & 1 : wrow;
-            float *buf = smem + slot * RB * 16 * DP;
+        for (int step = wk >> 1; step; step >>= 1) {      // the upper half hands over to the lower
+            float *at = out + (wkey & (step - 1)) * RB * 16 * DP + lane * 4;
             if (wkey >= step && wkey < 2 * step)
 #pragma unroll
                 for (int rb = 0; rb < RB; rb++)
 #pragma unroll
-                    for (int e = 0; e < NV; e++)
-                        *reinterpret_cast<f32x4 *>(buf + ((rb * NV + e) * 64 + lane) * 4) = acc[rb][e];
+                    for (int e = 0; e < NV; e++) *reinterpret_cast<f32x4 *>(at + (rb * NV + e) * 256) = acc[rb][e];
             __syncthreads();
-            if (wkey < step) {
-                buf = smem + (p.wk == 4 ? (wkey + step) & 1 : wrow) * RB * 16 * DP;
+            if (wkey < step)
 #pragma unroll
                 for (int rb = 0; rb < RB; rb++)
 #pragma unroll
-                    for (int e = 0; e < NV; e++)
-                        acc[rb][e] += *reinterpret_cast<const f32x4 *>(buf + ((rb * NV + e) * 64 + lane) * 4);
-            }
+                    for (int e = 0; e < NV; e++) acc[rb][e] += *reinterpret_cast<const f32x4 *>(at + (rb * NV + e) * 256);
             __syncthreads();
         }
-        if (wkey) return;
     }
 
+    // What masked_tile left out: adds values that are not finite, among the
+    // keys of the drafted tokens' tiles [lo, hi), to the stored output of the
+    // rows that see them. Rare, and so written for few registers: a lane goes
+    // over its own outputs, after store().
+    __device__ inline void poison(const AttendParams &p, int b, int h, int split, int n, int nd, int lo, int hi)
+    {
+        for (int rb = 0; rb < RB; rb++) {
+            const int r = row0 + rb * 16 + x, token = r / p.G, head = h * p.G + r % p.G;
+            if (r >= p.R || token >= nd) continue;
+            for (int i = 0; i < DP / 4; i++) {
+                const int d = (i / (DP / VC / 4)) * 128 + g * 4 * VE + i % (DP / VC / 4);
+                if (d >= p.D) continue;
+                bool up = false, down = false;
+                for (int key = lo; key < hi; key++) {
+                    if (key >= n && !(p.tree ? p.tree[b * p.tr0 + token * p.tr1 + (key - n)] != 0 : key - n <= token)) continue;
+                    int64_t off;
+                    if (!locate(p.c, b, (uint32_t)key, p.c.vs0, p.c.vs1, off)) continue;
+                    const char *at = p.c.v + off + h * p.c.vs2 + d * es;
+                    const float v = CT == kE5M2 ? f16_to_f32((uint16_t)(*reinterpret_cast<const uint8_t *>(at) << 8))
+                                                : CT == kBF16 ? bf16_to_f32(*reinterpret_cast<const uint16_t *>(at)) : f16_to_f32(*reinterpret_cast<const uint16_t *>(at));
+                    if (fabsf(v) < INFINITY) continue;
+                    up = up || !(v < 0.f);
+                    down = down || !(v > 0.f);
+                }
+                if (!up && !down) continue;
+                const float add = up && down ? NAN : up ? INFINITY : -INFINITY;
+                if (p.nsplit > 1) {
+                    p.part_o[((((int64_t)b * p.heads + h) * p.R + r) * p.nsplit + split) * DP + d] += add;
+                } else {
+                    uint16_t *o = reinterpret_cast<uint16_t *>(p.out + b * p.os0 + token * p.os1 + head * p.os2) + d;
+                    const bool half = f16 && (CT == kF16 || p.q_f16);
+                    const float sum = (half ? f16_to_f32(*o) : bf16_to_f32(*o)) + add;
+                    *o = (uint16_t)(half ? pack2<true>(sum, 0.f) : pack2<false>(sum, 0.f));
+                }
+            }
+        }
+    }
+
+    // The rows' output, or their part of it when the key axis is split.
+    __device__ inline void store(const AttendParams &p, int b, int h, int split, int nd)
+    {
 #pragma unroll
-    for (int rb = 0; rb < RB; rb++) {
-        const int r = row0 + rb * 16 + x;
-        if (r >= p.R) continue;
-        if (p.nsplit > 1) {
-            const int64_t at = (((int64_t)b * p.heads + h) * p.R + r) * p.nsplit + split;
-            if (g == 0) p.part_ml[at] = make_float2(m[rb], l[rb]);
-            float *o = p.part_o + at * DP;
+        for (int rb = 0; rb < RB; rb++) {
+            const int r = row0 + rb * 16 + x;
+            if (r >= p.R) continue;
+            if (p.nsplit > 1) {
+                const int64_t at = (((int64_t)b * p.heads + h) * p.R + r) * p.nsplit + split;
+                if (g == 0) p.part_ml[at] = make_float2(m[rb], l[rb]);
+                float *o = p.part_o + at * DP;
+#pragma unroll
+                for (int c = 0; c < VC; c++)
+#pragma unroll
+                    for (int ii = 0; ii < 4; ii++)
+#pragma unroll
+                        for (int e = 0; e < VE; e += 4)
+                            *reinterpret_cast<f32x4 *>(o + c * 128 + (4 * g + ii) * VE + e) =
+                                f32x4{acc[rb][c * VE + e][ii], acc[rb][c * VE + e + 1][ii], acc[rb][c * VE + e + 2][ii], acc[rb][c * VE + e + 3][ii]};
+                continue;
+            }
+            const bool empty = l[rb] == 0.f || tok[rb] >= nd;      // a seen key's weight is 1 at the maximum, or NaN
+            const float inv = 1.f / l[rb];
+            const int head = h * p.G + r % p.G;
+            if (g == 0 && p.lse) p.lse[((int64_t)b * p.T + tok[rb]) * (p.heads * p.G) + head] = empty ? -INFINITY : (m[rb] + __log2f(l[rb])) * 0.6931471805599453f;
+            char *o = p.out + b * p.os0 + tok[rb] * p.os1 + head * p.os2;
+            const bool half = f16 && (CT == kF16 || p.q_f16);
 #pragma unroll
             for (int c = 0; c < VC; c++)
 #pragma unroll
-                for (int ii = 0; ii < 4; ii++)
+                for (int ii = 0; ii < 4; ii++) {
+                    const int d = c * 128 + (4 * g + ii) * VE;
+                    if (PAD && d >= p.D) continue;
+                    uint32_t w[VE / 2];
 #pragma unroll
-                    for (int e = 0; e < VE; e += 4)
-                        *reinterpret_cast<f32x4 *>(o + c * 128 + (4 * g + ii) * VE + e) =
-                            f32x4{acc[rb][c * VE + e][ii], acc[rb][c * VE + e + 1][ii], acc[rb][c * VE + e + 2][ii], acc[rb][c * VE + e + 3][ii]};
-            continue;
-        }
-        const bool empty = l[rb] == 0.f || tok[rb] >= nd;      // a seen key's weight is 1 at the maximum, or NaN
-        const float inv = empty ? 0.f : 1.f / l[rb];
-        const int head = h * p.G + r % p.G;
-        if (g == 0 && p.lse) p.lse[((int64_t)b * p.T + tok[rb]) * (p.heads * p.G) + head] = empty ? -INFINITY : (m[rb] + __log2f(l[rb])) * 0.6931471805599453f;
-        char *o = p.out + b * p.os0 + tok[rb] * p.os1 + head * p.os2;
-        const bool half = f16 && (CT == kF16 || p.q_f16);
-#pragma unroll
-        for (int c = 0; c < VC; c++)
-#pragma unroll
-            for (int ii = 0; ii < 4; ii++) {
-                const int d = c * 128 + (4 * g + ii) * VE;
-                if (PAD && d >= p.D) continue;
-                uint32_t w[VE / 2];
-#pragma unroll
-                for (int e = 0; e < VE; e += 2) {
-                    const float u = empty ? 0.f : acc[rb][c * VE + e][ii] * inv, v = empty ? 0.f : acc[rb][c * VE + e + 1][ii] * inv;
-                    w[e / 2] = half ? pack2<true>(u, v) : pack2<false>(u, v);
+                    for (int e = 0; e < VE; e += 2) {
+                        const float u = empty ? 0.f : acc[rb][c * VE + e][ii] * inv, v = empty ? 0.f : acc[rb][c * VE + e + 1][ii] * inv;
+                        w[e / 2] = half ? pack2<true>(u, v) : pack2<false>(u, v);
+                    }
+                    if constexpr (VE == 8)
+                        *reinterpret_cast<u32x4 *>(o + d * 2) = u32x4{w[0], w[1], w[2], w[3]};
+                    else
+                        *reinterpret_cast<u32x2 *>(o + d * 2) = u32x2{w[0], w[1]};
                 }
-                if constexpr (VE == 8)
-                    *reinterpret_cast<u32x4 *>(o + d * 2) = u32x4{w[0], w[1], w[2], w[3]};
-                else
-                    *reinterpret_cast<u32x2 *>(o + d * 2) = u32x2{w[0], w[1]};
+        }
+    }
+};
+
+// What a workgroup works on.
+struct Place {
+    int b, h, split, rg, n, nd, end, t0, t1;
+
+    __device__ inline Place(const AttendParams &p)
+    {
+        int id = (int)blockIdx.x;
+        h = id % p.heads;
+        id /= p.heads;
+        rg = id % p.nrg;
+        id /= p.nrg;
+        split = id % p.nsplit, b = id / p.nsplit;
+        n = __builtin_amdgcn_readfirstlane(clamp_length(p.length, b, p.c.tokens));
+        nd = __builtin_amdgcn_readfirstlane(clamp_drafted(p.drafted, b, p.T));
+        end = nd == 0 ? 0 : (uint32_t)nd > p.c.tokens - (uint32_t)n ? (int)p.c.tokens : n + nd;
+        const int ntiles = (end + kTileKeys - 1) / kTileKeys, tps = tiles_per_split(ntiles, p);
+        t0 = split * tps, t1 = min(t0 + tps, ntiles);
+    }
+};
+
+// Few rows: bound by the cache's bytes. Waves work alone until they join, each
+// on every wk-th tile; keys one tile ahead in registers, values loaded while
+// the scores are worked out.
+template <int CT, int DP, int RB, bool PAD>
+__global__ __launch_bounds__(kWaves * 64, (RB == 4 && DP > 64) || DP == 256 ? 1 : 2) void k_attend(AttendParams p)
+{
+    using W = Rows<CT, DP, RB, PAD>;
+    constexpr int KS = W::KS;
+    __shared__ float smem[2 * RB * 16 * DP + W::join_words(kWaves)];
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const Place at(p);
+    if (p.nsplit > 1 && at.t0 >= at.t1) return;   // the joining kernel knows
+    const int wkey = wave & (p.wk - 1), wrow = wave / p.wk;
+    W w;
+    w.init(p, at.b, at.h, (at.rg * (kWaves / p.wk) + wrow) * RB * 16, at.n, at.end);
+
+    const int first = at.t0 + wkey, count = w.row0 < p.R ? (at.t1 - first + p.wk - 1) / p.wk : 0;
+    int i = 0;
+    if (count > 0) {
+        const uint32_t koff = (uint32_t)(w.x * p.c.ks1) + w.g * 8 * W::es;
+        TileFinder finder;
+        Tile t = finder.at(p, at.b, at.h, 0, first, at.n, w.lim);
+        Raw<CT> kr[2][KS];
+        if (t.fast) load_keys<CT, KS, PAD, false>(p, t, w.lim, w.x, w.g, koff, kr);
+        while (t.fast) {
+            Tile nxt = t;
+            nxt.fast = false;
+            if (++i < count) {
+                const Tile f = finder.at(p, at.b, at.h, i, first, at.n, w.lim);
+                if (f.fast) nxt = f;
             }
+            typename W::Values v[W::VC][8];
+            w.template load_values<false>(p, t, v);
+            u32x4 k[2][KS];
+#pragma unroll
+            for (int hf = 0; hf < 2; hf++)
+#pragma unroll
+                for (int ks = 0; ks < KS; ks++) k[hf][ks] = widen<CT>(kr[hf][ks]);
+            f32x4 s[RB][2];
+            u32x4 pw[RB][1];
+            w.score(k, &s[0][0], 2);
+            load_keys<CT, KS, PAD, false>(p, nxt, w.lim, w.x, w.g, koff, kr);      // the same ones again after the last
+            w.weigh(s, pw);
+            w.add(v, pw, 0);
+            t = nxt;
+        }
+    }
+    TileFinder finder;
+    for (; i < count; i++) {
+        const Tile t = finder.at(p, at.b, at.h, i, first, at.n, w.lim);
+        if (t.key >= w.lim) break;
+        w.masked_tile(p, t, at.b, at.n, at.nd);
+    }
+
+    w.close();
+    if (p.wk > 1) {
+        w.join(kWaves, p.wk, wkey, wave - wkey, smem + 2 * RB * 16 * DP, smem + (p.wk == 4 ? 0 : wrow) * RB * 16 * DP);
+        if (wkey) return;
+    }
+    w.store(p, at.b, at.h, at.split, at.nd);
+    if (w.odd) w.poison(p, at.b, at.h, at.split, at.n, at.nd, max(at.t0 * kTileKeys, at.n & ~(kTileKeys - 1)), min(at.t1 * kTileKeys, at.end));
+}
+
+// Many rows: bound by the matrix cores and the exponentials. Eight waves of 32
+// rows each, two on a SIMD so that one's products run beside the other's
+// exponentials, read keys and values from LDS. A workgroup keeps a ring of
+// stages of 64 keys there, and all but one of them are under way: a stage is
+// worked on in less than half the time memory takes to answer, so that it is
+// the bytes under way (96 KB a CU and more) that keep the matrix cores fed.
+// They go from memory to LDS without passing registers.
+//
+// A row is kept in 16-byte pieces, piece c of row r at place c ^ r (its low
+// bits), so that the rows and pieces that a product reads lie on all banks; a
+// load writes 64 places in order, so it is the source that is mixed.
+// wk == 1: every wave takes both tiles of a stage; wk == 2: pairs of waves
+// share rows and take one each.
+constexpr int kShared = 8;                        // waves
+
+__device__ const u32x4 kZeros[1] = {};            // what dims behind the head's own are read from
+
+template <int CT, int DP, bool PAD>
+__global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams p)
+{
+    constexpr int RB = 2;
+    using W = Rows<CT, DP, RB, PAD>;
+    constexpr int KS = W::KS, es = W::es, ROW = DP * es, PIECES = ROW / 16, MIX = PIECES < 8 ? PIECES - 1 : 7;
+    constexpr int LOADS = 2 * 64 * ROW / (kShared * 64 * 16);      // 16-byte pieces a thread loads a stage
+    constexpr int STAGE = 2 * 64 * ROW, RING = ROW == 256 ? 4 : 8;
+    static_assert(RING * STAGE >= 4 * RB * 16 * DP * 4, "the waves' outputs are joined in the ring");
+    __shared__ __attribute__((aligned(16))) char smem[RING * STAGE + W::join_words(kShared) * 4];
+    const int tid = (int)threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const Place at(p);
+    if (p.nsplit > 1 && at.t0 >= at.t1) return;
+    const int wkey = wave & (p.wk - 1), wrow = wave / p.wk;
+
+    // Stages whose keys are all cached tokens, which every row sees. In pages:
+    // up to the first that touches an absent one.
+    const int key0 = at.t0 * kTileKeys;
+    int stages = min((at.t1 - at.t0) / 2, max(at.n - key0, 0) / 64);
+    if (p.c.table) {
+        const int lane = tid & 63;
+        for (int i = 0; i < stages * 4; i += 64) {
+            const bool bad = i + lane < stages * 4 && (uint32_t)p.c.table[at.b * p.c.ts + ((key0 + (i + lane) * 16) >> p.c.shift)] >= p.c.pages;
+            const uint64_t any = __builtin_amdgcn_ballot_w64(bad);
+            if (any) stages = (i + __builtin_ctzll(any)) / 4;
+        }
+    }
+    // A thread's place `lin` of load j: the keys' 64 rows, then the values'. A
+    // wave's 64 places lie in one half tile, so that a page is looked up once.
+    const char *src[LOADS];
+    bool pad[LOADS];
+#pragma unroll
+    for (int j = 0; j < LOADS; j++) {
+        const int lin0 = j * kShared * 64 + wave * 64, lin = lin0 + (tid & 63);
+        const bool val = lin0 >= 64 * PIECES;
+        const int row = (lin / PIECES) & 63, piece = lin % PIECES ^ (row & MIX);
+        const int64_t step = val ? p.c.vs1 : p.c.ks1;
+        src[j] = (val ? p.c.v + at.h * p.c.vs2 : p.c.k + at.h * p.c.ks2) + piece * 16 + (p.c.table ? (row & 15) * step : at.b * (val ? p.c.vs0 : p.c.ks0) + (key0 + row) * step);
+        if (PAD) pad[j] = piece * 16 >= p.D * es;
+    }
+    int entry = 0;
+    const auto issue = [&](int i) {
+        char *to = smem + i % RING * STAGE + wave * 1024;
+        if (p.c.table && (i & 15) == 0) {         // page numbers of the next 64 half tiles, one a lane
+            const int half = i * 4 + (tid & 63);
+            entry = half < stages * 4 ? p.c.table[at.b * p.c.ts + ((key0 + half * 16) >> p.c.shift)] : 0;
+            __builtin_amdgcn_s_waitcnt(0x0f70);
+        }
+#pragma unroll
+        for (int j = 0; j < LOADS; j++) {
+            const int lin0 = j * kShared * 64 + wave * 64;
+            const bool val = lin0 >= 64 * PIECES;
+            const char *from = src[j];
+            if (p.c.table) {
+                const int half = (lin0 / PIECES & 63) >> 4;
+                const uint32_t page = (uint32_t)__builtin_amdgcn_readlane(entry, (i & 15) * 4 + half);
+                const uint32_t in = (uint32_t)(key0 + i * 64 + half * 16) & ((1u << p.c.shift) - 1);
+                from += (int64_t)page * (val ? p.c.vs0 : p.c.ks0) + (int64_t)in * (val ? p.c.vs1 : p.c.ks1);
+            } else {
+                src[j] += 64 * (val ? p.c.vs1 : p.c.ks1);
+            }
+            if (PAD && pad[j]) from = reinterpret_cast<const char *>(kZeros);
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
+                                             (__attribute__((address_space(3))) void *)(to + j * kShared * 1024), 16, 0, 0);
+        }
+    };
+    // The queries first, and waited for: a wait for them inside the loop would
+    // be one for every stage under way.
+    W w;
+    w.init(p, at.b, at.h, (at.rg * (kShared / p.wk) + wrow) * RB * 16, at.n, at.end);
+    __builtin_amdgcn_s_waitcnt(0x0f70);
+    int issued = 0;
+    while (issued < RING - 1 && issued < stages) issue(issued++);
+
+    const auto keys_of = [&](const char *stage, int tile, u32x4 (&k)[2][KS]) {
+        const char *kb = stage + (tile * 32 + w.x) * ROW;
+#pragma unroll
+        for (int hf = 0; hf < 2; hf++)
+#pragma unroll
+            for (int ks = 0; ks < KS; ks++) {
+                const int o = (ks * 32 + w.g * 8) * es;
+                k[hf][ks] = widen<CT>(*reinterpret_cast<const Raw<CT> *>(kb + hf * 16 * ROW + ((((o >> 4) ^ (w.x & MIX)) << 4) | (o & 15))));
+            }
+    };
+    const auto values_of = [&](const char *stage, int tile, typename W::Values (&v)[W::VC][8]) {
+        const char *vb = stage + (64 + tile * 32 + w.g * 4) * ROW;
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const int o = w.x * W::VE * es, mix = (w.g * 4 + (j & 3)) & MIX;
+            v[0][j] = *reinterpret_cast<const typename W::Values *>(vb + ((j >> 2) * 16 + (j & 3)) * ROW + ((((o >> 4) ^ mix) << 4) | (o & 15)));
+        }
+    };
+
+    int done = 0;
+    for (; done < stages; done++) {
+        // This wave's loads of the stage are done when no more than the later
+        // stages' are outstanding (they end in order); other loads in between
+        // make the wait longer, never shorter. Behind the barrier all waves'
+        // are, and all have read the stage before, whose place is free.
+        if (issued - done == RING - 1) __builtin_amdgcn_s_waitcnt(0x0f70 | ((RING - 2) * LOADS & 15) | ((RING - 2) * LOADS >> 4) << 14);
+        else __builtin_amdgcn_s_waitcnt(0x0f70);
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        if (issued < stages) issue(issued++);
+        const char *stage = smem + done % RING * STAGE;
+        typename W::Values v[W::VC][8];
+        u32x4 k[2][KS];
+        if (p.wk == 1) {
+            f32x4 s[RB][4];
+            u32x4 pw[RB][2];
+            keys_of(stage, 0, k);
+            w.score(k, &s[0][0], 4);
+            keys_of(stage, 1, k);
+            w.score(k, &s[0][2], 4);
+            w.weigh(s, pw);
+            values_of(stage, 0, v);
+            w.add(v, pw, 0);
+            values_of(stage, 1, v);
+            w.add(v, pw, 1);
+        } else {
+            f32x4 s[RB][2];
+            u32x4 pw[RB][1];
+            keys_of(stage, wkey, k);
+            w.score(k, &s[0][0], 2);
+            values_of(stage, wkey, v);
+            w.weigh(s, pw);
+            w.add(v, pw, 0);
+        }
+    }
+    // the other tiles, from the cache itself
+    if (w.row0 < p.R) {
+        TileFinder rest;
+        const int first = at.t0 + 2 * done + wkey;
+        for (int i = 0; first + i * p.wk < at.t1; i++) {
+            const Tile t = rest.at(p, at.b, at.h, i, first, at.n, w.lim);
+            if (t.key >= w.lim) break;
+            w.masked_tile(p, t, at.b, at.n, at.nd);
+        }
+    }
+    w.close();
+    if (p.wk == 2) {
+        __syncthreads();                          // the ring's memory is free
+        w.join(kShared, 2, wkey, wave - wkey, reinterpret_cast<float *>(smem + RING * STAGE), reinterpret_cast<float *>(smem) + wrow * RB * 16 * DP);
+        if (wkey) return;
+    }
+    w.store(p, at.b, at.h, at.split, at.nd);
+    if (w.odd) w.poison(p, at.b, at.h, at.split, at.n, at.nd, max(at.t0 * kTileKeys, at.n & ~(kTileKeys - 1)), min(at.t1 * kTileKeys, at.end));
+}
+
+// Joins a row's splits. Few of them: 16 lanes a row, one split a lane to weigh
+// and then DP / 16 dims a lane; a row's loads are few and wait for each other,
+// so rows must run side by side. Many: a workgroup a row, below.
+struct Joined {
+    int b, h, tok, head, nd, used;
+
+    __device__ inline Joined(const AttendParams &p, int64_t row)      // ((b * heads) + h) * R + r
+    {
+        const int r = (int)(row % p.R);
+        h = (int)(row / p.R % p.heads), b = (int)(row / p.R / p.heads);
+        const int n = clamp_length(p.length, b, p.c.tokens);
+        nd = clamp_drafted(p.drafted, b, p.T);
+        const int end = nd == 0 ? 0 : (uint32_t)nd > p.c.tokens - (uint32_t)n ? (int)p.c.tokens : n + nd;
+        const int ntiles = (end + kTileKeys - 1) / kTileKeys, tps = tiles_per_split(ntiles, p);
+        used = (ntiles + tps - 1) / tps;
+        tok = r / p.G, head = h * p.G + r % p.G;
+    }
+
+    __device__ inline bool empty(float sum) const { return sum == 0.f || tok >= nd; }
+    __device__ inline char *out(const AttendParams &p) const { return p.out + b * p.os0 + tok * p.os1 + head * p.os2; }
+    __device__ inline void put_lse(const AttendParams &p, float top, float sum) const
+    {
+        if (p.lse) p.lse[((int64_t)b * p.T + tok) * (p.heads * p.G) + head] = empty(sum) ? -INFINITY : (top + __log2f(sum)) * 0.6931471805599453f;
+    }
+};
+
+template <int DP>
+__global__ __launch_bounds__(256) void k_attend_join_few(AttendParams p, int64_t rows, int half)
+{
+    constexpr int E = DP / 64;                    // 16-byte pieces a lane, 64 dims apart
+    const int x = (int)(threadIdx.x & 15);
+    const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    if (row >= rows) return;
+    const Joined j(p, row);
+    const float *po = p.part_o + row * p.nsplit * DP + x * 4;
+    const float2 ml = x < j.used ? p.part_ml[row * p.nsplit + x] : make_float2(-INFINITY, 0.f);
+    f32x4 v[2][E];                                // two splits ahead
+#pragma unroll
+    for (int u = 0; u < 2; u++)
+#pragma unroll
+        for (int e = 0; e < E; e++) v[u][e] = u < j.used ? *reinterpret_cast<const f32x4 *>(po + u * DP + e * 64) : f32x4{0.f, 0.f, 0.f, 0.f};
+    float top = ml.x;
+    for (int y = 1; y < 16; y <<= 1) top = fmaxf(top, __shfl_xor(top, y));
+    const float a = ml.y == 0.f ? 0.f : __builtin_amdgcn_exp2f(ml.x - (top == -INFINITY ? 0.f : top));
+    float sum = ml.y * a;
+    for (int y = 1; y < 16; y <<= 1) sum += __shfl_xor(sum, y);
+    f32x4 o[E] = {};
+    for (int k = 0; k < j.used; k += 2)
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+            const float w = __shfl(a, (int)(threadIdx.x & 48) + ((k + u) & 15));
+#pragma unroll
+            for (int e = 0; e < E; e++) {
+                if (k + u < j.used) o[e] += v[u][e] * w;
+                if (k + u + 2 < j.used) v[u][e] = *reinterpret_cast<const f32x4 *>(po + (k + u + 2) * DP + e * 64);
+            }
+        }
+    if (x == 0) j.put_lse(p, top, sum);
+    const bool empty = j.empty(sum);
+    const float inv = 1.f / sum;
+#pragma unroll
+    for (int e = 0; e < E; e++) {
+        if (x * 4 + e * 64 >= p.D) continue;
+        float r[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) r[i] = empty ? 0.f : o[e][i] * inv;
+        *reinterpret_cast<u32x2 *>(j.out(p) + (x * 4 + e * 64) * 2) =
+            half ? u32x2{pack2<true>(r[0], r[1]), pack2<true>(r[2], r[3])} : u32x2{pack2<false>(r[0], r[1]), pack2<false>(r[2], r[3])};
     }
 }
 
-// Joins a row's splits: W waves a row, each taking every W-th split.
-template <int DP, int W>
-__global__ __launch_bounds__(kWaves * 64) void k_attend_join(AttendParams p, int64_t rows, int half)
+template <int DP>
+__global__ __launch_bounds__(kWaves * 64) void k_attend_join_many(AttendParams p, int half)
 {
     constexpr int E = DP / 64, U = 8;             // dims a lane, splits whose loads are under way together
-    __shared__ float so[W > 1 ? kWaves : 1][DP];
-    const int lane = (int)(threadIdx.x & 63), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int64_t row = (int64_t)blockIdx.x * (kWaves / W) + wave / W;      // ((b * heads) + h) * R + r
-    if (row >= rows) return;                      // W == 1 only: rows are whole workgroups otherwise
-    const int part = wave % W;
-    const int r = (int)(row % p.R), h = (int)(row / p.R % p.heads), b = (int)(row / p.R / p.heads);
-    const int n = clamp_length(p.length, b, p.c.tokens), nd = clamp_drafted(p.drafted, b, p.T);
-    const int end = nd == 0 ? 0 : (uint32_t)nd > p.c.tokens - (uint32_t)n ? (int)p.c.tokens : n + nd;
-    const int ntiles = (end + kTileKeys - 1) / kTileKeys, tps = tiles_per_split(ntiles, p);
-    const int used = (ntiles + tps - 1) / tps, tok = r / p.G, head = h * p.G + r % p.G;
+    typedef float fe __attribute__((ext_vector_type(E)));
+    __shared__ __attribute__((aligned(16))) float so[kWaves][DP];
+    const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
+    const int64_t row = blockIdx.x;
+    const Joined j(p, row);
     const float2 *ml = p.part_ml + row * p.nsplit;
     const float *po = p.part_o + row * p.nsplit * DP + lane * E;
 
     float top = -INFINITY;
-    for (int k = lane; k < used; k += 64) top = fmaxf(top, ml[k].x);
+    for (int k = lane; k < j.used; k += 64) top = fmaxf(top, ml[k].x);
     for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
     const float base = top == -INFINITY ? 0.f : top;
     float sum = 0.f;
-    for (int k = lane; k < used; k += 64) sum += ml[k].y * __builtin_amdgcn_exp2f(ml[k].x - base);
+    for (int k = lane; k < j.used; k += 64) sum += ml[k].y * __builtin_amdgcn_exp2f(ml[k].x - base);
     for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
 
-    typedef float fe __attribute__((ext_vector_type(E)));
     fe o = {};
-    for (int k0 = part; k0 < used; k0 += W * U) {
+    for (int k0 = wave; k0 < j.used; k0 += kWaves * U) {
         fe v[U];
         float a[U];
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            const int k = min(k0 + u * W, used - 1);
+            const int k = min(k0 + u * kWaves, j.used - 1);
             a[u] = ml[k].x;
             if constexpr (E == 1) v[u][0] = po[(int64_t)k * DP];
             else v[u] = *reinterpret_cast<const fe *>(po + (int64_t)k * DP);
         }
 #pragma unroll
         for (int u = 0; u < U; u++)
-            if (k0 + u * W < used) o += v[u] * __builtin_amdgcn_exp2f(a[u] - base);
+            if (k0 + u * kWaves < j.used) o += v[u] * __builtin_amdgcn_exp2f(a[u] - base);
     }
-    if constexpr (W > 1) {
-        if constexpr (E == 1) so[wave][lane] = o[0];
-        else *reinterpret_cast<fe *>(&so[wave][lane * E]) = o;
-        __syncthreads();
-        if (part) return;
-        for (int w = 1; w < W; w++)
-            if constexpr (E == 1) o[0] += so[wave + w][lane];
-            else o += *reinterpret_cast<const fe *>(&so[wave + w][lane * E]);
-    }
-    const bool empty = sum == 0.f || tok >= nd;
-    if (lane == 0 && p.lse) p.lse[((int64_t)b * p.T + tok) * (p.heads * p.G) + head] = empty ? -INFINITY : (top + __log2f(sum)) * 0.6931471805599453f;
-    if (lane * E >= p.D) return;
+    if constexpr (E == 1) so[wave][lane] = o[0];
+    else *reinterpret_cast<fe *>(&so[wave][lane * E]) = o;
+    __syncthreads();
+    if (threadIdx.x == 0) j.put_lse(p, top, sum);
+    const int d = 2 * (int)threadIdx.x;
+    if (d >= p.D) return;
+    const bool empty = j.empty(sum);
     const float inv = 1.f / sum;
-    char *out = p.out + b * p.os0 + tok * p.os1 + head * p.os2 + lane * E * 2;
-    if constexpr (E == 1) {
-        const float u = empty ? 0.f : o[0] * inv;
-        *reinterpret_cast<uint16_t *>(out) = (uint16_t)(half ? pack2<true>(u, 0.f) : pack2<false>(u, 0.f));
-    } else {
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-            const float u = empty ? 0.f : o[e] * inv, v = empty ? 0.f : o[e + 1] * inv;
-            *reinterpret_cast<uint32_t *>(out + e * 2) = half ? pack2<true>(u, v) : pack2<false>(u, v);
-        }
-    }
+    const float u = empty ? 0.f : (so[0][d] + so[1][d] + so[2][d] + so[3][d]) * inv;
+    const float v = empty ? 0.f : (so[0][d + 1] + so[1][d + 1] + so[2][d + 1] + so[3][d + 1]) * inv;
+    *reinterpret_cast<uint32_t *>(j.out(p) + d * 2) = half ? pack2<true>(u, v) : pack2<false>(u, v);
 }
 
 // score[key] += sum over a kv head's rows of exp(s - lse). With the rows' lse
@@ -725,26 +1019,30 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attend_weigh(AttendParams p)
 // ------------------------------------------------------------------- host --
 struct Plan {
     int DP, RB, wk, nrg, nsplit, min_tiles;
+    bool shared;                                  // k_attend_shared
     uint64_t rows, off_ml, off_lse, bytes;
 };
 
 // The split of the key axis: enough workgroups to fill the chip a few times,
 // as far as each still has a share of keys worth its joining.
-Plan make_plan(uint32_t seqs, uint32_t kv_heads, uint32_t dim, uint32_t cache_tokens, uint32_t T, uint32_t heads)
+// may_share: the cache's rows begin on 16 bytes and end on them.
+Plan make_plan(uint32_t seqs, uint32_t kv_heads, uint32_t dim, uint32_t cache_tokens, uint32_t T, uint32_t heads, bool may_share)
 {
     Plan a;
     const uint32_t G = heads / kv_heads;
     const uint64_t R = (uint64_t)T * G;
     a.DP = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
-    a.RB = R <= 16 ? 1 : R <= 32 || a.DP == 256 ? 2 : 4;
+    a.shared = may_share && R > 64 && a.DP <= 128;
+    a.RB = a.shared ? 2 : R <= 16 ? 1 : R <= 32 || a.DP == 256 ? 2 : 4;
+    const int waves = a.shared ? kShared : kWaves;
     const uint64_t blocks = (R + a.RB * 16 - 1) / (a.RB * 16);
-    const int wr = blocks >= 4 ? 4 : blocks >= 2 ? 2 : 1;
-    a.wk = kWaves / wr;
+    const int wr = a.shared ? (R > 128 ? 8 : 4) : blocks >= 4 ? 4 : blocks >= 2 ? 2 : 1;
+    a.wk = waves / wr;
     a.nrg = (int)((blocks + wr - 1) / wr);
-    a.min_tiles = 2 * a.wk;
+    a.min_tiles = a.shared ? 4 : 2 * a.wk;
     const uint64_t base = (uint64_t)seqs * kv_heads * a.nrg;
     const uint64_t tiles = ((uint64_t)cache_tokens + kTileKeys - 1) / kTileKeys;
-    const uint64_t want = a.RB == 1 ? 8 * kCUs : a.RB == 2 ? 4 * kCUs : 2 * kCUs;
+    const uint64_t want = a.shared ? kCUs : a.RB == 1 ? 8 * kCUs : a.RB == 2 ? 4 * kCUs : 2 * kCUs;
     uint64_t split = (want + base - 1) / base;
     const uint64_t most = (tiles + a.min_tiles - 1) / a.min_tiles;
     split = split > most ? most : split;
@@ -775,16 +1073,20 @@ template <int CT, int DP, bool PAD>
 int run(const AttendParams &p, const Plan &plan, int seqs, int half, hipStream_t s)
 {
     const uint64_t grid = (uint64_t)seqs * p.heads * p.nrg * p.nsplit;
-    int rc;
-    if (plan.RB == 1) rc = launch<CT, DP, 1, PAD>(p, grid, s);
+    int rc = UZIP_EINVAL;
+    if (plan.shared) {
+        if constexpr (DP <= 128) {
+            k_attend_shared<CT, DP, PAD><<<(unsigned)grid, kShared * 64, 0, s>>>(p);
+            UZIP_KV_LAUNCH_CHECK("k_attend_shared");
+            rc = UZIP_OK;
+        }
+    } else if (plan.RB == 1) rc = launch<CT, DP, 1, PAD>(p, grid, s);
     else if (plan.RB == 2) rc = launch<CT, DP, 2, PAD>(p, grid, s);
     else if constexpr (DP <= 128) rc = launch<CT, DP, 4, PAD>(p, grid, s);
-    else rc = UZIP_EINVAL;
     if (rc) return rc;
     if (p.nsplit > 1) {
-        // a wave a row while it can have all its splits' loads under way at once
-        if (p.nsplit <= 16) k_attend_join<DP, 1><<<(unsigned)((plan.rows + kWaves - 1) / kWaves), kWaves * 64, 0, s>>>(p, (int64_t)plan.rows, half);
-        else k_attend_join<DP, kWaves><<<(unsigned)plan.rows, kWaves * 64, 0, s>>>(p, (int64_t)plan.rows, half);
+        if (p.nsplit <= 16) k_attend_join_few<DP><<<(unsigned)((plan.rows + 15) / 16), 256, 0, s>>>(p, (int64_t)plan.rows, half);
+        else k_attend_join_many<DP><<<(unsigned)plan.rows, kWaves * 64, 0, s>>>(p, half);
         UZIP_KV_LAUNCH_CHECK("k_attend_join");
     }
     if (p.score) {
@@ -812,7 +1114,9 @@ uint64_t uzip_kv_attend_workspace_bytes(uint32_t seqs, uint32_t kv_heads, uint32
                                         uint32_t tokens, uint32_t heads)
 {
     if (!uzip_kv::valid_shapes(seqs, kv_heads, dim, cache_tokens, tokens, heads)) return 0;
-    return uzip_kv::make_plan(seqs, kv_heads, dim, cache_tokens, tokens, heads).bytes;
+    const uint64_t a = uzip_kv::make_plan(seqs, kv_heads, dim, cache_tokens, tokens, heads, true).bytes;
+    const uint64_t b = uzip_kv::make_plan(seqs, kv_heads, dim, cache_tokens, tokens, heads, false).bytes;
+    return a > b ? a : b;
 }
 
 int uzip_kv_attend(const uzip_kv_cache_t *cache, const uzip_kv_attend_args_t *a, void *d_ws, uint64_t ws_bytes,
@@ -827,8 +1131,10 @@ int uzip_kv_attend(const uzip_kv_cache_t *cache, const uzip_kv_attend_args_t *a,
     if (a->reserved || (a->score && (a->score_stride[0] < 0 || a->score_stride[1] < 0 || a->score_tokens > cache->tokens))) return UZIP_EINVAL;
     if (a->tree && (a->tree_stride[0] < 0 || a->tree_stride[1] < 0)) return UZIP_EINVAL;
     if (!d_ws || !aligned(d_ws, 16)) return UZIP_EINVAL;
-    const Plan plan = make_plan(cache->seqs, cache->heads, cache->dim, cache->tokens, a->tokens, a->heads);
-    if (ws_bytes < plan.bytes) return UZIP_ENOSPC;
+    if (ws_bytes < uzip_kv_attend_workspace_bytes(cache->seqs, cache->heads, cache->dim, cache->tokens, a->tokens, a->heads)) return UZIP_ENOSPC;
+    int64_t bits = cache->dim * elem_size((int)cache->dtype);
+    for (int i = 0; i < 3; i++) bits |= (cache->k_stride[i] | cache->v_stride[i]) * elem_size((int)cache->dtype);
+    const Plan plan = make_plan(cache->seqs, cache->heads, cache->dim, cache->tokens, a->tokens, a->heads, (bits & 15) == 0);
     if ((uint64_t)cache->seqs * cache->heads * plan.nrg * plan.nsplit >= (1ull << 31) ||
         (uint64_t)cache->seqs * cache->heads * ((cache->tokens + 127) / 128) >= (1ull << 31)) return UZIP_EINVAL;
 
@@ -859,6 +1165,7 @@ int uzip_kv_attend(const uzip_kv_cache_t *cache, const uzip_kv_attend_args_t *a,
     p.nrg = plan.nrg;
     p.min_tiles = plan.min_tiles;
     p.wk = plan.wk;
+    p.unit = plan.shared ? 2 : plan.wk;
     p.c2 = a->scale * 1.4426950408889634f;
     p.q_f16 = a->dtype == UZIP_KV_F16;
     const int seqs = (int)cache->seqs, half = p.q_f16;
