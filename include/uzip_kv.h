@@ -184,7 +184,8 @@ typedef struct uzip_kv_evict_args {
 int uzip_kv_evict(const uzip_kv_cache_t *cache, const uzip_kv_cache_t *out, const uzip_kv_evict_args_t *a,
                   void *d_ws, uint64_t ws_bytes, hipStream_t s);
 
-/* Workspace of uzip_kv_evict; 0 when the shapes are invalid. */
+/* Workspace of uzip_kv_evict, cache_tokens the scores a row holds; 0 when it
+ * needs none (d_ws may then be NULL) or the shapes are invalid. */
 uint64_t uzip_kv_evict_workspace_bytes(uint32_t seqs, uint32_t kv_heads, uint32_t cache_tokens);
 
 #ifdef __cplusplus

@@ -295,8 +295,18 @@ bool same_tensor(const uzip_kv_tensor_t &a, const uzip_kv_tensor_t &b)
 }
 
 // ------------------------------------------------------------------ evict --
+// The kept tokens of a row of scores are the first and last ones and the
+// need-th largest of the others and all above it. Scores become unsigned ranks
+// in the same order; the need-th largest rank is found by histograms of its
+// upper 11 bits, the next 11 and the last 10, each of the ranks that agree with
+// the bits found so far. Histograms in LDS are held in 8 copies, one for every
+// eighth lane: attention weights crowd into few bins, and lanes that add to
+// the same word wait for each other.
 constexpr int kSelThreads = 1024, kSelWaves = kSelThreads / 64;
 constexpr int kBins = 2048, kCopies = 8;
+constexpr int kOneTokens = 32 * kSelThreads;      // rows up to here are held in one workgroup's registers
+constexpr int kSlice = 8 * kSelThreads;           // tokens a workgroup takes of a longer row
+constexpr uint32_t kForced = 0xffffffffu, kOutside = 0;      // ranks of no score
 
 struct EvictParams {
     CacheView c, o;
@@ -306,145 +316,444 @@ struct EvictParams {
     int32_t *index, *length_out;
     float *score_out;
     int heads, D, keep, sink, recent;
+    int parts, share;                             // workgroups a row, slots each, where k_evict_one copies
+    // long rows: per row, slices' histograms of one level [3][slices][kBins],
+    // their numbers of kept tokens by level [2][slices], and what is found
+    uint16_t *hist;
+    uint32_t *count;
+    uint2 *found;                                 // [row][2]: rank bits, how many are still needed
+    int slices;
 };
 
-// scores in the order of unsigned integers; NaN as -inf, -0 as 0
-__device__ inline uint32_t rank_of(float f)
+// Scores in the order of unsigned integers; NaN as -inf, -0 as 0. Tokens that
+// are kept anyway rank above all, those outside the cache below.
+__device__ inline uint32_t rank_of(const EvictParams &p, float f, int i, int n)
 {
+    if (i >= n) return kOutside;
+    if (i < p.sink || i >= n - p.recent) return kForced;
     uint32_t u = __float_as_uint(f);
     if (f != f) u = 0xff800000u;
     if (f == 0.f) u = 0;
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// One workgroup a row of scores: the need-th largest of the tokens that are
-// not kept anyway, by three histograms of 11, 11 and 10 bits, then the kept
-// tokens in order. Histograms are held in 8 copies, one for every eighth lane:
-// attention weights crowd into few bins, and lanes that add to the same word
-// wait for each other.
-__global__ __launch_bounds__(kSelThreads) void k_evict_select(EvictParams p)
-{
-    __shared__ uint32_t hist[kBins * kCopies];
-    __shared__ uint32_t wsum[kSelWaves][2];
-    __shared__ uint32_t found[2];
-    const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int h = (int)(blockIdx.x % p.heads), b = (int)(blockIdx.x / p.heads);
-    const int n = clamp_length(p.length, b, p.c.tokens);
-    const int kept = min(n, p.keep);
-    const float *score = p.score + b * p.sc0 + h * p.sc1;
-    int32_t *index = p.index + ((int64_t)b * p.heads + h) * p.keep;
-    if (h == 0 && tid == 0 && p.length_out) p.length_out[b] = kept;
-    for (int j = kept + tid; j < p.keep; j += kSelThreads) index[j] = -1;
-    if (n <= p.keep) {
-        for (int j = tid; j < n; j += kSelThreads) index[j] = j;
-        return;
-    }
-    const int lo = p.sink, hi = n - p.recent;      // candidates: [lo, hi)
-    uint32_t need = (uint32_t)(p.keep - p.sink - p.recent);
-    uint32_t prefix = 0;                           // the bits found so far
-    if (need == 0) prefix = 0xffffffffu;           // above every rank
-    for (int level = 0; level < 3 && need; level++) {
-        const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bins = level == 2 ? 1024 : 2048;
-        for (int i = tid; i < kBins * kCopies; i += kSelThreads) hist[i] = 0;
-        __syncthreads();
-        for (int i = lo + tid; i < hi; i += kSelThreads) {
-            const uint32_t r = rank_of(score[i]);
-            const bool in = level == 0 || (level == 1 ? r >> 21 == prefix >> 21 : r >> 10 == prefix >> 10);
-            if (in) atomicAdd(&hist[((r >> shift) & (bins - 1)) * kCopies + (lane & (kCopies - 1))], 1u);
-        }
-        __syncthreads();
-        // thread t owns bins 2t and 2t + 1 from the top; prefix sums over them
-        uint32_t c0 = 0, c1 = 0;
-        const int top = kBins - 1 - 2 * tid;
-        for (int k = 0; k < kCopies; k++) c0 += hist[top * kCopies + k], c1 += hist[(top - 1) * kCopies + k];
-        uint32_t sum = c0 + c1;
-        for (int x = 1; x < 64; x <<= 1) {
-            const uint32_t v = __shfl_up(sum, x);
-            if (lane >= x) sum += v;
-        }
-        if (lane == 63) wsum[wave][0] = sum;
-        __syncthreads();
-        uint32_t before = sum - c0 - c1;
-        for (int w = 0; w < wave; w++) before += wsum[w][0];
-        if (before < need && need <= before + c0 + c1) {
-            const bool second = need > before + c0;
-            found[0] = (uint32_t)(second ? top - 1 : top);
-            found[1] = need - before - (second ? c0 : 0);
-        }
-        __syncthreads();
-        prefix |= found[0] << shift;
-        need = found[1];
-        __syncthreads();
-    }
-    // need: how many of the ranks equal to prefix are kept, the lowest tokens
+__device__ inline int level_shift(int level) { return level == 0 ? 21 : level == 1 ? 10 : 0; }
 
-    const int seg = ((n + kSelWaves - 1) / kSelWaves + 63) & ~63, s0 = wave * seg, s1 = min(s0 + seg, n);
-    uint32_t above = 0, equal = 0;
-    for (int i = s0 + lane; i < s1; i += 64) {
-        const bool free_ = i >= lo && i < hi;
-        const uint32_t r = rank_of(score[i]);
-        above += !free_ || r > prefix;
-        equal += free_ && r == prefix;
+// whether a rank is a score's and agrees with the bits found before this level
+__device__ inline bool agrees(uint32_t r, uint32_t prefix, int level)
+{
+    if (r == kForced || r == kOutside) return false;
+    return level == 0 || (level == 1 ? r >> 21 == prefix >> 21 : r >> 10 == prefix >> 10);
+}
+
+__device__ inline void add_to_hist(uint32_t *hist, uint32_t r, int level)
+{
+    atomicAdd(&hist[(r >> level_shift(level) & (level == 2 ? 1023 : 2047)) * kCopies + (threadIdx.x & (kCopies - 1))], 1u);
+}
+
+// Of bins counted from the top, two a thread (c0 in bin 2047 - 2 tid, c1 in the
+// next lower one): the bin that holds the need-th, and how many of it are
+// needed. out: {bin, needed}. wsum: one word a wave. Ends with a barrier.
+__device__ inline void find_bin(uint32_t c0, uint32_t c1, uint32_t need, uint32_t *wsum, uint32_t *out)
+{
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    uint32_t sum = c0 + c1;
+    for (int x = 1; x < 64; x <<= 1) {
+        const uint32_t v = __shfl_up(sum, x);
+        if (lane >= x) sum += v;
     }
-    for (int x = 1; x < 64; x <<= 1) above += __shfl_xor(above, x), equal += __shfl_xor(equal, x);
-    if (lane == 0) wsum[wave][0] = above, wsum[wave][1] = equal;
+    if (lane == 63) wsum[wave] = sum;
     __syncthreads();
-    above = equal = 0;
-    for (int w = 0; w < wave; w++) above += wsum[w][0], equal += wsum[w][1];
-    for (int i0 = s0; i0 < s1; i0 += 64) {
-        const int i = i0 + lane;
-        const bool free_ = i >= lo && i < hi;
-        const uint32_t r = i < s1 ? rank_of(score[i]) : 0;
-        const bool over = i < s1 && (!free_ || r > prefix), tie = i < s1 && free_ && r == prefix;
-        const uint64_t mo = __builtin_amdgcn_ballot_w64(over), mt = __builtin_amdgcn_ballot_w64(tie);
-        const uint64_t below = (1ull << lane) - 1;
-        const uint32_t a = above + (uint32_t)__popcll(mo & below), e = equal + (uint32_t)__popcll(mt & below);
-        if (over || (tie && e < need)) index[a + min(e, need)] = i;
-        above += (uint32_t)__popcll(mo);
-        equal += (uint32_t)__popcll(mt);
+    uint32_t before = sum - c0 - c1;
+#pragma unroll
+    for (int w = 0; w < kSelWaves; w += 4) {      // all waves' sums at once
+        const u32x4 v = *reinterpret_cast<const u32x4 *>(wsum + w);
+#pragma unroll
+        for (int i = 0; i < 4; i++) before += w + i < wave ? v[i] : 0;
+    }
+    if (before < need && need <= before + c0 + c1) {
+        const bool second = need > before + c0;
+        out[0] = (uint32_t)(kBins - 1 - 2 * tid - second);
+        out[1] = need - before - (second ? c0 : 0);
+    }
+    __syncthreads();
+}
+
+__device__ inline void fill_behind(const EvictParams &p, int32_t *index, int kept, int part, int parts)
+{
+    for (int j = kept + part * kSelThreads + (int)threadIdx.x; j < p.keep; j += parts * kSelThreads) index[j] = -1;
+}
+
+// Kept rows [j0, j1) of a sequence and head, to out in order: bound by memory.
+// slot(j) is the token of slot j, -1 for none.
+template <typename RawT, int SLOTS, typename Slot>
+__device__ inline void copy_rows(const EvictParams &p, int b, int h, int j0, int j1, int threads, Slot slot)
+{
+    constexpr int es = sizeof(RawT) / 8;
+    const int per = p.D / 8, rows = threads / per;           // 8-element pieces a row, rows a step
+    const int sub = (int)threadIdx.x / per, piece = (int)threadIdx.x - sub * per;
+    if (sub >= rows) return;
+    const int64_t row = ((int64_t)b * p.heads + h) * p.keep;
+    for (int base = j0 + sub; base < j1; base += rows * SLOTS) {
+        RawT k[SLOTS], v[SLOTS];
+        int idx[SLOTS];
+#pragma unroll
+        for (int i = 0; i < SLOTS; i++) idx[i] = base + i * rows < j1 ? slot(base + i * rows) : -1;
+#pragma unroll
+        for (int i = 0; i < SLOTS; i++) {
+            k[i] = RawT{}, v[i] = RawT{};
+            int64_t ko, vo;
+            if (idx[i] >= 0 && locate(p.c, b, (uint32_t)idx[i], p.c.ks0, p.c.ks1, ko)) {
+                locate(p.c, b, (uint32_t)idx[i], p.c.vs0, p.c.vs1, vo);
+                k[i] = *reinterpret_cast<const RawT *>(p.c.k + ko + h * p.c.ks2 + piece * 8 * es);
+                v[i] = *reinterpret_cast<const RawT *>(p.c.v + vo + h * p.c.vs2 + piece * 8 * es);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < SLOTS; i++) {
+            const int64_t j = base + i * rows;
+            if (j >= j1) continue;
+            *reinterpret_cast<RawT *>(p.o.k + b * p.o.ks0 + j * p.o.ks1 + h * p.o.ks2 + piece * 8 * es) = k[i];
+            *reinterpret_cast<RawT *>(p.o.v + b * p.o.vs0 + j * p.o.vs1 + h * p.o.vs2 + piece * 8 * es) = v[i];
+            if (piece == 0 && p.score_out) p.score_out[row + j] = idx[i] >= 0 ? p.score[b * p.sc0 + h * p.sc1 + idx[i]] : 0.f;
+        }
     }
 }
 
-// Copies the kept rows: bound by memory. A thread moves 8 elements of the key
-// and of the value of four slots.
-template <typename RawT>
-__global__ __launch_bounds__(256) void k_evict_gather(EvictParams p)
+// Rows of up to N * 1024 tokens, held in a workgroup's registers. COPY (short
+// rows): each of a row's workgroups finds the kept tokens for itself and copies
+// its share of them; a second launch would cost more than choosing again.
+// Without, one workgroup a row writes the index, and k_evict_copy copies.
+template <int N, bool COPY, typename RawT>
+__global__ __launch_bounds__(kSelThreads) void k_evict_one(EvictParams p)
 {
-    constexpr int kSlots = 4, es = sizeof(RawT) / 8;
-    const int per = p.D / 8, rows = 256 / per;     // rows a step
-    const int groups = (p.keep + rows * kSlots - 1) / (rows * kSlots);
-    int id = (int)blockIdx.x;
-    const int grp = id % groups;
-    id /= groups;
-    const int h = id % p.heads, b = id / p.heads;
-    const int sub = (int)threadIdx.x / per, chunk = (int)threadIdx.x - sub * per;
-    if (sub >= rows) return;
-    const int64_t row = ((int64_t)b * p.heads + h) * p.keep;
-    RawT k[kSlots], v[kSlots];
-    int idx[kSlots];
-#pragma unroll
-    for (int i = 0; i < kSlots; i++) {
-        const int j = grp * rows * kSlots + i * rows + sub;
-        idx[i] = j < p.keep ? p.index[row + j] : -1;
+    __shared__ __attribute__((aligned(16))) uint32_t hist[kBins * kCopies];    // later the tokens of this workgroup's slots
+    __shared__ uint32_t counts[N * kSelWaves];    // kept tokens before each wave's 64 of each round: above << 16 | equal
+    __shared__ __attribute__((aligned(16))) uint32_t wsum[kSelWaves];
+    __shared__ uint32_t out[2];
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int part = (int)(blockIdx.x % p.parts), row = (int)(blockIdx.x / p.parts);
+    const int h = row % p.heads, b = row / p.heads;
+    const int n = clamp_length(p.length, b, p.c.tokens), kept = min(n, p.keep);
+    const float *score = p.score + b * p.sc0 + h * p.sc1;
+    int32_t *index = p.index + (int64_t)row * p.keep;
+    const int j0 = part * p.share, j1 = min(j0 + p.share, p.keep);
+    if (h == 0 && part == 0 && tid == 0 && p.length_out) p.length_out[b] = kept;
+    fill_behind(p, index, kept, part, p.parts);
+    if (n <= p.keep) {
+        for (int j = j0 + tid; j < min(j1, n); j += kSelThreads) index[j] = j;
+        if constexpr (COPY) copy_rows<RawT, 4>(p, b, h, j0, j1, kSelThreads, [&](int j) { return j < n ? j : -1; });
+        return;
     }
+    uint32_t r[N];
 #pragma unroll
-    for (int i = 0; i < kSlots; i++) {
-        k[i] = RawT{}, v[i] = RawT{};
-        int64_t ko, vo;
-        if (idx[i] >= 0 && locate(p.c, b, (uint32_t)idx[i], p.c.ks0, p.c.ks1, ko)) {
-            locate(p.c, b, (uint32_t)idx[i], p.c.vs0, p.c.vs1, vo);
-            k[i] = *reinterpret_cast<const RawT *>(p.c.k + ko + h * p.c.ks2 + chunk * 8 * es);
-            v[i] = *reinterpret_cast<const RawT *>(p.c.v + vo + h * p.c.vs2 + chunk * 8 * es);
+    for (int k = 0; k < N; k++) {
+        const int i = k * kSelThreads + tid;
+        r[k] = rank_of(p, i < n ? score[i] : 0.f, i, n);
+    }
+    uint32_t need = (uint32_t)(p.keep - p.sink - p.recent), prefix = need ? 0 : kForced - 1;
+    for (int level = 0; level < 3 && need; level++) {
+        for (int i = tid; i < kBins * kCopies / 4; i += kSelThreads) reinterpret_cast<u32x4 *>(hist)[i] = u32x4{0, 0, 0, 0};
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < N; k++)
+            if (agrees(r[k], prefix, level)) add_to_hist(hist, r[k], level);
+        __syncthreads();
+        uint32_t c[2] = {0, 0};
+        const u32x4 *bin = reinterpret_cast<const u32x4 *>(hist) + (kBins - 2 - 2 * tid) * (kCopies / 4);
+#pragma unroll
+        for (int i = 0; i < 2 * kCopies / 4; i++) c[i < kCopies / 4] += bin[i].x + bin[i].y + bin[i].z + bin[i].w;
+        find_bin(c[0], c[1], need, wsum, out);
+        prefix |= out[0] << level_shift(level);
+        need = out[1];
+        __syncthreads();
+    }
+    // need: how many of the ranks equal to prefix are kept, the lowest tokens.
+    // A round's 64 tokens of a wave, rounds before waves, are in order.
+#pragma unroll
+    for (int k = 0; k < N; k++) {
+        const uint32_t above = (uint32_t)__popcll(__builtin_amdgcn_ballot_w64(r[k] > prefix)), equal = (uint32_t)__popcll(__builtin_amdgcn_ballot_w64(r[k] == prefix));
+        if (lane == 0) counts[k * kSelWaves + wave] = above << 16 | equal;
+    }
+    __syncthreads();
+    if (wave == 0) {                              // prefix sums; halves stay below 2^16: 32768 tokens
+        constexpr int each = (N * kSelWaves + 63) / 64;
+        uint32_t c[each], sum = 0;
+#pragma unroll
+        for (int i = 0; i < each; i++) {
+            c[i] = lane * each + i < N * kSelWaves ? counts[lane * each + i] : 0;
+            sum += c[i];
+        }
+        uint32_t before = sum;
+        for (int x = 1; x < 64; x <<= 1) {
+            const uint32_t v = __shfl_up(before, x);
+            if (lane >= x) before += v;
+        }
+        before -= sum;
+#pragma unroll
+        for (int i = 0; i < each; i++) {
+            if (lane * each + i < N * kSelWaves) counts[lane * each + i] = before;
+            before += c[i];
         }
     }
+    __syncthreads();
+    int *slots = reinterpret_cast<int *>(hist);
+    const uint64_t below = (1ull << lane) - 1;
 #pragma unroll
-    for (int i = 0; i < kSlots; i++) {
-        const int64_t j = grp * rows * kSlots + i * rows + sub;
-        if (j >= p.keep) continue;
-        *reinterpret_cast<RawT *>(p.o.k + b * p.o.ks0 + j * p.o.ks1 + h * p.o.ks2 + chunk * 8 * es) = k[i];
-        *reinterpret_cast<RawT *>(p.o.v + b * p.o.vs0 + j * p.o.vs1 + h * p.o.vs2 + chunk * 8 * es) = v[i];
-        if (chunk == 0 && p.score_out) p.score_out[row + j] = idx[i] >= 0 ? p.score[b * p.sc0 + h * p.sc1 + idx[i]] : 0.f;
+    for (int k = 0; k < N; k++) {
+        const uint32_t before = counts[k * kSelWaves + wave];
+        const bool over = r[k] > prefix, tie = r[k] == prefix;
+        const uint32_t a = (before >> 16) + (uint32_t)__popcll(__builtin_amdgcn_ballot_w64(over) & below);
+        const uint32_t e = (before & 0xffffu) + (uint32_t)__popcll(__builtin_amdgcn_ballot_w64(tie) & below);
+        const int at = (int)(a + min(e, need));
+        if (!over && !(tie && e < need)) continue;
+        if constexpr (COPY) {
+            if (at >= j0 && at < j1) slots[at - j0] = k * kSelThreads + tid;
+        } else {
+            index[at] = k * kSelThreads + tid;
+        }
     }
+    if constexpr (COPY) {
+        __syncthreads();
+        for (int j = j0 + tid; j < j1; j += kSelThreads) index[j] = slots[j - j0];  // n > keep: every slot has a token
+        copy_rows<RawT, 4>(p, b, h, j0, j1, kSelThreads, [&](int j) { return slots[j - j0]; });
+    }
+}
+
+// Longer rows, by slices: a launch a level, each of whose workgroups adds up
+// the slices' histograms of the level before, and one that writes the kept
+// tokens. Nothing needs clearing and no sum depends on an order.
+struct Slice {
+    int row, slice, b, h, n, i0;
+    const float *score;
+
+    __device__ inline Slice(const EvictParams &p)
+    {
+        slice = (int)(blockIdx.x % p.slices), row = (int)(blockIdx.x / p.slices);
+        h = row % p.heads, b = row / p.heads;
+        n = clamp_length(p.length, b, p.c.tokens);
+        i0 = slice * kSlice;
+        score = p.score + b * p.sc0 + h * p.sc1;
+    }
+
+    __device__ inline void load(const EvictParams &p, uint32_t (&r)[kSlice / kSelThreads]) const
+    {
+#pragma unroll
+        for (int k = 0; k < kSlice / kSelThreads; k++) {
+            const int i = i0 + k * kSelThreads + (int)threadIdx.x;
+            r[k] = rank_of(p, i < n ? score[i] : 0.f, i, n);
+        }
+    }
+
+    // a level's histograms, of this row; a thread's two bins of one are one word
+    __device__ inline const uint32_t *hist(const EvictParams &p, int level) const
+    {
+        return reinterpret_cast<const uint32_t *>(p.hist + ((int64_t)row * 3 + level) * p.slices * kBins) + (kBins / 2 - 1 - (int)threadIdx.x);
+    }
+};
+
+__device__ inline uint32_t slices_used(int n) { return (uint32_t)((n + kSlice - 1) / kSlice); }
+
+// adds up a level's histograms over the slices below `to`
+__device__ inline void sum_hist(const uint32_t *h, uint32_t from, uint32_t to, uint32_t &c0, uint32_t &c1)
+{
+    for (uint32_t s = from; s < to; s += 8) {     // eight loads at a time: they come from other XCDs' writes
+        uint32_t w[8];
+#pragma unroll
+        for (uint32_t i = 0; i < 8; i++) w[i] = s + i < to ? h[(s + i) * (kBins / 2)] : 0;
+#pragma unroll
+        for (uint32_t i = 0; i < 8; i++) c0 += w[i] >> 16, c1 += w[i] & 0xffffu;
+    }
+}
+
+template <int LEVEL>
+__global__ __launch_bounds__(kSelThreads) void k_evict_level(EvictParams p)
+{
+    __shared__ __attribute__((aligned(16))) uint32_t hist[kBins * kCopies];
+    __shared__ __attribute__((aligned(16))) uint32_t wsum[kSelWaves];
+    __shared__ uint32_t out[2], total;
+    const Slice s(p);
+    const int tid = (int)threadIdx.x;
+    const uint32_t first_need = (uint32_t)(p.keep - p.sink - p.recent);
+    if (s.n <= p.keep || s.i0 >= s.n || first_need == 0) return;       // nothing to choose
+    uint32_t r[kSlice / kSelThreads];
+    s.load(p, r);
+    for (int i = tid; i < kBins * kCopies / 4; i += kSelThreads) reinterpret_cast<u32x4 *>(hist)[i] = u32x4{0, 0, 0, 0};
+    if (tid == 0) total = 0;
+    uint32_t prefix = 0;
+    if constexpr (LEVEL > 0) {
+        uint2 before = make_uint2(0, first_need);
+        if constexpr (LEVEL == 2) before = p.found[s.row * 2];
+        uint32_t c0 = 0, c1 = 0;
+        sum_hist(s.hist(p, LEVEL - 1), 0, slices_used(s.n), c0, c1);
+        find_bin(c0, c1, before.y, wsum, out);
+        prefix = before.x | out[0] << level_shift(LEVEL - 1);
+        if (s.slice == 0 && tid == 0) p.found[s.row * 2 + LEVEL - 1] = make_uint2(prefix, out[1]);
+        // this slice's tokens that are kept for this level's bits
+        uint32_t mine = 0;
+#pragma unroll
+        for (int k = 0; k < kSlice / kSelThreads; k++) {
+            if (LEVEL == 1 && r[k] == kForced) mine++;
+            else if (agrees(r[k], prefix, LEVEL - 1) && (r[k] >> level_shift(LEVEL - 1)) > (prefix >> level_shift(LEVEL - 1))) mine++;
+        }
+        for (int x = 1; x < 64; x <<= 1) mine += __shfl_xor(mine, x);
+        if ((tid & 63) == 0 && mine) atomicAdd(&total, mine);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kSlice / kSelThreads; k++)
+        if (agrees(r[k], prefix, LEVEL)) add_to_hist(hist, r[k], LEVEL);
+    __syncthreads();
+    uint32_t c[2] = {0, 0};
+    const u32x4 *bin = reinterpret_cast<const u32x4 *>(hist) + (kBins - 2 - 2 * tid) * (kCopies / 4);
+#pragma unroll
+    for (int i = 0; i < 2 * kCopies / 4; i++) c[i < kCopies / 4] += bin[i].x + bin[i].y + bin[i].z + bin[i].w;
+    const_cast<uint32_t *>(s.hist(p, LEVEL))[s.slice * (kBins / 2)] = c[0] << 16 | c[1];      // at most 8192 each
+    if (LEVEL > 0 && tid == 0) p.count[((int64_t)s.row * 2 + LEVEL - 1) * p.slices + s.slice] = total;
+}
+
+__global__ __launch_bounds__(kSelThreads) void k_evict_index(EvictParams p)
+{
+    __shared__ __attribute__((aligned(16))) uint32_t wsum[kSelWaves];
+    __shared__ uint32_t counts[kSlice / kSelThreads * kSelWaves], out[2], sums[2];
+    const Slice s(p);
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int kept = min(s.n, p.keep);
+    int32_t *index = p.index + (int64_t)s.row * p.keep;
+    if (s.h == 0 && s.slice == 0 && tid == 0 && p.length_out) p.length_out[s.b] = kept;
+    fill_behind(p, index, kept, s.slice, p.slices);
+    if (s.i0 >= s.n) return;
+    if (s.n <= p.keep) {
+        for (int i = s.i0 + tid; i < min(s.i0 + kSlice, s.n); i += kSelThreads) index[i] = i;
+        return;
+    }
+    uint32_t r[kSlice / kSelThreads];
+    s.load(p, r);
+    uint32_t need = (uint32_t)(p.keep - p.sink - p.recent), prefix = kForced - 1;
+    uint32_t above0 = 0, equal0 = 0;              // kept in earlier slices: for sure, and by tokens of the last rank
+    if (need) {
+        const uint2 before = p.found[s.row * 2 + 1];
+        uint32_t p0 = 0, p1 = 0, c0, c1;
+        const uint32_t *h = s.hist(p, 2);
+        sum_hist(h, 0, (uint32_t)s.slice, p0, p1);
+        c0 = p0, c1 = p1;
+        sum_hist(h, (uint32_t)s.slice, slices_used(s.n), c0, c1);
+        if (tid < 2) sums[tid] = 0;
+        find_bin(c0, c1, before.y, wsum, out);
+        prefix = before.x | out[0];
+        need = out[1];
+        const uint32_t bin = (uint32_t)(kBins - 1 - 2 * tid);
+        uint32_t more = (bin > out[0] ? p0 : 0) + (bin - 1 > out[0] ? p1 : 0);
+        for (int i = tid; i < s.slice; i += kSelThreads)
+            more += p.count[(int64_t)s.row * 2 * p.slices + i] + p.count[((int64_t)s.row * 2 + 1) * p.slices + i];
+        for (int x = 1; x < 64; x <<= 1) more += __shfl_xor(more, x);
+        if (lane == 0 && more) atomicAdd(&sums[0], more);
+        if (bin == out[0]) sums[1] = p0;
+        if (bin - 1 == out[0]) sums[1] = p1;
+        __syncthreads();
+        above0 = sums[0], equal0 = sums[1];
+    } else {
+        above0 = (uint32_t)(min(s.i0, p.sink) + max(0, s.i0 - (s.n - p.recent)));      // the first and last tokens alone
+    }
+#pragma unroll
+    for (int k = 0; k < kSlice / kSelThreads; k++) {
+        const uint32_t above = (uint32_t)__popcll(__builtin_amdgcn_ballot_w64(r[k] > prefix)), equal = (uint32_t)__popcll(__builtin_amdgcn_ballot_w64(r[k] == prefix));
+        if (lane == 0) counts[k * kSelWaves + wave] = above << 16 | equal;
+    }
+    __syncthreads();
+    if (wave == 0) {
+        constexpr int each = kSlice / kSelThreads * kSelWaves / 64;
+        uint32_t c[each], sum = 0;
+#pragma unroll
+        for (int i = 0; i < each; i++) sum += c[i] = counts[lane * each + i];
+        uint32_t before = sum;
+        for (int x = 1; x < 64; x <<= 1) {
+            const uint32_t v = __shfl_up(before, x);
+            if (lane >= x) before += v;
+        }
+        before -= sum;
+#pragma unroll
+        for (int i = 0; i < each; i++) {
+            counts[lane * each + i] = before;
+            before += c[i];
+        }
+    }
+    __syncthreads();
+    const uint64_t below = (1ull << lane) - 1;
+#pragma unroll
+    for (int k = 0; k < kSlice / kSelThreads; k++) {
+        const uint32_t before = counts[k * kSelWaves + wave];
+        const bool over = r[k] > prefix, tie = r[k] == prefix;
+        const uint32_t a = above0 + (before >> 16) + (uint32_t)__popcll(__builtin_amdgcn_ballot_w64(over) & below);
+        const uint32_t e = equal0 + (before & 0xffffu) + (uint32_t)__popcll(__builtin_amdgcn_ballot_w64(tie) & below);
+        if (over || (tie && e < need)) index[a + min(e, need)] = s.i0 + k * kSelThreads + tid;
+    }
+}
+
+template <typename RawT>
+__global__ __launch_bounds__(256) void k_evict_copy(EvictParams p)
+{
+    const int each = 256 / (p.D / 8) * 4, groups = (p.keep + each - 1) / each;
+    const int grp = (int)(blockIdx.x % groups), row = (int)(blockIdx.x / groups);
+    const int32_t *index = p.index + (int64_t)row * p.keep;
+    copy_rows<RawT, 4>(p, row / p.heads, row % p.heads, grp * each, min(grp * each + each, p.keep), 256, [&](int j) { return index[j]; });
+}
+
+template <typename RawT>
+int launch_copy(const EvictParams &p, uint64_t rows, hipStream_t s)
+{
+    const int each = 256 / (p.D / 8) * 4;
+    const uint64_t grid = rows * ((p.keep + each - 1) / each);
+    k_evict_copy<RawT><<<(unsigned)grid, 256, 0, s>>>(p);
+    UZIP_KV_LAUNCH_CHECK("k_evict_copy");
+    return UZIP_OK;
+}
+
+template <typename RawT>
+int launch_evict(EvictParams &p, uint64_t rows, hipStream_t s)
+{
+    p.parts = 1, p.share = p.keep;
+    if (p.c.tokens <= 4 * kSelThreads && p.keep <= 4 * kSelThreads) {
+        // workgroups a row: two a CU, as long as each has some slots to copy
+        const uint64_t most = ((uint64_t)p.keep + 63) / 64, parts = 2 * kCUs / rows;
+        p.parts = (int)(parts < 1 ? 1 : parts > most ? most : parts);
+        p.share = (p.keep + p.parts - 1) / p.parts;
+        k_evict_one<4, true, RawT><<<(unsigned)(rows * p.parts), kSelThreads, 0, s>>>(p);
+        UZIP_KV_LAUNCH_CHECK("k_evict_one");
+        return UZIP_OK;
+    }
+    if (p.slices == 0) {
+        if (p.c.tokens <= 16 * kSelThreads) k_evict_one<16, false, RawT><<<(unsigned)rows, kSelThreads, 0, s>>>(p);
+        else k_evict_one<32, false, RawT><<<(unsigned)rows, kSelThreads, 0, s>>>(p);
+        UZIP_KV_LAUNCH_CHECK("k_evict_one");
+        return launch_copy<RawT>(p, rows, s);
+    }
+    const unsigned grid = (unsigned)(rows * p.slices);
+    k_evict_level<0><<<grid, kSelThreads, 0, s>>>(p);
+    UZIP_KV_LAUNCH_CHECK("k_evict_level");
+    k_evict_level<1><<<grid, kSelThreads, 0, s>>>(p);
+    UZIP_KV_LAUNCH_CHECK("k_evict_level");
+    k_evict_level<2><<<grid, kSelThreads, 0, s>>>(p);
+    UZIP_KV_LAUNCH_CHECK("k_evict_level");
+    k_evict_index<<<grid, kSelThreads, 0, s>>>(p);
+    UZIP_KV_LAUNCH_CHECK("k_evict_index");
+    return launch_copy<RawT>(p, rows, s);
+}
+
+struct EvictWs {
+    uint64_t slices, off_count, off_found, bytes;
+};
+
+EvictWs evict_ws(uint64_t rows, uint32_t tokens)
+{
+    EvictWs w{};
+    if (tokens <= (uint32_t)kOneTokens) return w;
+    w.slices = (tokens + kSlice - 1) / kSlice;
+    const auto up = [](uint64_t v) { return (v + 255) & ~255ull; };
+    w.off_count = up(rows * 3 * w.slices * kBins * 2);
+    w.off_found = w.off_count + up(rows * 2 * w.slices * 4);
+    w.bytes = w.off_found + up(rows * 2 * 8);
+    return w;
 }
 
 }  // namespace
@@ -504,7 +813,7 @@ int uzip_kv_append(const uzip_kv_cache_t *cache, const uzip_kv_append_args_t *a,
 uint64_t uzip_kv_evict_workspace_bytes(uint32_t seqs, uint32_t kv_heads, uint32_t cache_tokens)
 {
     if (!uzip_kv::valid_dims(seqs, kv_heads, 8) || cache_tokens < 1 || cache_tokens > (1u << 30)) return 0;
-    return 256;
+    return uzip_kv::evict_ws((uint64_t)seqs * kv_heads, cache_tokens).bytes;
 }
 
 int uzip_kv_evict(const uzip_kv_cache_t *cache, const uzip_kv_cache_t *out, const uzip_kv_evict_args_t *a,
@@ -517,9 +826,12 @@ int uzip_kv_evict(const uzip_kv_cache_t *cache, const uzip_kv_cache_t *out, cons
     if (a->keep < 1 || out->tokens != a->keep || a->sink > a->keep || a->recent > a->keep - a->sink) return UZIP_EINVAL;
     if (!a->score || !aligned(a->score, 4) || a->score_stride[0] < 0 || a->score_stride[1] < 0) return UZIP_EINVAL;
     if (!a->length || !aligned(a->length, 4) || !a->index || !aligned(a->index, 4)) return UZIP_EINVAL;
-    if (!aligned(a->score_out, 4) || !aligned(a->length_out, 4) || !d_ws || !aligned(d_ws, 16)) return UZIP_EINVAL;
+    if (!aligned(a->score_out, 4) || !aligned(a->length_out, 4) || !aligned(d_ws, 16)) return UZIP_EINVAL;
     if (cache->k == out->k || cache->v == out->v) return UZIP_EINVAL;
-    if (ws_bytes < uzip_kv_evict_workspace_bytes(cache->seqs, cache->heads, cache->tokens)) return UZIP_ENOSPC;
+    const uint64_t rows = (uint64_t)cache->seqs * cache->heads;
+    const EvictWs ws = evict_ws(rows, a->score_tokens);
+    if (ws.bytes && !d_ws) return UZIP_EINVAL;
+    if (ws_bytes < ws.bytes) return UZIP_ENOSPC;
     EvictParams p;
     memset(&p, 0, sizeof p);
     p.c = view_of(cache);
@@ -533,16 +845,13 @@ int uzip_kv_evict(const uzip_kv_cache_t *cache, const uzip_kv_cache_t *out, cons
     p.score_out = a->score_out;
     p.heads = (int)cache->heads, p.D = (int)cache->dim;
     p.keep = (int)a->keep, p.sink = (int)a->sink, p.recent = (int)a->recent;
-    const uint64_t rows = (uint64_t)cache->seqs * cache->heads;
-    const int each = 256 / (p.D / 8) * 4;
-    const uint64_t grid = rows * ((a->keep + each - 1) / each);
-    if (rows >= (1ull << 31) || grid >= (1ull << 31)) return UZIP_EINVAL;
-    k_evict_select<<<(unsigned)rows, kSelThreads, 0, s>>>(p);
-    UZIP_KV_LAUNCH_CHECK("k_evict_select");
-    if (cache->dtype == UZIP_KV_E5M2) k_evict_gather<u32x2><<<(unsigned)grid, 256, 0, s>>>(p);
-    else k_evict_gather<u32x4><<<(unsigned)grid, 256, 0, s>>>(p);
-    UZIP_KV_LAUNCH_CHECK("k_evict_gather");
-    return UZIP_OK;
+    p.hist = static_cast<uint16_t *>(d_ws);
+    p.count = reinterpret_cast<uint32_t *>(static_cast<char *>(d_ws) + ws.off_count);
+    p.found = reinterpret_cast<uint2 *>(static_cast<char *>(d_ws) + ws.off_found);
+    p.slices = (int)ws.slices;
+    const uint64_t each = 256 / (p.D / 8) * 4, groups = (a->keep + each - 1) / each;
+    if (rows * groups >= (1ull << 31) || rows * ws.slices >= (1ull << 31)) return UZIP_EINVAL;
+    return cache->dtype == UZIP_KV_E5M2 ? launch_evict<u32x2>(p, rows, s) : launch_evict<u32x4>(p, rows, s);
 }
 
 }  // extern "C"

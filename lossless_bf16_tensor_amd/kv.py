@@ -364,7 +364,7 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, length
 
 @functools.lru_cache(maxsize=4096)
 def evict_workspace_bytes(seqs: int, kv_heads: int, cache_tokens: int) -> int:
-    """Workspace that :func:`evict` needs; 0 when the shapes are invalid."""
+    """Workspace that :func:`evict` needs for scores of cache_tokens; 0 when it needs none or the shapes are invalid."""
     return int(lib().uzip_kv_evict_workspace_bytes(seqs, kv_heads, cache_tokens))
 
 
@@ -399,11 +399,12 @@ def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, score: torch.Tensor, len
         kept, index = torch.empty((B, heads, keep), device=dev), torch.empty((B, heads, keep), dtype=torch.int32, device=dev)
         left = torch.empty(B, dtype=torch.int32, device=dev)
         if ws is None:
-            ws = torch.empty(evict_workspace_bytes(B, heads, tokens), dtype=torch.uint8, device=dev)
-        else:
-            if not (ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev):
-                raise ValueError("ws: expected contiguous uint8")
+            need = evict_workspace_bytes(B, heads, seen)
+            ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        elif not (ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev):
+            raise ValueError("ws: expected contiguous uint8")
         args = _EVICT.pack(score.data_ptr(), *ss, _counts(length, B, dev, "length"),
                            index.data_ptr(), kept.data_ptr(), left.data_ptr(), keep, sink, recent, seen)
-        _check(lib().uzip_kv_evict(cache, _cache(*made, None, B)[0], args, ws.data_ptr(), ws.numel(), _stream(dev)), "evict")
+        _check(lib().uzip_kv_evict(cache, _cache(*made, None, B)[0], args, 0 if ws is None else ws.data_ptr(),
+                                   0 if ws is None else ws.numel(), _stream(dev)), "evict")
     return made[0], made[1], kept, left, index

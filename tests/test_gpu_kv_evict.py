@@ -84,6 +84,14 @@ def test_copies(cache, layout, D):
     run(5, 3, 200, D, [200, 0, 1, 33, 90], 33, 1, 9, "plain", cache, layout, seed=D)
 
 
+@pytest.mark.parametrize("S,keep,sink,recent", [(4096, 1000, 0, 0), (4097, 4000, 7, 100), (16385, 16384, 1, 0), (32768, 20000, 0, 9),
+                                                (32769, 17, 17, 0), (40000, 30, 10, 20), (40960, 40959, 0, 0), (50000, 25000, 9000, 10000)])
+@pytest.mark.parametrize("kind", ["plain", "ties", "equal", "odd"])
+def test_lengths_at_the_edges_of_what_a_workgroup_holds(S, keep, sink, recent, kind):
+    run(1, 2, S, 8, [S], keep, sink, recent, kind, seed=S)
+    run(2, 1, S, 8, [S - 3, keep + 1], keep, sink, recent, kind, seed=S + 1)
+
+
 def test_long_rows():
     run(1, 2, 70001, 8, [70001], 20011, 3, 1000, "ties", seed=1)
     run(2, 1, 131072, 8, [131072, 100000], 13000, 0, 0, "plain", seed=2)

@@ -140,13 +140,14 @@ def evict(c=None, out=None, score=1 << 24, ss=(256, 64), length=1 << 24, index=1
     dict(out=cache(k=1 << 26, v=1 << 27, tokens=16, seqs=2)), dict(out=cache(tokens=16)),
     dict(out=cache(k=1 << 26, v=1 << 27, tokens=16, table=1 << 24, page=16, pages=4)), dict(score=0), dict(score=2), dict(ss=(-1, 0)),
     dict(length=0), dict(index=0), dict(index=2), dict(score_out=2), dict(length_out=1), dict(keep=0), dict(sink=17), dict(sink=10, recent=7),
-    dict(seen=0), dict(seen=65), dict(ws=0), dict(ws=4)])
+    dict(seen=0), dict(seen=65), dict(ws=4), dict(c=cache(tokens=40000), seen=40000, ws=0)])
 def test_evict_refuses(bad):
     assert evict(**bad) == EINVAL
 
 
 def test_evict_refuses_a_small_workspace():
-    assert evict(ws_bytes=kv.evict_workspace_bytes(1, 4, 64) - 1) == ENOSPC
+    assert kv.evict_workspace_bytes(1, 4, 32768) == 0
+    assert evict(cache(tokens=40000), seen=40000, ws_bytes=kv.evict_workspace_bytes(1, 4, 40000) - 1) == ENOSPC
 
 
 def test_structures_have_the_headers_sizes():
