@@ -38,23 +38,164 @@ struct AttendParams {
     const uint8_t *tree;
     int64_t qs0, qs1, qs2, os0, os1, os2;     // bytes
     int64_t sc0, sc1, tr0, tr1;               // elements
-    int score_tokens;
+    int score_tokens, weigh_tiles;            // weigh_tiles: of each wave of k_attend_weigh
     float *part_o;                            // [row][split][DP], when nsplit > 1
     float2 *part_ml;                          // [row][split]: maximum (times c), sum
-    int T, G, R, D, heads;                    // heads: key/value heads
-    int nsplit, nrg, min_tiles, unit;         // unit: tiles that a workgroup takes in one step
+    int T, G, R, D, heads, seqs;              // heads: key/value heads
+    int *used;                                // parts of each sequence, when flat
+    int flat;                                 // Walk
+    int nsplit, nrg, slots, min_steps, unit;  // unit: tiles that a workgroup takes in one step
     int wk;                                   // waves of a workgroup that share rows and split keys
     float c2;                                 // scale * log2(e)
     int q_f16;
 };
 
-// tiles per split: the same for the kernel that fills and the one that joins
-__device__ inline int tiles_per_split(int ntiles, const AttendParams &p)
+__device__ inline int end_of(const AttendParams &p, int n, int nd)
 {
-    int t = (ntiles + p.nsplit - 1) / p.nsplit;
-    t = t < p.min_tiles ? p.min_tiles : t;
+    return nd == 0 ? 0 : (uint32_t)nd > p.c.tokens - (uint32_t)n ? (int)p.c.tokens : n + nd;
+}
+
+// What a workgroup works on: tiles [t0, t1) of sequence b for its rows.
+struct Place {
+    int b, h, rg, split, n, nd, end, t0, t1;
+    bool whole;                                   // all the tiles of b: the output is final
+};
+
+// Each sequence cut into p.nsplit parts or fewer, one workgroup each.
+__device__ inline int tiles_per_split(const AttendParams &p, int tiles)
+{
+    const int t = max((tiles + p.nsplit - 1) / p.nsplit, p.min_steps * p.unit);
     return (t + p.unit - 1) / p.unit * p.unit;
 }
+
+__device__ inline int tiles_of(const AttendParams &p, int b)
+{
+    return (end_of(p, clamp_length(p.length, b, p.c.tokens), clamp_drafted(p.drafted, b, p.T)) + kTileKeys - 1) / kTileKeys;
+}
+
+__device__ inline Place part_of_sequence(const AttendParams &p)
+{
+    Place at;
+    int id = (int)blockIdx.x;
+    at.h = id % p.heads;
+    id /= p.heads;
+    at.rg = id % p.nrg;
+    id /= p.nrg;
+    at.split = id % p.nsplit, at.b = id / p.nsplit;
+    at.n = __builtin_amdgcn_readfirstlane(clamp_length(p.length, at.b, p.c.tokens));
+    at.nd = __builtin_amdgcn_readfirstlane(clamp_drafted(p.drafted, at.b, p.T));
+    at.end = end_of(p, at.n, at.nd);
+    const int tiles = (at.end + kTileKeys - 1) / kTileKeys, each = tiles_per_split(p, tiles);
+    at.t0 = at.split * each, at.t1 = min(at.t0 + each, tiles);
+    at.whole = tiles <= each;
+    return at;
+}
+
+// The places of a workgroup of which there is one a CU, so that none may have
+// more to do than another: the steps (`unit` tiles) of all sequences lie in a
+// row, for each key/value head and group of rows, and each of p.slots
+// workgroups takes the next `chunk` of them, however the lengths differ. A
+// sequence that lies in several chunks is joined afterwards; p.used says of how
+// many parts. (nsplit == 1: a workgroup a sequence.)
+struct Walk {
+    int b, start, s0, s1, chunk, slot, h, rg;     // start: of b's steps
+    int len, cnt;                                 // lane i: of sequence i, when there are at most 64
+
+    __device__ inline static int steps(const AttendParams &p, int n, int nd)
+    {
+        return ((end_of(p, n, nd) + kTileKeys - 1) / kTileKeys + p.unit - 1) / p.unit;
+    }
+    __device__ inline static int steps(const AttendParams &p, int b)
+    {
+        return steps(p, clamp_length(p.length, b, p.c.tokens), clamp_drafted(p.drafted, b, p.T));
+    }
+
+    __device__ inline Walk(const AttendParams &p)
+    {
+        int id = (int)blockIdx.x;
+        h = id % p.heads;
+        id /= p.heads;
+        rg = id % p.nrg;
+        slot = id / p.nrg;
+        b = slot, start = s0 = 0, s1 = 1, chunk = 1, len = cnt = 0;
+        if (p.nsplit == 1) return;
+        const int lane = (int)(threadIdx.x & 63);
+        int total = 0, most = 0;
+        if (p.seqs <= 64) {
+            if (lane < p.seqs) len = clamp_length(p.length, lane, p.c.tokens), cnt = clamp_drafted(p.drafted, lane, p.T);
+            total = most = lane < p.seqs ? steps(p, len, cnt) : 0;
+        } else {
+            for (int i = lane; i < p.seqs; i += 64) {
+                const int st = steps(p, i);
+                total += st;
+                most = max(most, st);
+            }
+        }
+        if (p.seqs > 1)
+            for (int x = 1; x < 64; x <<= 1) total += __shfl_xor(total, x), most = max(most, __shfl_xor(most, x));
+        total = __builtin_amdgcn_readfirstlane(total);
+        most = __builtin_amdgcn_readfirstlane(most);
+        // a sequence is in one part more than its length asks for when it begins inside a chunk
+        const int parts = p.seqs > 1 ? p.nsplit - 1 : p.nsplit;
+        chunk = max(max(p.min_steps, (total + p.slots - 1) / p.slots), (most + parts - 1) / parts);
+        s0 = slot * chunk, s1 = s0 < total ? min(s0 + chunk, total) : 0;      // 0: nothing for this one, start is not below it
+        b = 0;
+        const bool tell = blockIdx.x == 0 && threadIdx.x < 64;
+        if (p.seqs == 1) {
+            if (tell && lane == 0) p.used[0] = (total + chunk - 1) / chunk;
+            return;
+        }
+        bool found = false;
+        for (int base = 0, before = 0; base < p.seqs && (!found || tell); base += 64) {
+            const int st = base + lane >= p.seqs ? 0 : p.seqs <= 64 ? steps(p, len, cnt) : steps(p, base + lane);
+            int sum = st;
+            for (int x = 1; x < 64; x <<= 1) {
+                const int v = __shfl_up(sum, x);
+                if (lane >= x) sum += v;
+            }
+            if (tell && base + lane < p.seqs)
+                p.used[base + lane] = st ? (before + sum - 1) / chunk - (before + sum - st) / chunk + 1 : 0;
+            const uint64_t past = __builtin_amdgcn_ballot_w64(before + sum > s0);
+            if (!found && past) {
+                const int at = __builtin_ctzll(past);
+                b = base + at;
+                start = before + __builtin_amdgcn_readlane(sum, at) - __builtin_amdgcn_readlane(st, at);
+                found = true;
+            }
+            before += __builtin_amdgcn_readlane(sum, 63);
+        }
+        if (!found) s1 = 0;
+    }
+
+    __device__ inline bool next(const AttendParams &p, Place &at)
+    {
+        at.h = h, at.rg = rg;
+        while (start < s1 && b < p.seqs) {
+            at.b = b++;
+            if (p.nsplit > 1 && p.seqs <= 64) {
+                at.n = __builtin_amdgcn_readlane(len, at.b);
+                at.nd = __builtin_amdgcn_readlane(cnt, at.b);
+            } else {
+                at.n = __builtin_amdgcn_readfirstlane(clamp_length(p.length, at.b, p.c.tokens));
+                at.nd = __builtin_amdgcn_readfirstlane(clamp_drafted(p.drafted, at.b, p.T));
+            }
+            at.end = end_of(p, at.n, at.nd);
+            const int tiles = (at.end + kTileKeys - 1) / kTileKeys, st = (tiles + p.unit - 1) / p.unit, from = start;
+            if (p.nsplit == 1) {
+                at.split = 0, at.t0 = 0, at.t1 = tiles, at.whole = true;
+                start = s1;
+                return true;
+            }
+            start += st;
+            if (st == 0) continue;
+            at.t0 = max(s0 - from, 0) * p.unit, at.t1 = min(min(s1 - from, st) * p.unit, tiles);
+            at.split = slot - from / chunk;
+            at.whole = (from + st - 1) / chunk == from / chunk;
+            return true;
+        }
+        return false;
+    }
+};
 
 template <int CT>
 using Raw = typename std::conditional<CT == kE5M2, u32x2, u32x4>::type;       // 8 elements
@@ -249,7 +390,9 @@ struct Rows {
 
     __device__ inline void init(const AttendParams &p, int b, int h, int first_row, int n, int end)
     {
-        x = (int)(threadIdx.x & 15), g = (int)(threadIdx.x & 63) >> 4;
+        int tid = (int)threadIdx.x;
+        asm volatile("" : "+v"(tid));             // what follows from it is made anew for each place, not kept in registers
+        x = tid & 15, g = (tid & 63) >> 4;
         row0 = first_row;
         odd = false;
 #pragma unroll
@@ -266,59 +409,62 @@ struct Rows {
         if (!p.tree) lim = min(end, n + min((min(row0 + RB * 16, p.R) - 1) / p.G, p.T - 1) + 1);
     }
 
-    __device__ inline void score(const u32x4 (&k)[2][KS], f32x4 *s0, int stride)
+    __device__ inline void score(const u32x4 (&k)[2][KS], f32x4 (&s)[RB][2])
     {
 #pragma unroll
         for (int hf = 0; hf < 2; hf++)
 #pragma unroll
             for (int ks = 0; ks < KS; ks++)
 #pragma unroll
-                for (int rb = 0; rb < RB; rb++) {
-                    f32x4 &s = s0[rb * stride + hf];
-                    s = mfma<CT>(k[hf][ks], q[rb][ks], ks ? s : f32x4{0.f, 0.f, 0.f, 0.f});
-                }
+                for (int rb = 0; rb < RB; rb++) s[rb][hf] = mfma<CT>(k[hf][ks], q[rb][ks], ks ? s[rb][hf] : f32x4{0.f, 0.f, 0.f, 0.f});
     }
 
-    // Scores of N half tiles to weights. m need not be the maximum so far, only
-    // near it: the weights stay below 2^kSlack and nothing is lost in binary32,
+    // Brings m near the maximum of a tile's scores. It need not be the maximum
+    // so far: the weights stay below 2^kSlack and nothing is lost in binary32,
     // while the output is scaled anew in the first tile and then hardly ever.
-    template <int N>
-    __device__ inline void weigh(f32x4 (&s)[RB][N], u32x4 (&pw)[RB][N / 2])
+    // A row with a NaN is NaN by its sum, whatever m.
+    __device__ inline void raise(const f32x4 (&s)[RB][2])
     {
+        float top[RB];
+        bool any = false;
 #pragma unroll
         for (int rb = 0; rb < RB; rb++) {
-            // A row with a NaN is NaN by its sum, whatever the maximum.
-            float part[N];
+            top[rb] = quad_max(larger(larger(larger(s[rb][0][0], s[rb][0][1]), larger(s[rb][0][2], s[rb][0][3])),
+                                      larger(larger(s[rb][1][0], s[rb][1][1]), larger(s[rb][1][2], s[rb][1][3]))));
+            any = any || (top[rb] - m[rb]) * c2[rb] > kSlack;
+        }
+        if (__builtin_expect(__builtin_amdgcn_ballot_w64(any) != 0, 0)) {
 #pragma unroll
-            for (int hf = 0; hf < N; hf++) part[hf] = larger(larger(s[rb][hf][0], s[rb][hf][1]), larger(s[rb][hf][2], s[rb][hf][3]));
-            float top = part[0];
-#pragma unroll
-            for (int hf = 1; hf < N; hf++) top = larger(top, part[hf]);
-            top = quad_max(top);
-            if (__builtin_amdgcn_ballot_w64((top - m[rb]) * c2[rb] > kSlack)) {
-                top = fmaxf(top, m[rb]);
-                const float a = __builtin_amdgcn_exp2f((m[rb] - (top == -INFINITY ? 0.f : top)) * c2[rb]);
-                m[rb] = top;
-                base[rb] = top == -INFINITY ? 0.f : top * c2[rb];
+            for (int rb = 0; rb < RB; rb++) {
+                const float up = fmaxf(top[rb], m[rb]);
+                const float a = __builtin_amdgcn_exp2f((m[rb] - (up == -INFINITY ? 0.f : up)) * c2[rb]);
+                m[rb] = up;
+                base[rb] = up == -INFINITY ? 0.f : up * c2[rb];
                 l[rb] *= a;
 #pragma unroll
                 for (int e = 0; e < NV; e++) acc[rb][e] *= a;
             }
+        }
+    }
+
+    // Scores to weights.
+    __device__ inline void weigh(const f32x4 (&s)[RB][2], u32x4 (&pw)[RB])
+    {
+#pragma unroll
+        for (int rb = 0; rb < RB; rb++) {
+            f32x4 w[2];
             float sum[2] = {0.f, 0.f};
 #pragma unroll
-            for (int hf = 0; hf < N; hf++)
+            for (int hf = 0; hf < 2; hf++)
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
-                    s[rb][hf][k] = __builtin_amdgcn_exp2f(fmaf(s[rb][hf][k], c2[rb], -base[rb]));
-                    sum[k & 1] += s[rb][hf][k];
+                    w[hf][k] = __builtin_amdgcn_exp2f(fmaf(s[rb][hf][k], c2[rb], -base[rb]));
+                    sum[hf] += w[hf][k];
                 }
             l[rb] += sum[0] + sum[1];
             // The one rounding of the weights, half a step of the products'
             // type. Their sum is taken before it: lse keeps binary32.
-#pragma unroll
-            for (int t = 0; t < N / 2; t++)
-                pw[rb][t] = u32x4{pack2<f16>(s[rb][2 * t][0], s[rb][2 * t][1]), pack2<f16>(s[rb][2 * t][2], s[rb][2 * t][3]),
-                                  pack2<f16>(s[rb][2 * t + 1][0], s[rb][2 * t + 1][1]), pack2<f16>(s[rb][2 * t + 1][2], s[rb][2 * t + 1][3])};
+            pw[rb] = u32x4{pack2<f16>(w[0][0], w[0][1]), pack2<f16>(w[0][2], w[0][3]), pack2<f16>(w[1][0], w[1][1]), pack2<f16>(w[1][2], w[1][3])};
         }
     }
 
@@ -338,8 +484,7 @@ struct Rows {
         return a;
     }
 
-    template <int N>
-    __device__ inline void add(const Values (&v)[VC][8], const u32x4 (&pw)[RB][N], int t)
+    __device__ inline void add(const Values (&v)[VC][8], const u32x4 (&pw)[RB])
     {
 #pragma unroll
         for (int c = 0; c < VC; c++)
@@ -347,7 +492,7 @@ struct Rows {
             for (int e = 0; e < VE; e++) {
                 const u32x4 a = fragment(v, c, e);
 #pragma unroll
-                for (int rb = 0; rb < RB; rb++) acc[rb][c * VE + e] = mfma<CT>(a, pw[rb][t], acc[rb][c * VE + e]);
+                for (int rb = 0; rb < RB; rb++) acc[rb][c * VE + e] = mfma<CT>(a, pw[rb], acc[rb][c * VE + e]);
             }
     }
 
@@ -366,36 +511,34 @@ struct Rows {
             }
     }
 
-    // A tile that not every row sees whole: the drafted tokens' own, the last
-    // one, one with an absent page.
-    __device__ inline void masked_tile(const AttendParams &p, const Tile &t, int b, int n, int nd)
+    // One tile. values() is called for the values when the scores are done.
+    // Not `fast`: one that not every row sees whole (the drafted tokens' own,
+    // the last one, one with an absent page).
+    template <typename F>
+    __device__ inline void tile(const AttendParams &p, const Tile &t, const Place &at, const u32x4 (&k)[2][KS], Values (&v)[VC][8], F values)
     {
-        Raw<CT> kr[2][KS];
-        u32x4 k[2][KS];
-        Values v[VC][8];
-        load_keys<CT, KS, PAD, true>(p, t, lim, x, g, (uint32_t)(x * p.c.ks1) + g * 8 * es, kr);
-#pragma unroll
-        for (int hf = 0; hf < 2; hf++)
-#pragma unroll
-            for (int ks = 0; ks < KS; ks++) k[hf][ks] = widen<CT>(kr[hf][ks]);
+        const int n = at.n, nd = at.nd;
         f32x4 s[RB][2];
-        u32x4 pw[RB][1];
-        score(k, &s[0][0], 2);
-        load_values<true>(p, t, v);
-        uint32_t seen[RB];
+        u32x4 pw[RB];
+        score(k, s);
+        values(v);
+        if (!t.fast) {
+            uint32_t seen[RB];
 #pragma unroll
-        for (int rb = 0; rb < RB; rb++) seen[rb] = 0;
-        if (p.tree) {
+            for (int rb = 0; rb < RB; rb++) seen[rb] = 0;
+            if (p.tree && t.key + kTileKeys > n) {
 #pragma unroll
-            for (int rb = 0; rb < RB; rb++) seen[rb] = tree_bits(p, b, tok[rb], t.key + 4 * g - n, nd);
+                for (int rb = 0; rb < RB; rb++) seen[rb] = tree_bits(p, at.b, tok[rb], t.key + 4 * g - n, nd);
+            }
+#pragma unroll
+            for (int rb = 0; rb < RB; rb++) {
+                seen[rb] |= leading_bits((p.tree ? n : min(lim, n + tok[rb] + 1)) - t.key - 4 * g);
+                seen[rb] &= there_bits(t);
+#pragma unroll
+                for (int i = 0; i < 8; i++) s[rb][i >> 2][i & 3] = seen[rb] >> i & 1 ? s[rb][i >> 2][i & 3] : -INFINITY;
+            }
         }
-#pragma unroll
-        for (int rb = 0; rb < RB; rb++) {
-            seen[rb] |= leading_bits((p.tree ? n : min(lim, n + tok[rb] + 1)) - t.key - 4 * g);
-            seen[rb] &= there_bits(t);
-#pragma unroll
-            for (int i = 0; i < 8; i++) s[rb][i >> 2][i & 3] = seen[rb] >> i & 1 ? s[rb][i >> 2][i & 3] : -INFINITY;
-        }
+        raise(s);
         weigh(s, pw);
         if (t.key + kTileKeys > n) {
             // A value that is not finite must reach only the rows that see its
@@ -413,7 +556,25 @@ struct Rows {
                     }
             odd = odd || __builtin_amdgcn_ballot_w64(any != 0) != 0;
         }
-        add(v, pw, 0);
+        add(v, pw);
+    }
+
+    // ... from the cache itself
+    __device__ inline void masked_tile(const AttendParams &p, const Tile &t, const Place &at)
+    {
+        Raw<CT> kr[2][KS];
+        u32x4 k[2][KS];
+        Values v[VC][8];
+        load_keys<CT, KS, PAD, true>(p, t, lim, x, g, (uint32_t)(x * p.c.ks1) + g * 8 * es, kr);
+        constexpr bool together = RB * NV <= 16;          // registers for keys and values at once: one wait, not two
+        if (together) load_values<true>(p, t, v);
+#pragma unroll
+        for (int hf = 0; hf < 2; hf++)
+#pragma unroll
+            for (int ks = 0; ks < KS; ks++) k[hf][ks] = widen<CT>(kr[hf][ks]);
+        tile(p, t, at, k, v, [&](Values (&u)[VC][8]) {
+            if (!together) load_values<true>(p, t, u);
+        });
     }
 
     // After the last tile: whole sums, and maxima that waves can compare.
@@ -475,11 +636,13 @@ struct Rows {
     }
 
     // What masked_tile left out: adds values that are not finite, among the
-    // keys of the drafted tokens' tiles [lo, hi), to the stored output of the
+    // keys [lo, hi) of the drafted tokens' tiles, to the stored output of the
     // rows that see them. Rare, and so written for few registers: a lane goes
     // over its own outputs, after store().
-    __device__ inline void poison(const AttendParams &p, int b, int h, int split, int n, int nd, int lo, int hi)
+    __device__ inline void poison(const AttendParams &p, const Place &at)
     {
+        const int b = at.b, h = at.h, n = at.n, nd = at.nd;
+        const int lo = max(at.t0 * kTileKeys, n & ~(kTileKeys - 1)), hi = min(at.t1 * kTileKeys, at.end);
         for (int rb = 0; rb < RB; rb++) {
             const int r = row0 + rb * 16 + x, token = r / p.G, head = h * p.G + r % p.G;
             if (r >= p.R || token >= nd) continue;
@@ -491,17 +654,17 @@ struct Rows {
                     if (key >= n && !(p.tree ? p.tree[b * p.tr0 + token * p.tr1 + (key - n)] != 0 : key - n <= token)) continue;
                     int64_t off;
                     if (!locate(p.c, b, (uint32_t)key, p.c.vs0, p.c.vs1, off)) continue;
-                    const char *at = p.c.v + off + h * p.c.vs2 + d * es;
-                    const float v = CT == kE5M2 ? f16_to_f32((uint16_t)(*reinterpret_cast<const uint8_t *>(at) << 8))
-                                                : CT == kBF16 ? bf16_to_f32(*reinterpret_cast<const uint16_t *>(at)) : f16_to_f32(*reinterpret_cast<const uint16_t *>(at));
+                    const char *from = p.c.v + off + h * p.c.vs2 + d * es;
+                    const float v = CT == kE5M2 ? f16_to_f32((uint16_t)(*reinterpret_cast<const uint8_t *>(from) << 8))
+                                                : CT == kBF16 ? bf16_to_f32(*reinterpret_cast<const uint16_t *>(from)) : f16_to_f32(*reinterpret_cast<const uint16_t *>(from));
                     if (fabsf(v) < INFINITY) continue;
                     up = up || !(v < 0.f);
                     down = down || !(v > 0.f);
                 }
                 if (!up && !down) continue;
                 const float add = up && down ? NAN : up ? INFINITY : -INFINITY;
-                if (p.nsplit > 1) {
-                    p.part_o[((((int64_t)b * p.heads + h) * p.R + r) * p.nsplit + split) * DP + d] += add;
+                if (!at.whole) {
+                    p.part_o[((((int64_t)b * p.heads + h) * p.R + r) * p.nsplit + at.split) * DP + d] += add;
                 } else {
                     uint16_t *o = reinterpret_cast<uint16_t *>(p.out + b * p.os0 + token * p.os1 + head * p.os2) + d;
                     const bool half = f16 && (CT == kF16 || p.q_f16);
@@ -513,14 +676,15 @@ struct Rows {
     }
 
     // The rows' output, or their part of it when the key axis is split.
-    __device__ inline void store(const AttendParams &p, int b, int h, int split, int nd)
+    __device__ inline void store(const AttendParams &p, const Place &place)
     {
+        const int b = place.b, h = place.h, nd = place.nd;
 #pragma unroll
         for (int rb = 0; rb < RB; rb++) {
             const int r = row0 + rb * 16 + x;
             if (r >= p.R) continue;
-            if (p.nsplit > 1) {
-                const int64_t at = (((int64_t)b * p.heads + h) * p.R + r) * p.nsplit + split;
+            if (!place.whole) {
+                const int64_t at = (((int64_t)b * p.heads + h) * p.R + r) * p.nsplit + place.split;
                 if (g == 0) p.part_ml[at] = make_float2(m[rb], l[rb]);
                 float *o = p.part_o + at * DP;
 #pragma unroll
@@ -560,26 +724,6 @@ struct Rows {
     }
 };
 
-// What a workgroup works on.
-struct Place {
-    int b, h, split, rg, n, nd, end, t0, t1;
-
-    __device__ inline Place(const AttendParams &p)
-    {
-        int id = (int)blockIdx.x;
-        h = id % p.heads;
-        id /= p.heads;
-        rg = id % p.nrg;
-        id /= p.nrg;
-        split = id % p.nsplit, b = id / p.nsplit;
-        n = __builtin_amdgcn_readfirstlane(clamp_length(p.length, b, p.c.tokens));
-        nd = __builtin_amdgcn_readfirstlane(clamp_drafted(p.drafted, b, p.T));
-        end = nd == 0 ? 0 : (uint32_t)nd > p.c.tokens - (uint32_t)n ? (int)p.c.tokens : n + nd;
-        const int ntiles = (end + kTileKeys - 1) / kTileKeys, tps = tiles_per_split(ntiles, p);
-        t0 = split * tps, t1 = min(t0 + tps, ntiles);
-    }
-};
-
 // Few rows: bound by the cache's bytes. Waves work alone until they join, each
 // on every wk-th tile; keys one tile ahead in registers, values loaded while
 // the scores are worked out.
@@ -590,9 +734,9 @@ __global__ __launch_bounds__(kWaves * 64, (RB == 4 && DP > 64) || DP == 256 ? 1 
     constexpr int KS = W::KS;
     __shared__ float smem[2 * RB * 16 * DP + W::join_words(kWaves)];
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const Place at(p);
-    if (p.nsplit > 1 && at.t0 >= at.t1) return;   // the joining kernel knows
     const int wkey = wave & (p.wk - 1), wrow = wave / p.wk;
+    const Place at = part_of_sequence(p);
+    if (at.split && at.t0 >= at.t1) return;
     W w;
     w.init(p, at.b, at.h, (at.rg * (kWaves / p.wk) + wrow) * RB * 16, at.n, at.end);
 
@@ -619,11 +763,12 @@ __global__ __launch_bounds__(kWaves * 64, (RB == 4 && DP > 64) || DP == 256 ? 1 
 #pragma unroll
                 for (int ks = 0; ks < KS; ks++) k[hf][ks] = widen<CT>(kr[hf][ks]);
             f32x4 s[RB][2];
-            u32x4 pw[RB][1];
-            w.score(k, &s[0][0], 2);
-            load_keys<CT, KS, PAD, false>(p, nxt, w.lim, w.x, w.g, koff, kr);      // the same ones again after the last
+            u32x4 pw[RB];
+            w.score(k, s);
+            if (nxt.fast) load_keys<CT, KS, PAD, false>(p, nxt, w.lim, w.x, w.g, koff, kr);
+            w.raise(s);
             w.weigh(s, pw);
-            w.add(v, pw, 0);
+            w.add(v, pw);
             t = nxt;
         }
     }
@@ -631,7 +776,7 @@ __global__ __launch_bounds__(kWaves * 64, (RB == 4 && DP > 64) || DP == 256 ? 1 
     for (; i < count; i++) {
         const Tile t = finder.at(p, at.b, at.h, i, first, at.n, w.lim);
         if (t.key >= w.lim) break;
-        w.masked_tile(p, t, at.b, at.n, at.nd);
+        w.masked_tile(p, t, at);
     }
 
     w.close();
@@ -639,8 +784,8 @@ __global__ __launch_bounds__(kWaves * 64, (RB == 4 && DP > 64) || DP == 256 ? 1 
         w.join(kWaves, p.wk, wkey, wave - wkey, smem + 2 * RB * 16 * DP, smem + (p.wk == 4 ? 0 : wrow) * RB * 16 * DP);
         if (wkey) return;
     }
-    w.store(p, at.b, at.h, at.split, at.nd);
-    if (w.odd) w.poison(p, at.b, at.h, at.split, at.n, at.nd, max(at.t0 * kTileKeys, at.n & ~(kTileKeys - 1)), min(at.t1 * kTileKeys, at.end));
+    w.store(p, at);
+    if (w.odd) w.poison(p, at);
 }
 
 // Many rows: bound by the matrix cores and the exponentials. Eight waves of 32
@@ -651,12 +796,24 @@ __global__ __launch_bounds__(kWaves * 64, (RB == 4 && DP > 64) || DP == 256 ? 1 
 // the bytes under way (96 KB a CU and more) that keep the matrix cores fed.
 // They go from memory to LDS without passing registers.
 //
-// A row is kept in 16-byte pieces, piece c of row r at place c ^ r (its low
-// bits), so that the rows and pieces that a product reads lie on all banks; a
-// load writes 64 places in order, so it is the source that is mixed.
+// A row is kept in 16-byte pieces, piece c of row r at place c ^ mixed(r), so
+// that what 16 lanes read at once lies on all 64 banks; a load writes 64 places
+// in order, so it is the source that is mixed.
 // wk == 1: every wave takes both tiles of a stage; wk == 2: pairs of waves
 // share rows and take one each.
 constexpr int kShared = 8;                        // waves
+
+// A 16-byte read takes lanes {0-3, 12-15, 20-27}, then {4-11, 16-19, 28-31} and
+// the same of the upper half. Keys: lane (x, g) reads piece 4 ks + g of row x;
+// values: piece x of row 4 g + j. With 16 pieces a row fills the banks, and
+// both are free of conflicts if flipping bit 2 of a row flips the upper two
+// bits of the mix (measured: row & 7 doubles the time of every read). With 8
+// pieces, two rows fill the banks, and a row's low bits do.
+template <int PIECES>
+__device__ constexpr int mixed(int row)
+{
+    return PIECES == 16 ? (row & 15) ^ (row & 4) << 1 : row & (PIECES < 8 ? PIECES - 1 : 7);
+}
 
 __device__ const u32x4 kZeros[1] = {};            // what dims behind the head's own are read from
 
@@ -665,26 +822,30 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
 {
     constexpr int RB = 2;
     using W = Rows<CT, DP, RB, PAD>;
-    constexpr int KS = W::KS, es = W::es, ROW = DP * es, PIECES = ROW / 16, MIX = PIECES < 8 ? PIECES - 1 : 7;
+    constexpr int KS = W::KS, es = W::es, ROW = DP * es, PIECES = ROW / 16;
     constexpr int LOADS = 2 * 64 * ROW / (kShared * 64 * 16);      // 16-byte pieces a thread loads a stage
     constexpr int STAGE = 2 * 64 * ROW, RING = ROW == 256 ? 4 : 8;
     static_assert(RING * STAGE >= 4 * RB * 16 * DP * 4, "the waves' outputs are joined in the ring");
     __shared__ __attribute__((aligned(16))) char smem[RING * STAGE + W::join_words(kShared) * 4];
-    const int tid = (int)threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const Place at(p);
-    if (p.nsplit > 1 && at.t0 >= at.t1) return;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int wkey = wave & (p.wk - 1), wrow = wave / p.wk;
+    Walk walk(p);
+    Place at;
+    while (walk.next(p, at)) {
+    int tid = (int)threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    __syncthreads();                              // the ring is free
 
-    // Stages whose keys are all cached tokens, which every row sees. In pages:
-    // up to the first that touches an absent one.
-    const int key0 = at.t0 * kTileKeys;
-    int stages = min((at.t1 - at.t0) / 2, max(at.n - key0, 0) / 64);
+    // Stages of 64 keys, the first `fast` of them all cached tokens, which
+    // every row sees; in pages, up to the first that touches an absent one.
+    const int key0 = at.t0 * kTileKeys, stages = (at.t1 - at.t0 + 1) / 2;
+    int fast = min((at.t1 - at.t0) / 2, max(at.n - key0, 0) / 64);
     if (p.c.table) {
         const int lane = tid & 63;
-        for (int i = 0; i < stages * 4; i += 64) {
-            const bool bad = i + lane < stages * 4 && (uint32_t)p.c.table[at.b * p.c.ts + ((key0 + (i + lane) * 16) >> p.c.shift)] >= p.c.pages;
+        for (int i = 0; i < fast * 4; i += 64) {
+            const bool bad = i + lane < fast * 4 && (uint32_t)p.c.table[at.b * p.c.ts + ((key0 + (i + lane) * 16) >> p.c.shift)] >= p.c.pages;
             const uint64_t any = __builtin_amdgcn_ballot_w64(bad);
-            if (any) stages = (i + __builtin_ctzll(any)) / 4;
+            if (any) fast = (i + __builtin_ctzll(any)) / 4;
         }
     }
     // A thread's place `lin` of load j: the keys' 64 rows, then the values'. A
@@ -695,7 +856,7 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
     for (int j = 0; j < LOADS; j++) {
         const int lin0 = j * kShared * 64 + wave * 64, lin = lin0 + (tid & 63);
         const bool val = lin0 >= 64 * PIECES;
-        const int row = (lin / PIECES) & 63, piece = lin % PIECES ^ (row & MIX);
+        const int row = (lin / PIECES) & 63, piece = lin % PIECES ^ mixed<PIECES>(row);
         const int64_t step = val ? p.c.vs1 : p.c.ks1;
         src[j] = (val ? p.c.v + at.h * p.c.vs2 : p.c.k + at.h * p.c.ks2) + piece * 16 + (p.c.table ? (row & 15) * step : at.b * (val ? p.c.vs0 : p.c.ks0) + (key0 + row) * step);
         if (PAD) pad[j] = piece * 16 >= p.D * es;
@@ -703,37 +864,41 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
     int entry = 0;
     const auto issue = [&](int i) {
         char *to = smem + i % RING * STAGE + wave * 1024;
-        if (p.c.table && (i & 15) == 0) {         // page numbers of the next 64 half tiles, one a lane
-            const int half = i * 4 + (tid & 63);
-            entry = half < stages * 4 ? p.c.table[at.b * p.c.ts + ((key0 + half * 16) >> p.c.shift)] : 0;
+        if (p.c.table && (i & 15) == 0) {         // page numbers of the next 64 half tiles, one a lane; -1 behind the last token
+            const int key = key0 + (i * 4 + (tid & 63)) * 16;
+            entry = key < at.end ? p.c.table[at.b * p.c.ts + (key >> p.c.shift)] : -1;
             __builtin_amdgcn_s_waitcnt(0x0f70);
         }
 #pragma unroll
         for (int j = 0; j < LOADS; j++) {
             const int lin0 = j * kShared * 64 + wave * 64;
             const bool val = lin0 >= 64 * PIECES;
+            const int64_t step = val ? p.c.vs1 : p.c.ks1;
             const char *from = src[j];
             if (p.c.table) {
                 const int half = (lin0 / PIECES & 63) >> 4;
                 const uint32_t page = (uint32_t)__builtin_amdgcn_readlane(entry, (i & 15) * 4 + half);
                 const uint32_t in = (uint32_t)(key0 + i * 64 + half * 16) & ((1u << p.c.shift) - 1);
-                from += (int64_t)page * (val ? p.c.vs0 : p.c.ks0) + (int64_t)in * (val ? p.c.vs1 : p.c.ks1);
+                from += (int64_t)page * (val ? p.c.vs0 : p.c.ks0) + (int64_t)in * step;
+                if (page >= p.c.pages) from = reinterpret_cast<const char *>(kZeros);
             } else {
-                src[j] += 64 * (val ? p.c.vs1 : p.c.ks1);
+                // behind the last token the last one again, which the mask leaves out
+                const int past = i < fast ? 0 : max(key0 + i * 64 + ((lin0 + (tid & 63)) / PIECES & 63) - (at.end - 1), 0);
+                from -= past * step;
+                src[j] += 64 * step;
             }
             if (PAD && pad[j]) from = reinterpret_cast<const char *>(kZeros);
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
                                              (__attribute__((address_space(3))) void *)(to + j * kShared * 1024), 16, 0, 0);
         }
     };
-    // The queries first, and waited for: a wait for them inside the loop would
-    // be one for every stage under way.
+    // The queries are waited for here: a wait for them inside the loop would be
+    // one for every stage under way. The first stages arrive meanwhile.
+    int issued = 0;
+    while (issued < RING - 2 && issued < stages) issue(issued++);
     W w;
     w.init(p, at.b, at.h, (at.rg * (kShared / p.wk) + wrow) * RB * 16, at.n, at.end);
     __builtin_amdgcn_s_waitcnt(0x0f70);
-    int issued = 0;
-    while (issued < RING - 1 && issued < stages) issue(issued++);
-
     const auto keys_of = [&](const char *stage, int tile, u32x4 (&k)[2][KS]) {
         const char *kb = stage + (tile * 32 + w.x) * ROW;
 #pragma unroll
@@ -741,73 +906,92 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
 #pragma unroll
             for (int ks = 0; ks < KS; ks++) {
                 const int o = (ks * 32 + w.g * 8) * es;
-                k[hf][ks] = widen<CT>(*reinterpret_cast<const Raw<CT> *>(kb + hf * 16 * ROW + ((((o >> 4) ^ (w.x & MIX)) << 4) | (o & 15))));
+                k[hf][ks] = widen<CT>(*reinterpret_cast<const Raw<CT> *>(kb + hf * 16 * ROW + ((((o >> 4) ^ mixed<PIECES>(w.x)) << 4) | (o & 15))));
             }
     };
     const auto values_of = [&](const char *stage, int tile, typename W::Values (&v)[W::VC][8]) {
         const char *vb = stage + (64 + tile * 32 + w.g * 4) * ROW;
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-            const int o = w.x * W::VE * es, mix = (w.g * 4 + (j & 3)) & MIX;
+            const int o = w.x * W::VE * es, mix = mixed<PIECES>(w.g * 4 + (j & 3));
             v[0][j] = *reinterpret_cast<const typename W::Values *>(vb + ((j >> 2) * 16 + (j & 3)) * ROW + ((((o >> 4) ^ mix) << 4) | (o & 15)));
         }
     };
 
-    int done = 0;
-    for (; done < stages; done++) {
-        // This wave's loads of the stage are done when no more than the later
-        // stages' are outstanding (they end in order); other loads in between
-        // make the wait longer, never shorter. Behind the barrier all waves'
-        // are, and all have read the stage before, whose place is free.
-        if (issued - done == RING - 1) __builtin_amdgcn_s_waitcnt(0x0f70 | ((RING - 2) * LOADS & 15) | ((RING - 2) * LOADS >> 4) << 14);
+    // Makes stage i readable and starts the load of a later one. This wave's
+    // loads of it are done when no more than the later stages' are outstanding
+    // (they end in order); other loads in between make the wait longer, never
+    // shorter. Behind the barrier all waves' are, and all are past the values
+    // of stage i - 2, whose place is free.
+    const auto enter = [&](int i) {
+        if (issued - i == RING - 2) __builtin_amdgcn_s_waitcnt(0x0f70 | ((RING - 3) * LOADS & 15) | ((RING - 3) * LOADS >> 4) << 14);
         else __builtin_amdgcn_s_waitcnt(0x0f70);
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         if (issued < stages) issue(issued++);
-        const char *stage = smem + done % RING * STAGE;
-        typename W::Values v[W::VC][8];
+    };
+    // One tile's weights and output beside the next tile's scores: a wave's
+    // exponentials run while its own products do (64 rows over 16384 keys: 379
+    // against 395 us without).
+    if (fast > 0) {
+        f32x4 s[RB][2];
+        const auto step = [&](const char *stage, int tile, const char *next_stage, int next_tile) {
+            typename W::Values v[W::VC][8];
+            u32x4 k[2][KS], pw[RB];
+            f32x4 next[RB][2];
+            keys_of(next_stage, next_tile, k);
+            values_of(stage, tile, v);
+            w.weigh(s, pw);
+            w.score(k, next);
+            w.add(v, pw);
+#pragma unroll
+            for (int rb = 0; rb < RB; rb++)
+#pragma unroll
+                for (int hf = 0; hf < 2; hf++) s[rb][hf] = next[rb][hf];
+            w.raise(s);
+        };
+        enter(0);
         u32x4 k[2][KS];
-        if (p.wk == 1) {
-            f32x4 s[RB][4];
-            u32x4 pw[RB][2];
-            keys_of(stage, 0, k);
-            w.score(k, &s[0][0], 4);
-            keys_of(stage, 1, k);
-            w.score(k, &s[0][2], 4);
-            w.weigh(s, pw);
-            values_of(stage, 0, v);
-            w.add(v, pw, 0);
-            values_of(stage, 1, v);
-            w.add(v, pw, 1);
-        } else {
-            f32x4 s[RB][2];
-            u32x4 pw[RB][1];
-            keys_of(stage, wkey, k);
-            w.score(k, &s[0][0], 2);
-            values_of(stage, wkey, v);
-            w.weigh(s, pw);
-            w.add(v, pw, 0);
+        keys_of(smem, p.wk == 1 ? 0 : wkey, k);
+        w.score(k, s);
+        w.raise(s);
+        for (int i = 0; i < fast; i++) {
+            const char *stage = smem + i % RING * STAGE, *next = i + 1 < fast ? smem + (i + 1) % RING * STAGE : stage;
+            // after the last tile its own scores again, which change nothing
+            if (p.wk == 1) step(stage, 0, stage, 1);
+            if (i + 1 < fast) enter(i + 1);
+            step(stage, p.wk == 1 ? 1 : wkey, next, p.wk == 1 ? 0 : wkey);
         }
     }
-    // the other tiles, from the cache itself
-    if (w.row0 < p.R) {
-        TileFinder rest;
-        const int first = at.t0 + 2 * done + wkey;
-        for (int i = 0; first + i * p.wk < at.t1; i++) {
-            const Tile t = rest.at(p, at.b, at.h, i, first, at.n, w.lim);
-            if (t.key >= w.lim) break;
-            w.masked_tile(p, t, at.b, at.n, at.nd);
+    for (int i = fast; i < stages; i++) {
+        enter(i);
+        const char *stage = smem + i % RING * STAGE;
+        for (int tile = wkey; tile < 2; tile += p.wk) {
+            Tile t;
+            t.key = key0 + i * 64 + tile * kTileKeys;
+            t.fast = false;
+            if (w.row0 >= p.R || t.key >= w.lim) break;
+#pragma unroll
+            for (int hf = 0; hf < 2; hf++) {
+                const int key = t.key + 16 * hf;
+                t.there[hf] = key < at.end && (!p.c.table || (uint32_t)p.c.table[at.b * p.c.ts + (key >> p.c.shift)] < p.c.pages);
+            }
+            u32x4 k[2][KS];
+            typename W::Values v[W::VC][8];
+            keys_of(stage, tile, k);
+            w.tile(p, t, at, k, v, [&](typename W::Values (&u)[W::VC][8]) { values_of(stage, tile, u); });
         }
     }
     w.close();
     if (p.wk == 2) {
         __syncthreads();                          // the ring's memory is free
         w.join(kShared, 2, wkey, wave - wkey, reinterpret_cast<float *>(smem + RING * STAGE), reinterpret_cast<float *>(smem) + wrow * RB * 16 * DP);
-        if (wkey) return;
+        if (wkey) continue;
     }
-    w.store(p, at.b, at.h, at.split, at.nd);
-    if (w.odd) w.poison(p, at.b, at.h, at.split, at.n, at.nd, max(at.t0 * kTileKeys, at.n & ~(kTileKeys - 1)), min(at.t1 * kTileKeys, at.end));
+    w.store(p, at);
+    if (w.odd) w.poison(p, at);
+    }
 }
 
 // Joins a row's splits. Few of them: 16 lanes a row, one split a lane to weigh
@@ -820,11 +1004,9 @@ struct Joined {
     {
         const int r = (int)(row % p.R);
         h = (int)(row / p.R % p.heads), b = (int)(row / p.R / p.heads);
-        const int n = clamp_length(p.length, b, p.c.tokens);
         nd = clamp_drafted(p.drafted, b, p.T);
-        const int end = nd == 0 ? 0 : (uint32_t)nd > p.c.tokens - (uint32_t)n ? (int)p.c.tokens : n + nd;
-        const int ntiles = (end + kTileKeys - 1) / kTileKeys, tps = tiles_per_split(ntiles, p);
-        used = (ntiles + tps - 1) / tps;
+        const int tiles = tiles_of(p, b), each = tiles_per_split(p, tiles);
+        used = p.flat ? p.used[b] : max((tiles + each - 1) / each, 1);
         tok = r / p.G, head = h * p.G + r % p.G;
     }
 
@@ -844,29 +1026,35 @@ __global__ __launch_bounds__(256) void k_attend_join_few(AttendParams p, int64_t
     const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
     if (row >= rows) return;
     const Joined j(p, row);
+    if (j.used == 1) return;                      // whole already
     const float *po = p.part_o + row * p.nsplit * DP + x * 4;
-    const float2 ml = x < j.used ? p.part_ml[row * p.nsplit + x] : make_float2(-INFINITY, 0.f);
+    const float2 *ml = p.part_ml + row * p.nsplit;
     f32x4 v[2][E];                                // two splits ahead
 #pragma unroll
     for (int u = 0; u < 2; u++)
 #pragma unroll
         for (int e = 0; e < E; e++) v[u][e] = u < j.used ? *reinterpret_cast<const f32x4 *>(po + u * DP + e * 64) : f32x4{0.f, 0.f, 0.f, 0.f};
-    float top = ml.x;
+    float top = -INFINITY;
+    for (int k = x; k < j.used; k += 16) top = fmaxf(top, ml[k].x);
     for (int y = 1; y < 16; y <<= 1) top = fmaxf(top, __shfl_xor(top, y));
-    const float a = ml.y == 0.f ? 0.f : __builtin_amdgcn_exp2f(ml.x - (top == -INFINITY ? 0.f : top));
-    float sum = ml.y * a;
-    for (int y = 1; y < 16; y <<= 1) sum += __shfl_xor(sum, y);
+    float sum = 0.f;
     f32x4 o[E] = {};
-    for (int k = 0; k < j.used; k += 2)
+    for (int k0 = 0; k0 < j.used; k0 += 16) {
+        const float2 mine = k0 + x < j.used ? ml[k0 + x] : make_float2(-INFINITY, 0.f);
+        const float a = __builtin_amdgcn_exp2f(mine.x - (top == -INFINITY ? 0.f : top));
+        sum += mine.y * a;
+        for (int k = k0; k < min(j.used, k0 + 16); k += 2)
 #pragma unroll
-        for (int u = 0; u < 2; u++) {
-            const float w = __shfl(a, (int)(threadIdx.x & 48) + ((k + u) & 15));
+            for (int u = 0; u < 2; u++) {
+                const float w = __shfl(a, (int)(threadIdx.x & 48) + ((k + u) & 15));
 #pragma unroll
-            for (int e = 0; e < E; e++) {
-                if (k + u < j.used) o[e] += v[u][e] * w;
-                if (k + u + 2 < j.used) v[u][e] = *reinterpret_cast<const f32x4 *>(po + (k + u + 2) * DP + e * 64);
+                for (int e = 0; e < E; e++) {
+                    if (k + u < j.used) o[e] += v[u][e] * w;
+                    if (k + u + 2 < j.used) v[u][e] = *reinterpret_cast<const f32x4 *>(po + (k + u + 2) * DP + e * 64);
+                }
             }
-        }
+    }
+    for (int y = 1; y < 16; y <<= 1) sum += __shfl_xor(sum, y);
     if (x == 0) j.put_lse(p, top, sum);
     const bool empty = j.empty(sum);
     const float inv = 1.f / sum;
@@ -890,6 +1078,7 @@ __global__ __launch_bounds__(kWaves * 64) void k_attend_join_many(AttendParams p
     const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
     const int64_t row = blockIdx.x;
     const Joined j(p, row);
+    if (j.used == 1) return;
     const float2 *ml = p.part_ml + row * p.nsplit;
     const float *po = p.part_o + row * p.nsplit * DP + lane * E;
 
@@ -930,101 +1119,119 @@ __global__ __launch_bounds__(kWaves * 64) void k_attend_join_many(AttendParams p
 }
 
 // score[key] += sum over a kv head's rows of exp(s - lse). With the rows' lse
-// known, a wave owns 32 keys, keeps them in registers and passes over the
-// rows: no atomics, each sum in one fixed order. The products are those of
-// k_attend, bit for bit.
+// known, a wave owns 32 keys at a time, keeps them in registers and passes over
+// the rows: no atomics, each sum in one fixed order. The products are those of
+// k_attend, bit for bit. A workgroup has its rows in LDS, as the matrix cores
+// take them, for p.weigh_tiles tiles of each wave; read from memory for every
+// tile they took twice the time (32 tokens of 32 heads over 4 x 16384 keys of
+// 64: 50 us).
 template <int CT, int DP, bool PAD>
 __global__ __launch_bounds__(kWaves * 64, 2) void k_attend_weigh(AttendParams p)
 {
     constexpr int KS = DP / 32;
     constexpr int es = CT == kE5M2 ? 1 : 2;
+    constexpr int BLOCKS = KS <= 4 ? 16 : 8;      // of 16 rows, at a time
+    __shared__ __attribute__((aligned(16))) u32x4 lq[BLOCKS * KS * 64];
+    __shared__ float2 lrow[BLOCKS * 16];          // factor of the scores, lse * log2(e); +inf: takes no part
     const int lane = (int)(threadIdx.x & 63), x = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     int id = (int)blockIdx.x;
     const int h = id % p.heads;
     id /= p.heads;
-    const int per = (int)((p.c.tokens + kTileKeys * kWaves - 1) / (kTileKeys * kWaves));
-    const int tile = (id % per) * kWaves + wave, b = id / per;
+    const int each = kWaves * p.weigh_tiles, per = (int)(((p.c.tokens + kTileKeys - 1) / kTileKeys + each - 1) / each);
+    const int first = id % per * each, b = id / per;
     const int n = __builtin_amdgcn_readfirstlane(clamp_length(p.length, b, p.c.tokens));
     const int nd = __builtin_amdgcn_readfirstlane(clamp_drafted(p.drafted, b, p.T));
-    const int end = nd == 0 ? 0 : (uint32_t)nd > p.c.tokens - (uint32_t)n ? (int)p.c.tokens : n + nd;
-    if (tile * kTileKeys >= end) return;
-    TileFinder finder;
-    const Tile t = finder.at(p, b, h, 0, tile, n, end);
-    Raw<CT> kr[2][KS];
-    load_keys<CT, KS, PAD, true>(p, t, end, x, g, (uint32_t)(x * p.c.ks1) + g * 8 * es, kr);
-    // the sum this lane will add to, on its way already
-    const int key = t.key + 16 * (x >> 2 & 1) + 4 * g + (x & 3);
-    const bool mine = (x & 4 ? t.there[1] : t.there[0]) && key < min(end, p.score_tokens);
-    float *at = p.score + b * p.sc0 + h * p.sc1 + key;
-    const float old = mine ? *at : 0.f;
-    f32x4 sum[2] = {};
-    const int rows = nd * p.G;
-    u32x4 q[KS];
-    float c2, lse;
-    int tok;
-    const auto load_row = [&](int r0) {
-        const int r = r0 + x;
-        tok = r / p.G;
-        const int head = h * p.G + r % p.G;
-        c2 = p.c2 * load_q<CT, KS, PAD>(p, p.q + b * p.qs0 + tok * p.qs1 + head * p.qs2, r < rows, g, q);
-        lse = r < rows ? p.lse[((int64_t)b * p.T + tok) * (p.heads * p.G) + head] : -INFINITY;
-    };
-    load_row(0);
-    for (int r0 = 0; r0 < rows; r0 += 16) {
-        f32x4 s[2];
+    const int end = end_of(p, n, nd), rows = nd * p.G;
+    if (first * kTileKeys >= end) return;
+    const uint32_t koff = (uint32_t)(x * p.c.ks1) + g * 8 * es;
+
+    for (int r0 = 0; r0 < rows; r0 += BLOCKS * 16) {
+        const int blocks = min((rows - r0 + 15) / 16, BLOCKS);
+        __syncthreads();                          // the rows before have been used
+        for (int i = wave; i < blocks; i += kWaves) {
+            const int r = r0 + i * 16 + x, tok = r / p.G, head = h * p.G + r % p.G;
+            u32x4 q[KS];
+            const float c2 = p.c2 * load_q<CT, KS, PAD>(p, p.q + b * p.qs0 + tok * p.qs1 + head * p.qs2, r < rows, g, q);
 #pragma unroll
-        for (int hf = 0; hf < 2; hf++)
-#pragma unroll
-            for (int ks = 0; ks < KS; ks++) s[hf] = mfma<CT>(widen<CT>(kr[hf][ks]), q[ks], ks ? s[hf] : f32x4{0.f, 0.f, 0.f, 0.f});
-        const float base = lse * 1.4426950408889634f, scale = c2;
-        const bool any = lse != -INFINITY;
-        const int me = tok;
-        if (r0 + 16 < rows) load_row(r0 + 16);
-        if (t.fast) {
+            for (int ks = 0; ks < KS; ks++) lq[(i * KS + ks) * 64 + lane] = q[ks];
+            const float lse = r < rows ? p.lse[((int64_t)b * p.T + tok) * (p.heads * p.G) + head] : -INFINITY;
+            if (g == 0) lrow[i * 16 + x] = make_float2(c2, lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f);
+        }
+        __syncthreads();
+
+        TileFinder finder;
+        Tile nxt;
+        Raw<CT> kr[2][KS];
+        // where this lane adds, and what is there, on its way with the keys
+        const auto fetch = [&](int i, float *&at, float &old) {
+            nxt = finder.find(p, b, h, i, first + wave, kWaves, n, end);
+            load_keys<CT, KS, PAD, true>(p, nxt, end, x, g, koff, kr);
+            const int key = nxt.key + 16 * (x >> 2 & 1) + 4 * g + (x & 3);
+            const bool mine = x < 8 && (x & 4 ? nxt.there[1] : nxt.there[0]) && key < min(end, p.score_tokens);
+            at = mine ? p.score + b * p.sc0 + h * p.sc1 + key : nullptr;
+            old = mine ? *at : 0.f;
+        };
+        float *at, *at_next = nullptr;
+        float old, old_next = 0.f;
+        if ((first + wave) * kTileKeys < end) fetch(0, at_next, old_next);
+        for (int i = 0; i < p.weigh_tiles && (first + wave + i * kWaves) * kTileKeys < end; i++) {
+            const Tile t = nxt;
+            at = at_next, old = old_next;
+            u32x4 k[2][KS];
 #pragma unroll
             for (int hf = 0; hf < 2; hf++)
 #pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    const float w = __builtin_amdgcn_exp2f(fmaf(s[hf][k], scale, -base));
-                    sum[hf][k] += any ? w : 0.f;
+                for (int ks = 0; ks < KS; ks++) k[hf][ks] = widen<CT>(kr[hf][ks]);
+            if (i + 1 < p.weigh_tiles && (first + wave + (i + 1) * kWaves) * kTileKeys < end) fetch(i + 1, at_next, old_next);
+            f32x4 sum[2] = {};
+            for (int j = 0; j < blocks; j++) {
+                const float2 row = lrow[j * 16 + x];
+                f32x4 s[2];
+#pragma unroll
+                for (int ks = 0; ks < KS; ks++) {
+                    const u32x4 q = lq[(j * KS + ks) * 64 + lane];
+#pragma unroll
+                    for (int hf = 0; hf < 2; hf++) s[hf] = mfma<CT>(k[hf][ks], q, ks ? s[hf] : f32x4{0.f, 0.f, 0.f, 0.f});
                 }
-            continue;
-        }
-        uint32_t seen = p.tree ? tree_bits(p, b, me, t.key + 4 * g - n, nd) : 0;
-        seen |= leading_bits((p.tree ? n : min(end, n + me + 1)) - t.key - 4 * g);
-        seen = any ? seen & there_bits(t) : 0;
+                uint32_t seen = row.y == INFINITY ? 0u : 0xffu;
+                if (!t.fast) {
+                    const int tok = (r0 + j * 16 + x) / p.G;
+                    uint32_t bits = p.tree ? tree_bits(p, b, tok, t.key + 4 * g - n, nd) : 0;
+                    bits |= leading_bits((p.tree ? n : min(end, n + tok + 1)) - t.key - 4 * g);
+                    seen &= bits & there_bits(t);
+                }
 #pragma unroll
-        for (int k = 0; k < 8; k++) {
-            const float w = __builtin_amdgcn_exp2f(fmaf(s[k >> 2][k & 3], scale, -base));
-            sum[k >> 2][k & 3] += seen >> k & 1 ? w : 0.f;
+                for (int i8 = 0; i8 < 8; i8++) {
+                    const float w = __builtin_amdgcn_exp2f(fmaf(s[i8 >> 2][i8 & 3], row.x, -row.y));
+                    sum[i8 >> 2][i8 & 3] += seen >> i8 & 1 ? w : 0.f;
+                }
+            }
+            // Sums over the 16 lanes of a row of lanes, halving the keys a lane
+            // holds with each step: lane x ends with key x % 8 of the eight.
+            float v[8] = {sum[0][0], sum[0][1], sum[0][2], sum[0][3], sum[1][0], sum[1][1], sum[1][2], sum[1][3]};
+#pragma unroll
+            for (int half = 4; half; half >>= 1) {
+                const bool up = x & half;
+#pragma unroll
+                for (int y = 0; y < half; y++) {
+                    const float give = up ? v[y] : v[y + half], keep = up ? v[y + half] : v[y];
+                    v[y] = keep + __shfl_xor(give, half);
+                }
+            }
+            v[0] += __shfl_xor(v[0], 8);
+            if (at) *at = old + v[0];
         }
     }
-    // Sums over the 16 lanes of a row of lanes, halving the keys a lane holds
-    // with each step: lane x ends with key x % 8 of the eight.
-    float v[8] = {sum[0][0], sum[0][1], sum[0][2], sum[0][3], sum[1][0], sum[1][1], sum[1][2], sum[1][3]};
-#pragma unroll
-    for (int half = 4; half; half >>= 1) {
-        const bool up = x & half;
-#pragma unroll
-        for (int k = 0; k < half; k++) {
-            const float give = up ? v[k] : v[k + half], keep = up ? v[k + half] : v[k];
-            v[k] = keep + __shfl_xor(give, half);
-        }
-    }
-    v[0] += __shfl_xor(v[0], 8);
-    if (x < 8 && mine) *at = old + v[0];
 }
 
 // ------------------------------------------------------------------- host --
 struct Plan {
-    int DP, RB, wk, nrg, nsplit, min_tiles;
-    bool shared;                                  // k_attend_shared
-    uint64_t rows, off_ml, off_lse, bytes;
+    int DP, RB, wk, nrg, nsplit, slots, min_steps, unit;
+    bool shared, flat;                            // k_attend_shared, Walk
+    uint64_t rows, grid, off_ml, off_used, off_lse, bytes;
 };
 
-// The split of the key axis: enough workgroups to fill the chip a few times,
-// as far as each still has a share of keys worth its joining.
 // may_share: the cache's rows begin on 16 bytes and end on them.
 Plan make_plan(uint32_t seqs, uint32_t kv_heads, uint32_t dim, uint32_t cache_tokens, uint32_t T, uint32_t heads, bool may_share)
 {
@@ -1039,18 +1246,32 @@ Plan make_plan(uint32_t seqs, uint32_t kv_heads, uint32_t dim, uint32_t cache_to
     const int wr = a.shared ? (R > 128 ? 8 : 4) : blocks >= 4 ? 4 : blocks >= 2 ? 2 : 1;
     a.wk = waves / wr;
     a.nrg = (int)((blocks + wr - 1) / wr);
-    a.min_tiles = a.shared ? 4 : 2 * a.wk;
-    const uint64_t base = (uint64_t)seqs * kv_heads * a.nrg;
-    const uint64_t tiles = ((uint64_t)cache_tokens + kTileKeys - 1) / kTileKeys;
-    const uint64_t want = a.shared ? kCUs : a.RB == 1 ? 8 * kCUs : a.RB == 2 ? 4 * kCUs : 2 * kCUs;
-    uint64_t split = (want + base - 1) / base;
-    const uint64_t most = (tiles + a.min_tiles - 1) / a.min_tiles;
-    split = split > most ? most : split;
-    a.nsplit = (int)(split < 1 ? 1 : split);
+    a.unit = a.shared ? 2 : a.wk;
+    a.min_steps = 2;
+    // Workgroups: one a CU where they are large, else a few, so that one's
+    // loads run beside another's join. With four times as many sequences as
+    // that leaves for each head, every one goes to a workgroup of its own.
+    const uint64_t want = a.shared ? kCUs : a.RB == 1 ? 8 * kCUs : a.RB == 2 ? 4 * kCUs : 2 * kCUs, each = (uint64_t)kv_heads * a.nrg;
+    const uint64_t slots = want > each ? want / each : 1;
+    const uint64_t steps = (((uint64_t)cache_tokens + kTileKeys - 1) / kTileKeys + a.unit - 1) / a.unit, most = (steps + a.min_steps - 1) / a.min_steps;
+    a.slots = (int)slots;
+    a.nsplit = 1;
+    a.flat = a.shared && most > 1 && seqs < 4 * slots && (slots > 1 || seqs > 1);
+    if (a.flat) {
+        // parts of one sequence: up to four times what equal lengths give
+        uint64_t n = seqs == 1 ? slots : 4 * ((slots + seqs - 1) / seqs) + 1;
+        n = n > most + 1 ? most + 1 : n;
+        a.nsplit = (int)(n < 2 ? 2 : n);
+    } else if (!a.shared) {
+        const uint64_t n = (slots + seqs - 1) / seqs;
+        a.nsplit = (int)(n > most ? most : n);
+    }
+    a.grid = each * (a.flat ? slots : (uint64_t)seqs * a.nsplit);
     a.rows = (uint64_t)seqs * heads * T;
     const auto up = [](uint64_t v) { return (v + 255) & ~255ull; };
     a.off_ml = a.nsplit > 1 ? up(a.rows * a.nsplit * a.DP * 4) : 0;
-    a.off_lse = a.off_ml + (a.nsplit > 1 ? up(a.rows * a.nsplit * 8) : 0);
+    a.off_used = a.off_ml + (a.nsplit > 1 ? up(a.rows * a.nsplit * 8) : 0);
+    a.off_lse = a.off_used + (a.nsplit > 1 ? up(seqs * 4ull) : 0);
     a.bytes = a.off_lse + up(a.rows * 4);
     return a;
 }
@@ -1072,7 +1293,7 @@ int launch(const AttendParams &p, uint64_t grid, hipStream_t s)
 template <int CT, int DP, bool PAD>
 int run(const AttendParams &p, const Plan &plan, int seqs, int half, hipStream_t s)
 {
-    const uint64_t grid = (uint64_t)seqs * p.heads * p.nrg * p.nsplit;
+    const uint64_t grid = plan.grid;
     int rc = UZIP_EINVAL;
     if (plan.shared) {
         if constexpr (DP <= 128) {
@@ -1085,13 +1306,13 @@ int run(const AttendParams &p, const Plan &plan, int seqs, int half, hipStream_t
     else if constexpr (DP <= 128) rc = launch<CT, DP, 4, PAD>(p, grid, s);
     if (rc) return rc;
     if (p.nsplit > 1) {
-        if (p.nsplit <= 16) k_attend_join_few<DP><<<(unsigned)((plan.rows + 15) / 16), 256, 0, s>>>(p, (int64_t)plan.rows, half);
+        if (p.nsplit <= 16 || (p.flat && p.nsplit <= 64)) k_attend_join_few<DP><<<(unsigned)((plan.rows + 15) / 16), 256, 0, s>>>(p, (int64_t)plan.rows, half);
         else k_attend_join_many<DP><<<(unsigned)plan.rows, kWaves * 64, 0, s>>>(p, half);
         UZIP_KV_LAUNCH_CHECK("k_attend_join");
     }
     if (p.score) {
-        const uint64_t per = ((uint64_t)p.c.tokens + kTileKeys * kWaves - 1) / (kTileKeys * kWaves);
-        k_attend_weigh<CT, DP, PAD><<<(unsigned)(per * seqs * p.heads), kWaves * 64, 0, s>>>(p);
+        const uint64_t each = (uint64_t)kWaves * p.weigh_tiles, tiles = ((uint64_t)p.c.tokens + kTileKeys - 1) / kTileKeys;
+        k_attend_weigh<CT, DP, PAD><<<(unsigned)((tiles + each - 1) / each * p.seqs * p.heads), kWaves * 64, 0, s>>>(p);
         UZIP_KV_LAUNCH_CHECK("k_attend_weigh");
     }
     return UZIP_OK;
@@ -1135,7 +1356,7 @@ int uzip_kv_attend(const uzip_kv_cache_t *cache, const uzip_kv_attend_args_t *a,
     int64_t bits = cache->dim * elem_size((int)cache->dtype);
     for (int i = 0; i < 3; i++) bits |= (cache->k_stride[i] | cache->v_stride[i]) * elem_size((int)cache->dtype);
     const Plan plan = make_plan(cache->seqs, cache->heads, cache->dim, cache->tokens, a->tokens, a->heads, (bits & 15) == 0);
-    if ((uint64_t)cache->seqs * cache->heads * plan.nrg * plan.nsplit >= (1ull << 31) ||
+    if (plan.grid >= (1ull << 31) || (uint64_t)cache->seqs * ((cache->tokens + 31) / 32) >= (1ull << 31) ||
         (uint64_t)cache->seqs * cache->heads * ((cache->tokens + 127) / 128) >= (1ull << 31)) return UZIP_EINVAL;
 
     AttendParams p;
@@ -1163,9 +1384,17 @@ int uzip_kv_attend(const uzip_kv_cache_t *cache, const uzip_kv_attend_args_t *a,
     p.heads = (int)cache->heads;
     p.nsplit = plan.nsplit;
     p.nrg = plan.nrg;
-    p.min_tiles = plan.min_tiles;
+    p.slots = plan.slots;
+    p.min_steps = plan.min_steps;
+    p.seqs = (int)cache->seqs;
+    p.used = reinterpret_cast<int *>(ws + plan.off_used);
+    p.flat = plan.flat;
+    // enough workgroups to fill the chip four times, rows read once for up to eight tiles of a wave
+    const uint64_t waves = (uint64_t)cache->seqs * cache->heads * ((cache->tokens + kTileKeys - 1) / kTileKeys);
+    const uint64_t share = waves / (4 * kCUs * kWaves);
+    p.weigh_tiles = (int)(share < 1 ? 1 : share > 8 ? 8 : share);
     p.wk = plan.wk;
-    p.unit = plan.shared ? 2 : plan.wk;
+    p.unit = plan.unit;
     p.c2 = a->scale * 1.4426950408889634f;
     p.q_f16 = a->dtype == UZIP_KV_F16;
     const int seqs = (int)cache->seqs, half = p.q_f16;
