@@ -23,17 +23,18 @@ struct RopeParams {
     int interleaved, inverse;
     int per_q, per_copy;                          // units of a rotated and of a copied head
     int units, share;                             // of a token; of a workgroup
-    int parts;                                    // workgroups a token
+    int parts, tokens;                            // workgroups a token, or tokens a workgroup
+    int64_t count;                                // tokens of all sequences
 };
 
 // A unit of work: 8 elements of a head, or 8 and the 8 they turn with.
 enum { kPair, kInterleaved, kCopy };
 struct Unit {
     const char *src;
-    char *dst;                                    // null: dropped
+    int64_t off;                                  // of the head from its token's place in `to`
     int kind, i;                                  // i: the first pair's number
     int d;                                        // the first element in the head
-    bool cached;                                  // dst is a cache row
+    int to, token;                                // to: 0 queries, 1 keys, 2 values, -1 nothing; token of the workgroup
 };
 
 template <int CT>
@@ -56,34 +57,36 @@ __device__ inline void unpack8(u32x4 w, float (&x)[8])
     }
 }
 
-// (head row of) unit u of a token: source, destination, place in the head
-__device__ inline Unit unit_at(const RopeParams &p, int u, int b, int t, char *krow, char *vrow)
+// unit u of a workgroup's tokens, the first of them number `first` of all
+__device__ inline Unit unit_at(const RopeParams &p, int u, int64_t first)
 {
     Unit r;
+    r.token = 0;
+    if (p.tokens > 1) r.token = u / p.units, u -= r.token * p.units;
+    const int64_t id = first + r.token;
+    const int64_t b = id / p.T, t = id - b * p.T;
     int head, in;
     const int nq = p.Hq * p.per_q, nk = p.H * p.per_q;
-    bool copy = false;
     if (u < nq) {
         head = u / p.per_q, in = u - head * p.per_q;
         r.src = p.q + b * p.qs0 + t * p.qs1 + head * p.qs2;
-        r.dst = p.y + b * p.ys0 + t * p.ys1 + head * p.ys2;
-        r.cached = false;
+        r.off = b * p.ys0 + t * p.ys1 + head * p.ys2;
+        r.to = 0;
     } else if (u < nq + nk) {
         u -= nq;
         head = u / p.per_q, in = u - head * p.per_q;
         r.src = p.k + b * p.ks0 + t * p.ks1 + head * p.ks2;
-        r.dst = krow ? krow + head * p.c.ks2 : nullptr;
-        r.cached = true;
+        r.off = head * p.c.ks2;
+        r.to = 1;
     } else {
         u -= nq + nk;
         head = u / p.per_copy, in = u - head * p.per_copy;
         r.src = p.v + b * p.vs0 + t * p.vs1 + head * p.vs2;
-        r.dst = vrow ? vrow + head * p.c.vs2 : nullptr;
-        r.cached = true;
-        copy = true;
+        r.off = head * p.c.vs2;
+        r.to = 2;
     }
     const int pairs = p.rot / 16;
-    if (copy || p.rot == 0) r.kind = kCopy, r.d = in * 8;
+    if (r.to == 2 || p.rot == 0) r.kind = kCopy, r.d = in * 8;
     else if (p.interleaved) r.kind = in * 8 < p.rot ? kInterleaved : kCopy, r.d = in * 8;
     else if (in < pairs) r.kind = kPair, r.d = in * 8;
     else r.kind = kCopy, r.d = p.rot + (in - pairs) * 8;
@@ -92,37 +95,30 @@ __device__ inline Unit unit_at(const RopeParams &p, int u, int b, int t, char *k
 }
 
 // Rotates queries and keys and writes keys and values into the cache, one
-// launch. A workgroup takes (a part of) one token: the angles of its rot / 2
-// pairs are worked out once, in binary64 up to the fraction of a turn (a
-// binary32 angle is wrong by 2^-24 of itself: 0.06 rad at position 2^20), and
-// serve all its heads. Bound by memory: every element is read and written
-// once, in 16-byte pieces; the loads of a thread's first units are on their
-// way while the angles are computed.
+// launch. A workgroup takes some tokens, as many as give its threads work (24
+// tokens of one head each took 71 us where they now take 11), or a part of one
+// when there are few: the angles of a token's rot / 2 pairs are worked out
+// once, in binary64 up to the fraction of a turn (a binary32 angle is wrong by
+// 2^-24 of itself: 0.06 rad at position 2^20), and serve all its heads. Bound
+// by memory: every element is read and written once, in 16-byte pieces; the
+// loads of a thread's first units are on their way while the angles are
+// computed. Queries of 2 x 16384 tokens of 64 heads of 128: 206 us, 5.2 TB/s,
+// which is the rate of a large copy.
 // LANES: rot is not a whole number of units; elements find their partner
 // through LDS instead.
+constexpr int kRopeTokens = 32, kRopeAngles = 1024;       // of a workgroup, at most
 template <bool F16, int CT, bool LANES>
 __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeParams p)
 {
     constexpr int ces = CT == kE5M2 ? 1 : 2;
-    __shared__ float2 cs[128];
+    __shared__ float2 cs[kRopeAngles];
+    __shared__ char *place[kRopeTokens][2];       // of a token's keys and values in the cache, null where dropped
     __shared__ uint16_t row[LANES ? kRopeThreads * 8 : 1];
-    const int part = (int)(blockIdx.x % p.parts), token = (int)(blockIdx.x / p.parts);
-    const int b = token / p.T, t = token - b * p.T;
+    const int part = (int)(blockIdx.x % p.parts);
+    const int64_t first = (int64_t)(blockIdx.x / p.parts) * p.tokens;
+    const int tokens = (int)min((int64_t)p.tokens, p.count - first), half = p.rot / 2;
     const int tid = (int)threadIdx.x;
-
-    char *krow = nullptr, *vrow = nullptr;
-    if (p.H) {
-        const int64_t slot = (int64_t)p.length[b] + t;
-        if (t < clamp_drafted(p.drafted, b, p.T) && slot >= 0 && slot < p.c.tokens) {
-            int64_t ko, vo;
-            if (locate(p.c, b, (uint32_t)slot, p.c.ks0, p.c.ks1, ko)) {
-                locate(p.c, b, (uint32_t)slot, p.c.vs0, p.c.vs1, vo);
-                krow = p.c.k + ko;
-                vrow = p.c.v + vo;
-            }
-        }
-    }
-    const int u0 = part * p.share, u1 = min(u0 + p.share, p.units);
+    const int u0 = part * p.share, u1 = min(u0 + p.share, p.units * tokens);
 
     Unit unit[kRopeUnits];
     u32x4 a[kRopeUnits], o[kRopeUnits];
@@ -130,60 +126,80 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeParams p)
 #pragma unroll
         for (int i = 0; i < kRopeUnits; i++) {
             const int u = base + i * kRopeThreads + tid;
-            unit[i].dst = nullptr;
+            unit[i].to = -1;
             if (u >= u1) continue;
-            unit[i] = unit_at(p, u, b, t, krow, vrow);
-            if (!unit[i].dst) continue;
+            unit[i] = unit_at(p, u, first);
             a[i] = *reinterpret_cast<const u32x4 *>(unit[i].src + unit[i].d * 2);
             if (unit[i].kind == kPair) o[i] = *reinterpret_cast<const u32x4 *>(unit[i].src + unit[i].d * 2 + p.rot);
         }
     };
     if (!LANES) load(u0);
 
-    if (tid < p.rot / 2) {
-        const int64_t pos = p.pos ? p.pos[b * p.pos_stride + t] : p.length[b] + (int64_t)t;
-        double turns = (double)pos * p.freq[tid];
+    for (int j = tid; j < tokens * half; j += kRopeThreads) {
+        const int token = j / half, i = j - token * half;
+        const int64_t id = first + token, b = id / p.T, t = id - b * p.T;
+        const int64_t pos = p.pos ? p.pos[b * p.pos_stride + t] : p.length[b] + t;
+        double turns = (double)pos * p.freq[i];
         turns -= rint(turns);
         float s, c;
         sincospif((float)(2.0 * turns), &s, &c);
-        cs[tid] = make_float2(c * p.amplitude, p.inverse ? -s * p.amplitude : s * p.amplitude);
+        cs[j] = make_float2(c * p.amplitude, p.inverse ? -s * p.amplitude : s * p.amplitude);
+    }
+    if (p.H && tid < tokens) {
+        const int64_t id = first + tid;
+        const int b = (int)(id / p.T), t = (int)(id - (int64_t)b * p.T);
+        const int64_t slot = (int64_t)p.length[b] + t;
+        char *k = nullptr, *v = nullptr;
+        if (t < clamp_drafted(p.drafted, b, p.T) && slot >= 0 && slot < p.c.tokens) {
+            int64_t ko, vo;
+            if (locate(p.c, b, (uint32_t)slot, p.c.ks0, p.c.ks1, ko)) {
+                locate(p.c, b, (uint32_t)slot, p.c.vs0, p.c.vs1, vo);
+                k = p.c.k + ko;
+                v = p.c.v + vo;
+            }
+        }
+        place[tid][0] = k, place[tid][1] = v;
     }
     __syncthreads();
+    const auto where = [&](const Unit &r) {
+        if (r.to < 0) return (char *)nullptr;
+        char *at = r.to == 0 ? p.y : place[r.token][r.to - 1];
+        return at ? at + r.off : at;
+    };
 
     if constexpr (LANES) {
         // whole heads a step: per_q units of 8 elements each
-        const int rows = kRopeThreads / p.per_q, half = p.rot / 2;
+        const int rows = kRopeThreads / p.per_q;
         for (int base = u0; base < u1; base += rows * p.per_q) {
             const int u = base + tid;
             Unit r;
-            r.dst = nullptr;
+            r.to = -1;
             u32x4 w = {};
             if (tid < rows * p.per_q && u < u1) {
-                r = unit_at(p, u, b, t, krow, vrow);
-                const int in = tid % p.per_q;
-                r.kind = u >= (p.Hq + p.H) * p.per_q ? kCopy : kPair;
-                r.d = in * 8;
-                if (r.dst) w = *reinterpret_cast<const u32x4 *>(r.src + r.d * 2);
+                r = unit_at(p, u, first);
+                r.d = u % p.per_q * 8;
+                w = *reinterpret_cast<const u32x4 *>(r.src + r.d * 2);
                 *reinterpret_cast<u32x4 *>(row + tid * 8) = w;
             }
             __syncthreads();
-            if (r.dst) {
+            if (char *dst = where(r)) {
+                const float2 *angle = cs + r.token * half;
                 float x[8], y[8];
                 unpack8<F16>(w, x);
 #pragma unroll
                 for (int e = 0; e < 8; e++) {
                     const int d = r.d + e;
                     y[e] = x[e];
-                    if (r.kind == kCopy || d >= p.rot) continue;
+                    if (r.to == 2 || d >= p.rot) continue;
                     const int i = p.interleaved ? d >> 1 : d < half ? d : d - half;
-                    const bool first = p.interleaved ? !(d & 1) : d < half;
-                    const int other = p.interleaved ? d ^ 1 : first ? d + half : d - half;
+                    const bool lead = p.interleaved ? !(d & 1) : d < half;
+                    const int other = p.interleaved ? d ^ 1 : lead ? d + half : d - half;
                     const uint16_t z = row[tid * 8 - r.d + other];
                     const float f = F16 ? f16_to_f32(z) : bf16_to_f32(z);
-                    y[e] = first ? x[e] * cs[i].x - f * cs[i].y : x[e] * cs[i].x + f * cs[i].y;
+                    y[e] = lead ? x[e] * angle[i].x - f * angle[i].y : x[e] * angle[i].x + f * angle[i].y;
                 }
-                if (r.cached) store8<CT>(r.dst + r.d * ces, y);
-                else store8<F16 ? kF16 : kBF16>(r.dst + r.d * 2, y);
+                if (r.to) store8<CT>(dst + r.d * ces, y);
+                else store8<F16 ? kF16 : kBF16>(dst + r.d * 2, y);
             }
             __syncthreads();
         }
@@ -194,7 +210,9 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeParams p)
 #pragma unroll
         for (int i = 0; i < kRopeUnits; i++) {
             const Unit &r = unit[i];
-            if (!r.dst) continue;
+            char *dst = where(r);
+            if (!dst) continue;
+            const float2 *angle = cs + r.token * half + r.i;
             float x[8], y[8], z[8];
             unpack8<F16>(a[i], x);
             if (r.kind == kPair) {
@@ -202,31 +220,31 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeParams p)
                 unpack8<F16>(o[i], w);
 #pragma unroll
                 for (int e = 0; e < 8; e++) {
-                    const float2 q = cs[r.i + e];
+                    const float2 q = angle[e];
                     y[e] = x[e] * q.x - w[e] * q.y;
                     z[e] = w[e] * q.x + x[e] * q.y;
                 }
             } else if (r.kind == kInterleaved) {
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
-                    const float2 q = cs[r.i + e / 2];
+                    const float2 q = angle[e / 2];
                     y[e] = x[e] * q.x - x[e + 1] * q.y;
                     y[e + 1] = x[e + 1] * q.x + x[e] * q.y;
                 }
             } else {
-                if (!r.cached || CT != kE5M2) {   // unchanged bits
-                    *reinterpret_cast<u32x4 *>(r.dst + r.d * 2) = a[i];
+                if (!r.to || CT != kE5M2) {       // unchanged bits
+                    *reinterpret_cast<u32x4 *>(dst + r.d * 2) = a[i];
                     continue;
                 }
 #pragma unroll
                 for (int e = 0; e < 8; e++) y[e] = x[e];
             }
-            if (r.cached) {
-                store8<CT>(r.dst + r.d * ces, y);
-                if (r.kind == kPair) store8<CT>(r.dst + (r.d + p.rot / 2) * ces, z);
+            if (r.to) {
+                store8<CT>(dst + r.d * ces, y);
+                if (r.kind == kPair) store8<CT>(dst + (r.d + half) * ces, z);
             } else {
-                store8<F16 ? kF16 : kBF16>(r.dst + r.d * 2, y);
-                if (r.kind == kPair) store8<F16 ? kF16 : kBF16>(r.dst + (r.d + p.rot / 2) * 2, z);
+                store8<F16 ? kF16 : kBF16>(dst + r.d * 2, y);
+                if (r.kind == kPair) store8<F16 ? kF16 : kBF16>(dst + (r.d + half) * 2, z);
             }
         }
         base += kRopeUnits * kRopeThreads;
@@ -256,12 +274,18 @@ int launch_rope(RopeParams &p, const uzip_kv_rope_t *r, uint32_t seqs, bool f16,
     p.per_copy = p.D / 8;
     p.per_q = lanes || p.interleaved ? p.D / 8 : p.rot / 16 + (p.D - p.rot) / 8;
     p.units = (p.Hq + p.H) * p.per_q + p.H * p.per_copy;
-    // A token's units in one workgroup, so that its angles are worked out
-    // once; with few tokens over several, whole heads each.
-    const int64_t tokens = (int64_t)seqs * p.T;
+    // A workgroup's units are a round of loads or two of its threads: of
+    // several tokens, as their angles and places fit; of a part of one (whole
+    // heads) when there are few tokens.
+    p.count = (int64_t)seqs * p.T;
+    int64_t tokens = kRopeUnits * kRopeThreads / p.units;
+    if (p.rot && tokens > kRopeAngles / (p.rot / 2)) tokens = kRopeAngles / (p.rot / 2);
+    if (tokens > kRopeTokens) tokens = kRopeTokens;
+    if (tokens > p.count / (4 * kCUs)) tokens = p.count / (4 * kCUs);
+    p.tokens = (int)(tokens < 1 ? 1 : tokens);
     int64_t parts = 1;
-    if (tokens < 4 * kCUs) {
-        parts = 4 * kCUs / tokens;
+    if (p.count < 4 * kCUs) {
+        parts = 4 * kCUs / p.count;
         const int64_t most = (p.units + kRopeThreads - 1) / kRopeThreads;
         parts = parts > most ? most : parts;
     }
@@ -273,8 +297,10 @@ int launch_rope(RopeParams &p, const uzip_kv_rope_t *r, uint32_t seqs, bool f16,
         p.share = (int)((p.units + parts - 1) / parts);
     }
     p.parts = (p.units + p.share - 1) / p.share;
-    if (tokens * p.parts >= (1ll << 31)) return UZIP_EINVAL;
-    const dim3 grid((unsigned)(tokens * p.parts));
+    if (p.tokens > 1) p.parts = 1, p.share = p.units * p.tokens;
+    const int64_t blocks = (p.count + p.tokens - 1) / p.tokens * p.parts;
+    if (blocks >= (1ll << 31)) return UZIP_EINVAL;
+    const dim3 grid((unsigned)blocks);
 #define UZIP_KV_ROPE(F, C)                                                                    \
     do {                                                                                      \
         if (lanes) k_rope<F, C, true><<<grid, kRopeThreads, 0, s>>>(p);                       \

@@ -817,7 +817,7 @@ __device__ constexpr int mixed(int row)
 
 __device__ const u32x4 kZeros[1] = {};            // what dims behind the head's own are read from
 
-template <int CT, int DP, bool PAD>
+template <int CT, int DP, bool PAD, bool PAGED>
 __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams p)
 {
     constexpr int RB = 2;
@@ -840,7 +840,7 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
     // every row sees; in pages, up to the first that touches an absent one.
     const int key0 = at.t0 * kTileKeys, stages = (at.t1 - at.t0 + 1) / 2;
     int fast = min((at.t1 - at.t0) / 2, max(at.n - key0, 0) / 64);
-    if (p.c.table) {
+    if constexpr (PAGED) {
         const int lane = tid & 63;
         for (int i = 0; i < fast * 4; i += 64) {
             const bool bad = i + lane < fast * 4 && (uint32_t)p.c.table[at.b * p.c.ts + ((key0 + (i + lane) * 16) >> p.c.shift)] >= p.c.pages;
@@ -858,13 +858,13 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
         const bool val = lin0 >= 64 * PIECES;
         const int row = (lin / PIECES) & 63, piece = lin % PIECES ^ mixed<PIECES>(row);
         const int64_t step = val ? p.c.vs1 : p.c.ks1;
-        src[j] = (val ? p.c.v + at.h * p.c.vs2 : p.c.k + at.h * p.c.ks2) + piece * 16 + (p.c.table ? (row & 15) * step : at.b * (val ? p.c.vs0 : p.c.ks0) + (key0 + row) * step);
+        src[j] = (val ? p.c.v + at.h * p.c.vs2 : p.c.k + at.h * p.c.ks2) + piece * 16 + (PAGED ? (row & 15) * step : at.b * (val ? p.c.vs0 : p.c.ks0) + (key0 + row) * step);
         if (PAD) pad[j] = piece * 16 >= p.D * es;
     }
     int entry = 0;
     const auto issue = [&](int i) {
         char *to = smem + i % RING * STAGE + wave * 1024;
-        if (p.c.table && (i & 15) == 0) {         // page numbers of the next 64 half tiles, one a lane; -1 behind the last token
+        if (PAGED && (i & 15) == 0) {         // page numbers of the next 64 half tiles, one a lane; -1 behind the last token
             const int key = key0 + (i * 4 + (tid & 63)) * 16;
             entry = key < at.end ? p.c.table[at.b * p.c.ts + (key >> p.c.shift)] : -1;
             __builtin_amdgcn_s_waitcnt(0x0f70);
@@ -875,7 +875,7 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
             const bool val = lin0 >= 64 * PIECES;
             const int64_t step = val ? p.c.vs1 : p.c.ks1;
             const char *from = src[j];
-            if (p.c.table) {
+            if constexpr (PAGED) {
                 const int half = (lin0 / PIECES & 63) >> 4;
                 const uint32_t page = (uint32_t)__builtin_amdgcn_readlane(entry, (i & 15) * 4 + half);
                 const uint32_t in = (uint32_t)(key0 + i * 64 + half * 16) & ((1u << p.c.shift) - 1);
@@ -883,8 +883,7 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
                 if (page >= p.c.pages) from = reinterpret_cast<const char *>(kZeros);
             } else {
                 // behind the last token the last one again, which the mask leaves out
-                const int past = i < fast ? 0 : max(key0 + i * 64 + ((lin0 + (tid & 63)) / PIECES & 63) - (at.end - 1), 0);
-                from -= past * step;
+                if (i >= fast) from -= max(key0 + i * 64 + ((lin0 + (tid & 63)) / PIECES & 63) - (at.end - 1), 0) * step;
                 src[j] += 64 * step;
             }
             if (PAD && pad[j]) from = reinterpret_cast<const char *>(kZeros);
@@ -975,7 +974,7 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
 #pragma unroll
             for (int hf = 0; hf < 2; hf++) {
                 const int key = t.key + 16 * hf;
-                t.there[hf] = key < at.end && (!p.c.table || (uint32_t)p.c.table[at.b * p.c.ts + (key >> p.c.shift)] < p.c.pages);
+                t.there[hf] = key < at.end && (!PAGED || (uint32_t)p.c.table[at.b * p.c.ts + (key >> p.c.shift)] < p.c.pages);
             }
             u32x4 k[2][KS];
             typename W::Values v[W::VC][8];
@@ -1297,7 +1296,8 @@ int run(const AttendParams &p, const Plan &plan, int seqs, int half, hipStream_t
     int rc = UZIP_EINVAL;
     if (plan.shared) {
         if constexpr (DP <= 128) {
-            k_attend_shared<CT, DP, PAD><<<(unsigned)grid, kShared * 64, 0, s>>>(p);
+            if (p.c.table) k_attend_shared<CT, DP, PAD, true><<<(unsigned)grid, kShared * 64, 0, s>>>(p);
+            else k_attend_shared<CT, DP, PAD, false><<<(unsigned)grid, kShared * 64, 0, s>>>(p);
             UZIP_KV_LAUNCH_CHECK("k_attend_shared");
             rc = UZIP_OK;
         }

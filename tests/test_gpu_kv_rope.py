@@ -54,6 +54,29 @@ def test_rope_in_place_and_in_views(rot, interleaved):
     assert torch.equal(whole[..., :8].cpu(), x[..., :8]) and torch.equal(whole[..., 136:].cpu(), x[..., 136:])
 
 
+@pytest.mark.parametrize("H,D,rot,interleaved", [(1, 8, 8, False), (1, 64, 64, True), (2, 128, 96, False), (1, 256, 256, False), (3, 72, 20, True),
+                                                (5, 64, 20, False)])
+def test_many_tokens_of_few_heads(H, D, rot, interleaved):
+    """Several tokens a workgroup, the last one not full; and the same of an append."""
+    g = torch.Generator().manual_seed(H + rot)
+    B, T = 3, 3457
+    x = torch.randn(B, T, H, D, generator=g).to(BF16)
+    pos = positions(B, T, 4)
+    freq = kv.rope_freq(rot)
+    want = ref.turned(x, pos, freq, 1.0, interleaved)
+    got = kv.rope(x.to(DEV), pos.to(DEV), freq.to(DEV), interleaved=interleaved)
+    ref.within(got, want, ref.rope_bound(x, want, freq, 1.0, BF16))
+    kc, vc = (torch.zeros(B, T + 5, H, D, dtype=BF16, device=DEV) for _ in range(2))
+    n = torch.tensor([0, 5, 2], dtype=torch.int32)
+    drafted = torch.tensor([T, T, 1000], dtype=torch.int32)
+    q = kv.append(x.to(DEV), x.to(DEV), x.to(DEV), kc, vc, n.to(DEV), freq.to(DEV), pos=pos.to(DEV), drafted=drafted.to(DEV), interleaved=interleaved)
+    assert torch.equal(q, got)
+    for b in range(B):
+        m, k = int(drafted[b]), int(n[b])
+        assert torch.equal(kc[b, k:k + m], got[b, :m]) and torch.equal(vc[b, k:k + m].cpu(), x[b, :m])
+        assert not kc[b, :k].any() and not kc[b, k + m:].any() and not vc[b, k + m:].any()
+
+
 def test_gradient_of_rope_by_differences():
     """The inverse with the same amplitude is the transposed map: <w, R x> = <R^-1 w, x>, and R x changes along d by R d."""
     g = torch.Generator().manual_seed(0)
