@@ -728,7 +728,7 @@ struct Rows {
 // on every wk-th tile; keys one tile ahead in registers, values loaded while
 // the scores are worked out.
 template <int CT, int DP, int RB, bool PAD>
-__global__ __launch_bounds__(kWaves * 64, (RB == 4 && DP > 64) || DP == 256 ? 1 : 2) void k_attend(AttendParams p)
+__global__ __launch_bounds__(kWaves * 64, DP == 256 ? 1 : 2) void k_attend(AttendParams p)
 {
     using W = Rows<CT, DP, RB, PAD>;
     constexpr int KS = W::KS;
@@ -933,6 +933,7 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
     // One tile's weights and output beside the next tile's scores: a wave's
     // exponentials run while its own products do (64 rows over 16384 keys: 379
     // against 395 us without).
+    const bool rows = w.row0 < p.R;               // else this wave only loads
     if (fast > 0) {
         f32x4 s[RB][2];
         const auto step = [&](const char *stage, int tile, const char *next_stage, int next_tile) {
@@ -951,16 +952,18 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
             w.raise(s);
         };
         enter(0);
-        u32x4 k[2][KS];
-        keys_of(smem, p.wk == 1 ? 0 : wkey, k);
-        w.score(k, s);
-        w.raise(s);
+        if (rows) {
+            u32x4 k[2][KS];
+            keys_of(smem, p.wk == 1 ? 0 : wkey, k);
+            w.score(k, s);
+            w.raise(s);
+        }
         for (int i = 0; i < fast; i++) {
             const char *stage = smem + i % RING * STAGE, *next = i + 1 < fast ? smem + (i + 1) % RING * STAGE : stage;
             // after the last tile its own scores again, which change nothing
-            if (p.wk == 1) step(stage, 0, stage, 1);
+            if (p.wk == 1 && rows) step(stage, 0, stage, 1);
             if (i + 1 < fast) enter(i + 1);
-            step(stage, p.wk == 1 ? 1 : wkey, next, p.wk == 1 ? 0 : wkey);
+            if (rows) step(stage, p.wk == 1 ? 1 : wkey, next, p.wk == 1 ? 0 : wkey);
         }
     }
     for (int i = fast; i < stages; i++) {
@@ -970,7 +973,7 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
             Tile t;
             t.key = key0 + i * 64 + tile * kTileKeys;
             t.fast = false;
-            if (w.row0 >= p.R || t.key >= w.lim) break;
+            if (!rows || t.key >= w.lim) break;
 #pragma unroll
             for (int hf = 0; hf < 2; hf++) {
                 const int key = t.key + 16 * hf;
@@ -1238,8 +1241,8 @@ Plan make_plan(uint32_t seqs, uint32_t kv_heads, uint32_t dim, uint32_t cache_to
     const uint32_t G = heads / kv_heads;
     const uint64_t R = (uint64_t)T * G;
     a.DP = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
-    a.shared = may_share && R > 64 && a.DP <= 128;
-    a.RB = a.shared ? 2 : R <= 16 ? 1 : R <= 32 || a.DP == 256 ? 2 : 4;
+    a.shared = may_share && R > 32 && a.DP <= 128;
+    a.RB = !a.shared && R <= 16 ? 1 : 2;
     const int waves = a.shared ? kShared : kWaves;
     const uint64_t blocks = (R + a.RB * 16 - 1) / (a.RB * 16);
     const int wr = a.shared ? (R > 128 ? 8 : 4) : blocks >= 4 ? 4 : blocks >= 2 ? 2 : 1;
@@ -1250,7 +1253,7 @@ Plan make_plan(uint32_t seqs, uint32_t kv_heads, uint32_t dim, uint32_t cache_to
     // Workgroups: one a CU where they are large, else a few, so that one's
     // loads run beside another's join. With four times as many sequences as
     // that leaves for each head, every one goes to a workgroup of its own.
-    const uint64_t want = a.shared ? kCUs : a.RB == 1 ? 8 * kCUs : a.RB == 2 ? 4 * kCUs : 2 * kCUs, each = (uint64_t)kv_heads * a.nrg;
+    const uint64_t want = a.shared ? kCUs : a.RB == 1 ? 8 * kCUs : 4 * kCUs, each = (uint64_t)kv_heads * a.nrg;
     const uint64_t slots = want > each ? want / each : 1;
     const uint64_t steps = (((uint64_t)cache_tokens + kTileKeys - 1) / kTileKeys + a.unit - 1) / a.unit, most = (steps + a.min_steps - 1) / a.min_steps;
     a.slots = (int)slots;
@@ -1302,8 +1305,7 @@ int run(const AttendParams &p, const Plan &plan, int seqs, int half, hipStream_t
             rc = UZIP_OK;
         }
     } else if (plan.RB == 1) rc = launch<CT, DP, 1, PAD>(p, grid, s);
-    else if (plan.RB == 2) rc = launch<CT, DP, 2, PAD>(p, grid, s);
-    else if constexpr (DP <= 128) rc = launch<CT, DP, 4, PAD>(p, grid, s);
+    else rc = launch<CT, DP, 2, PAD>(p, grid, s);
     if (rc) return rc;
     if (p.nsplit > 1) {
         if (p.nsplit <= 16 || (p.flat && p.nsplit <= 64)) k_attend_join_few<DP><<<(unsigned)((plan.rows + 15) / 16), 256, 0, s>>>(p, (int64_t)plan.rows, half);
