@@ -319,7 +319,7 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, length
     there is not added. lse (float32 [sequences, tokens, heads], contiguous) receives the log
     of each query's sum of exponentials. A query that sees nothing gives zeros
     and -inf, as do those from drafted on. Masked keys and values have no
-    effect, whatever they hold."""
+    effect, whatever they hold. out does not overlap the inputs."""
     _types(q, k_cache)
     qs = _strides(q)
     B, T, hq, D = q.shape
@@ -396,7 +396,7 @@ def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, score: torch.Tensor, len
                     raise ValueError(f"k_out, v_out: expected {k_cache.dtype} [{B}, {keep}, {heads}, {dim}] on {dev}")
                 _written(t, "k_out or v_out")
             made.append(t)
-        kept, index = torch.empty((B, heads, keep), device=dev), torch.empty((B, heads, keep), dtype=torch.int32, device=dev)
+        kept, index = torch.empty((B, heads, keep), dtype=torch.float32, device=dev), torch.empty((B, heads, keep), dtype=torch.int32, device=dev)
         left = torch.empty(B, dtype=torch.int32, device=dev)
         if ws is None:
             need = evict_workspace_bytes(B, heads, seen)

@@ -108,6 +108,36 @@ def test_lengths_outside_the_cache_and_absent_pages():
     assert (gk[0, :4] == 1).all() and not gk[0, 4:].any() and not gv[0, 4:].any()
 
 
+def test_scores_are_float32_whatever_the_default_type():
+    default = torch.get_default_dtype()
+    try:
+        for t in (BF16, torch.float64):
+            torch.set_default_dtype(t)
+            k = torch.ones(1, 40, 2, 64, dtype=BF16, device=DEV)
+            score = torch.rand(1, 2, 40, dtype=torch.float32).to(DEV)
+            kept = kv.evict(k, k, score, torch.tensor([40], dtype=torch.int32, device=DEV), 40)[2]
+            assert kept.dtype == torch.float32 and torch.equal(kept, score)
+    finally:
+        torch.set_default_dtype(default)
+
+
+def test_two_long_cuts_at_once():
+    """On two streams, each with a workspace of its own."""
+    B, H, S, keep = 2, 2, 60000, 9000
+    g = torch.Generator().manual_seed(5)
+    k = torch.randn(B, S, H, 16, generator=g).to(BF16).to(DEV)
+    score = [scores(kind, B, H, S, 6).to(DEV) for kind in ("plain", "ties")]
+    n = torch.tensor([S, 50001], dtype=torch.int32, device=DEV)
+    want = [kv.evict(k, k, x, n, keep, sink=2, recent=40) for x in score]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[kv.evict(k, k, x, n, keep, sink=2, recent=40, stream=s) for x, s in zip(score, streams)] for _ in range(4)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for a, b in zip(pair, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
 def test_same_choice_every_time_and_in_a_graph():
     B, H, S, D, keep = 2, 4, 9000, 64, 1000
     g = torch.Generator().manual_seed(0)
