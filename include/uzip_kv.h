@@ -136,7 +136,7 @@ int uzip_kv_append(const uzip_kv_cache_t *cache, const uzip_kv_append_args_t *a,
  * cache's capacity. Products are exact in binary32 sums; weights are rounded
  * to BF16 (BF16 caches) or F16 before the product with the values. lse and
  * score may be NULL. scale is in [2^-60, 2^60]. The result depends on
- * nothing but the inputs: no atomics. */
+ * nothing but the inputs: no atomics. Outputs overlap no input. */
 typedef struct uzip_kv_attend_args {
     uzip_kv_tensor_t q, out;
     float           *lse;       /* [seqs, tokens, heads], contiguous; 4-byte aligned */

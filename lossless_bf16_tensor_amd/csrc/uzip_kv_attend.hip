@@ -1349,6 +1349,7 @@ int uzip_kv_attend(const uzip_kv_cache_t *cache, const uzip_kv_attend_args_t *a,
     if (!a || !valid_cache(cache) || !valid_tensor(a->q) || !valid_tensor(a->out)) return UZIP_EINVAL;
     if (!valid_shapes(cache->seqs, cache->heads, cache->dim, cache->tokens, a->tokens, a->heads)) return UZIP_EINVAL;
     if (a->dtype > UZIP_KV_F16 || (cache->dtype != UZIP_KV_E5M2 && cache->dtype != a->dtype)) return UZIP_EINVAL;
+    if (a->q.data == a->out.data) return UZIP_EINVAL;          // the accumulated weights read q again
     if (!a->length || !aligned(a->length, 4) || !aligned(a->drafted, 4) || !aligned(a->lse, 4) || !aligned(a->score, 4)) return UZIP_EINVAL;
     if (!(a->scale >= 0x1p-60f) || !(a->scale <= 0x1p60f)) return UZIP_EINVAL;
     if (a->reserved || (a->score && (a->score_stride[0] < 0 || a->score_stride[1] < 0 || a->score_tokens > cache->tokens))) return UZIP_EINVAL;

@@ -268,3 +268,119 @@ def test_on_streams_and_in_a_graph():
         torch.cuda.synchronize()
         w = torch.zeros_like(score)
         assert torch.equal(out, kv.attend(dq, dk, dv, n, score=w)) and torch.equal(score, w)
+
+
+@pytest.mark.parametrize("layout,D,cache", [("paged16", 128, BF16), ("paged32", 64, E5M2), ("paged128", 72, F16), ("paged16", 72, E5M2),
+                                            ("hsd", 128, E5M2), ("hsd", 40, E5M2), ("shd", 96, BF16)])
+@pytest.mark.parametrize("T,hq,H", [(9, 8, 2), (20, 8, 2), (37, 4, 1), (70, 4, 1)])
+def test_many_rows_over_ragged_caches(layout, D, cache, T, hq, H):
+    """Rows that share keys: ends inside tiles and pages, absent pages, sequences of nothing between others."""
+    S = 900
+    q, k, v, table = make(5, T, hq, H, D, S, F16 if cache == F16 else BF16, cache, layout, seed=T + D)
+    if table is not None:
+        page = k.shape[1]
+        table[0, 160 // page] = -1
+        table[0, 700 // page] = 1 << 28
+        table[4, :3] = k.shape[0]
+    tree = tree_of(T, 4, 5)
+    tree[:, 3] = False
+    lens = dict(length=[S - T, 0, 33, 511, 640], drafted=[T, 0, T, T - 1, 1], table=table, layout=layout)
+    check(q, k, v, **lens)
+    check(q, k, v, tree=tree, **lens)
+
+
+@pytest.mark.parametrize("B,layout", [(3, "shd"), (64, "shd"), (65, "paged16"), (200, "shd"), (1100, "paged32")])
+def test_many_sequences_of_many_rows(B, layout):
+    """Lengths of every size side by side, those of nothing too; some of the sequences compared."""
+    T, hq, H, D, S = 5, 8, 1, 64, 400
+    q, k, v, table = make(B, T, hq, H, D, S, layout=layout, seed=B)
+    g = torch.Generator().manual_seed(B)
+    length = torch.randint(0, S - T, (B,), generator=g).to(torch.int32)
+    length[::7] = 0
+    length[1::9] = 3
+    drafted = torch.randint(0, T + 1, (B,), generator=g).to(torch.int32)
+    drafted[B // 2] = T
+    w, lse = torch.zeros(B, H, k.shape[1] if table is None else table.shape[1] * k.shape[1], device=DEV), torch.empty(B, T, hq, device=DEV)
+    out = kv.attend(put(q), put(k), put(v), length.to(DEV), table=put(table), drafted=drafted.to(DEV), score=w, lse=lse)
+    at = sorted({0, 1, 2, B // 2, B - 1, 63 % B, 64 % B})
+    want = ref.attend(q[at], *((k[at], v[at]) if table is None else (k, v)), length[at], table=None if table is None else table[at], drafted=drafted[at])
+    for name, got in (("out", out), ("lse", lse), ("weight", w)):
+        ref.within(got[at], want[name], want[name + "_bound"], name)
+    # the others: each alone, whose splits differ; and the weights' sum
+    total = (drafted * hq).double()
+    assert ((w.double().sum((1, 2)).cpu() - total).abs() <= total * 2.0 ** -10).all()
+    for b in range(0, B, max(1, B // 8)):
+        alone = kv.attend(put(q[b:b + 1]), *((put(k[b:b + 1]), put(v[b:b + 1])) if table is None else (put(k), put(v))), length[b:b + 1].to(DEV),
+                          table=None if table is None else put(table[b:b + 1]), drafted=drafted[b:b + 1].to(DEV))
+        one = ref.attend(q[b:b + 1], *((k[b:b + 1], v[b:b + 1]) if table is None else (k, v)), length[b:b + 1],
+                         table=None if table is None else table[b:b + 1], drafted=drafted[b:b + 1])
+        ref.within(alone, one["out"], one["out_bound"], "alone")
+        ref.within(out[b:b + 1], one["out"], one["out_bound"], "out")
+
+
+@pytest.mark.parametrize("T,hq,H,D,n", [(6, 4, 2, 128, 3001), (40, 4, 1, 64, 3001), (40, 4, 1, 128, 2990), (24, 8, 1, 256, 1001)])
+@pytest.mark.parametrize("cache", [BF16, E5M2])
+def test_masked_values_in_split_rows(T, hq, H, D, n, cache):
+    """Infinities that some queries see, in both signs, where the key axis is cut."""
+    q, k, v, _ = make(1, T, hq, H, D, n + T, BF16, cache, seed=T + D)
+    tree = torch.eye(T, dtype=torch.bool)
+    tree[2, 3] = True
+    for j, d, value in ((2, 0, math.inf), (3, 0, -math.inf), (3, 7, -math.inf), (4, 9, math.nan), (T - 1, 11, math.inf)):
+        bits(v)[:, n + j, :, d] = bits(torch.full((1,), value).to(cache))
+    out, _, _ = check(q, k, v, [n], tree=tree)
+    assert torch.isnan(out[0, 2, :, 0]).all() and (out[0, 2, :, 7] == -math.inf).all() and (out[0, 3, :, 0] == -math.inf).all()
+    assert torch.isnan(out[0, 4, :, 9]).all() and torch.isfinite(out[0, 5:T - 1]).all()
+
+
+@pytest.mark.parametrize("D,cache", [(64, F16), (256, BF16), (200, E5M2)])
+def test_weights_of_many_rows(D, cache):
+    """More rows than the weights' kernel holds at once."""
+    q, k, v, _ = make(2, 75, 8, 2, D, 330, F16 if cache == F16 else BF16, cache, seed=D)
+    check(q, k, v, [255, 0], drafted=[75, 70])
+
+
+def test_a_long_chain():
+    q, k, v, _ = make(1, 300, 2, 1, 128, 520, seed=1)
+    check(q, k, v, [211])
+
+
+def test_many_rows_over_a_long_cache():
+    """One sequence on every workgroup: more parts than a few lanes join."""
+    q, k, v, _ = make(1, 10, 4, 1, 64, 33000, seed=2)
+    check(q, k, v, [32985])
+
+
+def test_two_graphs_at_once():
+    """Each with a workspace and outputs of its own, replayed side by side."""
+    T, S = 24, 2500
+    q, k, v, _ = make(2, T, 8, 2, 128, S, seed=12)
+    dq, dk, dv = put(q), put(k), put(v)
+    lens = [torch.tensor(x, dtype=torch.int32, device=DEV) for x in ([2400, 100], [64, 2300])]
+    tree = put(tree_of(T, 3))
+    want = []
+    for n in lens:
+        w = torch.zeros(2, 2, S, device=DEV)
+        want.append((kv.attend(dq, dk, dv, n, tree=tree, score=w), w))
+    graphs, got = [], []
+    for n in lens:
+        w = torch.zeros(2, 2, S, device=DEV)
+        ws = torch.empty(kv.attend_workspace_bytes(2, 2, 128, S, T, 8), dtype=torch.uint8, device=DEV)
+        out = torch.empty_like(dq)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            kv.attend(dq, dk, dv, n, tree=tree, score=w, out=out, ws=ws)
+        graphs.append(g)
+        got.append((out, w))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(4):
+        for out, w in got:
+            out.fill_(5.0)
+            w.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))

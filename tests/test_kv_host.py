@@ -48,7 +48,7 @@ BAD_CACHES = [dict(k=0), dict(v=0), dict(k=(1 << 20) + 8), dict(ks=(0, 512, 100)
 
 def attend(c=None, q=None, out=None, lse=0, score=0, ss=(256, 64), length=1 << 24, drafted=0, tree=0, ts=(0, 4), dtype=0, T=4,
            heads=8, scale=0.1, seen=64, reserved=0, ws=1 << 25, ws_bytes=1 << 40):
-    args = kv._ATTEND.pack(*struct.unpack("=Q3q", q or tensor()), *struct.unpack("=Q3q", out or tensor()), lse, score, *ss, length,
+    args = kv._ATTEND.pack(*struct.unpack("=Q3q", q or tensor()), *struct.unpack("=Q3q", out or tensor(1 << 21)), lse, score, *ss, length,
                            drafted, tree, *ts, dtype, T, heads, scale, seen, reserved)
     return kv.lib().uzip_kv_attend(c or cache(), args, ws, ws_bytes, None)
 
@@ -66,7 +66,7 @@ def test_bad_caches_are_refused(bad):
     dict(length=0), dict(length=2), dict(drafted=2), dict(lse=1), dict(score=3), dict(score=1 << 20, ss=(-1, 64)),
     dict(tree=1 << 20, ts=(-4, 4)), dict(dtype=1), dict(dtype=2), dict(T=0), dict(T=(1 << 20) + 1), dict(heads=0), dict(heads=6),
     dict(heads=3), dict(scale=0.0), dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan), dict(scale=2.0 ** -61), dict(ws=0), dict(ws=8),
-    dict(score=1 << 20, seen=65), dict(reserved=1)])
+    dict(score=1 << 20, seen=65), dict(reserved=1), dict(q=tensor(1 << 22), out=tensor(1 << 22))])
 def test_attend_refuses(bad):
     assert attend(**bad) == EINVAL
 
