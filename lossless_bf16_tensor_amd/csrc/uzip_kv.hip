@@ -95,9 +95,9 @@ __device__ inline Unit unit_at(const RopeParams &p, int u, int64_t first)
 }
 
 // Rotates queries and keys and writes keys and values into the cache, one
-// launch. A workgroup takes some tokens, as many as give its threads work (24
-// tokens of one head each took 71 us where they now take 11), or a part of one
-// when there are few: the angles of a token's rot / 2 pairs are worked out
+// launch. A workgroup takes some tokens, as many as give its threads work (8 x
+// 3068 tokens of one head of 128: 11 us, with one token a workgroup 60), or a
+// part of one when there are few: the angles of a token's rot / 2 pairs are worked out
 // once, in binary64 up to the fraction of a turn (a binary32 angle is wrong by
 // 2^-24 of itself: 0.06 rad at position 2^20), and serve all its heads. Bound
 // by memory: every element is read and written once, in 16-byte pieces; the
@@ -325,11 +325,13 @@ bool same_tensor(const uzip_kv_tensor_t &a, const uzip_kv_tensor_t &b)
 // need-th largest of the others and all above it. Scores become unsigned ranks
 // in the same order; the need-th largest rank is found by histograms of its
 // upper 11 bits, the next 11 and the last 10, each of the ranks that agree with
-// the bits found so far. Histograms in LDS are held in 8 copies, one for every
-// eighth lane: attention weights crowd into few bins, and lanes that add to
-// the same word wait for each other.
+// the bits found so far. Histograms in LDS are held in 4 copies, one for every
+// fourth lane: attention weights crowd into few bins, and lanes that add to the
+// same word wait for each other; clearing and adding up more copies costs short
+// rows more than it saves (16 rows of 4096: 12 us, with 8 copies 13; 128 equal
+// rows of 16384 104 and 101).
 constexpr int kSelThreads = 1024, kSelWaves = kSelThreads / 64;
-constexpr int kBins = 2048, kCopies = 8;
+constexpr int kBins = 2048, kCopies = 4;
 constexpr int kOneTokens = 32 * kSelThreads;      // rows up to here are held in one workgroup's registers
 constexpr int kSlice = 8 * kSelThreads;           // tokens a workgroup takes of a longer row
 constexpr uint32_t kForced = 0xffffffffu, kOutside = 0;      // ranks of no score
@@ -446,10 +448,13 @@ __device__ inline void copy_rows(const EvictParams &p, int b, int h, int j0, int
     }
 }
 
-// Rows of up to N * 1024 tokens, held in a workgroup's registers. COPY (short
-// rows): each of a row's workgroups finds the kept tokens for itself and copies
-// its share of them; a second launch would cost more than choosing again.
-// Without, one workgroup a row writes the index, and k_evict_copy copies.
+// Rows of up to N * 1024 tokens, held in a workgroup's registers. COPY (rows
+// and cuts up to 4096): each of a row's workgroups finds the kept tokens for
+// itself and copies its share of them; a second launch would cost more than
+// choosing again (8 rows of 4096, 1024 of 128 16-bit elements kept: 11 us, in
+// two launches 17; 256 rows 45 and 55). Without, one workgroup a row writes the
+// index, and k_evict_copy copies. Choosing is bound by the steps of its three
+// levels, 23 us for 128 rows of 16384, where the copy of 4096 of each takes 78.
 template <int N, bool COPY, typename RawT>
 __global__ __launch_bounds__(kSelThreads) void k_evict_one(EvictParams p)
 {
@@ -548,7 +553,11 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_one(EvictParams p)
 
 // Longer rows, by slices: a launch a level, each of whose workgroups adds up
 // the slices' histograms of the level before, and one that writes the kept
-// tokens. Nothing needs clearing and no sum depends on an order.
+// tokens. Nothing needs clearing and no sum depends on an order. Bound by the
+// launches, which wait for each other: 16 rows of 120000 take 39 us to choose,
+// and 22 for the copy of 12345 of each. Rows up to 32768 stay in registers: 128
+// of them 122 us with their copy, by slices 128; only with few rows is it the
+// other way (16 rows: 43 and 40).
 struct Slice {
     int row, slice, b, h, n, i0;
     const float *score;
@@ -740,8 +749,9 @@ int launch_evict(EvictParams &p, uint64_t rows, hipStream_t s)
 {
     p.parts = 1, p.share = p.keep;
     if (p.c.tokens <= 4 * kSelThreads && p.keep <= 4 * kSelThreads) {
-        // workgroups a row: two a CU, as long as each has some slots to copy
-        const uint64_t most = ((uint64_t)p.keep + 63) / 64, parts = 2 * kCUs / rows;
+        // workgroups a row: one a CU, as long as each has some slots to copy
+        // (32 rows of 4096: 14 us, with two a CU 25)
+        const uint64_t most = ((uint64_t)p.keep + 63) / 64, parts = kCUs / rows;
         p.parts = (int)(parts < 1 ? 1 : parts > most ? most : parts);
         p.share = (p.keep + p.parts - 1) / p.parts;
         k_evict_one<4, true, RawT><<<(unsigned)(rows * p.parts), kSelThreads, 0, s>>>(p);
