@@ -7,9 +7,14 @@
 // output o = sum p v, all in binary32, in one pass over its keys:
 //   m' = max(m, max s),  l = l 2^(c (m - m')) + sum p,  o likewise.
 // Pieces of the key axis are joined by the same rule: first the waves of a
-// workgroup in LDS, then (k_attend_join) the workgroups of a row.
+// workgroup in LDS, then (k_attend_join_few, _many) the workgroups of a row.
 //
-// Nothing goes through LDS on the way to the matrix cores. With
+// Up to 32 rows the cache's bytes are the bound, and k_attend takes them from
+// memory into registers: nothing goes through LDS on the way to the matrix
+// cores. With more rows the products are, and k_attend_shared lets eight waves
+// read the keys and values that one workgroup loads.
+//
+// In both nothing but keys and values moves between lanes. With
 // v_mfma_f32_16x16x32 the wave computes S^T = K Q^T (16 keys x 16 rows): lane
 // (x = lane % 16, g = lane / 16) needs for key x the 8 dims 32 ks + 8 g ..
 // + 7, one 16-byte load, and gets for row x the keys 4 g .. 4 g + 3. Then
@@ -726,7 +731,12 @@ struct Rows {
 
 // Few rows: bound by the cache's bytes. Waves work alone until they join, each
 // on every wk-th tile; keys one tile ahead in registers, values loaded while
-// the scores are worked out.
+// the scores are worked out. One wave a SIMD at the larger head dims, two at
+// the others, keep 32 KB a CU on their way and more. A chain of 4 tokens of 64
+// heads over 2 x 131072 FP8 tokens of 8 heads of 128, 537 MB: 109 us, 4.9 TB/s
+// (a copy of 1 GiB: 5.2); one token of 32 heads over 32 ragged sequences in
+// pages: 101 us, 4.6 TB/s; one over 2048 tokens: 9.2 us, mostly the start of a
+// launch and a first trip to memory.
 template <int CT, int DP, int RB, bool PAD>
 __global__ __launch_bounds__(kWaves * 64, DP == 256 ? 1 : 2) void k_attend(AttendParams p)
 {
@@ -832,167 +842,167 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
     Walk walk(p);
     Place at;
     while (walk.next(p, at)) {
-    int tid = (int)threadIdx.x;
-    asm volatile("" : "+v"(tid));
-    __syncthreads();                              // the ring is free
+        int tid = (int)threadIdx.x;
+        asm volatile("" : "+v"(tid));
+        __syncthreads();                              // the ring is free
 
-    // Stages of 64 keys, the first `fast` of them all cached tokens, which
-    // every row sees; in pages, up to the first that touches an absent one.
-    const int key0 = at.t0 * kTileKeys, stages = (at.t1 - at.t0 + 1) / 2;
-    int fast = min((at.t1 - at.t0) / 2, max(at.n - key0, 0) / 64);
-    if constexpr (PAGED) {
-        const int lane = tid & 63;
-        for (int i = 0; i < fast * 4; i += 64) {
-            const bool bad = i + lane < fast * 4 && (uint32_t)p.c.table[at.b * p.c.ts + ((key0 + (i + lane) * 16) >> p.c.shift)] >= p.c.pages;
-            const uint64_t any = __builtin_amdgcn_ballot_w64(bad);
-            if (any) fast = (i + __builtin_ctzll(any)) / 4;
+        // Stages of 64 keys, the first `fast` of them all cached tokens, which
+        // every row sees; in pages, up to the first that touches an absent one.
+        const int key0 = at.t0 * kTileKeys, stages = (at.t1 - at.t0 + 1) / 2;
+        int fast = min((at.t1 - at.t0) / 2, max(at.n - key0, 0) / 64);
+        if constexpr (PAGED) {
+            const int lane = tid & 63;
+            for (int i = 0; i < fast * 4; i += 64) {
+                const bool bad = i + lane < fast * 4 && (uint32_t)p.c.table[at.b * p.c.ts + ((key0 + (i + lane) * 16) >> p.c.shift)] >= p.c.pages;
+                const uint64_t any = __builtin_amdgcn_ballot_w64(bad);
+                if (any) fast = (i + __builtin_ctzll(any)) / 4;
+            }
         }
-    }
-    // A thread's place `lin` of load j: the keys' 64 rows, then the values'. A
-    // wave's 64 places lie in one half tile, so that a page is looked up once.
-    const char *src[LOADS];
-    bool pad[LOADS];
-#pragma unroll
-    for (int j = 0; j < LOADS; j++) {
-        const int lin0 = j * kShared * 64 + wave * 64, lin = lin0 + (tid & 63);
-        const bool val = lin0 >= 64 * PIECES;
-        const int row = (lin / PIECES) & 63, piece = lin % PIECES ^ mixed<PIECES>(row);
-        const int64_t step = val ? p.c.vs1 : p.c.ks1;
-        src[j] = (val ? p.c.v + at.h * p.c.vs2 : p.c.k + at.h * p.c.ks2) + piece * 16 + (PAGED ? (row & 15) * step : at.b * (val ? p.c.vs0 : p.c.ks0) + (key0 + row) * step);
-        if (PAD) pad[j] = piece * 16 >= p.D * es;
-    }
-    int entry = 0;
-    const auto issue = [&](int i) {
-        char *to = smem + i % RING * STAGE + wave * 1024;
-        if (PAGED && (i & 15) == 0) {         // page numbers of the next 64 half tiles, one a lane; -1 behind the last token
-            const int key = key0 + (i * 4 + (tid & 63)) * 16;
-            entry = key < at.end ? p.c.table[at.b * p.c.ts + (key >> p.c.shift)] : -1;
-            __builtin_amdgcn_s_waitcnt(0x0f70);
-        }
-#pragma unroll
+        // A thread's place `lin` of load j: the keys' 64 rows, then the values'. A
+        // wave's 64 places lie in one half tile, so that a page is looked up once.
+        const char *src[LOADS];
+        bool pad[LOADS];
+    #pragma unroll
         for (int j = 0; j < LOADS; j++) {
-            const int lin0 = j * kShared * 64 + wave * 64;
+            const int lin0 = j * kShared * 64 + wave * 64, lin = lin0 + (tid & 63);
             const bool val = lin0 >= 64 * PIECES;
+            const int row = (lin / PIECES) & 63, piece = lin % PIECES ^ mixed<PIECES>(row);
             const int64_t step = val ? p.c.vs1 : p.c.ks1;
-            const char *from = src[j];
-            if constexpr (PAGED) {
-                const int half = (lin0 / PIECES & 63) >> 4;
-                const uint32_t page = (uint32_t)__builtin_amdgcn_readlane(entry, (i & 15) * 4 + half);
-                const uint32_t in = (uint32_t)(key0 + i * 64 + half * 16) & ((1u << p.c.shift) - 1);
-                from += (int64_t)page * (val ? p.c.vs0 : p.c.ks0) + (int64_t)in * step;
-                if (page >= p.c.pages) from = reinterpret_cast<const char *>(kZeros);
-            } else {
-                // behind the last token the last one again, which the mask leaves out
-                if (i >= fast) from -= max(key0 + i * 64 + ((lin0 + (tid & 63)) / PIECES & 63) - (at.end - 1), 0) * step;
-                src[j] += 64 * step;
-            }
-            if (PAD && pad[j]) from = reinterpret_cast<const char *>(kZeros);
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
-                                             (__attribute__((address_space(3))) void *)(to + j * kShared * 1024), 16, 0, 0);
+            src[j] = (val ? p.c.v + at.h * p.c.vs2 : p.c.k + at.h * p.c.ks2) + piece * 16 + (PAGED ? (row & 15) * step : at.b * (val ? p.c.vs0 : p.c.ks0) + (key0 + row) * step);
+            if (PAD) pad[j] = piece * 16 >= p.D * es;
         }
-    };
-    // The queries are waited for here: a wait for them inside the loop would be
-    // one for every stage under way. The first stages arrive meanwhile.
-    int issued = 0;
-    while (issued < RING - 2 && issued < stages) issue(issued++);
-    W w;
-    w.init(p, at.b, at.h, (at.rg * (kShared / p.wk) + wrow) * RB * 16, at.n, at.end);
-    __builtin_amdgcn_s_waitcnt(0x0f70);
-    const auto keys_of = [&](const char *stage, int tile, u32x4 (&k)[2][KS]) {
-        const char *kb = stage + (tile * 32 + w.x) * ROW;
-#pragma unroll
-        for (int hf = 0; hf < 2; hf++)
-#pragma unroll
-            for (int ks = 0; ks < KS; ks++) {
-                const int o = (ks * 32 + w.g * 8) * es;
-                k[hf][ks] = widen<CT>(*reinterpret_cast<const Raw<CT> *>(kb + hf * 16 * ROW + ((((o >> 4) ^ mixed<PIECES>(w.x)) << 4) | (o & 15))));
+        int entry = 0;
+        const auto issue = [&](int i) {
+            char *to = smem + i % RING * STAGE + wave * 1024;
+            if (PAGED && (i & 15) == 0) {         // page numbers of the next 64 half tiles, one a lane; -1 behind the last token
+                const int key = key0 + (i * 4 + (tid & 63)) * 16;
+                entry = key < at.end ? p.c.table[at.b * p.c.ts + (key >> p.c.shift)] : -1;
+                __builtin_amdgcn_s_waitcnt(0x0f70);
             }
-    };
-    const auto values_of = [&](const char *stage, int tile, typename W::Values (&v)[W::VC][8]) {
-        const char *vb = stage + (64 + tile * 32 + w.g * 4) * ROW;
-#pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const int o = w.x * W::VE * es, mix = mixed<PIECES>(w.g * 4 + (j & 3));
-            v[0][j] = *reinterpret_cast<const typename W::Values *>(vb + ((j >> 2) * 16 + (j & 3)) * ROW + ((((o >> 4) ^ mix) << 4) | (o & 15)));
-        }
-    };
-
-    // Makes stage i readable and starts the load of a later one. This wave's
-    // loads of it are done when no more than the later stages' are outstanding
-    // (they end in order); other loads in between make the wait longer, never
-    // shorter. Behind the barrier all waves' are, and all are past the values
-    // of stage i - 2, whose place is free.
-    const auto enter = [&](int i) {
-        if (issued - i == RING - 2) __builtin_amdgcn_s_waitcnt(0x0f70 | ((RING - 3) * LOADS & 15) | ((RING - 3) * LOADS >> 4) << 14);
-        else __builtin_amdgcn_s_waitcnt(0x0f70);
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_s_barrier();
-        asm volatile("" ::: "memory");
-        if (issued < stages) issue(issued++);
-    };
-    // One tile's weights and output beside the next tile's scores: a wave's
-    // exponentials run while its own products do (64 rows over 16384 keys: 379
-    // against 395 us without).
-    const bool rows = w.row0 < p.R;               // else this wave only loads
-    if (fast > 0) {
-        f32x4 s[RB][2];
-        const auto step = [&](const char *stage, int tile, const char *next_stage, int next_tile) {
-            typename W::Values v[W::VC][8];
-            u32x4 k[2][KS], pw[RB];
-            f32x4 next[RB][2];
-            keys_of(next_stage, next_tile, k);
-            values_of(stage, tile, v);
-            w.weigh(s, pw);
-            w.score(k, next);
-            w.add(v, pw);
-#pragma unroll
-            for (int rb = 0; rb < RB; rb++)
-#pragma unroll
-                for (int hf = 0; hf < 2; hf++) s[rb][hf] = next[rb][hf];
-            w.raise(s);
+    #pragma unroll
+            for (int j = 0; j < LOADS; j++) {
+                const int lin0 = j * kShared * 64 + wave * 64;
+                const bool val = lin0 >= 64 * PIECES;
+                const int64_t step = val ? p.c.vs1 : p.c.ks1;
+                const char *from = src[j];
+                if constexpr (PAGED) {
+                    const int half = (lin0 / PIECES & 63) >> 4;
+                    const uint32_t page = (uint32_t)__builtin_amdgcn_readlane(entry, (i & 15) * 4 + half);
+                    const uint32_t in = (uint32_t)(key0 + i * 64 + half * 16) & ((1u << p.c.shift) - 1);
+                    from += (int64_t)page * (val ? p.c.vs0 : p.c.ks0) + (int64_t)in * step;
+                    if (page >= p.c.pages) from = reinterpret_cast<const char *>(kZeros);
+                } else {
+                    // behind the last token the last one again, which the mask leaves out
+                    if (i >= fast) from -= max(key0 + i * 64 + ((lin0 + (tid & 63)) / PIECES & 63) - (at.end - 1), 0) * step;
+                    src[j] += 64 * step;
+                }
+                if (PAD && pad[j]) from = reinterpret_cast<const char *>(kZeros);
+                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
+                                                 (__attribute__((address_space(3))) void *)(to + j * kShared * 1024), 16, 0, 0);
+            }
         };
-        enter(0);
-        if (rows) {
-            u32x4 k[2][KS];
-            keys_of(smem, p.wk == 1 ? 0 : wkey, k);
-            w.score(k, s);
-            w.raise(s);
-        }
-        for (int i = 0; i < fast; i++) {
-            const char *stage = smem + i % RING * STAGE, *next = i + 1 < fast ? smem + (i + 1) % RING * STAGE : stage;
-            // after the last tile its own scores again, which change nothing
-            if (p.wk == 1 && rows) step(stage, 0, stage, 1);
-            if (i + 1 < fast) enter(i + 1);
-            if (rows) step(stage, p.wk == 1 ? 1 : wkey, next, p.wk == 1 ? 0 : wkey);
-        }
-    }
-    for (int i = fast; i < stages; i++) {
-        enter(i);
-        const char *stage = smem + i % RING * STAGE;
-        for (int tile = wkey; tile < 2; tile += p.wk) {
-            Tile t;
-            t.key = key0 + i * 64 + tile * kTileKeys;
-            t.fast = false;
-            if (!rows || t.key >= w.lim) break;
-#pragma unroll
-            for (int hf = 0; hf < 2; hf++) {
-                const int key = t.key + 16 * hf;
-                t.there[hf] = key < at.end && (!PAGED || (uint32_t)p.c.table[at.b * p.c.ts + (key >> p.c.shift)] < p.c.pages);
+        // The queries are waited for here: a wait for them inside the loop would be
+        // one for every stage under way. The first stages arrive meanwhile.
+        int issued = 0;
+        while (issued < RING - 2 && issued < stages) issue(issued++);
+        W w;
+        w.init(p, at.b, at.h, (at.rg * (kShared / p.wk) + wrow) * RB * 16, at.n, at.end);
+        __builtin_amdgcn_s_waitcnt(0x0f70);
+        const auto keys_of = [&](const char *stage, int tile, u32x4 (&k)[2][KS]) {
+            const char *kb = stage + (tile * 32 + w.x) * ROW;
+    #pragma unroll
+            for (int hf = 0; hf < 2; hf++)
+    #pragma unroll
+                for (int ks = 0; ks < KS; ks++) {
+                    const int o = (ks * 32 + w.g * 8) * es;
+                    k[hf][ks] = widen<CT>(*reinterpret_cast<const Raw<CT> *>(kb + hf * 16 * ROW + ((((o >> 4) ^ mixed<PIECES>(w.x)) << 4) | (o & 15))));
+                }
+        };
+        const auto values_of = [&](const char *stage, int tile, typename W::Values (&v)[W::VC][8]) {
+            const char *vb = stage + (64 + tile * 32 + w.g * 4) * ROW;
+    #pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const int o = w.x * W::VE * es, mix = mixed<PIECES>(w.g * 4 + (j & 3));
+                v[0][j] = *reinterpret_cast<const typename W::Values *>(vb + ((j >> 2) * 16 + (j & 3)) * ROW + ((((o >> 4) ^ mix) << 4) | (o & 15)));
             }
-            u32x4 k[2][KS];
-            typename W::Values v[W::VC][8];
-            keys_of(stage, tile, k);
-            w.tile(p, t, at, k, v, [&](typename W::Values (&u)[W::VC][8]) { values_of(stage, tile, u); });
+        };
+
+        // Makes stage i readable and starts the load of a later one. This wave's
+        // loads of it are done when no more than the later stages' are outstanding
+        // (they end in order); other loads in between make the wait longer, never
+        // shorter. Behind the barrier all waves' are, and all are past the values
+        // of stage i - 2, whose place is free.
+        const auto enter = [&](int i) {
+            if (issued - i == RING - 2) __builtin_amdgcn_s_waitcnt(0x0f70 | ((RING - 3) * LOADS & 15) | ((RING - 3) * LOADS >> 4) << 14);
+            else __builtin_amdgcn_s_waitcnt(0x0f70);
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            if (issued < stages) issue(issued++);
+        };
+        // One tile's weights and output beside the next tile's scores: a wave's
+        // exponentials run while its own products do (64 rows over 16384 keys: 379
+        // against 395 us without).
+        const bool rows = w.row0 < p.R;               // else this wave only loads
+        if (fast > 0) {
+            f32x4 s[RB][2];
+            const auto step = [&](const char *stage, int tile, const char *next_stage, int next_tile) {
+                typename W::Values v[W::VC][8];
+                u32x4 k[2][KS], pw[RB];
+                f32x4 next[RB][2];
+                keys_of(next_stage, next_tile, k);
+                values_of(stage, tile, v);
+                w.weigh(s, pw);
+                w.score(k, next);
+                w.add(v, pw);
+    #pragma unroll
+                for (int rb = 0; rb < RB; rb++)
+    #pragma unroll
+                    for (int hf = 0; hf < 2; hf++) s[rb][hf] = next[rb][hf];
+                w.raise(s);
+            };
+            enter(0);
+            if (rows) {
+                u32x4 k[2][KS];
+                keys_of(smem, p.wk == 1 ? 0 : wkey, k);
+                w.score(k, s);
+                w.raise(s);
+            }
+            for (int i = 0; i < fast; i++) {
+                const char *stage = smem + i % RING * STAGE, *next = i + 1 < fast ? smem + (i + 1) % RING * STAGE : stage;
+                // after the last tile its own scores again, which change nothing
+                if (p.wk == 1 && rows) step(stage, 0, stage, 1);
+                if (i + 1 < fast) enter(i + 1);
+                if (rows) step(stage, p.wk == 1 ? 1 : wkey, next, p.wk == 1 ? 0 : wkey);
+            }
         }
-    }
-    w.close();
-    if (p.wk == 2) {
-        __syncthreads();                          // the ring's memory is free
-        w.join(kShared, 2, wkey, wave - wkey, reinterpret_cast<float *>(smem + RING * STAGE), reinterpret_cast<float *>(smem) + wrow * RB * 16 * DP);
-        if (wkey) continue;
-    }
-    w.store(p, at);
-    if (w.odd) w.poison(p, at);
+        for (int i = fast; i < stages; i++) {
+            enter(i);
+            const char *stage = smem + i % RING * STAGE;
+            for (int tile = wkey; tile < 2; tile += p.wk) {
+                Tile t;
+                t.key = key0 + i * 64 + tile * kTileKeys;
+                t.fast = false;
+                if (!rows || t.key >= w.lim) break;
+    #pragma unroll
+                for (int hf = 0; hf < 2; hf++) {
+                    const int key = t.key + 16 * hf;
+                    t.there[hf] = key < at.end && (!PAGED || (uint32_t)p.c.table[at.b * p.c.ts + (key >> p.c.shift)] < p.c.pages);
+                }
+                u32x4 k[2][KS];
+                typename W::Values v[W::VC][8];
+                keys_of(stage, tile, k);
+                w.tile(p, t, at, k, v, [&](typename W::Values (&u)[W::VC][8]) { values_of(stage, tile, u); });
+            }
+        }
+        w.close();
+        if (p.wk == 2) {
+            __syncthreads();                          // the ring's memory is free
+            w.join(kShared, 2, wkey, wave - wkey, reinterpret_cast<float *>(smem + RING * STAGE), reinterpret_cast<float *>(smem) + wrow * RB * 16 * DP);
+            if (wkey) continue;
+        }
+        w.store(p, at);
+        if (w.odd) w.poison(p, at);
     }
 }
 
@@ -1241,21 +1251,38 @@ Plan make_plan(uint32_t seqs, uint32_t kv_heads, uint32_t dim, uint32_t cache_to
     const uint32_t G = heads / kv_heads;
     const uint64_t R = (uint64_t)T * G;
     a.DP = dim <= 64 ? 64 : dim <= 128 ? 128 : 256;
-    a.shared = may_share && R > 32 && a.DP <= 128;
+    const uint64_t tiles = ((uint64_t)cache_tokens + kTileKeys - 1) / kTileKeys;
+    // Sharing keys doubles the rate of many rows but begins and ends slowly:
+    // it has to have more than 100 tiles of 32 keys by 32 rows for each CU, and
+    // with several sequences a workgroup they have to be long. Of 8 key/value
+    // heads of 128, shared against not: 4 x 16384 keys of 96 rows 69 against 93
+    // us, of 64 rows 59 against 64 (not worth the losses: 64 ragged sequences
+    // of up to 1024 93 against 40); 16 x 1024 keys of 512 rows 61 against 81,
+    // 1 x 2048 of them 40 against 31; 64 ragged sequences of up to 1024 keys
+    // of 96 rows 113 against 62, 16 of up to 4096 66 against 77.
+    const uint64_t groups = (uint64_t)seqs * kv_heads * (R > 128 ? (R + 255) / 256 : 1);
+    a.shared = may_share && R > 64 && a.DP <= 128 && seqs * kv_heads * ((R + 31) / 32) * tiles > 100 * kCUs && (tiles >= 64 || groups <= kCUs);
     a.RB = !a.shared && R <= 16 ? 1 : 2;
     const int waves = a.shared ? kShared : kWaves;
     const uint64_t blocks = (R + a.RB * 16 - 1) / (a.RB * 16);
+    // Waves side by side on rows; the others split the keys. Shared, up to 128
+    // rows: 128 rows of 64 over 4 x 16384 keys 53 us, with 8 instead of 4 waves
+    // 56; 160 rows of 128 over 4 x 8192 keys with 4 instead of 8 68, not 61.
     const int wr = a.shared ? (R > 128 ? 8 : 4) : blocks >= 4 ? 4 : blocks >= 2 ? 2 : 1;
     a.wk = waves / wr;
     a.nrg = (int)((blocks + wr - 1) / wr);
     a.unit = a.shared ? 2 : a.wk;
-    a.min_steps = 2;
-    // Workgroups: one a CU where they are large, else a few, so that one's
-    // loads run beside another's join. With four times as many sequences as
-    // that leaves for each head, every one goes to a workgroup of its own.
-    const uint64_t want = a.shared ? kCUs : a.RB == 1 ? 8 * kCUs : 4 * kCUs, each = (uint64_t)kv_heads * a.nrg;
+    a.min_steps = 2;                              // 1: 24 for 20 us where 16384 keys are split; 4: 15 for 13 at 2048
+    // Workgroups: one a CU, and eight where they are small, so that one's loads
+    // run beside another's join and long sequences are cut as short as others
+    // end: 16 rows, 32 sequences of very different lengths up to 8192 101 us,
+    // with three a CU 116 (64 of up to 1024 37 and 33, 4 equal ones of 16384
+    // FP8 keys 39 and 34). 32 rows, 2 x 131072 FP8 keys: 120 us, with two 140,
+    // with four 143; a head dim of 256, 16 rows, 9155 keys: 36 us, with two 38.
+    // More sequences than that leaves for each head: a workgroup each.
+    const uint64_t want = !a.shared && a.RB == 1 && a.DP < 256 ? 8 * kCUs : kCUs, each = (uint64_t)kv_heads * a.nrg;
     const uint64_t slots = want > each ? want / each : 1;
-    const uint64_t steps = (((uint64_t)cache_tokens + kTileKeys - 1) / kTileKeys + a.unit - 1) / a.unit, most = (steps + a.min_steps - 1) / a.min_steps;
+    const uint64_t steps = (tiles + a.unit - 1) / a.unit, most = (steps + a.min_steps - 1) / a.min_steps;
     a.slots = (int)slots;
     a.nsplit = 1;
     a.flat = a.shared && most > 1 && seqs < 4 * slots && (slots > 1 || seqs > 1);
@@ -1293,7 +1320,7 @@ int launch(const AttendParams &p, uint64_t grid, hipStream_t s)
 }
 
 template <int CT, int DP, bool PAD>
-int run(const AttendParams &p, const Plan &plan, int seqs, int half, hipStream_t s)
+int run(const AttendParams &p, const Plan &plan, int half, hipStream_t s)
 {
     const uint64_t grid = plan.grid;
     int rc = UZIP_EINVAL;
@@ -1321,11 +1348,11 @@ int run(const AttendParams &p, const Plan &plan, int seqs, int half, hipStream_t
 }
 
 template <int CT>
-int run_type(const AttendParams &p, const Plan &plan, int seqs, int half, hipStream_t s)
+int run_type(const AttendParams &p, const Plan &plan, int half, hipStream_t s)
 {
-    if (plan.DP == 64) return p.D == 64 ? run<CT, 64, false>(p, plan, seqs, half, s) : run<CT, 64, true>(p, plan, seqs, half, s);
-    if (plan.DP == 128) return p.D == 128 ? run<CT, 128, false>(p, plan, seqs, half, s) : run<CT, 128, true>(p, plan, seqs, half, s);
-    return p.D == 256 ? run<CT, 256, false>(p, plan, seqs, half, s) : run<CT, 256, true>(p, plan, seqs, half, s);
+    if (plan.DP == 64) return p.D == 64 ? run<CT, 64, false>(p, plan, half, s) : run<CT, 64, true>(p, plan, half, s);
+    if (plan.DP == 128) return p.D == 128 ? run<CT, 128, false>(p, plan, half, s) : run<CT, 128, true>(p, plan, half, s);
+    return p.D == 256 ? run<CT, 256, false>(p, plan, half, s) : run<CT, 256, true>(p, plan, half, s);
 }
 
 }  // namespace
@@ -1400,10 +1427,10 @@ int uzip_kv_attend(const uzip_kv_cache_t *cache, const uzip_kv_attend_args_t *a,
     p.unit = plan.unit;
     p.c2 = a->scale * 1.4426950408889634f;
     p.q_f16 = a->dtype == UZIP_KV_F16;
-    const int seqs = (int)cache->seqs, half = p.q_f16;
-    if (cache->dtype == UZIP_KV_BF16) return run_type<kBF16>(p, plan, seqs, half, s);
-    if (cache->dtype == UZIP_KV_F16) return run_type<kF16>(p, plan, seqs, half, s);
-    return run_type<kE5M2>(p, plan, seqs, half, s);
+    const int half = p.q_f16;
+    if (cache->dtype == UZIP_KV_BF16) return run_type<kBF16>(p, plan, half, s);
+    if (cache->dtype == UZIP_KV_F16) return run_type<kF16>(p, plan, half, s);
+    return run_type<kE5M2>(p, plan, half, s);
 }
 
 }  // extern "C"

@@ -384,3 +384,86 @@ def test_two_graphs_at_once():
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def large(B, T, hq, H, D, S, cache, layout, seed):
+    """q, k, v, table on the device, as make() has them."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    mk = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    q = mk(B, T, hq, D).to(F16 if cache == F16 else BF16)
+    if layout.startswith("paged"):
+        page = int(layout[5:])
+        per = -(-S // page)
+        k, v = (mk(B * per + 2, page, H, D).to(cache) for _ in range(2))
+        return q, k, v, torch.randperm(B * per + 2, generator=g, device=DEV)[:B * per].view(B, per).to(torch.int32)
+    shape = (B, H, S, D) if layout == "hsd" else (B, S, H, D)
+    k, v = (mk(*shape).to(cache) for _ in range(2))
+    return (q, k.transpose(1, 2), v.transpose(1, 2), None) if layout == "hsd" else (q, k, v, None)
+
+
+SHARED = [(5, 24, 96, 32, 128, 1760, BF16, "shd"), (5, 70, 32, 8, 128, 2400, BF16, "paged16"), (5, 70, 32, 8, 64, 2400, E5M2, "paged32"),
+          (5, 24, 96, 32, 72, 1760, F16, "hsd"), (5, 33, 64, 32, 48, 1800, E5M2, "hsd"), (1, 64, 64, 8, 128, 6500, BF16, "paged128"),
+          (100, 24, 32, 8, 64, 2080, BF16, "shd"), (20, 24, 256, 64, 64, 2080, F16, "paged64"), (5, 66, 32, 16, 128, 2100, E5M2, "shd")]
+
+
+@pytest.mark.parametrize("B,T,hq,H,D,S,cache,layout", SHARED)
+@pytest.mark.parametrize("with_tree", [False, True])
+def test_work_enough_for_shared_keys(B, T, hq, H, D, S, cache, layout, with_tree):
+    """Rows enough for a workgroup's waves to share keys, over lengths of every
+    size, NaN behind them, absent pages, infinities that some queries see; some
+    key/value heads compared, all of them from call to call."""
+    q, k, v, table = large(B, T, hq, H, D, S, cache, layout, B + T + with_tree)
+    g = torch.Generator().manual_seed(B)
+    G = hq // H
+    length = torch.randint(S // 2, S - T, (B,), generator=g).to(torch.int32)
+    drafted = torch.full((B,), T, dtype=torch.int32)
+    if B > 1:
+        length[1], length[2], drafted[2], drafted[B - 1] = 0, 77, 0, 3
+        length[3] = S - T
+    if table is None:
+        for t in (k, v):
+            for b in range(B):
+                bits(t)[b, int(length[b]) + int(drafted[b]):] = bits(torch.full((1,), math.nan).to(cache)).to(DEV)
+        bits(v)[0, int(length[0]) + 1, :, 1] = bits(torch.full((1,), math.inf).to(cache)).to(DEV)
+    else:
+        table[0, 300 // k.shape[1]] = -1
+        table[B - 1, :2] = k.shape[0]
+    tree = None
+    if with_tree:
+        tree = torch.rand(B, T, T, generator=g) < 0.2
+        tree[:, 4] = False
+    kw = dict(table=table, tree=put(tree), drafted=drafted.to(DEV))
+    ws = torch.empty(kv.attend_workspace_bytes(B, H, D, S if table is None else table.shape[1] * k.shape[1], T, hq), dtype=torch.uint8, device=DEV)
+    first = None
+    for fill in (0, 255):
+        ws.fill_(fill)
+        w, lse = torch.zeros(B, H, S, device=DEV), torch.full((B, T, hq), 3.0, device=DEV)
+        got = (kv.attend(q, k, v, length.to(DEV), score=w, lse=lse, ws=ws, **kw), lse, w)
+        first = first or got
+        assert all(torch.equal(a.nan_to_num(nan=-9.0), b.nan_to_num(nan=-9.0)) for a, b in zip(first, got))
+    out, lse, w = got
+    for b, h in {(0, 0), (min(1, B - 1), H - 1), (min(2, B - 1), 1), (B - 1, H // 2)}:
+        at, heads = slice(b, b + 1), slice(h * G, h * G + G)
+        one = (k[at, :, h:h + 1], v[at, :, h:h + 1]) if table is None else (k[:, :, h:h + 1], v[:, :, h:h + 1])
+        want = ref.attend(q[at, :, heads].cpu(), *(t.cpu() for t in one), length[at], table=None if table is None else table[at].cpu(),
+                          tree=None if tree is None else tree[at], drafted=drafted[at])
+        ref.within(out[at, :, heads], want["out"], want["out_bound"], f"out {b} {h}")
+        ref.within(lse[at, :, heads], want["lse"], want["lse_bound"], f"lse {b} {h}")
+        ref.within(w[at, h:h + 1], want["weight"][..., :S], want["weight_bound"][..., :S], f"score {b} {h}")
+
+
+def test_shared_keys_in_a_graph():
+    q, k, v, _ = large(16, 24, 32, 8, 64, 2200, BF16, "shd", 1)
+    n = torch.full((16,), 2000, dtype=torch.int32, device=DEV)
+    kv.attend(q, k, v, n)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = kv.attend(q, k, v, n)
+    for i in range(4):
+        n.copy_((torch.arange(16) * 137 * i).clamp(max=2176).to(torch.int32))
+        out.fill_(9.0)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, kv.attend(q, k, v, n))
