@@ -454,7 +454,7 @@ __device__ inline void copy_rows(const EvictParams &p, int b, int h, int j0, int
 // choosing again (8 rows of 4096, 1024 of 128 16-bit elements kept: 11 us, in
 // two launches 17; 256 rows 45 and 55). Without, one workgroup a row writes the
 // index, and k_evict_copy copies. Choosing is bound by the steps of its three
-// levels, 23 us for 128 rows of 16384, where the copy of 4096 of each takes 78.
+// levels, 22 us for 128 rows of 16384, where the copy of 4096 of each takes 104.
 template <int N, bool COPY, typename RawT>
 __global__ __launch_bounds__(kSelThreads) void k_evict_one(EvictParams p)
 {
@@ -554,8 +554,8 @@ __global__ __launch_bounds__(kSelThreads) void k_evict_one(EvictParams p)
 // Longer rows, by slices: a launch a level, each of whose workgroups adds up
 // the slices' histograms of the level before, and one that writes the kept
 // tokens. Nothing needs clearing and no sum depends on an order. Bound by the
-// launches, which wait for each other: 16 rows of 120000 take 39 us to choose,
-// and 22 for the copy of 12345 of each. Rows up to 32768 stay in registers: 128
+// launches, which wait for each other: 16 rows of 120000 take 35 us to choose,
+// and 28 for the copy of 12345 FP8 rows of 128 of each. Rows up to 32768 stay in registers: 128
 // of them 122 us with their copy, by slices 128; only with few rows is it the
 // other way (16 rows: 43 and 40).
 struct Slice {
