@@ -341,8 +341,10 @@ __device__ inline uint32_t leading_bits(int left)
 __device__ inline uint32_t there_bits(const Tile &t) { return (t.there[0] ? 0x0fu : 0) | (t.there[1] ? 0xf0u : 0); }
 
 // ... those of the drafted tokens, the first of them drafted token j0, that
-// the mask names. Its bytes are read at places held inside it, all at once.
-__device__ inline uint32_t tree_bits(const AttendParams &p, int b, int tok, int j0, int nd)
+// the mask names and that lie in the cache: `in` of them, which may be fewer
+// than the nd (> 0) that the mask is for. Its bytes are read at places held
+// inside it, all at once.
+__device__ inline uint32_t tree_bits(const AttendParams &p, int b, int tok, int j0, int nd, int in)
 {
     const uint8_t *row = p.tree + b * p.tr0 + min(tok, nd - 1) * p.tr1;
     uint32_t bits = 0, named[8];
@@ -351,7 +353,7 @@ __device__ inline uint32_t tree_bits(const AttendParams &p, int b, int tok, int 
 #pragma unroll
     for (int k = 0; k < 8; k++) {
         const int j = j0 + 16 * (k >> 2) + (k & 3);
-        bits |= named[k] && j >= 0 && j < nd ? 1u << k : 0;
+        bits |= named[k] && j >= 0 && j < min(nd, in) ? 1u << k : 0;
     }
     return bits;
 }
@@ -533,7 +535,7 @@ struct Rows {
             for (int rb = 0; rb < RB; rb++) seen[rb] = 0;
             if (p.tree && t.key + kTileKeys > n) {
 #pragma unroll
-                for (int rb = 0; rb < RB; rb++) seen[rb] = tree_bits(p, at.b, tok[rb], t.key + 4 * g - n, nd);
+                for (int rb = 0; rb < RB; rb++) seen[rb] = tree_bits(p, at.b, tok[rb], t.key + 4 * g - n, nd, at.end - n);
             }
 #pragma unroll
             for (int rb = 0; rb < RB; rb++) {
@@ -1212,7 +1214,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attend_weigh(AttendParams p)
                 uint32_t seen = row.y == INFINITY ? 0u : 0xffu;
                 if (!t.fast) {
                     const int tok = (r0 + j * 16 + x) / p.G;
-                    uint32_t bits = p.tree ? tree_bits(p, b, tok, t.key + 4 * g - n, nd) : 0;
+                    uint32_t bits = p.tree ? tree_bits(p, b, tok, t.key + 4 * g - n, nd, end - n) : 0;
                     bits |= leading_bits((p.tree ? n : min(end, n + tok + 1)) - t.key - 4 * g);
                     seen &= bits & there_bits(t);
                 }
