@@ -389,9 +389,10 @@ struct Rows {
 
     int x, g, row0, lim;
     bool odd;                                     // poison() has something to add
+    bool far;                                     // raise() has a row to bring near zero
     int tok[RB];                                  // of the lane's rows
     float c2[RB], m[RB], l[RB];                   // l: of this lane's keys
-    float base[RB];                               // m c2, or 0 while m is -inf
+    float base[RB];                               // m c2; 0 while m is -inf, or when raise() has taken m off the scores
     u32x4 q[RB][KS];
     f32x4 acc[RB][NV];
 
@@ -401,7 +402,7 @@ struct Rows {
         asm volatile("" : "+v"(tid));             // what follows from it is made anew for each place, not kept in registers
         x = tid & 15, g = (tid & 63) >> 4;
         row0 = first_row;
-        odd = false;
+        odd = far = false;
 #pragma unroll
         for (int rb = 0; rb < RB; rb++) {
             const int r = row0 + rb * 16 + x;
@@ -430,7 +431,10 @@ struct Rows {
     // so far: the weights stay below 2^kSlack and nothing is lost in binary32,
     // while the output is scaled anew in the first tile and then hardly ever.
     // A row with a NaN is NaN by its sum, whatever m.
-    __device__ inline void raise(const f32x4 (&s)[RB][2])
+    // m c2 is rounded, and where a step of binary32 is a power of two the
+    // weights would not be near 1 but anything, infinite in FP16: scores of
+    // rows beyond 2^16 have m taken off, which is exact near it.
+    __device__ inline void raise(f32x4 (&s)[RB][2])
     {
         float top[RB];
         bool any = false;
@@ -440,13 +444,17 @@ struct Rows {
                                       larger(larger(s[rb][1][0], s[rb][1][1]), larger(s[rb][1][2], s[rb][1][3]))));
             any = any || (top[rb] - m[rb]) * c2[rb] > kSlack;
         }
-        if (__builtin_expect(__builtin_amdgcn_ballot_w64(any) != 0, 0)) {
+        if (__builtin_expect(__builtin_amdgcn_ballot_w64(any) != 0 || far, 0)) {
+            far = false;
 #pragma unroll
             for (int rb = 0; rb < RB; rb++) {
                 const float up = fmaxf(top[rb], m[rb]);
                 const float a = __builtin_amdgcn_exp2f((m[rb] - (up == -INFINITY ? 0.f : up)) * c2[rb]);
                 m[rb] = up;
                 base[rb] = up == -INFINITY ? 0.f : up * c2[rb];
+                const bool off = fabsf(base[rb]) > 65536.f;
+                far = far || __builtin_amdgcn_ballot_w64(off) != 0;
+                if (off) s[rb][0] -= up, s[rb][1] -= up, base[rb] = 0.f;
                 l[rb] *= a;
 #pragma unroll
                 for (int e = 0; e < NV; e++) acc[rb][e] *= a;
