@@ -32,7 +32,6 @@ namespace {
 
 constexpr int kWaves = 4;                     // per workgroup
 constexpr int kTileKeys = 32;
-constexpr float kSlack = 8.f;
 
 struct AttendParams {
     CacheView c;
@@ -45,7 +44,7 @@ struct AttendParams {
     int64_t sc0, sc1, tr0, tr1;               // elements
     int score_tokens, weigh_tiles;            // weigh_tiles: of each wave of k_attend_weigh
     float *part_o;                            // [row][split][DP], when nsplit > 1
-    float2 *part_ml;                          // [row][split]: maximum (times c), sum
+    float2 *part_ml;                          // [row][split]: maximum (times c, less Rows::kLift), sum
     int T, G, R, D, heads, seqs;              // heads: key/value heads
     int *used;                                // parts of each sequence, when flat
     int flat;                                 // Walk
@@ -384,7 +383,14 @@ struct Rows {
     static constexpr int NV = VE * VC;                   // output products; dim = c * 128 + (4 g + i) * VE + e
     static constexpr int VW = VE * (CT == kE5M2 ? 1 : 2) / 4;   // dwords of a lane's dims
     static constexpr int es = CT == kE5M2 ? 1 : 2;
-    static constexpr bool f16 = CT != kBF16;             // type of the products
+    static constexpr bool f16 = CT != kBF16;             // type of the products with the values
+    // Weights are 2^kLift at the row's maximum so far and below 2^(kLift +
+    // kSlack) until it is raised. FP16 has no bits below 2^-24, and a first
+    // token often has a score 15 to 20 above thousands of others: with the
+    // range used up to 2^15, their weights are kept to half a step of 2^-36 of
+    // the maximum, where without a lift and with a slack of 8 those below
+    // 2^-25 were lost from the output. BF16 reaches as low as binary32.
+    static constexpr float kSlack = f16 ? 4.f : 8.f, kLift = f16 ? 11.f : 0.f;
     typedef uint32_t Values __attribute__((ext_vector_type(VW)));
 
     int x, g, row0, lim;
@@ -392,7 +398,7 @@ struct Rows {
     bool far;                                     // raise() has a row to bring near zero
     int tok[RB];                                  // of the lane's rows
     float c2[RB], m[RB], l[RB];                   // l: of this lane's keys
-    float base[RB];                               // m c2; 0 while m is -inf, or when raise() has taken m off the scores
+    float base[RB];                               // m c2 - kLift; without m c2 when raise() has taken it off the scores; 0 while m is -inf
     u32x4 q[RB][KS];
     f32x4 acc[RB][NV];
 
@@ -428,7 +434,7 @@ struct Rows {
     }
 
     // Brings m near the maximum of a tile's scores. It need not be the maximum
-    // so far: the weights stay below 2^kSlack and nothing is lost in binary32,
+    // so far: the weights stay below 2^(kLift + kSlack) and nothing is lost in binary32,
     // while the output is scaled anew in the first tile and then hardly ever.
     // A row with a NaN is NaN by its sum, whatever m.
     // m c2 is rounded, and where a step of binary32 is a power of two the
@@ -451,10 +457,10 @@ struct Rows {
                 const float up = fmaxf(top[rb], m[rb]);
                 const float a = __builtin_amdgcn_exp2f((m[rb] - (up == -INFINITY ? 0.f : up)) * c2[rb]);
                 m[rb] = up;
-                base[rb] = up == -INFINITY ? 0.f : up * c2[rb];
+                base[rb] = up == -INFINITY ? 0.f : fmaf(up, c2[rb], -kLift);
                 const bool off = fabsf(base[rb]) > 65536.f;
                 far = far || __builtin_amdgcn_ballot_w64(off) != 0;
-                if (off) s[rb][0] -= up, s[rb][1] -= up, base[rb] = 0.f;
+                if (off) s[rb][0] -= up, s[rb][1] -= up, base[rb] = -kLift;
                 l[rb] *= a;
 #pragma unroll
                 for (int e = 0; e < NV; e++) acc[rb][e] *= a;
@@ -598,7 +604,7 @@ struct Rows {
 #pragma unroll
         for (int rb = 0; rb < RB; rb++) {
             l[rb] = quad_sum(l[rb]);
-            m[rb] *= c2[rb];
+            m[rb] = fmaf(m[rb], c2[rb], -kLift);
         }
     }
 
@@ -712,7 +718,7 @@ struct Rows {
                                 f32x4{acc[rb][c * VE + e][ii], acc[rb][c * VE + e + 1][ii], acc[rb][c * VE + e + 2][ii], acc[rb][c * VE + e + 3][ii]};
                 continue;
             }
-            const bool empty = l[rb] == 0.f || tok[rb] >= nd;      // a seen key's weight is 1 at the maximum, or NaN
+            const bool empty = l[rb] == 0.f || tok[rb] >= nd;      // the weight of the row's maximum is at least 1, or NaN
             const float inv = 1.f / l[rb];
             const int head = h * p.G + r % p.G;
             if (g == 0 && p.lse) p.lse[((int64_t)b * p.T + tok[rb]) * (p.heads * p.G) + head] = empty ? -INFINITY : (m[rb] + __log2f(l[rb])) * 0.6931471805599453f;

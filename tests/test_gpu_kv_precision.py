@@ -1,0 +1,39 @@
+"""kv.attend where few bits would show: many small weights beside a large one."""
+import math
+
+import pytest
+import torch
+
+import kv_reference as ref
+from lossless_bf16_tensor_amd import kv
+from test_gpu_kv_attend import BF16, DEV, E5M2, F16
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("q,cache", [(F16, F16), (BF16, BF16), (F16, E5M2), (BF16, E5M2)])
+@pytest.mark.parametrize("B,T,hq,H,S,D", [(1, 1, 1, 1, 4096, 64), (2, 1, 24, 1, 3000, 256), (2048, 1, 1, 1, 4096, 128), (1, 65, 1, 1, 20000, 64),
+                                          (128, 65, 8, 8, 4160, 64), (128, 65, 8, 8, 4160, 128)])
+@pytest.mark.parametrize("at", [0, 2000])
+def test_small_weights_beside_a_large_one(q, cache, B, T, hq, H, S, D, at):
+    """One token's score is 18 above all others', as a first token's often is.
+    Its values are zero, so the output is the others' share, N e^-18 / (1 + N
+    e^-18) of their common value: a kernel that rounds weights of 2^-26 away
+    loses them. Weights of FP16 products may be off by half a step, 2^-36 of
+    the largest, of which there are N; the sums of N weights in binary32 and
+    the score's own rounding are far below the output's half step."""
+    k, v = torch.zeros(1, S, 1, D), torch.full((1, S, 1, D), 1.5)
+    k[:, at, :, 0], v[:, at] = 20.0, 0.0
+    k, v = (t.to(cache).to(DEV).expand(B, S, H, D) for t in (k, v))
+    x = torch.zeros(1, 1, 1, D)
+    x[..., 0] = 1.0
+    x = x.expand(B, T, hq, D).contiguous().to(q).to(DEV)
+    n = torch.full((B,), S - T, dtype=torch.int32, device=DEV)
+    seen = (S - T + 1 + torch.arange(T, dtype=torch.float64)).view(1, T, 1)       # a chain
+    lse = torch.empty(B, T, hq, device=DEV)
+    out = kv.attend(x, k, v, n, scale=0.9, lse=lse)
+    small = (seen - 1) * math.exp(-18.0)
+    want = (1.5 * small / (1 + small))[..., None].expand(B, T, hq, D)
+    bound = want * (ref.HALF[q] + 2.0 ** -16) + 1.5 * S * 2.0 ** -36
+    ref.within(out, want, bound, "out")
+    ref.within(lse, (18.0 + torch.log1p(small)).expand(B, T, hq), torch.tensor(2.0 ** -17), "lse")
