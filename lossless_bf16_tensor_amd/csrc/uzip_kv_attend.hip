@@ -24,7 +24,8 @@
 // stay where they are, and only V^T must follow that order: lane (x, g) loads
 // 8 (or 4) dims of its 8 keys and transposes them with byte permutes.
 // Maximum and sum of a row need only the four lanes with the same x.
-// E5M2 is the upper byte of FP16, so the permute that transposes also widens.
+// E5M2 is the upper byte of FP16, so the permute that transposes also widens;
+// keys become the queries' type, BF16 by a conversion of two at a time.
 #include "kv_common.h"
 
 namespace uzip_kv {
@@ -51,7 +52,6 @@ struct AttendParams {
     int nsplit, nrg, slots, min_steps, unit;  // unit: tiles that a workgroup takes in one step
     int wk;                                   // waves of a workgroup that share rows and split keys
     float c2;                                 // scale * log2(e)
-    int q_f16;
 };
 
 __device__ inline int end_of(const AttendParams &p, int n, int nd)
@@ -201,26 +201,40 @@ struct Walk {
     }
 };
 
-template <int CT>
-using Raw = typename std::conditional<CT == kE5M2, u32x2, u32x4>::type;       // 8 elements
+// What a kernel is made for: the types of the cache and, where that is E5M2, of
+// the queries.
+constexpr int kE5M2BF = 3;                    // BF16 queries; kE5M2: FP16 ones
+constexpr bool is_fp8(int ct) { return ct == kE5M2 || ct == kE5M2BF; }
+constexpr bool f16_queries(int ct) { return ct == kF16 || ct == kE5M2; }      // the output's type, and that of the products with keys
+constexpr bool f16_weights(int ct) { return ct != kBF16; }                    // the type of the products with values
 
+template <int CT>
+using Raw = typename std::conditional<is_fp8(CT), u32x2, u32x4>::type;        // 8 elements
+
+// Eight elements of a key, in the queries' type: any E5M2 value is one of FP16
+// and one of BF16, so products with either are exact.
 template <int CT>
 __device__ inline u32x4 widen(const Raw<CT> &r)
 {
-    if constexpr (CT == kE5M2)
+    if constexpr (CT == kE5M2BF)
+        return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(r.x, 1.f, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(r.x, 1.f, true)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(r.y, 1.f, false)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8(r.y, 1.f, true))};
+    else if constexpr (CT == kE5M2)
         return u32x4{__builtin_amdgcn_perm(r.x, r.x, 0x010c000cu), __builtin_amdgcn_perm(r.x, r.x, 0x030c020cu),
                      __builtin_amdgcn_perm(r.y, r.y, 0x010c000cu), __builtin_amdgcn_perm(r.y, r.y, 0x030c020cu)};
     else
         return r;
 }
 
-template <int CT>
+template <bool F16>
 __device__ inline f32x4 mfma(u32x4 a, u32x4 b, f32x4 c)
 {
-    if constexpr (CT == kBF16)
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-    else
+    if constexpr (F16)
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
 // infinities and NaN of packed elements: their bits where an element is not
@@ -228,7 +242,7 @@ __device__ inline f32x4 mfma(u32x4 a, u32x4 b, f32x4 c)
 template <int CT>
 __device__ inline uint32_t not_finite(uint32_t w)
 {
-    if constexpr (CT == kE5M2) {
+    if constexpr (is_fp8(CT)) {
         // exponent bits 6..2 of a byte all set: adding the lowest one carries into bit 7
         const uint32_t t = ((w & 0x7c7c7c7cu) + 0x04040404u) & 0x80808080u;
         return (t << 1) - (t >> 7);                  // 0xff in each such byte
@@ -240,38 +254,14 @@ __device__ inline uint32_t not_finite(uint32_t w)
 }
 
 // A row's 16-byte fragments of Q for the matrix cores (8 dims at 32 ks + 8 g).
-// FP8 caches are multiplied in FP16. A BF16 row for them is scaled by a power
-// of two that brings its largest finite element to [1, 2): what FP16 then
-// rounds is below 2^-24 of that element, the last bit of the binary32 sum.
-// Returns the factor that undoes it.
-template <int CT, int KS, bool PAD>
-__device__ inline float load_q(const AttendParams &p, const char *row, bool there, int g, u32x4 (&f)[KS])
+template <int KS, bool PAD>
+__device__ inline void load_q(const AttendParams &p, const char *row, bool there, int g, u32x4 (&f)[KS])
 {
 #pragma unroll
     for (int ks = 0; ks < KS; ks++) {
         f[ks] = u32x4{0, 0, 0, 0};
         if (there && (!PAD || ks * 32 + g * 8 < p.D)) f[ks] = *reinterpret_cast<const u32x4 *>(row + (ks * 32 + g * 8) * 2);
     }
-    if (CT != kE5M2 || p.q_f16) return 1.f;
-    float top = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < KS; ks++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const uint32_t w = f[ks][i] & ~not_finite<kBF16>(f[ks][i]);
-            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w << 16)), fabsf(__uint_as_float(w & 0xffff0000u))));
-        }
-    top = quad_max(top);
-    int e = top > 0.f ? ilogbf(top) : 0;
-    e = e < -60 ? -60 : e;                        // keeps c2 normal; smaller rows lose nothing a sum would keep
-#pragma unroll
-    for (int ks = 0; ks < KS; ks++)
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const f32x2 v = unpack2<false>(f[ks][i]);
-            f[ks][i] = pack2<true>(ldexpf(v.x, -e), ldexpf(v.y, -e));
-        }
-    return ldexpf(1.f, e);
 }
 
 // The two 16-key halves of a tile: where their rows start, and whether every
@@ -361,7 +351,7 @@ __device__ inline uint32_t tree_bits(const AttendParams &p, int b, int tok, int 
 template <int CT, int KS, bool PAD, bool MASKED>
 __device__ inline void load_keys(const AttendParams &p, const Tile &t, int end, int x, int g, uint32_t off, Raw<CT> (&r)[2][KS])
 {
-    constexpr int es = CT == kE5M2 ? 1 : 2;
+    constexpr int es = is_fp8(CT) ? 1 : 2;
 #pragma unroll
     for (int hf = 0; hf < 2; hf++) {
         const bool row = !MASKED || (t.there[hf] && t.key + 16 * hf + x < end);
@@ -381,9 +371,9 @@ struct Rows {
     static constexpr int VE = DP >= 128 ? 8 : 4;         // dims that a lane takes at once
     static constexpr int VC = DP >= 128 ? DP / 128 : 1;  // ... and how often
     static constexpr int NV = VE * VC;                   // output products; dim = c * 128 + (4 g + i) * VE + e
-    static constexpr int VW = VE * (CT == kE5M2 ? 1 : 2) / 4;   // dwords of a lane's dims
-    static constexpr int es = CT == kE5M2 ? 1 : 2;
-    static constexpr bool f16 = CT != kBF16;             // type of the products with the values
+    static constexpr int VW = VE * (is_fp8(CT) ? 1 : 2) / 4;    // dwords of a lane's dims
+    static constexpr int es = is_fp8(CT) ? 1 : 2;
+    static constexpr bool f16 = f16_weights(CT), half = f16_queries(CT);
     // Weights are 2^kLift at the row's maximum so far and below 2^(kLift +
     // kSlack) until it is raised. FP16 has no bits below 2^-24, and a first
     // token often has a score 15 to 20 above thousands of others: with the
@@ -397,7 +387,7 @@ struct Rows {
     bool odd;                                     // poison() has something to add
     bool far;                                     // raise() has a row to bring near zero
     int tok[RB];                                  // of the lane's rows
-    float c2[RB], m[RB], l[RB];                   // l: of this lane's keys
+    float m[RB], l[RB];                           // l: of this lane's keys
     float base[RB];                               // m c2 - kLift; without m c2 when raise() has taken it off the scores; 0 while m is -inf
     u32x4 q[RB][KS];
     f32x4 acc[RB][NV];
@@ -413,7 +403,7 @@ struct Rows {
         for (int rb = 0; rb < RB; rb++) {
             const int r = row0 + rb * 16 + x;
             tok[rb] = r / p.G;
-            c2[rb] = p.c2 * load_q<CT, KS, PAD>(p, p.q + b * p.qs0 + tok[rb] * p.qs1 + (int64_t)(h * p.G + r % p.G) * p.qs2, r < p.R, g, q[rb]);
+            load_q<KS, PAD>(p, p.q + b * p.qs0 + tok[rb] * p.qs1 + (int64_t)(h * p.G + r % p.G) * p.qs2, r < p.R, g, q[rb]);
             m[rb] = -INFINITY, l[rb] = 0.f, base[rb] = 0.f;
 #pragma unroll
             for (int e = 0; e < NV; e++) acc[rb][e] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -430,7 +420,7 @@ struct Rows {
 #pragma unroll
             for (int ks = 0; ks < KS; ks++)
 #pragma unroll
-                for (int rb = 0; rb < RB; rb++) s[rb][hf] = mfma<CT>(k[hf][ks], q[rb][ks], ks ? s[rb][hf] : f32x4{0.f, 0.f, 0.f, 0.f});
+                for (int rb = 0; rb < RB; rb++) s[rb][hf] = mfma<half>(k[hf][ks], q[rb][ks], ks ? s[rb][hf] : f32x4{0.f, 0.f, 0.f, 0.f});
     }
 
     // Brings m near the maximum of a tile's scores. It need not be the maximum
@@ -440,7 +430,7 @@ struct Rows {
     // m c2 is rounded, and where a step of binary32 is a power of two the
     // weights would not be near 1 but anything, infinite in FP16: scores of
     // rows beyond 2^16 have m taken off, which is exact near it.
-    __device__ inline void raise(f32x4 (&s)[RB][2])
+    __device__ inline void raise(float c2, f32x4 (&s)[RB][2])
     {
         float top[RB];
         bool any = false;
@@ -448,16 +438,16 @@ struct Rows {
         for (int rb = 0; rb < RB; rb++) {
             top[rb] = quad_max(larger(larger(larger(s[rb][0][0], s[rb][0][1]), larger(s[rb][0][2], s[rb][0][3])),
                                       larger(larger(s[rb][1][0], s[rb][1][1]), larger(s[rb][1][2], s[rb][1][3]))));
-            any = any || (top[rb] - m[rb]) * c2[rb] > kSlack;
+            any = any || (top[rb] - m[rb]) * c2 > kSlack;
         }
         if (__builtin_expect(__builtin_amdgcn_ballot_w64(any) != 0 || far, 0)) {
             far = false;
 #pragma unroll
             for (int rb = 0; rb < RB; rb++) {
                 const float up = fmaxf(top[rb], m[rb]);
-                const float a = __builtin_amdgcn_exp2f((m[rb] - (up == -INFINITY ? 0.f : up)) * c2[rb]);
+                const float a = __builtin_amdgcn_exp2f((m[rb] - (up == -INFINITY ? 0.f : up)) * c2);
                 m[rb] = up;
-                base[rb] = up == -INFINITY ? 0.f : fmaf(up, c2[rb], -kLift);
+                base[rb] = up == -INFINITY ? 0.f : fmaf(up, c2, -kLift);
                 const bool off = fabsf(base[rb]) > 65536.f;
                 far = far || __builtin_amdgcn_ballot_w64(off) != 0;
                 if (off) s[rb][0] -= up, s[rb][1] -= up, base[rb] = -kLift;
@@ -469,7 +459,7 @@ struct Rows {
     }
 
     // Scores to weights.
-    __device__ inline void weigh(const f32x4 (&s)[RB][2], u32x4 (&pw)[RB])
+    __device__ inline void weigh(float c2, const f32x4 (&s)[RB][2], u32x4 (&pw)[RB])
     {
 #pragma unroll
         for (int rb = 0; rb < RB; rb++) {
@@ -479,7 +469,7 @@ struct Rows {
             for (int hf = 0; hf < 2; hf++)
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
-                    w[hf][k] = __builtin_amdgcn_exp2f(fmaf(s[rb][hf][k], c2[rb], -base[rb]));
+                    w[hf][k] = __builtin_amdgcn_exp2f(fmaf(s[rb][hf][k], c2, -base[rb]));
                     sum[hf] += w[hf][k];
                 }
             l[rb] += sum[0] + sum[1];
@@ -495,7 +485,7 @@ struct Rows {
         u32x4 a;
 #pragma unroll
         for (int k = 0; k < 4; k++) {
-            if constexpr (CT == kE5M2) {
+            if constexpr (is_fp8(CT)) {
                 const uint32_t sel = ((4u + e % 4) << 24) | (0x0cu << 16) | ((uint32_t)(e % 4) << 8) | 0x0cu;
                 a[k] = __builtin_amdgcn_perm(v[c][2 * k + 1][e / 4], v[c][2 * k][e / 4], sel);
             } else {
@@ -513,7 +503,7 @@ struct Rows {
             for (int e = 0; e < VE; e++) {
                 const u32x4 a = fragment(v, c, e);
 #pragma unroll
-                for (int rb = 0; rb < RB; rb++) acc[rb][c * VE + e] = mfma<CT>(a, pw[rb], acc[rb][c * VE + e]);
+                for (int rb = 0; rb < RB; rb++) acc[rb][c * VE + e] = mfma<f16>(a, pw[rb], acc[rb][c * VE + e]);
             }
     }
 
@@ -559,8 +549,8 @@ struct Rows {
                 for (int i = 0; i < 8; i++) s[rb][i >> 2][i & 3] = seen[rb] >> i & 1 ? s[rb][i >> 2][i & 3] : -INFINITY;
             }
         }
-        raise(s);
-        weigh(s, pw);
+        raise(p.c2, s);
+        weigh(p.c2, s, pw);
         if (t.key + kTileKeys > n) {
             // A value that is not finite must reach only the rows that see its
             // key, and in a product it would reach all (0 * inf): poison() adds it.
@@ -599,12 +589,12 @@ struct Rows {
     }
 
     // After the last tile: whole sums, and maxima that waves can compare.
-    __device__ inline void close()
+    __device__ inline void close(float c2)
     {
 #pragma unroll
         for (int rb = 0; rb < RB; rb++) {
             l[rb] = quad_sum(l[rb]);
-            m[rb] = fmaf(m[rb], c2[rb], -kLift);
+            m[rb] = fmaf(m[rb], c2, -kLift);
         }
     }
 
@@ -676,7 +666,7 @@ struct Rows {
                     int64_t off;
                     if (!locate(p.c, b, (uint32_t)key, p.c.vs0, p.c.vs1, off)) continue;
                     const char *from = p.c.v + off + h * p.c.vs2 + d * es;
-                    const float v = CT == kE5M2 ? f16_to_f32((uint16_t)(*reinterpret_cast<const uint8_t *>(from) << 8))
+                    const float v = is_fp8(CT) ? f16_to_f32((uint16_t)(*reinterpret_cast<const uint8_t *>(from) << 8))
                                                 : CT == kBF16 ? bf16_to_f32(*reinterpret_cast<const uint16_t *>(from)) : f16_to_f32(*reinterpret_cast<const uint16_t *>(from));
                     if (fabsf(v) < INFINITY) continue;
                     up = up || !(v < 0.f);
@@ -688,7 +678,6 @@ struct Rows {
                     p.part_o[((((int64_t)b * p.heads + h) * p.R + r) * p.nsplit + at.split) * DP + d] += add;
                 } else {
                     uint16_t *o = reinterpret_cast<uint16_t *>(p.out + b * p.os0 + token * p.os1 + head * p.os2) + d;
-                    const bool half = f16 && (CT == kF16 || p.q_f16);
                     const float sum = (half ? f16_to_f32(*o) : bf16_to_f32(*o)) + add;
                     *o = (uint16_t)(half ? pack2<true>(sum, 0.f) : pack2<false>(sum, 0.f));
                 }
@@ -723,7 +712,6 @@ struct Rows {
             const int head = h * p.G + r % p.G;
             if (g == 0 && p.lse) p.lse[((int64_t)b * p.T + tok[rb]) * (p.heads * p.G) + head] = empty ? -INFINITY : (m[rb] + __log2f(l[rb])) * 0.6931471805599453f;
             char *o = p.out + b * p.os0 + tok[rb] * p.os1 + head * p.os2;
-            const bool half = f16 && (CT == kF16 || p.q_f16);
 #pragma unroll
             for (int c = 0; c < VC; c++)
 #pragma unroll
@@ -792,8 +780,8 @@ __global__ __launch_bounds__(kWaves * 64, DP == 256 ? 1 : 2) void k_attend(Atten
             u32x4 pw[RB];
             w.score(k, s);
             if (nxt.fast) load_keys<CT, KS, PAD, false>(p, nxt, w.lim, w.x, w.g, koff, kr);
-            w.raise(s);
-            w.weigh(s, pw);
+            w.raise(p.c2, s);
+            w.weigh(p.c2, s, pw);
             w.add(v, pw);
             t = nxt;
         }
@@ -805,7 +793,7 @@ __global__ __launch_bounds__(kWaves * 64, DP == 256 ? 1 : 2) void k_attend(Atten
         w.masked_tile(p, t, at);
     }
 
-    w.close();
+    w.close(p.c2);
     if (p.wk > 1) {
         w.join(kWaves, p.wk, wkey, wave - wkey, smem + 2 * RB * 16 * DP, smem + (p.wk == 4 ? 0 : wrow) * RB * 16 * DP);
         if (wkey) return;
@@ -971,21 +959,21 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
                 f32x4 next[RB][2];
                 keys_of(next_stage, next_tile, k);
                 values_of(stage, tile, v);
-                w.weigh(s, pw);
+                w.weigh(p.c2, s, pw);
                 w.score(k, next);
                 w.add(v, pw);
     #pragma unroll
                 for (int rb = 0; rb < RB; rb++)
     #pragma unroll
                     for (int hf = 0; hf < 2; hf++) s[rb][hf] = next[rb][hf];
-                w.raise(s);
+                w.raise(p.c2, s);
             };
             enter(0);
             if (rows) {
                 u32x4 k[2][KS];
                 keys_of(smem, p.wk == 1 ? 0 : wkey, k);
                 w.score(k, s);
-                w.raise(s);
+                w.raise(p.c2, s);
             }
             for (int i = 0; i < fast; i++) {
                 const char *stage = smem + i % RING * STAGE, *next = i + 1 < fast ? smem + (i + 1) % RING * STAGE : stage;
@@ -1014,7 +1002,7 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
                 w.tile(p, t, at, k, v, [&](typename W::Values (&u)[W::VC][8]) { values_of(stage, tile, u); });
             }
         }
-        w.close();
+        w.close(p.c2);
         if (p.wk == 2) {
             __syncthreads();                          // the ring's memory is free
             w.join(kShared, 2, wkey, wave - wkey, reinterpret_cast<float *>(smem + RING * STAGE), reinterpret_cast<float *>(smem) + wrow * RB * 16 * DP);
@@ -1160,10 +1148,10 @@ template <int CT, int DP, bool PAD>
 __global__ __launch_bounds__(kWaves * 64, 2) void k_attend_weigh(AttendParams p)
 {
     constexpr int KS = DP / 32;
-    constexpr int es = CT == kE5M2 ? 1 : 2;
+    constexpr int es = is_fp8(CT) ? 1 : 2;
     constexpr int BLOCKS = KS <= 4 ? 16 : 8;      // of 16 rows, at a time
     __shared__ __attribute__((aligned(16))) u32x4 lq[BLOCKS * KS * 64];
-    __shared__ float2 lrow[BLOCKS * 16];          // factor of the scores, lse * log2(e); +inf: takes no part
+    __shared__ float lrow[BLOCKS * 16];           // lse * log2(e); +inf: takes no part
     const int lane = (int)(threadIdx.x & 63), x = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     int id = (int)blockIdx.x;
@@ -1183,11 +1171,11 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attend_weigh(AttendParams p)
         for (int i = wave; i < blocks; i += kWaves) {
             const int r = r0 + i * 16 + x, tok = r / p.G, head = h * p.G + r % p.G;
             u32x4 q[KS];
-            const float c2 = p.c2 * load_q<CT, KS, PAD>(p, p.q + b * p.qs0 + tok * p.qs1 + head * p.qs2, r < rows, g, q);
+            load_q<KS, PAD>(p, p.q + b * p.qs0 + tok * p.qs1 + head * p.qs2, r < rows, g, q);
 #pragma unroll
             for (int ks = 0; ks < KS; ks++) lq[(i * KS + ks) * 64 + lane] = q[ks];
             const float lse = r < rows ? p.lse[((int64_t)b * p.T + tok) * (p.heads * p.G) + head] : -INFINITY;
-            if (g == 0) lrow[i * 16 + x] = make_float2(c2, lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f);
+            if (g == 0) lrow[i * 16 + x] = lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
         }
         __syncthreads();
 
@@ -1217,15 +1205,15 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attend_weigh(AttendParams p)
             if (i + 1 < p.weigh_tiles && (first + wave + (i + 1) * kWaves) * kTileKeys < end) fetch(i + 1, at_next, old_next);
             f32x4 sum[2] = {};
             for (int j = 0; j < blocks; j++) {
-                const float2 row = lrow[j * 16 + x];
+                const float row = lrow[j * 16 + x];
                 f32x4 s[2];
 #pragma unroll
                 for (int ks = 0; ks < KS; ks++) {
                     const u32x4 q = lq[(j * KS + ks) * 64 + lane];
 #pragma unroll
-                    for (int hf = 0; hf < 2; hf++) s[hf] = mfma<CT>(k[hf][ks], q, ks ? s[hf] : f32x4{0.f, 0.f, 0.f, 0.f});
+                    for (int hf = 0; hf < 2; hf++) s[hf] = mfma<f16_queries(CT)>(k[hf][ks], q, ks ? s[hf] : f32x4{0.f, 0.f, 0.f, 0.f});
                 }
-                uint32_t seen = row.y == INFINITY ? 0u : 0xffu;
+                uint32_t seen = row == INFINITY ? 0u : 0xffu;
                 if (!t.fast) {
                     const int tok = (r0 + j * 16 + x) / p.G;
                     uint32_t bits = p.tree ? tree_bits(p, b, tok, t.key + 4 * g - n, nd, end - n) : 0;
@@ -1234,7 +1222,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attend_weigh(AttendParams p)
                 }
 #pragma unroll
                 for (int i8 = 0; i8 < 8; i8++) {
-                    const float w = __builtin_amdgcn_exp2f(fmaf(s[i8 >> 2][i8 & 3], row.x, -row.y));
+                    const float w = __builtin_amdgcn_exp2f(fmaf(s[i8 >> 2][i8 & 3], p.c2, -row));
                     sum[i8 >> 2][i8 & 3] += seen >> i8 & 1 ? w : 0.f;
                 }
             }
@@ -1445,11 +1433,10 @@ int uzip_kv_attend(const uzip_kv_cache_t *cache, const uzip_kv_attend_args_t *a,
     p.wk = plan.wk;
     p.unit = plan.unit;
     p.c2 = a->scale * 1.4426950408889634f;
-    p.q_f16 = a->dtype == UZIP_KV_F16;
-    const int half = p.q_f16;
+    const int half = a->dtype == UZIP_KV_F16;
     if (cache->dtype == UZIP_KV_BF16) return run_type<kBF16>(p, plan, half, s);
     if (cache->dtype == UZIP_KV_F16) return run_type<kF16>(p, plan, half, s);
-    return run_type<kE5M2>(p, plan, half, s);
+    return half ? run_type<kE5M2>(p, plan, half, s) : run_type<kE5M2BF>(p, plan, half, s);
 }
 
 }  // extern "C"

@@ -1,4 +1,5 @@
-"""kv.attend where few bits would show: many small weights beside a large one."""
+"""kv.attend where few bits would show: many small weights beside a large one,
+and queries whose elements lie far apart."""
 import math
 
 import pytest
@@ -6,7 +7,7 @@ import torch
 
 import kv_reference as ref
 from lossless_bf16_tensor_amd import kv
-from test_gpu_kv_attend import BF16, DEV, E5M2, F16
+from test_gpu_kv_attend import BF16, DEV, E5M2, F16, check, make
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +38,37 @@ def test_small_weights_beside_a_large_one(q, cache, B, T, hq, H, S, D, at):
     bound = want * (ref.HALF[q] + 2.0 ** -16) + 1.5 * S * 2.0 ** -36
     ref.within(out, want, bound, "out")
     ref.within(lse, (18.0 + torch.log1p(small)).expand(B, T, hq), torch.tensor(2.0 ** -17), "lse")
+
+
+@pytest.mark.parametrize("T,hq,H,D", [(1, 4, 2, 128), (6, 8, 2, 64), (20, 6, 2, 72), (9, 8, 2, 256)])
+@pytest.mark.parametrize("far", [20, 40, 100])
+def test_queries_of_far_apart_elements(T, hq, H, D, far):
+    """BF16 queries of an E5M2 cache with one element 2^far above the others,
+    where the keys are zero, but for one where that still leaves the others a say."""
+    q, k, v, _ = make(2, T, hq, H, D, 300, BF16, E5M2, seed=far + D)
+    q[..., 3] = 2.0 ** far * torch.sign(q[..., 3])
+    k = k.float()
+    k[..., 3] = 0.0
+    if far == 20:
+        k[:, 7, :, 3] = 2.0 ** -14
+    check(q, k.to(E5M2), v, [300 - T, 100])
+
+
+def test_queries_of_far_apart_elements_share_keys():
+    B, T, hq, H, D, S = 5, 70, 32, 8, 64, 2405
+    g = torch.Generator().manual_seed(3)
+    q = torch.randn(B, T, hq, D, generator=g)
+    q[..., 5] *= 2.0 ** 30
+    k, v = torch.randn(B, S, H, D, generator=g), torch.randn(B, S, H, D, generator=g).to(E5M2)
+    k[..., 5] = 0.0
+    q, k = q.to(BF16), k.to(E5M2)
+    n = torch.tensor([S - T, 1000, 0, 2000, 1999], dtype=torch.int32)
+    lse = torch.empty(B, T, hq, device=DEV)
+    w = torch.zeros(B, H, S, device=DEV)
+    out = kv.attend(q.to(DEV), k.to(DEV), v.to(DEV), n.to(DEV), lse=lse, score=w)
+    for b, h in ((0, 0), (1, 7), (2, 3), (4, 5)):
+        at, heads = slice(b, b + 1), slice(4 * h, 4 * h + 4)
+        want = ref.attend(q[at, :, heads], k[at, :, h:h + 1], v[at, :, h:h + 1], n[at])
+        ref.within(out[at, :, heads], want["out"], want["out_bound"], f"out {b} {h}")
+        ref.within(lse[at, :, heads], want["lse"], want["lse_bound"], f"lse {b} {h}")
+        ref.within(w[at, h:h + 1], want["weight"], want["weight_bound"], f"score {b} {h}")
