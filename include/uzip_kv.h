@@ -132,7 +132,9 @@ int uzip_kv_append(const uzip_kv_cache_t *cache, const uzip_kv_append_args_t *a,
  *                             of exp(s - lse)
  * A query that sees nothing, or only keys with s = -inf, gives zeros and lse
  * -inf; so does a token i >= drafted[b]. Keys and values that a query does not
- * see have no effect on it, whatever they hold. Lengths are clamped to the
+ * see have no effect on it, whatever they hold. A seen value that is not finite
+ * leaves its element of the other queries' output not finite, an infinity or
+ * NaN, also where the weight of its key rounds to zero. Lengths are clamped to the
  * cache's capacity. Products are exact in binary32 sums; weights are rounded
  * to BF16 (BF16 caches) or F16 before the product with the values. lse and
  * score may be NULL. scale is in [2^-60, 2^60]. The result depends on

@@ -648,15 +648,19 @@ struct Rows {
 
     // What masked_tile left out: adds values that are not finite, among the
     // keys [lo, hi) of the drafted tokens' tiles, to the stored output of the
-    // rows that see them. Rare, and so written for few registers: a lane goes
-    // over its own outputs, after store().
+    // rows that see them, unless all their scores are -inf: those are zeros (of
+    // a split row the join says so). Rare, and so written for few registers: a
+    // lane goes over its own outputs, after store().
     __device__ inline void poison(const AttendParams &p, const Place &at)
     {
         const int b = at.b, h = at.h, n = at.n, nd = at.nd;
         const int lo = max(at.t0 * kTileKeys, n & ~(kTileKeys - 1)), hi = min(at.t1 * kTileKeys, at.end);
+        uint32_t none = 0;
+#pragma unroll
+        for (int rb = 0; rb < RB; rb++) none |= at.whole && l[rb] == 0.f ? 1u << rb : 0;
         for (int rb = 0; rb < RB; rb++) {
             const int r = row0 + rb * 16 + x, token = r / p.G, head = h * p.G + r % p.G;
-            if (r >= p.R || token >= nd) continue;
+            if (r >= p.R || token >= nd || none >> rb & 1) continue;
             for (int i = 0; i < DP / 4; i++) {
                 const int d = (i / (DP / VC / 4)) * 128 + g * 4 * VE + i % (DP / VC / 4);
                 if (d >= p.D) continue;
