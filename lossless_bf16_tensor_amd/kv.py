@@ -22,6 +22,10 @@ outside the pool are absent pages.
 Calls run on the current stream of the tensors' device, or on ``stream=``, and
 can be captured. A workspace passed as ``ws=`` must not be shared by calls that
 may overlap.
+
+No gradient is recorded: tensors that require one are refused unless gradients
+are switched off (``torch.no_grad``). :func:`rope` with ``inverse`` is the
+gradient of :func:`rope`; the others serve inference.
 """
 from __future__ import annotations
 
@@ -108,6 +112,14 @@ def _on(device: torch.device, stream):
 
 def _stream(device: torch.device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _no_gradient(*tensors):
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError("these operators record no gradient: call them under torch.no_grad(), or pass detached tensors "
+                                 "(the gradient of rope is rope with inverse=True)")
 
 
 def _strides(t: torch.Tensor):
@@ -231,6 +243,7 @@ def rope(x: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, *, amplitude: f
     turn, as halves (i, i + len(freq)) or interleaved (2i, 2i + 1). inverse
     turns back: the gradient, and what moves kept keys to other positions. out
     may be x."""
+    _no_gradient(x, freq, out)
     if x.dtype not in (torch.bfloat16, torch.float16):
         raise ValueError(f"expected bfloat16 or float16, got {x.dtype}")
     xs = _strides(x)
@@ -259,6 +272,7 @@ def append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, k_cache: to
     dim]; q may be None. pos defaults to length + 0, 1, ...; without freq
     nothing turns. length is not changed. Tokens from drafted on, past the
     cache's end or in an absent page are not written."""
+    _no_gradient(q, k, v, k_cache, v_cache, freq, out)
     B, T, H, D = k.shape
     if not (v.shape == k.shape and v.dtype == k.dtype and v.device == k.device):
         raise ValueError("k and v differ in shape, type or device")
@@ -320,6 +334,7 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, length
     of each query's sum of exponentials. A query that sees nothing gives zeros
     and -inf, as do those from drafted on. Masked keys and values have no
     effect, whatever they hold. out does not overlap the inputs."""
+    _no_gradient(q, k_cache, v_cache, score, lse, out)
     _types(q, k_cache)
     qs = _strides(q)
     B, T, hq, D = q.shape
@@ -380,6 +395,7 @@ def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, score: torch.Tensor, len
     ready for ``uzip.encode``; their scores [sequences, kv heads, keep]; min(length,
     keep); and where each came from, int32 [sequences, kv heads, keep], -1
     behind the last. Keys keep the positions they were turned to."""
+    _no_gradient(k_cache, v_cache, score, k_out, v_out)
     B = length.numel()
     cache, heads, dim, tokens = _cache(k_cache, v_cache, table, B)
     dev = k_cache.device
