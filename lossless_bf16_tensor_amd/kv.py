@@ -7,11 +7,12 @@ shapes, which the library cannot see, and passes pointers on.
 
 Caches. ``k`` and ``v`` are [sequences, tokens, kv heads, head dim], or with a
 page ``table`` (int32 [sequences, entries]) pools [pages, page, kv heads, head
-dim]; page is a power of two, at least 16. They may be any views whose last dim
-is contiguous and whose other strides are multiples of 8, so a cache kept
-[sequences, kv heads, tokens, head dim] is passed transposed. Element types:
-bfloat16, float16, or float8_e5m2 beside queries of either. The head dim is a
-multiple of 8 up to 256.
+dim]; page is a power of two, at least 16. They, queries and outputs may be any
+views that start on a 16-byte boundary, whose last dim is contiguous and whose
+other strides are multiples of 8 (that between tokens below 2^26), so a cache
+kept [sequences, kv heads, tokens, head dim] is passed transposed. Element
+types: bfloat16, float16, or float8_e5m2 beside queries of either. The head dim
+is a multiple of 8 up to 256. No tensor is empty.
 
 ``length`` (int32 [sequences], on the device) counts the tokens each sequence
 has; ``drafted`` (int32, optional) the new ones, when they are fewer than the
@@ -122,16 +123,28 @@ def _no_gradient(*tensors):
                                  "(the gradient of rope is rope with inverse=True)")
 
 
-def _strides(t: torch.Tensor):
+def _strides(t: torch.Tensor, what: str):
     """Strides of the first three dims; 0 for a dim of one element where its own does not fit the library's rules."""
     st = t.stride()
     if len(st) != 4:
-        raise ValueError(f"expected four dims, got {len(st)}")
+        raise ValueError(f"{what}: expected four dims, got {len(st)}")
+    if not t.numel():
+        raise ValueError(f"{what} is empty: {tuple(t.shape)}")
     s0, s1, s2, s3 = st
-    if s3 != 1 and t.shape[3] != 1:
-        raise ValueError("the head dim is not contiguous")
+    dim = t.shape[3]
+    if dim & 7 or dim > 256:
+        raise ValueError(f"{what}: the head dim is a multiple of 8 up to 256, got {dim}")
+    if s3 != 1:
+        raise ValueError(f"{what}: the head dim is not contiguous")
+    if t.data_ptr() & 15:
+        raise ValueError(f"{what} does not start on a 16-byte boundary")
     if (s0 | s1 | s2) & 7 or s1 >= 1 << 26:
-        return tuple(0 if t.shape[i] == 1 else st[i] for i in range(3))
+        st = tuple(0 if t.shape[i] == 1 else st[i] for i in range(3))
+        if (st[0] | st[1] | st[2]) & 7:
+            raise ValueError(f"{what}: strides are multiples of 8, got {t.stride()}")
+        if st[1] >= 1 << 26:
+            raise ValueError(f"{what}: the stride between tokens is below 2^26, got {st[1]}")
+        return st
     return s0, s1, s2
 
 
@@ -158,7 +171,7 @@ def _cache(k: torch.Tensor, v: torch.Tensor, table, seqs: int):
     dtype = _DTYPE.get(k.dtype)
     if dtype is None:
         raise ValueError(f"caches are bfloat16, float16 or float8_e5m2, got {k.dtype}")
-    ks, vs = _strides(k), _strides(v)
+    ks, vs = _strides(k, "the key cache"), _strides(v, "the value cache")
     first, second, heads, dim = k.shape
     if table is None:
         if first != seqs:
@@ -167,6 +180,8 @@ def _cache(k: torch.Tensor, v: torch.Tensor, table, seqs: int):
     if not (table.dtype == torch.int32 and table.dim() == 2 and table.shape[0] == seqs and table.device == k.device
             and table.shape[1] >= 1 and (table.stride(1) == 1 or table.shape[1] == 1)):
         raise ValueError(f"table: expected int32 [{seqs}, entries] with contiguous rows on {k.device}")
+    if second < 16 or second & (second - 1):
+        raise ValueError(f"pages hold a power of two of tokens, at least 16, got {second}")
     tokens = table.shape[1] * second
     return (_CACHE.pack(k.data_ptr(), v.data_ptr(), table.data_ptr(), *ks, *vs, table.stride(0) if seqs > 1 else 0, dtype,
                         seqs, heads, dim, tokens, second, first, 0), heads, dim, tokens)
@@ -246,7 +261,7 @@ def rope(x: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, *, amplitude: f
     _no_gradient(x, freq, out)
     if x.dtype not in (torch.bfloat16, torch.float16):
         raise ValueError(f"expected bfloat16 or float16, got {x.dtype}")
-    xs = _strides(x)
+    xs = _strides(x, "x")
     B, T, H, D = x.shape
     dev = x.device
     packed = _rope(freq, pos, amplitude, interleaved * _INTERLEAVED | inverse * _INVERSE, B, T, D, dev)
@@ -257,7 +272,7 @@ def rope(x: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, *, amplitude: f
             if not (out.shape == x.shape and out.dtype == x.dtype and out.device == dev):
                 raise ValueError("out differs from x in shape, type or device")
             _written(out, "out")
-        _check(lib().uzip_kv_rope(_TENSOR.pack(x.data_ptr(), *xs), _TENSOR.pack(out.data_ptr(), *_strides(out)),
+        _check(lib().uzip_kv_rope(_TENSOR.pack(x.data_ptr(), *xs), _TENSOR.pack(out.data_ptr(), *_strides(out, "out")),
                                   _DTYPE[x.dtype], B, T, H, D, packed, _stream(dev)), "rope")
     return out
 
@@ -277,6 +292,9 @@ def append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, k_cache: to
     if not (v.shape == k.shape and v.dtype == k.dtype and v.device == k.device):
         raise ValueError("k and v differ in shape, type or device")
     _types(k, k_cache)
+    new = (k.data_ptr(), *_strides(k, "k"), v.data_ptr(), *_strides(v, "v"))
+    if q is not None:
+        qs = _strides(q, "q")
     cache, heads, dim, _ = _cache(k_cache, v_cache, table, B)
     _written(k_cache, "the key cache")
     _written(v_cache, "the value cache")
@@ -290,7 +308,7 @@ def append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, k_cache: to
         packed = _rope(freq, pos, amplitude, interleaved * _INTERLEAVED, B, T, D, dev)
     with _on(dev, stream):
         if q is None:
-            qs = (0,) * 8
+            queries = (0,) * 8
             hq = 0
         else:
             if not (q.dim() == 4 and q.shape[0] == B and q.shape[1] == T and q.shape[3] == D and q.dtype == k.dtype
@@ -303,9 +321,8 @@ def append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, k_cache: to
                 if not (out.shape == q.shape and out.dtype == q.dtype and out.device == dev):
                     raise ValueError("out differs from q in shape, type or device")
                 _written(out, "out")
-            qs = (q.data_ptr(), *_strides(q), out.data_ptr(), *_strides(out))
-        args = _APPEND.pack(*qs, k.data_ptr(), *_strides(k), v.data_ptr(), *_strides(v), _counts(length, B, dev, "length"),
-                            _counts(drafted, B, dev, "drafted"), _DTYPE[k.dtype], T, hq, 0)
+            queries = (q.data_ptr(), *qs, out.data_ptr(), *_strides(out, "out"))
+        args = _APPEND.pack(*queries, *new, _counts(length, B, dev, "length"), _counts(drafted, B, dev, "drafted"), _DTYPE[k.dtype], T, hq, 0)
         _check(lib().uzip_kv_append(cache, args, packed, _stream(dev)), "append")
     return out if q is not None else None
 
@@ -336,7 +353,7 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, length
     effect, whatever they hold. out does not overlap the inputs."""
     _no_gradient(q, k_cache, v_cache, score, lse, out)
     _types(q, k_cache)
-    qs = _strides(q)
+    qs = _strides(q, "q")
     B, T, hq, D = q.shape
     dev = q.device
     cache, heads, dim, tokens = _cache(k_cache, v_cache, table, B)
@@ -367,9 +384,9 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, length
         if ws is None:
             ws = torch.empty(attend_workspace_bytes(B, heads, D, tokens, T, hq), dtype=torch.uint8, device=dev)
         else:
-            if not (ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev):
-                raise ValueError("ws: expected contiguous uint8")
-        args = _ATTEND.pack(q.data_ptr(), *qs, out.data_ptr(), *_strides(out), lse.data_ptr() if lse is not None else 0,
+            if not (ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev and not ws.data_ptr() & 15):
+                raise ValueError(f"ws: expected contiguous uint8 on {dev} from a 16-byte boundary")
+        args = _ATTEND.pack(q.data_ptr(), *qs, out.data_ptr(), *_strides(out, "out"), lse.data_ptr() if lse is not None else 0,
                             score.data_ptr() if score is not None else 0, *ss, _counts(length, B, dev, "length"),
                             _counts(drafted, B, dev, "drafted"), tree.data_ptr() if tree is not None else 0, *ts,
                             _DTYPE[q.dtype], T, hq, 1.0 / math.sqrt(D) if scale is None else scale, seen, 0)
@@ -417,8 +434,8 @@ def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, score: torch.Tensor, len
         if ws is None:
             need = evict_workspace_bytes(B, heads, seen)
             ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        elif not (ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev):
-            raise ValueError("ws: expected contiguous uint8")
+        elif not (ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev and not ws.data_ptr() & 15):
+            raise ValueError(f"ws: expected contiguous uint8 on {dev} from a 16-byte boundary")
         args = _EVICT.pack(score.data_ptr(), *ss, _counts(length, B, dev, "length"),
                            index.data_ptr(), kept.data_ptr(), left.data_ptr(), keep, sink, recent, seen)
         _check(lib().uzip_kv_evict(cache, _cache(*made, None, B)[0], args, 0 if ws is None else ws.data_ptr(),

@@ -35,3 +35,57 @@ def test_tensors_that_require_a_gradient(call, names):
             CALLS[call](o)
     with pytest.raises(ValueError, match="device tensors"):
         CALLS[call](operands())
+
+
+def moved(t, by):
+    """t's values `by` elements behind the start of its memory."""
+    whole = torch.zeros(t.numel() + by, dtype=t.dtype)
+    return whole[by:].view(t.shape)
+
+
+@pytest.mark.parametrize("call,names", [("rope", ("q", "out")), ("append", ("q", "new", "new_v", "k", "v", "out")), ("attend", ("q", "k", "v", "out")),
+                                        ("evict", ("k", "v"))])
+def test_views_that_do_not_fit_are_named(call, names):
+    """Off a 16-byte boundary, of strides that are not multiples of 8, empty, of
+    a head dim that is none: each says so. (Outputs are looked at last, on the
+    device: their rules are the inputs'.)"""
+    for name in names:
+        if name == "out":
+            continue
+        o = operands()
+        o[name] = moved(o[name], 4)
+        with pytest.raises(ValueError, match="16-byte"):
+            CALLS[call](o)
+        o = operands()
+        shape = o[name].shape
+        o[name] = torch.zeros(shape[0], shape[1], shape[2], 68, dtype=BF16)[..., :64]
+        with pytest.raises(ValueError, match="multiples of 8"):
+            CALLS[call](o)
+
+
+@pytest.mark.parametrize("shape,why", [((2, 0, 4, 64), "empty"), ((2, 1, 4, 60), "multiple of 8"), ((2, 1, 4, 264), "multiple of 8"), ((2, 4, 64), "four dims")])
+def test_shapes_that_do_not_fit_are_named(shape, why):
+    q = torch.zeros(shape, dtype=BF16)
+    with pytest.raises(ValueError, match=why):
+        kv._strides(q, "q")
+    if len(shape) == 4:
+        with pytest.raises(ValueError, match=why):
+            kv.rope(q, torch.zeros(shape[1], dtype=torch.int32), kv.rope_freq(8))
+        with pytest.raises(ValueError, match=why):
+            kv.attend(q, torch.zeros(2, 8, 2, shape[3], dtype=BF16), torch.zeros(2, 8, 2, shape[3], dtype=BF16), torch.zeros(2, dtype=torch.int32))
+
+
+def test_strides_of_one_element_are_free():
+    whole = torch.zeros(1, 3, 1, 68, dtype=BF16)
+    assert kv._strides(whole[:, :1, :, :64], "q") == (0, 0, 0)
+    assert kv._strides(torch.empty(1, 1, 1, 1 << 27, dtype=BF16, device="meta")[..., :64], "q") == (0, 0, 0)
+    with pytest.raises(ValueError, match="below 2"):
+        kv._strides(torch.empty(1, 2, 1, 1 << 26, dtype=BF16, device="meta")[..., :64], "q")
+
+
+def test_pages_that_do_not_fit_are_named():
+    o = operands()
+    with pytest.raises(ValueError, match="power of two"):
+        kv.attend(o["q"], o["k"], o["v"], o["n"], table=torch.zeros(2, 1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="power of two"):
+        kv.attend(o["q"], torch.zeros(2, 24, 2, 64, dtype=BF16), torch.zeros(2, 24, 2, 64, dtype=BF16), o["n"], table=torch.zeros(2, 1, dtype=torch.int32))
