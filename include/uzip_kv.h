@@ -107,7 +107,8 @@ int uzip_kv_rope(const uzip_kv_tensor_t *x, const uzip_kv_tensor_t *y, uint32_t 
  * capacity or in an absent page are dropped; nothing else in the cache is
  * written. q, k and v have the dtype BF16 or F16, and it is the cache's unless
  * the cache is E5M2. length is not changed. No two sequences may share a page
- * that is written. */
+ * that is written. q_out may be q with the same strides; otherwise nothing that
+ * is written overlaps anything else: not q_out and k or v, nor the two caches. */
 typedef struct uzip_kv_append_args {
     uzip_kv_tensor_t q, q_out, k, v;
     const int32_t   *length;    /* device, one per sequence */
@@ -169,7 +170,7 @@ uint64_t uzip_kv_attend_workspace_bytes(uint32_t seqs, uint32_t kv_heads, uint32
  * Kept tokens stay in order: slot j of out holds token index[b, h, j]; slots
  * from min(n, keep) on are zeros with index -1. out is contiguous (table
  * NULL), with cache's seqs, heads, dim and dtype and tokens = keep; its memory
- * does not overlap the cache. score_out (the kept tokens' scores, 0 behind
+ * does not overlap the cache, nor its keys its values. score_out (the kept tokens' scores, 0 behind
  * them) and length_out (min(n, keep)) may be NULL. sink + recent <= keep. */
 typedef struct uzip_kv_evict_args {
     const float   *score;

@@ -824,11 +824,13 @@ int uzip_kv_append(const uzip_kv_cache_t *cache, const uzip_kv_append_args_t *a,
     if (!a->length || !aligned(a->length, 4) || !aligned(a->drafted, 4)) return UZIP_EINVAL;
     if (a->tokens < 1 || a->tokens > (1u << 30) || (uint64_t)cache->seqs * a->tokens >= (1ull << 31)) return UZIP_EINVAL;
     if (rope && !valid_rope(rope, cache->dim)) return UZIP_EINVAL;
+    if (cache->k == cache->v) return UZIP_EINVAL;
     RopeParams p;
     memset(&p, 0, sizeof p);
     if (a->q.data || a->q_out.data) {
         if (!valid_tensor(a->q) || !valid_tensor(a->q_out) || a->heads < 1 || a->heads > 65535) return UZIP_EINVAL;
         if (a->q.data == a->q_out.data && !same_tensor(a->q, a->q_out)) return UZIP_EINVAL;
+        if (a->q_out.data == a->k.data || a->q_out.data == a->v.data) return UZIP_EINVAL;      // read beside it
         p.q = static_cast<const char *>(a->q.data);
         p.y = static_cast<char *>(a->q_out.data);
         p.qs0 = a->q.stride[0] * 2, p.qs1 = a->q.stride[1] * 2, p.qs2 = a->q.stride[2] * 2;
@@ -863,7 +865,7 @@ int uzip_kv_evict(const uzip_kv_cache_t *cache, const uzip_kv_cache_t *out, cons
     if (!a->score || !aligned(a->score, 4) || a->score_stride[0] < 0 || a->score_stride[1] < 0) return UZIP_EINVAL;
     if (!a->length || !aligned(a->length, 4) || !a->index || !aligned(a->index, 4)) return UZIP_EINVAL;
     if (!aligned(a->score_out, 4) || !aligned(a->length_out, 4) || !aligned(d_ws, 16)) return UZIP_EINVAL;
-    if (cache->k == out->k || cache->v == out->v) return UZIP_EINVAL;
+    if (cache->k == out->k || cache->v == out->v || cache->k == out->v || cache->v == out->k || out->k == out->v) return UZIP_EINVAL;
     const uint64_t rows = (uint64_t)cache->seqs * cache->heads;
     const EvictWs ws = evict_ws(rows, a->score_tokens);
     if (ws.bytes && !d_ws) return UZIP_EINVAL;

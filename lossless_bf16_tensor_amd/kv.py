@@ -286,7 +286,8 @@ def append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, k_cache: to
     length tokens, and returns the turned queries q [sequences, tokens, heads,
     dim]; q may be None. pos defaults to length + 0, 1, ...; without freq
     nothing turns. length is not changed. Tokens from drafted on, past the
-    cache's end or in an absent page are not written."""
+    cache's end or in an absent page are not written. out may be q; nothing else
+    that is written may overlap another tensor."""
     _no_gradient(q, k, v, k_cache, v_cache, freq, out)
     B, T, H, D = k.shape
     if not (v.shape == k.shape and v.dtype == k.dtype and v.device == k.device):

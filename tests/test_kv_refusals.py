@@ -89,3 +89,14 @@ def test_pages_that_do_not_fit_are_named():
         kv.attend(o["q"], o["k"], o["v"], o["n"], table=torch.zeros(2, 1, dtype=torch.int32))
     with pytest.raises(ValueError, match="power of two"):
         kv.attend(o["q"], torch.zeros(2, 24, 2, 64, dtype=BF16), torch.zeros(2, 24, 2, 64, dtype=BF16), o["n"], table=torch.zeros(2, 1, dtype=torch.int32))
+
+
+def test_outputs_that_are_other_operands():
+    """By their addresses, which the library sees: the caches' keys as values,
+    turned queries over the new keys or values, kept keys as kept values."""
+    import test_kv_host as host
+    assert host.append(host.cache(v=1 << 20)) == host.EINVAL
+    assert host.append(out=host.tensor(1 << 23), k=host.tensor(1 << 23)) == host.EINVAL
+    assert host.append(out=host.tensor(1 << 23), v=host.tensor(1 << 23)) == host.EINVAL
+    for k, v in ((1 << 26, 1 << 26), (1 << 21, 1 << 27), (1 << 26, 1 << 20)):
+        assert host.evict(out=host.cache(k=k, v=v, tokens=16)) == host.EINVAL
