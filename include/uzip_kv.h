@@ -136,9 +136,11 @@ int uzip_kv_append(const uzip_kv_cache_t *cache, const uzip_kv_append_args_t *a,
  * see have no effect on it, whatever they hold. A seen value that is not finite
  * leaves its element of the other queries' output not finite, an infinity or
  * NaN, also where the weight of its key rounds to zero. Lengths are clamped to the
- * cache's capacity. Products are exact in binary32 sums; weights are rounded
- * to BF16 (BF16 caches) or F16 before the product with the values. lse and
- * score may be NULL. scale is in [2^-60, 2^60]. The result depends on
+ * cache's capacity. Products are exact in binary32 sums. Weights are multiplied
+ * with the values in two terms of the cache's type (F16 beside E5M2), so that
+ * little but the output's rounding shows; in one, rounded to half a step, where
+ * more than 64 rows (tokens * heads / cache->heads) share keys over much work,
+ * and for BF16 queries of an E5M2 cache. lse and score may be NULL. scale is in [2^-60, 2^60]. The result depends on
  * nothing but the inputs: no atomics. Outputs overlap no input. */
 typedef struct uzip_kv_attend_args {
     uzip_kv_tensor_t q, out;

@@ -364,9 +364,12 @@ __device__ inline void load_keys(const AttendParams &p, const Tile &t, int end, 
 }
 
 // A wave's RB blocks of 16 query rows and what it holds for them. DP: the head
-// dim rounded up to 64, 128 or 256 (PAD: it is smaller than that).
-template <int CT, int DP, int RB, bool PAD>
+// dim rounded up to 64, 128 or 256 (PAD: it is smaller than that). FINE: the
+// products with the values take the weights in two terms, the rounded ones and
+// what that left over, so that nothing but the output's rounding shows.
+template <int CT, int DP, int RB, bool PAD, bool FINE>
 struct Rows {
+    static constexpr int TERMS = FINE ? 2 : 1;           // of a weight
     static constexpr int KS = DP / 32;                   // steps of the product over the head dim
     static constexpr int VE = DP >= 128 ? 8 : 4;         // dims that a lane takes at once
     static constexpr int VC = DP >= 128 ? DP / 128 : 1;  // ... and how often
@@ -459,7 +462,7 @@ struct Rows {
     }
 
     // Scores to weights.
-    __device__ inline void weigh(float c2, const f32x4 (&s)[RB][2], u32x4 (&pw)[RB])
+    __device__ inline void weigh(float c2, const f32x4 (&s)[RB][2], u32x4 (&pw)[TERMS][RB])
     {
 #pragma unroll
         for (int rb = 0; rb < RB; rb++) {
@@ -473,9 +476,16 @@ struct Rows {
                     sum[hf] += w[hf][k];
                 }
             l[rb] += sum[0] + sum[1];
-            // The one rounding of the weights, half a step of the products'
-            // type. Their sum is taken before it: lse keeps binary32.
-            pw[rb] = u32x4{pack2<f16>(w[0][0], w[0][1]), pack2<f16>(w[0][2], w[0][3]), pack2<f16>(w[1][0], w[1][1]), pack2<f16>(w[1][2], w[1][3])};
+            // Without a second term this is a rounding to half a step of the
+            // products' type. The sum is taken before it: lse keeps binary32.
+            pw[0][rb] = u32x4{pack2<f16>(w[0][0], w[0][1]), pack2<f16>(w[0][2], w[0][3]), pack2<f16>(w[1][0], w[1][1]), pack2<f16>(w[1][2], w[1][3])};
+            if constexpr (FINE) {
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const f32x2 had = unpack2<f16>(pw[0][rb][i]);
+                    pw[1][rb][i] = pack2<f16>(w[i >> 1][2 * (i & 1)] - had.x, w[i >> 1][2 * (i & 1) + 1] - had.y);
+                }
+            }
         }
     }
 
@@ -495,7 +505,7 @@ struct Rows {
         return a;
     }
 
-    __device__ inline void add(const Values (&v)[VC][8], const u32x4 (&pw)[RB])
+    __device__ inline void add(const Values (&v)[VC][8], const u32x4 (&pw)[TERMS][RB])
     {
 #pragma unroll
         for (int c = 0; c < VC; c++)
@@ -503,7 +513,9 @@ struct Rows {
             for (int e = 0; e < VE; e++) {
                 const u32x4 a = fragment(v, c, e);
 #pragma unroll
-                for (int rb = 0; rb < RB; rb++) acc[rb][c * VE + e] = mfma<f16>(a, pw[rb], acc[rb][c * VE + e]);
+                for (int t = 0; t < TERMS; t++)
+#pragma unroll
+                    for (int rb = 0; rb < RB; rb++) acc[rb][c * VE + e] = mfma<f16>(a, pw[t][rb], acc[rb][c * VE + e]);
             }
     }
 
@@ -530,7 +542,7 @@ struct Rows {
     {
         const int n = at.n, nd = at.nd;
         f32x4 s[RB][2];
-        u32x4 pw[RB];
+        u32x4 pw[TERMS][RB];
         score(k, s);
         values(v);
         if (!t.fast) {
@@ -745,10 +757,15 @@ struct Rows {
 // (a copy of 1 GiB: 5.2); one token of 32 heads over 32 ragged sequences in
 // pages: 101 us, 4.6 TB/s; one over 2048 tokens: 9.3 us, mostly the start of a
 // launch and a first trip to memory.
+// Weights go in two terms, which the matrix cores have the time for: BF16 rows
+// of 128 over 2048 keys are off by 1.72e-3 of their norm, as if only the output
+// were rounded, and by 2.22e-3 with one; in 14.9 us both. Not so the FP16
+// weights of BF16 queries, three bits finer than the output: 1.689e-3 and
+// 1.698e-3, in 130 and 120 us (2 x 4 tokens over 131072 FP8 keys).
 template <int CT, int DP, int RB, bool PAD>
 __global__ __launch_bounds__(kWaves * 64, DP == 256 ? 1 : 2) void k_attend(AttendParams p)
 {
-    using W = Rows<CT, DP, RB, PAD>;
+    using W = Rows<CT, DP, RB, PAD, CT != kE5M2BF>;
     constexpr int KS = W::KS;
     __shared__ float smem[2 * RB * 16 * DP + W::join_words(kWaves)];
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -781,7 +798,7 @@ __global__ __launch_bounds__(kWaves * 64, DP == 256 ? 1 : 2) void k_attend(Atten
 #pragma unroll
                 for (int ks = 0; ks < KS; ks++) k[hf][ks] = widen<CT>(kr[hf][ks]);
             f32x4 s[RB][2];
-            u32x4 pw[RB];
+            u32x4 pw[W::TERMS][RB];
             w.score(k, s);
             if (nxt.fast) load_keys<CT, KS, PAD, false>(p, nxt, w.lim, w.x, w.g, koff, kr);
             w.raise(p.c2, s);
@@ -822,6 +839,10 @@ __global__ __launch_bounds__(kWaves * 64, DP == 256 ? 1 : 2) void k_attend(Atten
 // in order, so it is the source that is mixed.
 // wk == 1: every wave takes both tiles of a stage; wk == 2: pairs of waves
 // share rows and take one each.
+//
+// Weights go in one term here, rounded to half a step: the trees above take 118
+// us with two, 105 with one, and are off by 1.68e-3 and 2.08e-3 of their norm;
+// 32 FP16 rows' weights over 4 x 16384 keys 102 and 91 us, 2.16e-4 and 2.41e-4.
 constexpr int kShared = 8;                        // waves
 
 // A 16-byte read takes lanes {0-3, 12-15, 20-27}, then {4-11, 16-19, 28-31} and
@@ -842,7 +863,7 @@ template <int CT, int DP, bool PAD, bool PAGED>
 __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams p)
 {
     constexpr int RB = 2;
-    using W = Rows<CT, DP, RB, PAD>;
+    using W = Rows<CT, DP, RB, PAD, false>;
     constexpr int KS = W::KS, es = W::es, ROW = DP * es, PIECES = ROW / 16;
     constexpr int LOADS = 2 * 64 * ROW / (kShared * 64 * 16);      // 16-byte pieces a thread loads a stage
     constexpr int STAGE = 2 * 64 * ROW, RING = ROW == 256 ? 4 : 8;
@@ -959,7 +980,7 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
             f32x4 s[RB][2];
             const auto step = [&](const char *stage, int tile, const char *next_stage, int next_tile) {
                 typename W::Values v[W::VC][8];
-                u32x4 k[2][KS], pw[RB];
+                u32x4 k[2][KS], pw[W::TERMS][RB];
                 f32x4 next[RB][2];
                 keys_of(next_stage, next_tile, k);
                 values_of(stage, tile, v);

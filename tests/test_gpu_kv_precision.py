@@ -1,5 +1,5 @@
 """kv.attend where few bits would show: many small weights beside a large one,
-and queries whose elements lie far apart."""
+queries whose elements lie far apart, weights rounded before their product."""
 import math
 
 import pytest
@@ -7,7 +7,7 @@ import torch
 
 import kv_reference as ref
 from lossless_bf16_tensor_amd import kv
-from test_gpu_kv_attend import BF16, DEV, E5M2, F16, check, make
+from test_gpu_kv_attend import BF16, DEV, E5M2, F16, check, make, put, tree_of
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +72,25 @@ def test_queries_of_far_apart_elements_share_keys():
         ref.within(out[at, :, heads], want["out"], want["out_bound"], f"out {b} {h}")
         ref.within(lse[at, :, heads], want["lse"], want["lse_bound"], f"lse {b} {h}")
         ref.within(w[at, h:h + 1], want["weight"], want["weight_bound"], f"score {b} {h}")
+
+
+@pytest.mark.parametrize("q,cache", [(BF16, BF16), (F16, F16), (F16, E5M2)])
+@pytest.mark.parametrize("T,hq,H,D", [(1, 4, 2, 64), (3, 8, 2, 128), (30, 2, 2, 72), (9, 2, 2, 256)])
+@pytest.mark.parametrize("n", [0, 3, 40, 1000])
+def test_weights_are_not_rounded_to_the_caches_type(q, cache, T, hq, H, D, n):
+    """Where the keys are not shared: weights in two terms, each rounded to half
+    a step, so to (2^-8)^2 or (2^-11)^2 of themselves or, in FP16, to 2^-36 of
+    the largest; the rest is binary32. Scores are small, so that their own
+    rounding is."""
+    x, k, v, _ = make(2, T, hq, H, D, n + T, q, cache, seed=n + D, kscale=2.0 ** -7)
+    tree = tree_of(T, n, 2) | torch.eye(T, dtype=torch.bool)
+    length = torch.tensor([n, n // 2], dtype=torch.int32)
+    want = ref.attend(x, k, v, length, tree=tree)["out"]
+    spread = ref.attend(x, k, v.float().abs().to(cache), length, tree=tree)["out"]
+    out = kv.attend(put(x), put(k), put(v), length.to(DEV), tree=put(tree))
+    # a score's terms add up to less than 1/8: sums of D of them and a few roundings, and of 2^x; sums of n + T weights and
+    # of their products
+    assert float((x.float().abs().view(-1, D) @ k.float().abs().view(-1, D).t()).max()) / math.sqrt(D) < 0.125
+    ds = (D + 16) * 2.0 ** -23 / 8 + 2.0 ** -21
+    two = max(ref.HALF[BF16 if cache == BF16 else F16] ** 2, 2.0 ** -36 if cache != BF16 else 0.0)
+    ref.within(out, want, want.abs() * ref.HALF[q] * (1 + 2.0 ** -10) + ref.TINY[q] + spread * (1.01 * two + 2 * ds + 2 * (n + T) * 2.0 ** -24), "out")
