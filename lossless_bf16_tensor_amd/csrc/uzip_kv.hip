@@ -198,8 +198,16 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeParams p)
                     const float f = F16 ? f16_to_f32(z) : bf16_to_f32(z);
                     y[e] = lead ? x[e] * angle[i].x - f * angle[i].y : x[e] * angle[i].x + f * angle[i].y;
                 }
-                if (r.to) store8<CT>(dst + r.d * ces, y);
-                else store8<F16 ? kF16 : kBF16>(dst + r.d * 2, y);
+                const int keep = r.to == 2 ? 0 : max(0, min(p.rot - r.d, 8));   // elements from here on keep their bits
+                if (r.to && CT == kE5M2) {
+                    store8<CT>(dst + r.d * ces, y);
+                } else {
+                    u32x4 z;
+#pragma unroll
+                    for (int e = 0; e < 4; e++)    // rot is even
+                        z[e] = 2 * e < keep ? pack2<F16>(y[2 * e], y[2 * e + 1]) : w[e];
+                    *reinterpret_cast<u32x4 *>(dst + r.d * 2) = z;
+                }
             }
             __syncthreads();
         }
