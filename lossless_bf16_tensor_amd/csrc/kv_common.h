@@ -97,18 +97,13 @@ __device__ inline uint32_t pack4_e5m2(float a, float b, float c, float d)
     return (uint32_t)__builtin_amdgcn_cvt_pk_bf8_f32(c, d, w, true);
 }
 
-// The larger number, as the median with infinity: fmaxf takes another
-// instruction per operand to quiet a NaN that a product may hold. Of a NaN
-// this says nothing.
-__device__ inline float larger(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, INFINITY); }
-
-// max and sum over the four lanes l, l ^ 16, l ^ 32, l ^ 48
+// max (a NaN loses) and sum over the four lanes l, l ^ 16, l ^ 32, l ^ 48
 __device__ inline float quad_max(float x)
 {
     u32x2 r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false));
-    x = larger(__uint_as_float(r.x), __uint_as_float(r.y));
+    x = fmaxf(__uint_as_float(r.x), __uint_as_float(r.y));
     r = __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false));
-    return larger(__uint_as_float(r.x), __uint_as_float(r.y));
+    return fmaxf(__uint_as_float(r.x), __uint_as_float(r.y));
 }
 
 __device__ inline float quad_sum(float x)

@@ -9,10 +9,11 @@
 // Pieces of the key axis are joined by the same rule: first the waves of a
 // workgroup in LDS, then (k_attend_join_few, _many) the workgroups of a row.
 //
-// Up to 32 rows the cache's bytes are the bound, and k_attend takes them from
+// With few rows the cache's bytes are the bound, and k_attend takes them from
 // memory into registers: nothing goes through LDS on the way to the matrix
-// cores. With more rows the products are, and k_attend_shared lets eight waves
-// read the keys and values that one workgroup loads.
+// cores. With more than 64, over enough keys, the products are, and
+// k_attend_shared lets eight waves read the keys and values that one workgroup
+// loads.
 //
 // In both nothing but keys and values moves between lanes. With
 // v_mfma_f32_16x16x32 the wave computes S^T = K Q^T (16 keys x 16 rows): lane
@@ -411,7 +412,8 @@ struct Rows {
 #pragma unroll
             for (int e = 0; e < NV; e++) acc[rb][e] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
-        // keys these rows can see: a chain's later tokens are not read for earlier rows
+        // keys these rows can see: of a chain's later tokens, earlier rows need
+        // neither products nor, in k_attend, loads
         lim = end;
         if (!p.tree) lim = min(end, n + min((min(row0 + RB * 16, p.R) - 1) / p.G, p.T - 1) + 1);
     }
@@ -439,8 +441,8 @@ struct Rows {
         bool any = false;
 #pragma unroll
         for (int rb = 0; rb < RB; rb++) {
-            top[rb] = quad_max(larger(larger(larger(s[rb][0][0], s[rb][0][1]), larger(s[rb][0][2], s[rb][0][3])),
-                                      larger(larger(s[rb][1][0], s[rb][1][1]), larger(s[rb][1][2], s[rb][1][3]))));
+            top[rb] = quad_max(fmaxf(fmaxf(fmaxf(s[rb][0][0], s[rb][0][1]), fmaxf(s[rb][0][2], s[rb][0][3])),
+                                     fmaxf(fmaxf(s[rb][1][0], s[rb][1][1]), fmaxf(s[rb][1][2], s[rb][1][3]))));
             any = any || (top[rb] - m[rb]) * c2 > kSlack;
         }
         if (__builtin_expect(__builtin_amdgcn_ballot_w64(any) != 0 || far, 0)) {
@@ -826,10 +828,14 @@ __global__ __launch_bounds__(kWaves * 64, DP == 256 ? 1 : 2) void k_attend(Atten
 // Many rows: bound by the matrix cores and the exponentials. Eight waves of 32
 // rows each, two on a SIMD so that one's products run beside the other's
 // exponentials, read keys and values from LDS. A workgroup keeps a ring of
-// stages of 64 keys there, and all but one of them are under way: a stage is
-// worked on in less than half the time memory takes to answer, so that it is
-// the bytes under way (96 KB a CU and more) that keep the matrix cores fed.
-// They go from memory to LDS without passing registers. Trees of 64 tokens of
+// stages of 64 keys there. All but two are under way, one being worked on and
+// one just done with: a stage is worked on in less than half the time memory
+// takes to answer, so that it is the bytes under way that keep the matrix cores
+// fed (two stages of 32 KB of 16-bit heads of 128, six of 16 KB of half that,
+// six of 8 KB of FP8 heads of 64). They go from memory to LDS without passing
+// registers. Every wave's rows go over all of the workgroup's stages, also
+// those of a chain's tokens that they do not see: their products are left out,
+// their loads are not. Trees of 64 tokens of
 // 64 heads over 8 ragged sequences of up to 4109 keys of 128: 90 us, of which
 // 28 are the products at the rate of a large matrix product; a place begins in
 // 9 us and ends in 4, and a stage takes 3.
@@ -906,7 +912,9 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
         int entry = 0;
         const auto issue = [&](int i) {
             char *to = smem + i % RING * STAGE + wave * 1024;
-            if (PAGED && (i & 15) == 0) {         // page numbers of the next 64 half tiles, one a lane; -1 behind the last token
+            // page numbers of the next 64 half tiles, one a lane; -1 behind the
+            // last token. The wait for them is one for the stages under way too.
+            if (PAGED && (i & 15) == 0) {
                 const int key = key0 + (i * 4 + (tid & 63)) * 16;
                 entry = key < at.end ? p.c.table[at.b * p.c.ts + (key >> p.c.shift)] : -1;
                 __builtin_amdgcn_s_waitcnt(0x0f70);
@@ -1292,6 +1300,10 @@ Plan make_plan(uint32_t seqs, uint32_t kv_heads, uint32_t dim, uint32_t cache_to
     // of up to 1024 93 against 40); 16 x 1024 keys of 512 rows 61 against 81,
     // 1 x 2048 of them 40 against 31; 64 ragged sequences of up to 1024 keys
     // of 96 rows 113 against 62, 16 of up to 4096 66 against 77.
+    // The lengths are on the device, so this goes by the capacity, and where
+    // that is loose shares keys of too few tokens: 16 sequences of 480, 96 rows,
+    // 20 us in capacities up to 2048 and 32 from 8192; one of 1000, 512 rows, 28
+    // and 35; 64 of 480 55 and 59; from 1000 tokens and 96 rows on, within 5 %.
     const uint64_t groups = (uint64_t)seqs * kv_heads * (R > 128 ? (R + 255) / 256 : 1);
     a.shared = may_share && R > 64 && a.DP <= 128 && seqs * kv_heads * ((R + 31) / 32) * tiles > 100 * kCUs && (tiles >= 64 || groups <= kCUs);
     a.RB = !a.shared && R <= 16 ? 1 : 2;

@@ -412,7 +412,9 @@ def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, score: torch.Tensor, len
     keep, kv heads, dim] with the kept tokens in order and zeros behind them,
     ready for ``uzip.encode``; their scores [sequences, kv heads, keep]; min(length,
     keep); and where each came from, int32 [sequences, kv heads, keep], -1
-    behind the last. Keys keep the positions they were turned to."""
+    behind the last. Keys keep the positions they were turned to. Launches are
+    sized by what score can hold, not by length: where caches are much larger
+    than what is in them, pass slices that end behind the longest sequence."""
     _no_gradient(k_cache, v_cache, score, k_out, v_out)
     B = length.numel()
     cache, heads, dim, tokens = _cache(k_cache, v_cache, table, B)
