@@ -79,9 +79,34 @@ def lib():
     return _lib
 
 
-def _check(rc: int, what: str):
+_EINVAL = -1
+
+
+def _check(rc: int, what: str, **tensors):
+    """Raises for a refusal; one of these tensors may be the reason. What the
+    library checks is looked at here only then: a look at each tensor of a
+    call takes longer than the smallest kernels."""
     if rc != 0:
+        if rc == _EINVAL:
+            for name, t in tensors.items():
+                if t is not None:
+                    _fits(t, name)
         raise UzipError(rc, f"{what}: {lib().uzip_strerror(rc).decode()}")
+
+
+def _fits(t: torch.Tensor, what: str):
+    """Raises with the reason why the library takes no such tensor [sequences, tokens, heads, head dim]."""
+    if not t.numel():
+        raise ValueError(f"{what} is empty: {tuple(t.shape)}")
+    if t.shape[3] % 8 or t.shape[3] > 256:
+        raise ValueError(f"{what}: the head dim is a multiple of 8 up to 256, got {t.shape[3]}")
+    if t.data_ptr() % 16:
+        raise ValueError(f"{what} does not start on a 16-byte boundary")
+    st = _strides(t)
+    if any(s % 8 for s in st):
+        raise ValueError(f"{what}: strides are multiples of 8, got {t.stride()}")
+    if st[1] >= 1 << 26:
+        raise ValueError(f"{what}: the stride between tokens is below 2^26, got {st[1]}")
 
 
 class _Here:
@@ -115,36 +140,22 @@ def _stream(device: torch.device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
-def _no_gradient(*tensors):
+def _no_gradient():
     if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad:
-                raise ValueError("these operators record no gradient: call them under torch.no_grad(), or pass detached tensors "
-                                 "(the gradient of rope is rope with inverse=True)")
+        raise ValueError("these operators record no gradient: call them under torch.no_grad(), or pass detached tensors "
+                         "(the gradient of rope is rope with inverse=True)")
 
 
-def _strides(t: torch.Tensor, what: str):
+def _strides(t: torch.Tensor):
     """Strides of the first three dims; 0 for a dim of one element where its own does not fit the library's rules."""
     st = t.stride()
     if len(st) != 4:
-        raise ValueError(f"{what}: expected four dims, got {len(st)}")
-    if not t.numel():
-        raise ValueError(f"{what} is empty: {tuple(t.shape)}")
+        raise ValueError(f"expected four dims, got {len(st)}")
     s0, s1, s2, s3 = st
-    dim = t.shape[3]
-    if dim & 7 or dim > 256:
-        raise ValueError(f"{what}: the head dim is a multiple of 8 up to 256, got {dim}")
-    if s3 != 1:
-        raise ValueError(f"{what}: the head dim is not contiguous")
-    if t.data_ptr() & 15:
-        raise ValueError(f"{what} does not start on a 16-byte boundary")
+    if s3 != 1 and t.shape[3] != 1:
+        raise ValueError("the head dim is not contiguous")
     if (s0 | s1 | s2) & 7 or s1 >= 1 << 26:
-        st = tuple(0 if t.shape[i] == 1 else st[i] for i in range(3))
-        if (st[0] | st[1] | st[2]) & 7:
-            raise ValueError(f"{what}: strides are multiples of 8, got {t.stride()}")
-        if st[1] >= 1 << 26:
-            raise ValueError(f"{what}: the stride between tokens is below 2^26, got {st[1]}")
-        return st
+        return tuple(0 if t.shape[i] == 1 else st[i] for i in range(3))
     return s0, s1, s2
 
 
@@ -171,7 +182,7 @@ def _cache(k: torch.Tensor, v: torch.Tensor, table, seqs: int):
     dtype = _DTYPE.get(k.dtype)
     if dtype is None:
         raise ValueError(f"caches are bfloat16, float16 or float8_e5m2, got {k.dtype}")
-    ks, vs = _strides(k, "the key cache"), _strides(v, "the value cache")
+    ks, vs = _strides(k), _strides(v)
     first, second, heads, dim = k.shape
     if table is None:
         if first != seqs:
@@ -258,10 +269,11 @@ def rope(x: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, *, amplitude: f
     turn, as halves (i, i + len(freq)) or interleaved (2i, 2i + 1). inverse
     turns back: the gradient, and what moves kept keys to other positions. out
     may be x."""
-    _no_gradient(x, freq, out)
+    if x.requires_grad or freq.requires_grad or (out is not None and out.requires_grad):
+        _no_gradient()
     if x.dtype not in (torch.bfloat16, torch.float16):
         raise ValueError(f"expected bfloat16 or float16, got {x.dtype}")
-    xs = _strides(x, "x")
+    xs = _strides(x)
     B, T, H, D = x.shape
     dev = x.device
     packed = _rope(freq, pos, amplitude, interleaved * _INTERLEAVED | inverse * _INVERSE, B, T, D, dev)
@@ -272,8 +284,10 @@ def rope(x: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, *, amplitude: f
             if not (out.shape == x.shape and out.dtype == x.dtype and out.device == dev):
                 raise ValueError("out differs from x in shape, type or device")
             _written(out, "out")
-        _check(lib().uzip_kv_rope(_TENSOR.pack(x.data_ptr(), *xs), _TENSOR.pack(out.data_ptr(), *_strides(out, "out")),
-                                  _DTYPE[x.dtype], B, T, H, D, packed, _stream(dev)), "rope")
+        rc = lib().uzip_kv_rope(_TENSOR.pack(x.data_ptr(), *xs), _TENSOR.pack(out.data_ptr(), *_strides(out)),
+                                _DTYPE[x.dtype], B, T, H, D, packed, _stream(dev))
+    if rc:
+        _check(rc, "rope", x=x, out=out)
     return out
 
 
@@ -288,14 +302,13 @@ def append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, k_cache: to
     nothing turns. length is not changed. Tokens from drafted on, past the
     cache's end or in an absent page are not written. out may be q; nothing else
     that is written may overlap another tensor."""
-    _no_gradient(q, k, v, k_cache, v_cache, freq, out)
+    if (k.requires_grad or v.requires_grad or k_cache.requires_grad or v_cache.requires_grad or (q is not None and q.requires_grad)
+            or (freq is not None and freq.requires_grad) or (out is not None and out.requires_grad)):
+        _no_gradient()
     B, T, H, D = k.shape
     if not (v.shape == k.shape and v.dtype == k.dtype and v.device == k.device):
         raise ValueError("k and v differ in shape, type or device")
     _types(k, k_cache)
-    new = (k.data_ptr(), *_strides(k, "k"), v.data_ptr(), *_strides(v, "v"))
-    if q is not None:
-        qs = _strides(q, "q")
     cache, heads, dim, _ = _cache(k_cache, v_cache, table, B)
     _written(k_cache, "the key cache")
     _written(v_cache, "the value cache")
@@ -309,7 +322,7 @@ def append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, k_cache: to
         packed = _rope(freq, pos, amplitude, interleaved * _INTERLEAVED, B, T, D, dev)
     with _on(dev, stream):
         if q is None:
-            queries = (0,) * 8
+            qs = (0,) * 8
             hq = 0
         else:
             if not (q.dim() == 4 and q.shape[0] == B and q.shape[1] == T and q.shape[3] == D and q.dtype == k.dtype
@@ -322,9 +335,12 @@ def append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, k_cache: to
                 if not (out.shape == q.shape and out.dtype == q.dtype and out.device == dev):
                     raise ValueError("out differs from q in shape, type or device")
                 _written(out, "out")
-            queries = (q.data_ptr(), *qs, out.data_ptr(), *_strides(out, "out"))
-        args = _APPEND.pack(*queries, *new, _counts(length, B, dev, "length"), _counts(drafted, B, dev, "drafted"), _DTYPE[k.dtype], T, hq, 0)
-        _check(lib().uzip_kv_append(cache, args, packed, _stream(dev)), "append")
+            qs = (q.data_ptr(), *_strides(q), out.data_ptr(), *_strides(out))
+        args = _APPEND.pack(*qs, k.data_ptr(), *_strides(k), v.data_ptr(), *_strides(v), _counts(length, B, dev, "length"),
+                            _counts(drafted, B, dev, "drafted"), _DTYPE[k.dtype], T, hq, 0)
+        rc = lib().uzip_kv_append(cache, args, packed, _stream(dev))
+    if rc:
+        _check(rc, "append", q=q, k=k, v=v, k_cache=k_cache, v_cache=v_cache, out=out)
     return out if q is not None else None
 
 
@@ -352,15 +368,17 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, length
     of each query's sum of exponentials. A query that sees nothing gives zeros
     and -inf, as do those from drafted on. Masked keys and values have no
     effect, whatever they hold. out does not overlap the inputs."""
-    _no_gradient(q, k_cache, v_cache, score, lse, out)
+    if (q.requires_grad or k_cache.requires_grad or v_cache.requires_grad or (score is not None and score.requires_grad)
+            or (lse is not None and lse.requires_grad) or (out is not None and out.requires_grad)):
+        _no_gradient()
     _types(q, k_cache)
-    qs = _strides(q, "q")
+    qs = _strides(q)
     B, T, hq, D = q.shape
     dev = q.device
     cache, heads, dim, tokens = _cache(k_cache, v_cache, table, B)
     if k_cache.device != dev:
         raise ValueError("the cache is on another device")
-    if not (dim == D and hq >= heads and hq % heads == 0):
+    if not (dim == D and hq >= heads > 0 and hq % heads == 0):
         raise ValueError(f"{hq} query heads of {D} do not go with {heads} heads of {dim}")
     ts = (0, 0)
     if tree is not None:
@@ -385,13 +403,15 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, length
         if ws is None:
             ws = torch.empty(attend_workspace_bytes(B, heads, D, tokens, T, hq), dtype=torch.uint8, device=dev)
         else:
-            if not (ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev and not ws.data_ptr() & 15):
+            if not (ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev):
                 raise ValueError(f"ws: expected contiguous uint8 on {dev} from a 16-byte boundary")
-        args = _ATTEND.pack(q.data_ptr(), *qs, out.data_ptr(), *_strides(out, "out"), lse.data_ptr() if lse is not None else 0,
+        args = _ATTEND.pack(q.data_ptr(), *qs, out.data_ptr(), *_strides(out), lse.data_ptr() if lse is not None else 0,
                             score.data_ptr() if score is not None else 0, *ss, _counts(length, B, dev, "length"),
                             _counts(drafted, B, dev, "drafted"), tree.data_ptr() if tree is not None else 0, *ts,
                             _DTYPE[q.dtype], T, hq, 1.0 / math.sqrt(D) if scale is None else scale, seen, 0)
-        _check(lib().uzip_kv_attend(cache, args, ws.data_ptr(), ws.numel(), _stream(dev)), "attend")
+        rc = lib().uzip_kv_attend(cache, args, ws.data_ptr(), ws.numel(), _stream(dev))
+    if rc:
+        _check(rc, "attend", q=q, k_cache=k_cache, v_cache=v_cache, out=out)
     return out
 
 
@@ -415,7 +435,9 @@ def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, score: torch.Tensor, len
     behind the last. Keys keep the positions they were turned to. Launches are
     sized by what score can hold, not by length: where caches are much larger
     than what is in them, pass slices that end behind the longest sequence."""
-    _no_gradient(k_cache, v_cache, score, k_out, v_out)
+    if (k_cache.requires_grad or v_cache.requires_grad or score.requires_grad or (k_out is not None and k_out.requires_grad)
+            or (v_out is not None and v_out.requires_grad)):
+        _no_gradient()
     B = length.numel()
     cache, heads, dim, tokens = _cache(k_cache, v_cache, table, B)
     dev = k_cache.device
@@ -437,10 +459,12 @@ def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, score: torch.Tensor, len
         if ws is None:
             need = evict_workspace_bytes(B, heads, seen)
             ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        elif not (ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev and not ws.data_ptr() & 15):
+        elif not (ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev):
             raise ValueError(f"ws: expected contiguous uint8 on {dev} from a 16-byte boundary")
         args = _EVICT.pack(score.data_ptr(), *ss, _counts(length, B, dev, "length"),
                            index.data_ptr(), kept.data_ptr(), left.data_ptr(), keep, sink, recent, seen)
-        _check(lib().uzip_kv_evict(cache, _cache(*made, None, B)[0], args, 0 if ws is None else ws.data_ptr(),
-                                   0 if ws is None else ws.numel(), _stream(dev)), "evict")
+        rc = lib().uzip_kv_evict(cache, _cache(*made, None, B)[0], args, 0 if ws is None else ws.data_ptr(),
+                                 0 if ws is None else ws.numel(), _stream(dev))
+    if rc:
+        _check(rc, "evict", k_cache=k_cache, v_cache=v_cache, k_out=made[0], v_out=made[1])
     return made[0], made[1], kept, left, index

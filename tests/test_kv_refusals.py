@@ -3,6 +3,7 @@ import pytest
 import torch
 
 from lossless_bf16_tensor_amd import kv
+from lossless_bf16_tensor_amd.uzip import UzipError
 
 BF16 = torch.bfloat16
 
@@ -37,58 +38,44 @@ def test_tensors_that_require_a_gradient(call, names):
         CALLS[call](operands())
 
 
-def moved(t, by):
-    """t's values `by` elements behind the start of its memory."""
-    whole = torch.zeros(t.numel() + by, dtype=t.dtype)
-    return whole[by:].view(t.shape)
-
-
-@pytest.mark.parametrize("call,names", [("rope", ("q", "out")), ("append", ("q", "new", "new_v", "k", "v", "out")), ("attend", ("q", "k", "v", "out")),
-                                        ("evict", ("k", "v"))])
-def test_views_that_do_not_fit_are_named(call, names):
-    """Off a 16-byte boundary, of strides that are not multiples of 8, empty, of
-    a head dim that is none: each says so. (Outputs are looked at last, on the
-    device: their rules are the inputs'.)"""
-    for name in names:
-        if name == "out":
-            continue
-        o = operands()
-        o[name] = moved(o[name], 4)
-        with pytest.raises(ValueError, match="16-byte"):
-            CALLS[call](o)
-        o = operands()
-        shape = o[name].shape
-        o[name] = torch.zeros(shape[0], shape[1], shape[2], 68, dtype=BF16)[..., :64]
-        with pytest.raises(ValueError, match="multiples of 8"):
-            CALLS[call](o)
-
-
-@pytest.mark.parametrize("shape,why", [((2, 0, 4, 64), "empty"), ((2, 1, 4, 60), "multiple of 8"), ((2, 1, 4, 264), "multiple of 8"), ((2, 4, 64), "four dims")])
-def test_shapes_that_do_not_fit_are_named(shape, why):
-    q = torch.zeros(shape, dtype=BF16)
-    with pytest.raises(ValueError, match=why):
-        kv._strides(q, "q")
-    if len(shape) == 4:
+def test_views_that_do_not_fit_are_named():
+    """What the library refuses without a reason: off a 16-byte boundary, strides
+    that are not multiples of 8, too far apart, empty, of a head dim that is none."""
+    q = torch.zeros(2, 1, 4, 64, dtype=BF16)
+    kv._fits(q, "q")
+    for t, why in ((torch.zeros(q.numel() + 4, dtype=BF16)[4:].view(q.shape), "q does not start on a 16-byte"),
+                   (torch.zeros(2, 1, 4, 68, dtype=BF16)[..., :64], "multiples of 8"),
+                   (torch.empty(1, 2, 1, 1 << 26, dtype=BF16, device="meta")[..., :64], "below 2"),
+                   (torch.zeros(2, 0, 4, 64, dtype=BF16), "q is empty"), (torch.zeros(2, 1, 4, 60, dtype=BF16), "multiple of 8"),
+                   (torch.zeros(2, 1, 4, 264, dtype=BF16), "multiple of 8")):
         with pytest.raises(ValueError, match=why):
-            kv.rope(q, torch.zeros(shape[1], dtype=torch.int32), kv.rope_freq(8))
+            kv._fits(t, "q")
         with pytest.raises(ValueError, match=why):
-            kv.attend(q, torch.zeros(2, 8, 2, shape[3], dtype=BF16), torch.zeros(2, 8, 2, shape[3], dtype=BF16), torch.zeros(2, dtype=torch.int32))
+            kv._check(-1, "attend", x=q, q=t, out=None)
+    with pytest.raises(UzipError, match="attend"):
+        kv._check(-1, "attend", q=q)
+    with pytest.raises(UzipError, match="attend"):
+        kv._check(-2, "attend", q=torch.zeros(2, 1, 4, 60, dtype=BF16))
 
 
 def test_strides_of_one_element_are_free():
-    whole = torch.zeros(1, 3, 1, 68, dtype=BF16)
-    assert kv._strides(whole[:, :1, :, :64], "q") == (0, 0, 0)
-    assert kv._strides(torch.empty(1, 1, 1, 1 << 27, dtype=BF16, device="meta")[..., :64], "q") == (0, 0, 0)
-    with pytest.raises(ValueError, match="below 2"):
-        kv._strides(torch.empty(1, 2, 1, 1 << 26, dtype=BF16, device="meta")[..., :64], "q")
+    for t in (torch.zeros(1, 3, 1, 68, dtype=BF16)[:, :1, :, :64], torch.empty(1, 1, 1, 1 << 27, dtype=BF16, device="meta")[..., :64]):
+        assert kv._strides(t) == (0, 0, 0)
+        kv._fits(t, "q")
 
 
-def test_pages_that_do_not_fit_are_named():
+def test_no_heads():
     o = operands()
+    with pytest.raises(ValueError, match="query heads"):
+        kv.attend(o["q"], o["k"][:, :, :0], o["v"][:, :, :0], o["n"])
+
+
+@pytest.mark.parametrize("page", [8, 24])
+def test_pages_that_do_not_fit(page):
+    o = operands()
+    k, v = (torch.zeros(2, page, 2, 64, dtype=BF16) for _ in range(2))
     with pytest.raises(ValueError, match="power of two"):
-        kv.attend(o["q"], o["k"], o["v"], o["n"], table=torch.zeros(2, 1, dtype=torch.int32))
-    with pytest.raises(ValueError, match="power of two"):
-        kv.attend(o["q"], torch.zeros(2, 24, 2, 64, dtype=BF16), torch.zeros(2, 24, 2, 64, dtype=BF16), o["n"], table=torch.zeros(2, 1, dtype=torch.int32))
+        kv.attend(o["q"], k, v, o["n"], table=torch.zeros(2, 1, dtype=torch.int32))
 
 
 def test_outputs_that_are_other_operands():
