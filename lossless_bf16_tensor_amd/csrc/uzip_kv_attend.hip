@@ -755,9 +755,9 @@ struct Rows {
 // on every wk-th tile; keys one tile ahead in registers, values loaded while
 // the scores are worked out. One wave a SIMD at the larger head dims, two at
 // the others, keep 32 KB a CU on their way and more. A chain of 4 tokens of 64
-// heads over 2 x 131072 FP8 tokens of 8 heads of 128, 537 MB: 109 us, 4.9 TB/s
+// heads over 2 x 131072 FP8 tokens of 8 heads of 128, 537 MB: 108 us, 5.0 TB/s
 // (a copy of 1 GiB: 5.2); one token of 32 heads over 32 ragged sequences in
-// pages: 101 us, 4.6 TB/s; one over 2048 tokens: 9.3 us, mostly the start of a
+// pages: 105 us, 4.4 TB/s; one over 2048 tokens: 9.4 us, mostly the start of a
 // launch and a first trip to memory.
 // Weights go in two terms, which the matrix cores have the time for: BF16 rows
 // of 128 over 2048 keys are off by 1.72e-3 of their norm, as if only the output
@@ -835,10 +835,13 @@ __global__ __launch_bounds__(kWaves * 64, DP == 256 ? 1 : 2) void k_attend(Atten
 // six of 8 KB of FP8 heads of 64). They go from memory to LDS without passing
 // registers. Every wave's rows go over all of the workgroup's stages, also
 // those of a chain's tokens that they do not see: their products are left out,
-// their loads are not. Trees of 64 tokens of
-// 64 heads over 8 ragged sequences of up to 4109 keys of 128: 90 us, of which
-// 28 are the products at the rate of a large matrix product; a place begins in
-// 9 us and ends in 4, and a stage takes 3.
+// their loads are not.
+// Trees of 64 tokens of 64 heads over 8 ragged sequences of up to 4109 keys of
+// 128: 91 us, of which 28 are the products at the rate of a large matrix
+// product; a place begins in 9 us and ends in 4, and a stage takes 3. The
+// matrix cores are busy for 20 % of the time and the vector units for 45, with
+// permutes, maxima and moves (one vector instruction of 17 is an exponential);
+// waves wait a third of it for loads and barriers, and a third to issue.
 //
 // A row is kept in 16-byte pieces, piece c of row r at place c ^ mixed(r), so
 // that what 16 lanes read at once lies on all 64 banks; a load writes 64 places
@@ -1176,7 +1179,8 @@ __global__ __launch_bounds__(kWaves * 64) void k_attend_join_many(AttendParams p
 // k_attend, bit for bit. A workgroup has its rows in LDS, as the matrix cores
 // take them, for p.weigh_tiles tiles of each wave; read from memory for every
 // tile they took twice the time (32 tokens of 32 heads over 4 x 16384 keys of
-// 64: 50 us).
+// 64: 30 and 50 us). Bound by vector instructions, busy for 76 % of that; the
+// matrix cores are for 13, LDS for 12.
 template <int CT, int DP, bool PAD>
 __global__ __launch_bounds__(kWaves * 64, 2) void k_attend_weigh(AttendParams p)
 {
