@@ -78,6 +78,16 @@ __device__ inline uint32_t pack2(float a, float b)
         return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
+// ... each cut off toward zero
+template <bool F16>
+__device__ inline uint32_t cut2(float a, float b)
+{
+    if constexpr (F16)
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
+    else
+        return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
+
 template <bool F16>
 __device__ inline f32x2 unpack2(uint32_t w)
 {

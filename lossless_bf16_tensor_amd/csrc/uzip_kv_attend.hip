@@ -381,10 +381,11 @@ struct Rows {
     // Weights are 2^kLift at the row's maximum so far and below 2^(kLift +
     // kSlack) until it is raised. FP16 has no bits below 2^-24, and a first
     // token often has a score 15 to 20 above thousands of others: with the
-    // range used up to 2^15, their weights are kept to half a step of 2^-36 of
-    // the maximum, where without a lift and with a slack of 8 those below
-    // 2^-25 were lost from the output. BF16 reaches as low as binary32.
+    // range used up to 2^15, their weights are kept to 2^-35 of the maximum,
+    // where without a lift and with a slack of 8 those below 2^-25 were lost
+    // from the output. BF16 reaches as low as binary32.
     static constexpr float kSlack = f16 ? 4.f : 8.f, kLift = f16 ? 11.f : 0.f;
+    static constexpr float kLeast = f16 ? 0x1p-24f : 0x1p-126f;
     typedef uint32_t Values __attribute__((ext_vector_type(VW)));
 
     int x, g, row0, lim;
@@ -478,14 +479,21 @@ struct Rows {
                     sum[hf] += w[hf][k];
                 }
             l[rb] += sum[0] + sum[1];
-            // Without a second term this is a rounding to half a step of the
-            // products' type. The sum is taken before it: lse keeps binary32.
-            pw[0][rb] = u32x4{pack2<f16>(w[0][0], w[0][1]), pack2<f16>(w[0][2], w[0][3]), pack2<f16>(w[1][0], w[1][1]), pack2<f16>(w[1][2], w[1][3])};
-            if constexpr (FINE) {
+            // One term is a rounding to half a step of the products' type; the
+            // sum was taken before it: lse keeps binary32. Of two the first is
+            // cut off toward zero, so that the second is never negative, and
+            // that is made kLeast at least where the weight is not less: an
+            // infinite value times zero would be NaN, and infinities of both
+            // signs too.
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
+            for (int i = 0; i < 4; i++) {
+                const float a = w[i >> 1][2 * (i & 1)], b = w[i >> 1][2 * (i & 1) + 1];
+                if constexpr (FINE) {
+                    pw[0][rb][i] = cut2<f16>(a, b);
                     const f32x2 had = unpack2<f16>(pw[0][rb][i]);
-                    pw[1][rb][i] = pack2<f16>(w[i >> 1][2 * (i & 1)] - had.x, w[i >> 1][2 * (i & 1) + 1] - had.y);
+                    pw[1][rb][i] = pack2<f16>(__builtin_amdgcn_fmed3f(a - had.x, kLeast, a), __builtin_amdgcn_fmed3f(b - had.y, kLeast, b));
+                } else {
+                    pw[0][rb][i] = pack2<f16>(a, b);
                 }
             }
         }

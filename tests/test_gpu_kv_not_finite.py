@@ -58,3 +58,28 @@ def test_an_infinite_value_of_a_weight_near_zero_shows(dtype, cache, n, where):
     rest = [d for d in range(64) if d != 9]
     assert not torch.isfinite(got[..., 9]).any()
     assert torch.equal(got[..., rest], want[..., rest])
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF16, BF16), (F16, F16), (BF16, E5M2), (F16, E5M2)])
+@pytest.mark.parametrize("B,T,hq,H,D,n", [(1, 1, 1, 1, 64, 5), (2, 1, 8, 2, 128, 3000), (1, 6, 4, 1, 128, 900), (1, 3, 16, 2, 256, 500),
+                                          (16, 66, 32, 32, 64, 2334)])
+@pytest.mark.parametrize("equal", [False, True])
+def test_infinite_values_of_cached_tokens(dtype, cache, B, T, hq, H, D, n, equal):
+    """Infinities that every query sees, of weights that are powers of two
+    (equal keys) and any others: infinities of their sign, NaN where both signs
+    meet, and the other elements as they would be."""
+    g = torch.Generator().manual_seed(n + D)
+    q = torch.randn(B, T, hq, D, generator=g).to(dtype).to(DEV)
+    k = torch.randn(B, n + T, H, D, generator=g) * (0.0 if equal else 0.5)
+    v = torch.randn(B, n + T, H, D, generator=g).to(cache)
+    k, v = k.to(cache).to(DEV), v.to(DEV)
+    length = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    want = kv.attend(q, k, v, length)
+    assert torch.isfinite(want).all()
+    for key, d, value in ((0, 3, math.inf), (n // 2, 4, -math.inf), (n - 1, 60, math.inf), (n - 1, 5, math.inf), (1, 5, -math.inf), (2, 6, math.nan)):
+        bits(v)[:, key, :, d] = bits(torch.full((1,), value).to(cache)).to(DEV)
+    got = kv.attend(q, k, v, length)
+    assert (got[..., 3] == math.inf).all() and (got[..., 4] == -math.inf).all() and (got[..., 60] == math.inf).all()
+    assert torch.isnan(got[..., 5:7]).all()
+    rest = [d for d in range(D) if d not in (3, 4, 5, 6, 60)]
+    assert torch.equal(got[..., rest], want[..., rest])

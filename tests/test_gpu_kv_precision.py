@@ -20,9 +20,9 @@ def test_small_weights_beside_a_large_one(q, cache, B, T, hq, H, S, D, at):
     """One token's score is 18 above all others', as a first token's often is.
     Its values are zero, so the output is the others' share, N e^-18 / (1 + N
     e^-18) of their common value: a kernel that rounds weights of 2^-26 away
-    loses them. Weights of FP16 products may be off by half a step, 2^-36 of
-    the largest, of which there are N; the sums of N weights in binary32 and
-    the score's own rounding are far below the output's half step."""
+    loses them. Weights of FP16 products may be off by FP16's last step, 2^-24
+    where the largest is 2^11, so by 2^-35 of it each; the sums of N weights in
+    binary32 and the score's own rounding are far below the output's half step."""
     k, v = torch.zeros(1, S, 1, D), torch.full((1, S, 1, D), 1.5)
     k[:, at, :, 0], v[:, at] = 20.0, 0.0
     k, v = (t.to(cache).to(DEV).expand(B, S, H, D) for t in (k, v))
@@ -35,7 +35,7 @@ def test_small_weights_beside_a_large_one(q, cache, B, T, hq, H, S, D, at):
     out = kv.attend(x, k, v, n, scale=0.9, lse=lse)
     small = (seen - 1) * math.exp(-18.0)
     want = (1.5 * small / (1 + small))[..., None].expand(B, T, hq, D)
-    bound = want * (ref.HALF[q] + 2.0 ** -16) + 1.5 * S * 2.0 ** -36
+    bound = want * (ref.HALF[q] + 2.0 ** -16) + 1.5 * S * 2.0 ** -35
     ref.within(out, want, bound, "out")
     ref.within(lse, (18.0 + torch.log1p(small)).expand(B, T, hq), torch.tensor(2.0 ** -17), "lse")
 
@@ -78,9 +78,10 @@ def test_queries_of_far_apart_elements_share_keys():
 @pytest.mark.parametrize("T,hq,H,D", [(1, 4, 2, 64), (3, 8, 2, 128), (30, 2, 2, 72), (9, 2, 2, 256)])
 @pytest.mark.parametrize("n", [0, 3, 40, 1000])
 def test_weights_are_not_rounded_to_the_caches_type(q, cache, T, hq, H, D, n):
-    """Where the keys are not shared: weights in two terms, each rounded to half
-    a step, so to (2^-8)^2 or (2^-11)^2 of themselves or, in FP16, to 2^-36 of
-    the largest; the rest is binary32. Scores are small, so that their own
+    """Where the keys are not shared: weights in two terms, the first cut off, so
+    that less than a step is left, and that rounded to half a step of itself:
+    2^-7 2^-8 of the weight, or 2^-10 2^-11, or in FP16 its last step, 2^-35 of
+    the largest. The rest is binary32. Scores are small, so that their own
     rounding is."""
     x, k, v, _ = make(2, T, hq, H, D, n + T, q, cache, seed=n + D, kscale=2.0 ** -7)
     tree = tree_of(T, n, 2) | torch.eye(T, dtype=torch.bool)
@@ -92,5 +93,5 @@ def test_weights_are_not_rounded_to_the_caches_type(q, cache, T, hq, H, D, n):
     # of their products
     assert float((x.float().abs().view(-1, D) @ k.float().abs().view(-1, D).t()).max()) / math.sqrt(D) < 0.125
     ds = (D + 16) * 2.0 ** -23 / 8 + 2.0 ** -21
-    two = max(ref.HALF[BF16 if cache == BF16 else F16] ** 2, 2.0 ** -36 if cache != BF16 else 0.0)
-    ref.within(out, want, want.abs() * ref.HALF[q] * (1 + 2.0 ** -10) + ref.TINY[q] + spread * (1.01 * two + 2 * ds + 2 * (n + T) * 2.0 ** -24), "out")
+    two = 2.0 ** -15 if cache == BF16 else 2.0 ** -21
+    ref.within(out, want, want.abs() * ref.HALF[q] * (1 + 2.0 ** -10) + ref.TINY[q] + spread * (two + 2.0 ** -35 + 2 * ds + 2 * (n + T) * 2.0 ** -24), "out")
