@@ -763,9 +763,9 @@ struct Rows {
 // on every wk-th tile; keys one tile ahead in registers, values loaded while
 // the scores are worked out. One wave a SIMD at the larger head dims, two at
 // the others, keep 32 KB a CU on their way and more. A chain of 4 tokens of 64
-// heads over 2 x 131072 FP8 tokens of 8 heads of 128, 537 MB: 108 us, 5.0 TB/s
+// heads over 2 x 131072 FP8 tokens of 8 heads of 128, 537 MB: 110 us, 4.9 TB/s
 // (a copy of 1 GiB: 5.2); one token of 32 heads over 32 ragged sequences in
-// pages: 105 us, 4.4 TB/s; one over 2048 tokens: 9.4 us, mostly the start of a
+// pages: 103 us, 4.5 TB/s; one over 2048 tokens: 9.4 us, mostly the start of a
 // launch and a first trip to memory.
 // Weights go in two terms, which the matrix cores have the time for: BF16 rows
 // of 128 over 2048 keys are off by 1.72e-3 of their norm, as if only the output
