@@ -1315,7 +1315,7 @@ Plan make_plan(uint32_t seqs, uint32_t kv_heads, uint32_t dim, uint32_t cache_to
     // The lengths are on the device, so this goes by the capacity, and where
     // that is loose shares keys of too few tokens: 16 sequences of 480, 96 rows,
     // 20 us in capacities up to 2048 and 32 from 8192; one of 1000, 512 rows, 28
-    // and 35; 64 of 480 55 and 59; from 1000 tokens and 96 rows on, within 5 %.
+    // and 35; 64 of 480, 96 rows, 55 and 59; 16 of 2000 49 both.
     const uint64_t groups = (uint64_t)seqs * kv_heads * (R > 128 ? (R + 255) / 256 : 1);
     a.shared = may_share && R > 64 && a.DP <= 128 && seqs * kv_heads * ((R + 31) / 32) * tiles > 100 * kCUs && (tiles >= 64 || groups <= kCUs);
     a.RB = !a.shared && R <= 16 ? 1 : 2;
