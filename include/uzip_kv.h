@@ -140,7 +140,9 @@ int uzip_kv_append(const uzip_kv_cache_t *cache, const uzip_kv_append_args_t *a,
  * with the values in two terms of the cache's type (F16 beside E5M2), so that
  * little but the output's rounding shows; in one, rounded to half a step, where
  * more than 64 rows (tokens * heads / cache->heads) share keys over much work,
- * and for BF16 queries of an E5M2 cache. lse and score may be NULL. scale is in [2^-60, 2^60]. The result depends on
+ * and for BF16 queries of an E5M2 cache. What score adds is taken with lse as
+ * binary32 holds it, so it is off by 2^-23 |lse| of itself: of use below |lse|
+ * of about 2^16. lse and score may be NULL. scale is in [2^-60, 2^60]. The result depends on
  * nothing but the inputs: no atomics. Outputs overlap no input. */
 typedef struct uzip_kv_attend_args {
     uzip_kv_tensor_t q, out;
