@@ -12,6 +12,16 @@
  *   uzip_kv_evict   the cache cut to a number of tokens per head by that
  *                   weight, in the layout uzip_encode takes
  *
+ * and, where a small model drafts what the large one answers with:
+ *
+ *   uzip_kv_append_scaled, uzip_kv_attend_scaled
+ *                   the same over a cache in 8 bits with a scale for each
+ *                   block of tokens and head
+ *   uzip_kv_verify  which drafted tokens the target's probabilities accept
+ *   uzip_kv_accept  the accepted tokens of a tree moved up in the cache
+ *   uzip_kv_fork, uzip_kv_compact, uzip_kv_copy_pages
+ *                   the page table of the next step, and the pages it moves
+ *
  * Conventions are those of uzip.h: device pointers (d_* and the pointers in
  * the structures below) are memory that the caller owns, 16-byte aligned
  * unless a comment says otherwise; the library allocates no device memory and
@@ -40,6 +50,9 @@ extern "C" {
 #define UZIP_KV_BF16 0u
 #define UZIP_KV_F16  1u
 #define UZIP_KV_E5M2 2u       /* caches only */
+#define UZIP_KV_F32  2u       /* probabilities only */
+#define UZIP_KV_E4M3 3u       /* caches with scales only: no infinities, largest value 448 */
+#define UZIP_KV_I8   4u       /* caches with scales only: integers, -128 too though none is written */
 
 /* A cache of keys and values.
  * Contiguous (table NULL): element (sequence b, token t, head h, dim d) of the
@@ -194,6 +207,163 @@ int uzip_kv_evict(const uzip_kv_cache_t *cache, const uzip_kv_cache_t *out, cons
 /* Workspace of uzip_kv_evict, cache_tokens the scores a row holds; 0 when it
  * needs none (d_ws may then be NULL) or the shapes are invalid. */
 uint64_t uzip_kv_evict_workspace_bytes(uint32_t seqs, uint32_t kv_heads, uint32_t cache_tokens);
+
+/* Scales of an 8-bit cache: `block` tokens (a power of two, at least 16, at
+ * most the page) of a head share one for their keys and one for their values,
+ * and an element stands for itself times it. That of token t of sequence b,
+ * head h: k[b * k_stride[0] + t / block * k_stride[1] + h * k_stride[2]]; in
+ * pages, of row r of page p: k[p * k_stride[0] + r / block * k_stride[1] + ...].
+ * Strides are any that are not negative; 4-byte aligned. Scales of blocks that
+ * are seen are positive, in [2^-100, 2^100]. */
+typedef struct uzip_kv_scales {
+    float   *k;
+    float   *v;
+    int64_t  k_stride[3];
+    int64_t  v_stride[3];
+    uint32_t block;
+    uint32_t reserved;          /* 0 */
+} uzip_kv_scales_t;
+
+/* async. uzip_kv_append for a cache of E4M3 or I8. The new tokens that a block
+ * of a head receives (before they are rounded to any other type) have a largest
+ * finite magnitude a, and MAX is 448 or 127. If the block has earlier tokens
+ * (below length[b]) and a <= scale * MAX, its scale stays; otherwise it becomes
+ * the smallest power of two, at least 2^-60, with a <= scale * MAX, and earlier
+ * tokens of the block are rounded to it, each element times old scale / new
+ * scale. An element is x / scale rounded to nearest even in binary32; beyond
+ * MAX it is MAX with its sign, and NaN is NaN in E4M3, 0 in I8. Of a block that
+ * receives nothing nothing is written. */
+int uzip_kv_append_scaled(const uzip_kv_cache_t *cache, const uzip_kv_scales_t *scales, const uzip_kv_append_args_t *a,
+                          const uzip_kv_rope_t *rope, hipStream_t s);
+
+/* async. uzip_kv_attend over a cache of E4M3 or I8, with queries of BF16 or
+ * F16. The workspace is that of uzip_kv_attend. Weights times the values'
+ * scales are multiplied with the values in two terms of BF16; in one, for BF16
+ * queries, where more than 64 rows share keys over much work. */
+int uzip_kv_attend_scaled(const uzip_kv_cache_t *cache, const uzip_kv_scales_t *scales, const uzip_kv_attend_args_t *a,
+                          void *d_ws, uint64_t ws_bytes, hipStream_t s);
+
+/* async. Which drafted tokens the target accepts. Each sequence has a tree of
+ * nodes: node 0 is its last token, node i > 0 is a drafted token tokens[b, i]
+ * that follows node parent[b, i] < i (without parent, node i - 1); the children
+ * of a node are tried in their order. target[b, i] holds the target's
+ * probabilities of the token behind node i. draft[b, i], if there, holds those
+ * that the children of node i were drawn from, each anew; without draft they
+ * were chosen, not drawn. With c = 0 and mass = 1 at a node's first child, x =
+ * tokens[b, i] and u = uniform[b, i] in [0, 1):
+ *   with draft     child i is accepted if u q(x) mass < max(p(x) - c q(x), 0);
+ *                  else c += mass, and mass = sum max(p - c q, 0)
+ *   without        child i is accepted if u mass < p(x), of a token not tried
+ *                  there before; else mass -= p(x), and x is taken out of p
+ * and the walk goes on at an accepted child. Where none is, the next token is
+ * the first one t with sum_{i <= t} left(i) > uniform[b, 0] sum left, left(i) =
+ * max(p(i) - c q(i), 0), or p without what was taken out; or p itself if that
+ * leaves nothing. All in binary64. The tokens are then distributed as the
+ * target's.
+ *   path[b]    the accepted nodes in order, node 0 first; -1 behind them
+ *   count[b]   how many they are
+ *   token[b]   the next token; -1 where there is no probability at all
+ * Sequences with drafted[b] = 0 have count 0 and token -1. Probabilities that
+ * are not finite or not positive count as 0; nodes with a parent or token that
+ * is none are passed over. */
+typedef struct uzip_kv_verify_args {
+    const void    *target;      /* [seqs, nodes, vocab] of dtype; a row is contiguous */
+    const void    *draft;       /* likewise, or NULL */
+    int64_t        target_stride[2];   /* sequence, node */
+    int64_t        draft_stride[2];
+    const int32_t *tokens;      /* [seqs, nodes], rows contiguous, as the next three */
+    const int32_t *parent;      /* or NULL: a chain */
+    const int32_t *drafted;     /* nodes of each sequence, node 0 among them; NULL: all */
+    const float   *uniform;
+    int64_t        tokens_stride;
+    int64_t        parent_stride;      /* 0: one tree for all */
+    int64_t        uniform_stride;
+    int32_t       *path;        /* [seqs, nodes], contiguous */
+    int32_t       *count;
+    int32_t       *token;
+    uint32_t       dtype;       /* BF16, F16 or F32 */
+    uint32_t       seqs;
+    uint32_t       nodes;       /* at most 1024 */
+    uint32_t       vocab;
+    uint64_t       reserved;    /* 0 */
+} uzip_kv_verify_args_t;
+int uzip_kv_verify(const uzip_kv_verify_args_t *a, void *d_ws, uint64_t ws_bytes, hipStream_t s);
+
+/* Workspace of uzip_kv_verify for these shapes; 0 when they are invalid. */
+uint64_t uzip_kv_verify_workspace_bytes(uint32_t seqs, uint32_t nodes, uint32_t vocab);
+
+/* async. Moves token length[b] + path[b, j] of sequence b to length[b] + j, for
+ * j < count[b]: what a tree's accepted nodes appended is then what a chain would
+ * have. path[b] increases, as uzip_kv_verify's does; entries with path[b, j] <=
+ * j or >= nodes, tokens outside the cache and absent pages are passed over.
+ * length is not changed. A cache without scales. */
+typedef struct uzip_kv_accept_args {
+    const int32_t *length;
+    const int32_t *path;        /* [seqs, nodes], rows contiguous */
+    int64_t        path_stride;
+    const int32_t *count;
+    uint32_t       nodes;       /* at most 1024 */
+    uint32_t       reserved;    /* 0 */
+} uzip_kv_accept_args_t;
+int uzip_kv_accept(const uzip_kv_cache_t *cache, const uzip_kv_accept_args_t *a, hipStream_t s);
+
+/* The page table of the next step. A page is in use if a sequence's table has
+ * it for its tokens, or if held[page] is not zero; all others are free. Entries
+ * of the tables behind the tokens are not looked at. */
+typedef struct uzip_kv_pages {
+    const int32_t *table;       /* [rows, entries], rows contiguous */
+    int64_t        table_stride;
+    const int32_t *length;      /* [rows] */
+    const int32_t *parent;      /* [seqs]; fork only */
+    const uint8_t *held;        /* [pages], or NULL */
+    int32_t       *out_table;   /* [seqs, entries], contiguous; not the table */
+    int32_t       *out_length;  /* [seqs]; fork only; not length */
+    int32_t       *moves;       /* fork: [seqs, 2]; compact: [min(seqs * entries, pages / 2), 2]; (from, to), -1 where there is none */
+    int32_t       *left;        /* fork: pages still free, or, negative, those that were lacking; compact: pages in use */
+    uint32_t       rows;
+    uint32_t       seqs;        /* compact: rows */
+    uint32_t       entries;
+    uint32_t       pages;
+    uint32_t       page;        /* tokens: a power of two, at least 16 */
+    uint32_t       room;        /* fork only */
+    uint64_t       reserved;    /* 0 */
+} uzip_kv_pages_t;
+
+/* async. Sequence b goes on where row parent[b] of the table is: it has its
+ * tokens, and pages for `room` more as far as the table has entries. A parent
+ * outside [0, rows) leaves an empty sequence; rows that are no parent are
+ * freed. Whole pages are shared. Of the sequences that have the same partly
+ * filled last page the first one keeps it, unless it is held or whole for
+ * another; the others get a copy (moves, for uzip_kv_copy_pages). New pages are
+ * the lowest free ones, in the order of sequences and entries; entries for which
+ * none is left are -1 (absent), and a copy that is not made loses its tokens.
+ * Absent pages stay absent. */
+int uzip_kv_fork(const uzip_kv_pages_t *a, void *d_ws, uint64_t ws_bytes, hipStream_t s);
+
+/* async. Moves pages so that those in use, n of them, are the first n of the
+ * pool: the tables' pages from n on go to the free ones below n, lowest to
+ * lowest. Held pages stay where they are, so with those above n some below it
+ * stay free. */
+int uzip_kv_compact(const uzip_kv_pages_t *a, void *d_ws, uint64_t ws_bytes, hipStream_t s);
+
+/* Workspace of both; 0 when the shapes are invalid. */
+uint64_t uzip_kv_pages_workspace_bytes(uint32_t pages, uint32_t seqs, uint32_t entries);
+
+/* A tensor of pages: byte address of a page's part (i, j), i < n[0], j < n[1]:
+ * data + page * page_stride + i * stride[0] + j * stride[1], each `run` bytes. */
+typedef struct uzip_kv_pool {
+    void    *data;
+    int64_t  page_stride;       /* bytes, as the others */
+    int64_t  stride[2];
+    uint32_t n[2];
+    uint32_t run;
+    uint32_t reserved;          /* 0 */
+} uzip_kv_pool_t;
+
+/* async. Copies page moves[i, 0] to page moves[i, 1] in each of n <= 8 pools,
+ * i < count. Entries outside [0, pages) are passed over. Pages that are copied
+ * to are distinct and none of those that are copied from. */
+int uzip_kv_copy_pages(const int32_t *moves, uint32_t count, const uzip_kv_pool_t *pools, uint32_t n, uint32_t pages, hipStream_t s);
 
 #ifdef __cplusplus
 }

@@ -8,7 +8,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 # the codec, and the KV-cache operators
-SRCS = [os.path.join(CSRC, f) for f in ("uzip.hip", "uzip_kv.hip", "uzip_kv_attend.hip")]
+SRCS = [os.path.join(CSRC, f) for f in ("uzip.hip", "uzip_kv.hip", "uzip_kv_attend.hip", "uzip_kv_attend8.hip",
+                                             "uzip_kv_append8.hip", "uzip_kv_step.hip")]
 LIB = os.path.join(HERE, "libuzip.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

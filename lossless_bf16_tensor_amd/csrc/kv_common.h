@@ -26,7 +26,7 @@ constexpr int kBF16 = (int)UZIP_KV_BF16, kF16 = (int)UZIP_KV_F16, kE5M2 = (int)U
 constexpr uint32_t kCUs = 256;                   // of the one GPU this library is for
 constexpr int64_t kMaxTokenStride = 1ll << 26;   // elements: 16 rows' offsets fit 32 bits
 
-constexpr uint32_t elem_size(int dtype) { return dtype == kE5M2 ? 1u : 2u; }
+constexpr uint32_t elem_size(int dtype) { return dtype >= kE5M2 ? 1u : 2u; }
 
 // A cache as kernels see it; strides in bytes. Capacity, page table and pool
 // bounds are the host's, so no device value can lead outside them.
@@ -36,6 +36,20 @@ struct CacheView {
     int64_t ks0, ks1, ks2, vs0, vs1, vs2, ts;
     uint32_t tokens, shift, pages;
 };
+
+// Scales of an 8-bit cache as kernels see them; strides in elements: page or
+// sequence, block, head.
+struct ScaleView {
+    float *k, *v;
+    int64_t k0, k1, k2, v0, v1, v2;
+    int shift;                                       // of a block's tokens
+};
+
+// a load at an address that is the same for a whole wave, of memory that the kernel does not write
+__device__ inline float scalar_load(const float *p)
+{
+    return *(const __attribute__((address_space(4))) float *)p;
+}
 
 // Byte offset of token t's page or sequence plus its row, or false when it
 // lies in an absent page. t < c.tokens.
@@ -148,20 +162,52 @@ inline bool valid_strides(const int64_t s[3])
 
 inline bool valid_tensor(const uzip_kv_tensor_t &t) { return t.data && aligned(t.data, 16) && valid_strides(t.stride); }
 
+inline bool same_tensor(const uzip_kv_tensor_t &a, const uzip_kv_tensor_t &b)
+{
+    return a.stride[0] == b.stride[0] && a.stride[1] == b.stride[1] && a.stride[2] == b.stride[2];
+}
+
+// a's queries, whose output they are, turned; checked by the caller
+int turn_in_place(const uzip_kv_append_args_t *a, uint32_t seqs, uint32_t dim, const uzip_kv_rope_t *rope, hipStream_t s);
+
 inline bool valid_dims(uint32_t seqs, uint32_t heads, uint32_t dim)
 {
     return seqs >= 1 && seqs <= 65535 && heads >= 1 && heads <= 4096 && dim >= 8 && dim <= 256 && dim % 8 == 0;
 }
 
-inline bool valid_cache(const uzip_kv_cache_t *c)
+// scaled: of the types that go with scales, else of the others
+inline bool valid_cache(const uzip_kv_cache_t *c, bool scaled = false)
 {
-    if (!c || !c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16) || c->dtype > UZIP_KV_E5M2) return false;
+    if (!c || !c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16)) return false;
+    if (scaled ? c->dtype != UZIP_KV_E4M3 && c->dtype != UZIP_KV_I8 : c->dtype > UZIP_KV_E5M2) return false;
     if (!valid_dims(c->seqs, c->heads, c->dim) || !valid_strides(c->k_stride) || !valid_strides(c->v_stride)) return false;
     if (c->tokens < 1 || c->tokens > (1u << 30) || c->reserved) return false;
     if (!c->table) return true;
     return aligned(c->table, 4) && c->page >= 16 && c->page <= (1u << 30) && !(c->page & (c->page - 1)) &&
            c->tokens % c->page == 0 && c->pages >= 1 && c->pages <= 0x7fffffffu && c->table_stride >= 0 &&
            c->table_stride <= (1ll << 40);
+}
+
+inline bool valid_scales(const uzip_kv_scales_t *f, const uzip_kv_cache_t *c)
+{
+    if (!f || !f->k || !f->v || !aligned(f->k, 4) || !aligned(f->v, 4) || f->reserved) return false;
+    if (f->block < 16 || f->block > (1u << 30) || (f->block & (f->block - 1)) || (c->table && f->block > c->page)) return false;
+    for (int i = 0; i < 3; i++)
+        if (f->k_stride[i] < 0 || f->v_stride[i] < 0 || f->k_stride[i] > (1ll << 40) || f->v_stride[i] > (1ll << 40)) return false;
+    return true;
+}
+
+inline ScaleView view_of(const uzip_kv_scales_t *f)
+{
+    return {f->k, f->v, f->k_stride[0], f->k_stride[1], f->k_stride[2], f->v_stride[0], f->v_stride[1], f->v_stride[2], __builtin_ctz(f->block)};
+}
+
+inline bool valid_rope(const uzip_kv_rope_t *r, uint32_t dim)
+{
+    if (r->reserved || (r->rot & 1) || r->rot > dim || (r->flags & ~(UZIP_KV_INTERLEAVED | UZIP_KV_INVERSE))) return false;
+    if (r->rot && (!r->freq || !aligned(r->freq, 8))) return false;
+    if (!(fabsf(r->amplitude) < INFINITY) || r->pos_stride < 0) return false;
+    return aligned(r->pos, 4);
 }
 
 inline CacheView view_of(const uzip_kv_cache_t *c)

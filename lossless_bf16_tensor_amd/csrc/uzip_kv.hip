@@ -261,14 +261,6 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope(RopeParams p)
     }
 }
 
-bool valid_rope(const uzip_kv_rope_t *r, uint32_t dim)
-{
-    if (r->reserved || (r->rot & 1) || r->rot > dim || (r->flags & ~(UZIP_KV_INTERLEAVED | UZIP_KV_INVERSE))) return false;
-    if (r->rot && (!r->freq || !aligned(r->freq, 8))) return false;
-    if (!(fabsf(r->amplitude) < INFINITY) || r->pos_stride < 0) return false;
-    return aligned(r->pos, 4);
-}
-
 int launch_rope(RopeParams &p, const uzip_kv_rope_t *r, uint32_t seqs, bool f16, int ct, hipStream_t s)
 {
     p.freq = r ? r->freq : nullptr;
@@ -321,11 +313,6 @@ int launch_rope(RopeParams &p, const uzip_kv_rope_t *r, uint32_t seqs, bool f16,
 #undef UZIP_KV_ROPE
     UZIP_KV_LAUNCH_CHECK("k_rope");
     return UZIP_OK;
-}
-
-bool same_tensor(const uzip_kv_tensor_t &a, const uzip_kv_tensor_t &b)
-{
-    return a.stride[0] == b.stride[0] && a.stride[1] == b.stride[1] && a.stride[2] == b.stride[2];
 }
 
 // ------------------------------------------------------------------ evict --
@@ -803,6 +790,19 @@ EvictWs evict_ws(uint64_t rows, uint32_t tokens)
 }
 
 }  // namespace
+
+int turn_in_place(const uzip_kv_append_args_t *a, uint32_t seqs, uint32_t dim, const uzip_kv_rope_t *rope, hipStream_t s)
+{
+    RopeParams p;
+    memset(&p, 0, sizeof p);
+    p.q = static_cast<const char *>(a->q.data);
+    p.y = static_cast<char *>(a->q_out.data);
+    p.qs0 = p.ys0 = a->q.stride[0] * 2, p.qs1 = p.ys1 = a->q.stride[1] * 2, p.qs2 = p.ys2 = a->q.stride[2] * 2;
+    p.length = a->length;
+    p.T = (int)a->tokens, p.Hq = (int)a->heads, p.D = (int)dim;
+    return launch_rope(p, rope, seqs, a->dtype == UZIP_KV_F16, (int)a->dtype, s);
+}
+
 }  // namespace uzip_kv
 
 extern "C" {

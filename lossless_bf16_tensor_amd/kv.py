@@ -1,8 +1,8 @@
 """KV-cache operators (C-ABI: include/uzip_kv.h) over torch tensors.
 
 What a serving step does to a cache before it is encoded for its transfer and
-after it is decoded: :func:`rope`, :func:`append`, :func:`attend` and
-:func:`evict`. Every step runs in the library's HIP kernels; this module checks
+after it is decoded: :func:`rope`, :func:`append`, :func:`attend`,
+:func:`evict`, and those of drafted tokens and pages below. Every step runs in the library's HIP kernels; this module checks
 shapes, which the library cannot see, and passes pointers on.
 
 Caches. ``k`` and ``v`` are [sequences, tokens, kv heads, head dim], or with a
@@ -13,6 +13,15 @@ other strides are multiples of 8 (that between tokens below 2^26), so a cache
 kept [sequences, kv heads, tokens, head dim] is passed transposed. Element
 types: bfloat16, float16, or float8_e5m2 beside queries of either. The head dim
 is a multiple of 8 up to 256. No tensor is empty.
+
+Caches in 8 bits with scales (:func:`append` and :func:`attend` with k_scale and
+v_scale) are float8_e4m3fn or int8. A block of tokens of a head, a power of two,
+at least 16, shares a scale for its keys and one for its values: float32
+[sequences, blocks, kv heads], or [pages, blocks of a page, kv heads], any
+strides; the number of blocks says how long they are.
+
+Steps with drafted tokens go on with :func:`verify`, :func:`accept` and, where
+caches are in pages, :func:`fork`, :func:`compact` and :func:`copy_pages`.
 
 ``length`` (int32 [sequences], on the device) counts the tokens each sequence
 has; ``drafted`` (int32, optional) the new ones, when they are fewer than the
@@ -41,18 +50,28 @@ from .uzip import UzipError, lib as _codec_lib
 
 # every symbol include/uzip_kv.h declares
 EXPORTS = ("uzip_kv_rope", "uzip_kv_append", "uzip_kv_attend", "uzip_kv_attend_workspace_bytes", "uzip_kv_evict",
-           "uzip_kv_evict_workspace_bytes")
+           "uzip_kv_evict_workspace_bytes", "uzip_kv_append_scaled", "uzip_kv_attend_scaled", "uzip_kv_verify",
+           "uzip_kv_verify_workspace_bytes", "uzip_kv_accept", "uzip_kv_fork", "uzip_kv_compact", "uzip_kv_copy_pages",
+           "uzip_kv_pages_workspace_bytes")
 
 _DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e5m2: 2}
+_SCALED = {torch.float8_e4m3fn: 3, torch.int8: 4}
+_PROBABILITY = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 _INTERLEAVED, _INVERSE = 1, 2
 
-# uzip_kv_cache_t, uzip_kv_rope_t, uzip_kv_append_args_t, uzip_kv_attend_args_t, uzip_kv_evict_args_t
+# uzip_kv_cache_t, uzip_kv_rope_t, uzip_kv_append_args_t, uzip_kv_attend_args_t, uzip_kv_evict_args_t,
+# uzip_kv_scales_t, uzip_kv_verify_args_t, uzip_kv_accept_args_t, uzip_kv_pages_t, uzip_kv_pool_t
 _CACHE = struct.Struct("=3Q7q8I")
 _ROPE = struct.Struct("=2Qq2IfI")
 _TENSOR = struct.Struct("=Q3q")
 _APPEND = struct.Struct("=16q2Q4I")
 _ATTEND = struct.Struct("=8q2Q2q3Q2q3If2I")
 _EVICT = struct.Struct("=Q2q4Q4I")
+_SCALES = struct.Struct("=2Q6q2I")
+_VERIFY = struct.Struct("=2Q4q4Q3q3Q4IQ")
+_ACCEPT = struct.Struct("=2QqQ2I")
+_PAGES = struct.Struct("=Qq7Q6IQ")
+_POOL = struct.Struct("=Q3q4I")
 
 _lib = None
 
@@ -70,6 +89,15 @@ def lib():
             "uzip_kv_attend_workspace_bytes": (u64, [u32] * 6),
             "uzip_kv_evict": (ctypes.c_int, [st, st, st, vp, u64, vp]),
             "uzip_kv_evict_workspace_bytes": (u64, [u32] * 3),
+            "uzip_kv_append_scaled": (ctypes.c_int, [st, st, st, st, vp]),
+            "uzip_kv_attend_scaled": (ctypes.c_int, [st, st, st, vp, u64, vp]),
+            "uzip_kv_verify": (ctypes.c_int, [st, vp, u64, vp]),
+            "uzip_kv_verify_workspace_bytes": (u64, [u32] * 3),
+            "uzip_kv_accept": (ctypes.c_int, [st, st, vp]),
+            "uzip_kv_fork": (ctypes.c_int, [st, vp, u64, vp]),
+            "uzip_kv_compact": (ctypes.c_int, [st, vp, u64, vp]),
+            "uzip_kv_copy_pages": (ctypes.c_int, [vp, u32, st, u32, u32, vp]),
+            "uzip_kv_pages_workspace_bytes": (u64, [u32] * 3),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -175,13 +203,15 @@ def _counts(t, seqs: int, device, what: str) -> int:
     return t.data_ptr()
 
 
-def _cache(k: torch.Tensor, v: torch.Tensor, table, seqs: int):
+def _cache(k: torch.Tensor, v: torch.Tensor, table, seqs: int, scaled: bool = False):
     """(packed uzip_kv_cache_t, kv heads, head dim, tokens a sequence)"""
     if not (k.shape == v.shape and k.dtype == v.dtype and k.device == v.device):
         raise ValueError("k and v caches differ in shape, type or device")
-    dtype = _DTYPE.get(k.dtype)
+    dtype = (_SCALED if scaled else _DTYPE).get(k.dtype)
     if dtype is None:
-        raise ValueError(f"caches are bfloat16, float16 or float8_e5m2, got {k.dtype}")
+        if k.dtype in _SCALED:
+            raise ValueError(f"caches of {k.dtype} go with k_scale and v_scale, where a call takes them")
+        raise ValueError(f"caches are bfloat16, float16 or float8_e5m2, with scales float8_e4m3fn or int8, got {k.dtype}")
     ks, vs = _strides(k), _strides(v)
     first, second, heads, dim = k.shape
     if table is None:
@@ -198,6 +228,27 @@ def _cache(k: torch.Tensor, v: torch.Tensor, table, seqs: int):
                         seqs, heads, dim, tokens, second, first, 0), heads, dim, tokens)
 
 
+def _block(scale: torch.Tensor, tokens: int) -> int:
+    """Tokens that share a scale: the power of two, at least 16, of which a tensor of `tokens` has scale.shape[1]."""
+    block = 16
+    while block < tokens and -(-tokens // block) > scale.shape[1]:
+        block *= 2
+    return block if -(-tokens // block) == scale.shape[1] else 0
+
+
+def _scales(k_scale, v_scale, cache: torch.Tensor):
+    """Packed uzip_kv_scales_t."""
+    if k_scale is None or v_scale is None:
+        raise ValueError("k_scale and v_scale go together")
+    first, second, heads, _ = cache.shape
+    block = _block(k_scale, second) if k_scale.dim() == 3 else 0
+    for t in (k_scale, v_scale):
+        if not (t.dtype == torch.float32 and t.device == cache.device and block and t.shape == (first, -(-second // block), heads)):
+            raise ValueError(f"k_scale, v_scale: expected float32 [{first}, blocks, {heads}] on {cache.device}, blocks of a power of two "
+                             f"of tokens, at least 16, {second} tokens in all")
+    return _SCALES.pack(k_scale.data_ptr(), v_scale.data_ptr(), *k_scale.stride(), *v_scale.stride(), block, 0)
+
+
 def _score(score, seqs: int, heads: int, tokens: int, table, device):
     """((sequence, head) strides, tokens) of accumulated weights: as many tokens as the cache, or fewer when it is in pages."""
     n = score.shape[-1]
@@ -210,7 +261,7 @@ def _score(score, seqs: int, heads: int, tokens: int, table, device):
 def _types(new: torch.Tensor, cache: torch.Tensor):
     if new.dtype not in (torch.bfloat16, torch.float16):
         raise ValueError(f"expected bfloat16 or float16, got {new.dtype}")
-    if cache.dtype not in (new.dtype, torch.float8_e5m2):
+    if cache.dtype not in (new.dtype, torch.float8_e5m2, torch.float8_e4m3fn, torch.int8):
         raise ValueError(f"{new.dtype} does not go with a {cache.dtype} cache")
 
 
@@ -294,22 +345,34 @@ def rope(x: torch.Tensor, pos: torch.Tensor, freq: torch.Tensor, *, amplitude: f
 def append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
            length: torch.Tensor, freq: torch.Tensor | None = None, *, pos: torch.Tensor | None = None,
            table: torch.Tensor | None = None, drafted: torch.Tensor | None = None, amplitude: float = 1.0,
-           interleaved: bool = False, out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+           interleaved: bool = False, k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None,
+           out: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
     """Writes new tokens' keys k (turned to their positions) and values v
     [sequences, tokens, kv heads, dim] into the cache behind each sequence's
     length tokens, and returns the turned queries q [sequences, tokens, heads,
     dim]; q may be None. pos defaults to length + 0, 1, ...; without freq
     nothing turns. length is not changed. Tokens from drafted on, past the
     cache's end or in an absent page are not written. out may be q; nothing else
-    that is written may overlap another tensor."""
+    that is written may overlap another tensor.
+
+    With k_scale and v_scale the cache is float8_e4m3fn or int8, and a block of a
+    head that receives tokens gets a scale that holds them: its own, if it has
+    earlier tokens and that does, else the smallest power of two that does, to
+    which its earlier tokens are rounded."""
+    scaled = k_scale is not None or v_scale is not None
     if (k.requires_grad or v.requires_grad or k_cache.requires_grad or v_cache.requires_grad or (q is not None and q.requires_grad)
-            or (freq is not None and freq.requires_grad) or (out is not None and out.requires_grad)):
+            or (freq is not None and freq.requires_grad) or (out is not None and out.requires_grad)
+            or (k_scale is not None and k_scale.requires_grad) or (v_scale is not None and v_scale.requires_grad)):
         _no_gradient()
     B, T, H, D = k.shape
     if not (v.shape == k.shape and v.dtype == k.dtype and v.device == k.device):
         raise ValueError("k and v differ in shape, type or device")
     _types(k, k_cache)
-    cache, heads, dim, _ = _cache(k_cache, v_cache, table, B)
+    cache, heads, dim, _ = _cache(k_cache, v_cache, table, B, scaled)
+    if scaled:
+        scales = _scales(k_scale, v_scale, k_cache)
+        _written(k_scale, "k_scale")
+        _written(v_scale, "v_scale")
     _written(k_cache, "the key cache")
     _written(v_cache, "the value cache")
     dev = k.device
@@ -338,7 +401,10 @@ def append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, k_cache: to
             qs = (q.data_ptr(), *_strides(q), out.data_ptr(), *_strides(out))
         args = _APPEND.pack(*qs, k.data_ptr(), *_strides(k), v.data_ptr(), *_strides(v), _counts(length, B, dev, "length"),
                             _counts(drafted, B, dev, "drafted"), _DTYPE[k.dtype], T, hq, 0)
-        rc = lib().uzip_kv_append(cache, args, packed, _stream(dev))
+        if scaled:
+            rc = lib().uzip_kv_append_scaled(cache, scales, args, packed, _stream(dev))
+        else:
+            rc = lib().uzip_kv_append(cache, args, packed, _stream(dev))
     if rc:
         _check(rc, "append", q=q, k=k, v=v, k_cache=k_cache, v_cache=v_cache, out=out)
     return out if q is not None else None
@@ -353,6 +419,7 @@ def attend_workspace_bytes(seqs: int, kv_heads: int, dim: int, cache_tokens: int
 def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, length: torch.Tensor, *,
            table: torch.Tensor | None = None, tree: torch.Tensor | None = None, drafted: torch.Tensor | None = None,
            scale: float | None = None, score: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+           k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None,
            out: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Attention of the drafted tokens q [sequences, tokens, heads, dim] over a
     cache that holds length earlier tokens and, behind them, the drafted ones'
@@ -367,15 +434,22 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, length
     there is not added. lse (float32 [sequences, tokens, heads], contiguous) receives the log
     of each query's sum of exponentials. A query that sees nothing gives zeros
     and -inf, as do those from drafted on. Masked keys and values have no
-    effect, whatever they hold. out does not overlap the inputs."""
+    effect, whatever they hold. out does not overlap the inputs.
+
+    With k_scale and v_scale the cache is float8_e4m3fn or int8, and an element
+    stands for itself times the scale of its block and head."""
     if (q.requires_grad or k_cache.requires_grad or v_cache.requires_grad or (score is not None and score.requires_grad)
-            or (lse is not None and lse.requires_grad) or (out is not None and out.requires_grad)):
+            or (lse is not None and lse.requires_grad) or (out is not None and out.requires_grad)
+            or (k_scale is not None and k_scale.requires_grad) or (v_scale is not None and v_scale.requires_grad)):
         _no_gradient()
     _types(q, k_cache)
     qs = _strides(q)
     B, T, hq, D = q.shape
     dev = q.device
-    cache, heads, dim, tokens = _cache(k_cache, v_cache, table, B)
+    scaled = k_scale is not None or v_scale is not None
+    cache, heads, dim, tokens = _cache(k_cache, v_cache, table, B, scaled)
+    if scaled:
+        scales = _scales(k_scale, v_scale, k_cache)
     if k_cache.device != dev:
         raise ValueError("the cache is on another device")
     if not (dim == D and hq >= heads > 0 and hq % heads == 0):
@@ -409,7 +483,10 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, length
                             score.data_ptr() if score is not None else 0, *ss, _counts(length, B, dev, "length"),
                             _counts(drafted, B, dev, "drafted"), tree.data_ptr() if tree is not None else 0, *ts,
                             _DTYPE[q.dtype], T, hq, 1.0 / math.sqrt(D) if scale is None else scale, seen, 0)
-        rc = lib().uzip_kv_attend(cache, args, ws.data_ptr(), ws.numel(), _stream(dev))
+        if scaled:
+            rc = lib().uzip_kv_attend_scaled(cache, scales, args, ws.data_ptr(), ws.numel(), _stream(dev))
+        else:
+            rc = lib().uzip_kv_attend(cache, args, ws.data_ptr(), ws.numel(), _stream(dev))
     if rc:
         _check(rc, "attend", q=q, k_cache=k_cache, v_cache=v_cache, out=out)
     return out
@@ -468,3 +545,217 @@ def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, score: torch.Tensor, len
     if rc:
         _check(rc, "evict", k_cache=k_cache, v_cache=v_cache, k_out=made[0], v_out=made[1])
     return made[0], made[1], kept, left, index
+
+
+@functools.lru_cache(maxsize=4096)
+def verify_workspace_bytes(seqs: int, nodes: int, vocab: int) -> int:
+    """Workspace that :func:`verify` needs for these shapes; 0 when they are invalid."""
+    return int(lib().uzip_kv_verify_workspace_bytes(seqs, nodes, vocab))
+
+
+def _ints(t: torch.Tensor, seqs: int, n: int, device, what: str, dtype=torch.int32):
+    """(address, stride) of a tensor [seqs, n] with contiguous rows."""
+    if not (t.dtype == dtype and t.shape == (seqs, n) and t.device == device and (t.stride(1) == 1 or n == 1)):
+        raise ValueError(f"{what}: expected {dtype} [{seqs}, {n}] with contiguous rows on {device}")
+    return t.data_ptr(), t.stride(0) if seqs > 1 else 0
+
+
+def _probabilities(t: torch.Tensor, what: str):
+    if t.requires_grad:
+        _no_gradient()
+    if t.dim() != 3 or not t.numel():
+        raise ValueError(f"{what}: expected [sequences, nodes, vocabulary], got {tuple(t.shape)}")
+    if t.stride(2) != 1 and t.shape[2] != 1:
+        raise ValueError(f"{what}: the vocabulary is not contiguous")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def verify(tokens: torch.Tensor, target: torch.Tensor, uniform: torch.Tensor, *, draft: torch.Tensor | None = None,
+           parent: torch.Tensor | None = None, drafted: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """Which drafted tokens the target accepts, so that what is accepted and the
+    token that follows are distributed as the target's. Each sequence has up to
+    1024 nodes: node 0 its last token, the others drafted ones, tokens int32
+    [sequences, nodes] (the first of each is not read). parent (int32
+    [sequences, nodes] or [nodes]) names the node that each one follows, a lower
+    number; without it they are a chain. target [sequences, nodes, vocabulary],
+    float32, bfloat16 or float16, holds the probabilities of the token behind
+    each node; draft, of the same type and shape, those that a node's children
+    were drawn from, independently. Without draft they were chosen, like the most
+    likely ones. uniform (float32 [sequences, nodes], in [0, 1)) are the random
+    numbers: of a node's own test, and node 0's of the last token. drafted counts
+    each sequence's nodes, node 0 among them.
+
+    Returns (path, count, token), int32: the accepted nodes in order, node 0
+    first, -1 behind them [sequences, nodes]; how many they are; the token that
+    follows. A sequence without nodes has count 0 and token -1."""
+    p, ps = _probabilities(target, "target")
+    B, T, V = target.shape
+    dev = target.device
+    dtype = _PROBABILITY.get(target.dtype)
+    if dtype is None:
+        raise ValueError(f"probabilities are float32, bfloat16 or float16, got {target.dtype}")
+    if T > 1024 or V > 1 << 30:
+        raise ValueError(f"at most 1024 nodes and 2^30 tokens, got {T} and {V}")
+    q, qs = 0, (0, 0)
+    if draft is not None:
+        q, qs = _probabilities(draft, "draft")
+        if not (draft.shape == target.shape and draft.dtype == target.dtype and draft.device == dev):
+            raise ValueError("draft differs from target in shape, type or device")
+    at, tok = _ints(tokens, B, T, dev, "tokens")
+    ua, us = _ints(uniform, B, T, dev, "uniform", torch.float32)
+    pa = par = 0
+    if parent is not None:
+        pa, par = _ints(parent, B, T, dev, "parent") if parent.dim() == 2 else (_ints(parent[None], 1, T, dev, "parent")[0], 0)
+    with _on(dev, stream):
+        path = torch.empty((B, T), dtype=torch.int32, device=dev)
+        count, token = torch.empty(B, dtype=torch.int32, device=dev), torch.empty(B, dtype=torch.int32, device=dev)
+        if ws is None:
+            ws = torch.empty(verify_workspace_bytes(B, T, V), dtype=torch.uint8, device=dev)
+        elif not (ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev):
+            raise ValueError(f"ws: expected contiguous uint8 on {dev} from a 16-byte boundary")
+        args = _VERIFY.pack(p, q, *ps, *qs, at, pa, _counts(drafted, B, dev, "drafted"), ua, tok, par, us,
+                            path.data_ptr(), count.data_ptr(), token.data_ptr(), dtype, B, T, V, 0)
+        rc = lib().uzip_kv_verify(args, ws.data_ptr(), ws.numel(), _stream(dev))
+    if rc:
+        _check(rc, "verify")
+    return path, count, token
+
+
+def accept(k_cache: torch.Tensor, v_cache: torch.Tensor, length: torch.Tensor, path: torch.Tensor, count: torch.Tensor, *,
+           table: torch.Tensor | None = None, stream=None) -> None:
+    """Moves the accepted tokens of a tree up: token length + path[j] of each
+    sequence becomes token length + j, for j < count, as if they had been
+    appended as a chain. path [sequences, nodes] and count as :func:`verify`
+    returns them. length is not changed: the tokens that the cache then has are
+    length + count. Caches with scales are not taken: draft chains over them,
+    whose accepted tokens are in place."""
+    if k_cache.requires_grad or v_cache.requires_grad:
+        _no_gradient()
+    B = length.numel()
+    cache, _, _, _ = _cache(k_cache, v_cache, table, B)
+    _written(k_cache, "the key cache")
+    _written(v_cache, "the value cache")
+    dev = k_cache.device
+    if path.dim() != 2 or not 1 <= path.shape[1] <= 1024:
+        raise ValueError(f"path: expected int32 [{B}, nodes], at most 1024 nodes")
+    at, stride = _ints(path, B, path.shape[1], dev, "path")
+    with _on(dev, stream):
+        args = _ACCEPT.pack(_counts(length, B, dev, "length"), at, stride, _counts(count, B, dev, "count"), path.shape[1], 0)
+        rc = lib().uzip_kv_accept(cache, args, _stream(dev))
+    if rc:
+        _check(rc, "accept", k_cache=k_cache, v_cache=v_cache)
+
+
+@functools.lru_cache(maxsize=4096)
+def pages_workspace_bytes(pages: int, seqs: int, entries: int) -> int:
+    """Workspace that :func:`fork` and :func:`compact` need for these shapes; 0 when they are invalid."""
+    return int(lib().uzip_kv_pages_workspace_bytes(pages, seqs, entries))
+
+
+def _pages(table, length, parent, pages: int, page: int, room: int, held, ws, stream, call: str):
+    if not (table.dtype == torch.int32 and table.dim() == 2 and table.numel() and (table.stride(1) == 1 or table.shape[1] == 1)):
+        raise ValueError("table: expected int32 [sequences, entries] with contiguous rows")
+    rows, entries = table.shape
+    dev = table.device
+    if page < 16 or page & (page - 1) or entries * page > 1 << 30:
+        raise ValueError(f"pages hold a power of two of tokens, at least 16, and a table at most 2^30 of them; got {page}")
+    if not (1 <= pages <= 1 << 30 and 0 <= room <= 1 << 30):
+        raise ValueError(f"{pages} pages, room for {room}: expected 1 to 2^30 pages and no negative room")
+    if held is not None and not (held.dtype in (torch.bool, torch.uint8) and held.shape == (pages,) and held.is_contiguous() and held.device == dev):
+        raise ValueError(f"held: expected contiguous bool [{pages}] on {dev}")
+    seqs = rows if parent is None else parent.numel()
+    if parent is not None and not seqs:
+        raise ValueError("no sequences")
+    with _on(dev, stream):
+        out = torch.empty((seqs, entries), dtype=torch.int32, device=dev)
+        most = min(seqs * entries, pages // 2) if parent is None else seqs
+        moves, left = torch.empty((most, 2), dtype=torch.int32, device=dev), torch.empty(1, dtype=torch.int32, device=dev)
+        lengths = torch.empty(seqs, dtype=torch.int32, device=dev) if parent is not None else None
+        if ws is None:
+            ws = torch.empty(pages_workspace_bytes(pages, seqs, entries), dtype=torch.uint8, device=dev)
+        elif not (ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev):
+            raise ValueError(f"ws: expected contiguous uint8 on {dev} from a 16-byte boundary")
+        args = _PAGES.pack(table.data_ptr(), table.stride(0) if rows > 1 else 0, _counts(length, rows, dev, "length"),
+                           _counts(parent, seqs, dev, "parent"), held.data_ptr() if held is not None else 0, out.data_ptr(),
+                           lengths.data_ptr() if lengths is not None else 0, moves.data_ptr() or left.data_ptr(), left.data_ptr(),
+                           rows, seqs, entries, pages, page, room, 0)
+        rc = getattr(lib(), call)(args, ws.data_ptr(), ws.numel(), _stream(dev))
+    if rc:
+        _check(rc, call[8:])
+    return out, lengths, moves, left
+
+
+def fork(table: torch.Tensor, length: torch.Tensor, parent: torch.Tensor, pages: int, page: int, *, room: int = 0,
+         held: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """The page table of the next step. Sequence b goes on where row parent[b]
+    (int32 [sequences]) of table (int32 [rows, entries]) with its length (int32
+    [rows]) is; a parent outside the table, like -1, leaves it empty. Rows that
+    are no parent are freed: a page is in use if a sequence has it for its
+    tokens, or if held (bool [pages]) says so. Whole pages of `page` tokens are
+    shared; a partly filled last page stays with the first sequence that has it,
+    and the others get copies. Each sequence gets pages for `room` more tokens,
+    as far as the table has entries. New pages are the lowest free ones of
+    `pages`.
+
+    Returns (table, length, moves, left): the new table [sequences, entries], -1
+    where there is no page; lengths; the copies to make (:func:`copy_pages`, for
+    each layer's caches and scales); and how many pages are still free, int32 [1],
+    or, negative, how many were lacking: their entries are absent, and the tokens
+    of a page that could not be copied are lost."""
+    return _pages(table, length, parent, pages, page, room, held, ws, stream, "uzip_kv_fork")
+
+
+def compact(table: torch.Tensor, length: torch.Tensor, pages: int, page: int, *, held: torch.Tensor | None = None,
+            ws: torch.Tensor | None = None, stream=None):
+    """Moves the pages in use, n of them, to the front of the pool: those from n
+    on to the free ones below, lowest to lowest. Held pages stay. Returns (table,
+    moves, n): the new table, the copies to make (:func:`copy_pages`) padded with
+    -1, and n, int32 [1]."""
+    out, _, moves, used = _pages(table, length, None, pages, page, 0, held, ws, stream, "uzip_kv_compact")
+    return out, moves, used
+
+
+@functools.lru_cache(maxsize=4096)
+def _pool(shape, stride, size: int):
+    """(page stride, two strides, two counts, run) of a tensor of pages, in bytes."""
+    dims = sorted(((st * size, n) for n, st in zip(shape[1:], stride[1:]) if n != 1), reverse=True)
+    run = size
+    while dims and dims[-1][0] == run:
+        run *= dims.pop()[1]
+    merged = []
+    for st, n in dims:
+        if merged and merged[-1][0] == st * n:
+            merged[-1] = (st, merged[-1][1] * n)
+        else:
+            merged.append((st, n))
+    if len(merged) > 2 or any(st < run for st, _ in merged):
+        raise ValueError(f"pages of shape {shape[1:]} and strides {stride[1:]} are no two dims of contiguous runs")
+    merged = [(0, 1)] * (2 - len(merged)) + merged
+    return stride[0] * size if shape[0] > 1 else 0, merged[0][0], merged[1][0], merged[0][1], merged[1][1], run
+
+
+def copy_pages(moves: torch.Tensor, *pools: torch.Tensor, stream=None) -> None:
+    """Copies page moves[i, 0] to page moves[i, 1] (int32 [n, 2], as :func:`fork`
+    and :func:`compact` return it) in each of up to 8 pools [pages, ...]: keys,
+    values and scales, of any type. Pages outside the pools are passed over. None
+    is copied to twice, or to and from."""
+    if not 1 <= len(pools) <= 8:
+        raise ValueError(f"expected 1 to 8 pools, got {len(pools)}")
+    if not (moves.dtype == torch.int32 and moves.dim() == 2 and moves.shape[1] == 2 and moves.is_contiguous()):
+        raise ValueError("moves: expected contiguous int32 [n, 2]")
+    dev = moves.device
+    packed = b""
+    for t in pools:
+        if t.requires_grad:
+            _no_gradient()
+        if t.device != dev or t.dim() < 2 or not t.numel() or t.shape[0] != pools[0].shape[0]:
+            raise ValueError(f"pools: expected [pages, ...] with as many pages each on {dev}, got {tuple(t.shape)} on {t.device}")
+        _written(t, "a pool")
+        page, s0, s1, n0, n1, run = _pool(t.shape, t.stride(), t.element_size())
+        packed += _POOL.pack(t.data_ptr(), page, s0, s1, n0, n1, run, 0)
+    with _on(dev, stream):
+        if not moves.shape[0]:
+            return
+        rc = lib().uzip_kv_copy_pages(moves.data_ptr(), moves.shape[0], packed, len(pools), pools[0].shape[0], _stream(dev))
+    if rc:
+        _check(rc, "copy_pages")
