@@ -213,8 +213,8 @@ uint64_t uzip_kv_evict_workspace_bytes(uint32_t seqs, uint32_t kv_heads, uint32_
  * and an element stands for itself times it. That of token t of sequence b,
  * head h: k[b * k_stride[0] + t / block * k_stride[1] + h * k_stride[2]]; in
  * pages, of row r of page p: k[p * k_stride[0] + r / block * k_stride[1] + ...].
- * Strides are any that are not negative; 4-byte aligned. Scales of blocks that
- * are seen are positive, in [2^-100, 2^100]. */
+ * Strides are any that are not negative and lead to no element 2^30; 4-byte
+ * aligned. Scales of blocks that are seen are positive, in [2^-100, 2^100]. */
 typedef struct uzip_kv_scales {
     float   *k;
     float   *v;

@@ -38,11 +38,11 @@ struct CacheView {
 };
 
 // Scales of an 8-bit cache as kernels see them; strides in elements: page or
-// sequence, block, head.
+// sequence, block, head. No offset reaches 2^30, so 32 bits do.
 struct ScaleView {
     float *k, *v;
-    int64_t k0, k1, k2, v0, v1, v2;
-    int shift;                                       // of a block's tokens
+    uint32_t k0, k1, k2, v0, v1, v2;
+    uint32_t shift;                                  // of a block's tokens
 };
 
 // a load at an address that is the same for a whole wave, of memory that the kernel does not write
@@ -191,15 +191,21 @@ inline bool valid_cache(const uzip_kv_cache_t *c, bool scaled = false)
 inline bool valid_scales(const uzip_kv_scales_t *f, const uzip_kv_cache_t *c)
 {
     if (!f || !f->k || !f->v || !aligned(f->k, 4) || !aligned(f->v, 4) || f->reserved) return false;
-    if (f->block < 16 || f->block > (1u << 30) || (f->block & (f->block - 1)) || (c->table && f->block > c->page)) return false;
-    for (int i = 0; i < 3; i++)
-        if (f->k_stride[i] < 0 || f->v_stride[i] < 0 || f->k_stride[i] > (1ll << 40) || f->v_stride[i] > (1ll << 40)) return false;
-    return true;
+    if (f->block < 16 || f->block > 65536 || (f->block & (f->block - 1)) || (c->table && f->block > c->page)) return false;
+    const uint64_t most[3] = {c->table ? c->pages : c->seqs, ((c->table ? c->page : c->tokens) + (uint64_t)f->block - 1) / f->block, c->heads};
+    uint64_t k = 0, v = 0;
+    for (int i = 0; i < 3; i++) {
+        if (f->k_stride[i] < 0 || f->v_stride[i] < 0 || f->k_stride[i] >= (1ll << 30) || f->v_stride[i] >= (1ll << 30)) return false;
+        k += (most[i] - 1) * (uint64_t)f->k_stride[i], v += (most[i] - 1) * (uint64_t)f->v_stride[i];
+    }
+    return k < (1ull << 30) && v < (1ull << 30);
 }
 
 inline ScaleView view_of(const uzip_kv_scales_t *f)
 {
-    return {f->k, f->v, f->k_stride[0], f->k_stride[1], f->k_stride[2], f->v_stride[0], f->v_stride[1], f->v_stride[2], __builtin_ctz(f->block)};
+    const auto u = [](int64_t x) { return (uint32_t)x; };
+    return {f->k, f->v, u(f->k_stride[0]), u(f->k_stride[1]), u(f->k_stride[2]), u(f->v_stride[0]), u(f->v_stride[1]), u(f->v_stride[2]),
+            (uint32_t)__builtin_ctz(f->block)};
 }
 
 inline bool valid_rope(const uzip_kv_rope_t *r, uint32_t dim)

@@ -15,7 +15,7 @@ namespace uzip_kv {
 namespace {
 
 constexpr int kThreads = 256, kAppendWaves = kThreads / 64;
-constexpr int kKeep = 8;                          // units of 8 elements that a lane holds between the two passes
+constexpr int kKeep = 4;                          // units of 8 elements that a lane holds between the two passes, at most
 constexpr int kAngles = 8192;                     // of a workgroup in LDS, at most
 
 struct Append8Params {
@@ -31,6 +31,7 @@ struct Append8Params {
     float amplitude;
     int T, Hq, H, D, rot;
     int interleaved, inverse;
+    uint32_t per_magic;                           // 2^32 / (D / 8), rounded up; unused where that is 2^32
     int blocks, groups, items, waves;             // of a sequence; workgroups a block; heads' keys or values a workgroup; waves an item
     int kv_grid;                                  // workgroups before those of the queries
     int q_tokens, q_parts, q_share;               // tokens a workgroup, or workgroups a token and units of each
@@ -53,54 +54,88 @@ __device__ inline float2 angle_of(const Append8Params &p, int64_t pos, int i)
     return make_float2(c1 * p.amplitude, p.inverse ? -s1 * p.amplitude : s1 * p.amplitude);
 }
 
-__device__ __attribute__((noinline)) float2 far_angle(const Append8Params &p, int64_t pos, int i) { return angle_of(p, pos, i); }
+// How heads turn: not at all; as halves of whole units of 8 elements; in any
+// other way, a unit's elements one by one; and so with more angles than LDS
+// holds for a workgroup, which are worked out where they are used.
+enum { kStill, kHalves, kAny, kFar };
+constexpr int kept_units(int mode) { return mode <= kHalves ? kKeep : 1; }
+
+// Eight elements of a head as they are read, and those they turn with.
+struct Eight {
+    u32x4 w, z;
+};
 
 template <bool F16>
-__device__ inline float to_f32(uint16_t x)
+__device__ inline void unpack8(u32x4 w, float (&x)[8])
 {
-    return F16 ? f16_to_f32(x) : bf16_to_f32(x);
-}
-
-// Elements d .. d + 7 of a head, turned. cs: the token's angles, or null.
-template <bool F16>
-__device__ inline void turned8(const Append8Params &p, const char *row, int d, bool turns, const float2 *cs, int64_t pos, u32x4 &w, float (&y)[8])
-{
-    w = *reinterpret_cast<const u32x4 *>(row + d * 2);
 #pragma unroll
     for (int e = 0; e < 4; e++) {
         const f32x2 v = unpack2<F16>(w[e]);
-        y[2 * e] = v.x, y[2 * e + 1] = v.y;
+        x[2 * e] = v.x, x[2 * e + 1] = v.y;
     }
+}
+
+template <int MODE>
+__device__ inline Eight load8(const Append8Params &p, const char *row, int d, bool turns)
+{
+    Eight r;
+    r.w = *reinterpret_cast<const u32x4 *>(row + d * 2);
+    if constexpr (MODE == kHalves) {
+        const int half = p.rot / 2;
+        r.z = r.w;
+        if (turns && d < p.rot) r.z = *reinterpret_cast<const u32x4 *>(row + (d < half ? d + half : d - half) * 2);
+    } else if constexpr (MODE != kStill) {
+        r.z = u32x4{0, 0, 0, 0};
+        const int half = p.rot / 2;
+        if (turns && !p.interleaved)
+            for (int e = 0; e < 8; e += 2) {      // rot is even, so both turn or neither does
+                if (d + e >= p.rot) break;
+                const int i = d + e < half ? d + e + half : d + e - half, j = d + e + 1 < half ? d + e + 1 + half : d + e + 1 - half;
+                const uint32_t two = *reinterpret_cast<const uint16_t *>(row + i * 2) | (uint32_t)*reinterpret_cast<const uint16_t *>(row + j * 2) << 16;
+                r.z[0] = e == 0 ? two : r.z[0], r.z[1] = e == 2 ? two : r.z[1], r.z[2] = e == 4 ? two : r.z[2], r.z[3] = e == 6 ? two : r.z[3];
+            }
+    }
+    return r;
+}
+
+// ... turned. cs: the token's angles.
+template <bool F16, int MODE>
+__device__ inline void turned8(const Append8Params &p, const Eight &r, int d, bool turns, const float2 *cs, int64_t pos, float (&y)[8])
+{
+    unpack8<F16>(r.w, y);
+    if constexpr (MODE == kStill) return;
     if (!turns || d >= p.rot) return;
     const int half = p.rot / 2;
-    float x[8], o[8];                             // the elements and their partners
-#pragma unroll
-    for (int e = 0; e < 8; e++) x[e] = y[e];
-    if (p.interleaved) {
-#pragma unroll
-        for (int e = 0; e < 8; e++) o[e] = x[e ^ 1];
-    } else if ((half & 7) == 0) {
-        const u32x4 z = *reinterpret_cast<const u32x4 *>(row + (d < half ? d + half : d - half) * 2);
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            const f32x2 v = unpack2<F16>(z[e]);
-            o[2 * e] = v.x, o[2 * e + 1] = v.y;
-        }
-    } else {
+    float o[8];                                   // the elements' partners
+    if constexpr (MODE == kHalves) {
+        unpack8<F16>(r.z, o);
+        const bool lead = d < half;
+        const float sign = lead ? -1.f : 1.f;
+        const float2 *at = cs + (lead ? d : d - half);
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-            const int at = d + e < half ? d + e + half : d + e - half;
-            o[e] = d + e < p.rot ? to_f32<F16>(*reinterpret_cast<const uint16_t *>(row + at * 2)) : 0.f;
+            const float2 a = at[e];
+            y[e] = fmaf(y[e], a.x, o[e] * a.y * sign);
         }
-    }
+    } else {
+        unpack8<F16>(r.z, o);
 #pragma unroll
-    for (int e = 0; e < 8; e++) {
-        if (d + e >= p.rot) continue;
-        const bool lead = p.interleaved ? !(e & 1) : d + e < half;
-        const int i = p.interleaved ? (d + e) >> 1 : lead ? d + e : d + e - half;
-        const float2 a = cs ? cs[i] : far_angle(p, pos, i);
-        const float turn = lead ? -a.y : a.y;
-        y[e] = fmaf(x[e], a.x, o[e] * turn);
+        for (int e = 0; e < 8; e += 2) {
+            float2 a[2];
+            float sign[2];
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+                const int at = min(d + e + k, p.rot - 1);
+                const bool lead = p.interleaved ? k == 0 : at < half;
+                const int i = p.interleaved ? at >> 1 : lead ? at : at - half;
+                a[k] = MODE == kFar ? angle_of(p, pos, i) : cs[i];
+                sign[k] = lead ? -a[k].y : a[k].y;
+            }
+            const float x0 = y[e], x1 = y[e + 1], o0 = p.interleaved ? x1 : o[e], o1 = p.interleaved ? x0 : o[e + 1];
+            const bool in = d + e < p.rot;
+            y[e] = in ? fmaf(x0, a[0].x, o0 * sign[0]) : x0;
+            y[e + 1] = in ? fmaf(x1, a[1].x, o1 * sign[1]) : x1;
+        }
     }
 }
 
@@ -128,10 +163,12 @@ struct Byte {
     __device__ inline static uint32_t pack4(float a, float b, float c, float d)
     {
         if constexpr (I8) {
-            const int i = (int)rintf(held(a)), j = (int)rintf(held(b)), k = (int)rintf(held(c)), l = (int)rintf(held(d));
-            return (uint32_t)(i & 255) | (uint32_t)(j & 255) << 8 | (uint32_t)(k & 255) << 16 | (uint32_t)l << 24;
+            // an integer added to 1.5 * 2^23 is its low bits, rounded to nearest even
+            constexpr float k = 12582912.f;
+            const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(held(b) + k), __float_as_uint(held(a) + k), 0x0c0c0400u);
+            return __builtin_amdgcn_perm(__float_as_uint(held(d) + k), __float_as_uint(held(c) + k), 0x04000c0cu) | lo;
         } else {
-            int w = __builtin_amdgcn_cvt_pk_fp8_f32(held(a), held(b), 0, false);
+            const int w = __builtin_amdgcn_cvt_pk_fp8_f32(held(a), held(b), 0, false);
             return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(held(c), held(d), w, true);
         }
     }
@@ -163,9 +200,10 @@ __device__ inline void divide8(float (&y)[8], float s)
     }
 }
 
-template <bool F16>
+template <bool F16, int MODE>
 __device__ inline void turn_queries(const Append8Params &p, float2 *cs)
 {
+    constexpr int KEEP = kept_units(MODE);
     const int id = (int)blockIdx.x - p.kv_grid, part = id % p.q_parts, tid = (int)threadIdx.x;
     const int64_t first = (int64_t)(id / p.q_parts) * p.q_tokens;
     const int tokens = (int)min((int64_t)p.q_tokens, p.q_count - first), half = p.rot / 2, per = p.D / 8;
@@ -173,20 +211,38 @@ __device__ inline void turn_queries(const Append8Params &p, float2 *cs)
         const int64_t b = at / p.T, t = at - b * p.T;
         return p.pos ? (int64_t)p.pos[b * p.pos_stride + t] : (int64_t)p.length[b] + t;
     };
-    if (p.angles)
-        for (int j = tid; j < tokens * half; j += kThreads) cs[j] = angle_of(p, position(first + j / half), j % half);
-    __syncthreads();
     const int u0 = part * p.q_share, u1 = min(u0 + p.q_share, tokens * p.Hq * per);
-    for (int u = u0 + tid; u < u1; u += kThreads) {
-        const int d = u % per * 8, head = u / per % p.Hq, token = u / per / p.Hq;
-        const int64_t at = first + token, b = at / p.T, t = at - b * p.T;
-        u32x4 w;
-        float y[8];
-        turned8<F16>(p, p.q + b * p.qs0 + t * p.qs1 + head * p.qs2, d, true, p.angles ? cs + token * half : nullptr, p.angles ? 0 : position(at), w, y);
-        const int keep = max(0, min(p.rot - d, 8));       // elements from here on keep their bits
+    Eight raw[KEEP];
+    const auto fetch = [&](int base) {
 #pragma unroll
-        for (int e = 0; e < 4; e++) w[e] = 2 * e < keep ? pack2<F16>(y[2 * e], y[2 * e + 1]) : w[e];
-        *reinterpret_cast<u32x4 *>(p.y + b * p.ys0 + t * p.ys1 + head * p.ys2 + d * 2) = w;
+        for (int r = 0; r < KEEP; r++) {
+            if (base + r * kThreads >= u1) continue;
+            const int u = min(base + r * kThreads + tid, u1 - 1), head = u / per % p.Hq;
+            const int64_t at = first + u / per / p.Hq, b = at / p.T, t = at - b * p.T;
+            raw[r] = load8<MODE>(p, p.q + b * p.qs0 + t * p.qs1 + head * p.qs2, u % per * 8, true);
+        }
+    };
+    fetch(u0);
+    if (MODE != kFar && MODE != kStill) {
+        for (int j = tid; j < tokens * half; j += kThreads) cs[j] = angle_of(p, position(first + j / half), j % half);
+        __syncthreads();
+    }
+    for (int base = u0; base < u1; base += KEEP * kThreads) {
+        if (base > u0) fetch(base);
+#pragma unroll
+        for (int r = 0; r < KEEP; r++) {
+            const int u = base + r * kThreads + tid;
+            if (u >= u1) continue;
+            const int d = u % per * 8, head = u / per % p.Hq, token = u / per / p.Hq;
+            const int64_t at = first + token, b = at / p.T, t = at - b * p.T;
+            float y[8];
+            turned8<F16, MODE>(p, raw[r], d, true, cs + token * half, MODE == kFar ? position(at) : 0, y);
+            u32x4 w = raw[r].w;
+            const int keep = max(0, min(p.rot - d, 8));       // elements from here on keep their bits
+#pragma unroll
+            for (int e = 0; e < 4; e++) w[e] = 2 * e < keep ? pack2<F16>(y[2 * e], y[2 * e + 1]) : w[e];
+            *reinterpret_cast<u32x4 *>(p.y + b * p.ys0 + t * p.ys1 + head * p.ys2 + d * 2) = w;
+        }
     }
 }
 
@@ -194,14 +250,15 @@ __device__ inline void turn_queries(const Append8Params &p, float2 *cs)
 // heads, then those that turn queries. A wave (or, of long blocks, the four of
 // a workgroup) takes the keys or values of a head: turns the new tokens, finds
 // their largest magnitude, and rounds what it holds in registers.
-template <bool F16, bool I8>
-__global__ __launch_bounds__(kThreads) void k_append8(Append8Params p)
+template <bool F16, bool I8, int MODE>
+__global__ __launch_bounds__(kThreads, MODE == kStill ? 4 : 3) void k_append8(Append8Params p)
 {
     using E = Byte<I8>;
+    constexpr int KEEP = kept_units(MODE);
     extern __shared__ float2 cs[];
     __shared__ float wave_top[kAppendWaves];
     if ((int)blockIdx.x >= p.kv_grid) {
-        turn_queries<F16>(p, cs);
+        turn_queries<F16, MODE>(p, cs);
         return;
     }
     int id = (int)blockIdx.x;
@@ -209,6 +266,7 @@ __global__ __launch_bounds__(kThreads) void k_append8(Append8Params p)
     id /= p.groups;
     const int b = id / p.blocks, j = id % p.blocks;
     const int tid = (int)threadIdx.x, half = p.rot / 2;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // the block's tokens [s0, ..), of which [lo, hi) are new
     const int64_t n = p.length[b], nd = clamp_drafted(p.drafted, b, p.T);
     const int64_t s0 = ((max(n, (int64_t)0) >> p.f.shift) + j) << p.f.shift;
@@ -217,52 +275,70 @@ __global__ __launch_bounds__(kThreads) void k_append8(Append8Params p)
     if (lo >= hi || !locate(p.c, b, (uint32_t)s0, p.c.ks0, p.c.ks1, ko)) return;
     locate(p.c, b, (uint32_t)s0, p.c.vs0, p.c.vs1, vo);
     const int rows = (int)(hi - lo), skip = (int)(lo - s0), t0 = (int)(lo - n);    // skip: earlier tokens
-    const int64_t first = p.c.table ? (int64_t)p.c.table[b * p.c.ts + (s0 >> p.c.shift)] : b;
-    const int64_t block = (p.c.table ? s0 & ((1ll << p.c.shift) - 1) : s0) >> p.f.shift;
+    const uint32_t first = p.c.table ? (uint32_t)p.c.table[b * p.c.ts + (s0 >> p.c.shift)] : (uint32_t)b;
+    const uint32_t block = (uint32_t)((p.c.table ? s0 & ((1ll << p.c.shift) - 1) : s0) >> p.f.shift);
     const auto position = [&](int row) { return p.pos ? (int64_t)p.pos[b * p.pos_stride + t0 + row] : lo + row; };
-    if (p.angles) {
+    const int per = p.D / 8, units = rows * per;
+    const int lanes = p.waves * 64, lane = p.waves == 1 ? tid & 63 : tid;
+    const int step = p.waves == 1 ? kAppendWaves : 1, end = min((group + 1) * p.items, 2 * p.H);
+    const auto row_of = [&](int u) { return per == 1 ? u : (int)__umulhi((uint32_t)u, p.per_magic); };
+
+    bool val;
+    const char *src;
+    char *dst;
+    float *scale, before;
+    int64_t ss, ds;
+    Eight raw[KEEP];
+    const auto fetch = [&](int item) {            // where an item is, its scale and its first elements
+        val = item >= p.H;
+        const int h = val ? item - p.H : item;
+        src = val ? p.v + b * p.vs0 + t0 * p.vs1 + h * p.vs2 : p.k + b * p.ks0 + t0 * p.ks1 + h * p.ks2;
+        ss = val ? p.vs1 : p.ks1, ds = val ? p.c.vs1 : p.c.ks1;
+        dst = val ? p.c.v + vo + h * p.c.vs2 : p.c.k + ko + h * p.c.ks2;
+        scale = val ? p.f.v + (first * p.f.v0 + block * p.f.v1 + h * p.f.v2) : p.f.k + (first * p.f.k0 + block * p.f.k1 + h * p.f.k2);
+#pragma unroll
+        for (int r = 0; r < KEEP; r++) {
+            if (r * lanes >= units) continue;
+            const int u = min(r * lanes + lane, units - 1), row = row_of(u);
+            raw[r] = load8<MODE>(p, src + row * ss, (u - row * per) * 8, !val);
+        }
+        before = *scale;
+    };
+    int item = group * p.items + (p.waves == 1 ? wave : 0);
+    if (item < end) fetch(item);
+    if (MODE != kFar && MODE != kStill && group * p.items < p.H) {
         for (int i = tid; i < rows * half; i += kThreads) cs[i] = angle_of(p, position(i / half), i % half);
         __syncthreads();
     }
-    const int per = p.D / 8, units = rows * per;
-    const int lanes = p.waves * 64, lane = p.waves == 1 ? tid & 63 : tid;
-    const int step = p.waves == 1 ? kAppendWaves : 1;
-    const int end = min((group + 1) * p.items, 2 * p.H);
-    for (int item = group * p.items + (p.waves == 1 ? tid >> 6 : 0); item < end; item += step) {
-        const bool val = item >= p.H;
-        const int h = val ? item - p.H : item;
-        const char *src = val ? p.v + b * p.vs0 + t0 * p.vs1 + h * p.vs2 : p.k + b * p.ks0 + t0 * p.ks1 + h * p.ks2;
-        const int64_t ss = val ? p.vs1 : p.ks1, ds = val ? p.c.vs1 : p.c.ks1;
-        char *dst = val ? p.c.v + vo + h * p.c.vs2 : p.c.k + ko + h * p.c.ks2;
-        float *scale = val ? p.f.v + first * p.f.v0 + block * p.f.v1 + h * p.f.v2 : p.f.k + first * p.f.k0 + block * p.f.k1 + h * p.f.k2;
-        const float before = *scale;
-        const auto unit = [&](int u, float (&y)[8]) {
-            const int row = u / per, d = (u - row * per) * 8;
-            u32x4 w;
-            turned8<F16>(p, src + row * ss, d, !val, p.angles ? cs + row * half : nullptr, !val && !p.angles ? position(row) : 0, w, y);
+    for (; item < end;) {
+        const auto elements = [&](const Eight &r, int u, float (&y)[8]) {
+            const int row = row_of(u);
+            turned8<F16, MODE>(p, r, (u - row * per) * 8, !val, cs + row * half, MODE == kFar && !val ? position(row) : 0, y);
+        };
+        const auto again = [&](int u) {
+            const int row = row_of(u);
+            return load8<MODE>(p, src + row * ss, (u - row * per) * 8, !val);
         };
         float top = 0.f;
         const auto look = [&](const float (&y)[8]) {
 #pragma unroll
             for (int e = 0; e < 8; e++) top = fabsf(y[e]) < INFINITY ? fmaxf(top, fabsf(y[e])) : top;
         };
-        float kept[kKeep][8];
+        float kept[KEEP][8];
 #pragma unroll
-        for (int r = 0; r < kKeep; r++) {
-            const int u = r * lanes + lane;
-            if (u < units) {
-                unit(u, kept[r]);
-                look(kept[r]);
-            }
+        for (int r = 0; r < KEEP; r++) {
+            if (r * lanes >= units) continue;
+            elements(raw[r], min(r * lanes + lane, units - 1), kept[r]);
+            look(kept[r]);
         }
-        for (int u = kKeep * lanes + lane; u < units; u += lanes) {
+        for (int u = KEEP * lanes + lane; u < units; u += lanes) {
             float y[8];
-            unit(u, y);
+            elements(again(u), u, y);
             look(y);
         }
         for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
         if (p.waves > 1) {
-            if ((tid & 63) == 0) wave_top[tid >> 6] = top;
+            if ((tid & 63) == 0) wave_top[wave] = top;
             __syncthreads();                      // and all waves have read the scale
             top = fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3]));
         }
@@ -270,7 +346,7 @@ __global__ __launch_bounds__(kThreads) void k_append8(Append8Params p)
         if (skip && now != before) {              // the earlier tokens in the new scale
             const float ratio = before / now;
             for (int u = lane; u < skip * per; u += lanes) {
-                const int row = u / per;
+                const int row = row_of(u);
                 u32x2 *at = reinterpret_cast<u32x2 *>(dst + row * ds + (u - row * per) * 8);
                 const u32x2 w = *at;
                 float y[8];
@@ -282,22 +358,37 @@ __global__ __launch_bounds__(kThreads) void k_append8(Append8Params p)
             }
         }
         const auto put = [&](int u, float (&y)[8]) {
-            const int row = u / per;
+            const int row = row_of(u);
             divide8(y, now);
             *reinterpret_cast<u32x2 *>(dst + (skip + row) * ds + (u - row * per) * 8) = E::pack8(y);
         };
 #pragma unroll
-        for (int r = 0; r < kKeep; r++) {
+        for (int r = 0; r < KEEP; r++) {
             const int u = r * lanes + lane;
             if (u < units) put(u, kept[r]);
         }
-        for (int u = kKeep * lanes + lane; u < units; u += lanes) {
+        for (int u = KEEP * lanes + lane; u < units; u += lanes) {
             float y[8];
-            unit(u, y);
+            elements(again(u), u, y);
             put(u, y);
         }
         if (lane == 0) *scale = now;
         if (p.waves > 1) __syncthreads();         // wave_top is free
+        item += step;
+        if (item < end) fetch(item);
+    }
+}
+
+template <int MODE>
+void launch_append8(const Append8Params &p, dim3 grid, bool f16, bool i8, hipStream_t s)
+{
+    const size_t lds = (size_t)p.angles * sizeof(float2);
+    if (i8) {
+        if (f16) k_append8<true, true, MODE><<<grid, kThreads, lds, s>>>(p);
+        else k_append8<false, true, MODE><<<grid, kThreads, lds, s>>>(p);
+    } else {
+        if (f16) k_append8<true, false, MODE><<<grid, kThreads, lds, s>>>(p);
+        else k_append8<false, false, MODE><<<grid, kThreads, lds, s>>>(p);
     }
 }
 
@@ -342,14 +433,11 @@ extern "C" int uzip_kv_append_scaled(const uzip_kv_cache_t *cache, const uzip_kv
     const int64_t unit = 1ll << p.f.shift, T = p.T, most = T < unit ? T : unit;    // new tokens a block, at most
     p.blocks = (int)((T + unit - 2) / unit + 1);
     const int64_t places = (int64_t)cache->seqs * p.blocks;
-    // a wave an item where it can hold the block's elements; workgroups enough to fill the chip eight times
+    // a wave an item where it can hold the block's elements; an item a wave
     p.waves = most * (p.D / 8) <= 64 * kKeep ? 1 : kAppendWaves;
-    const int at_once = p.waves == 1 ? kAppendWaves : 1;
-    int64_t groups = (8 * kCUs + places - 1) / places;
-    const int64_t steps = (2 * p.H + at_once - 1) / at_once;
-    if (groups > steps) groups = steps;
-    p.items = (int)((steps + groups - 1) / groups) * at_once;
+    p.items = p.waves == 1 ? kAppendWaves : 1;
     p.groups = (2 * p.H + p.items - 1) / p.items;
+    p.per_magic = (uint32_t)(((1ull << 32) + p.D / 8 - 1) / (p.D / 8));
     int64_t in_lds = most * (p.rot / 2), q_blocks = 0;
     if (p.Hq) {
         // queries: a round of loads or two for each workgroup's threads
@@ -370,21 +458,19 @@ extern "C" int uzip_kv_append_scaled(const uzip_kv_cache_t *cache, const uzip_kv
         q_blocks = (p.q_count + p.q_tokens - 1) / p.q_tokens * p.q_parts;
         if (in_lds < p.q_tokens * (p.rot / 2)) in_lds = p.q_tokens * (p.rot / 2);
     }
-    p.angles = in_lds <= kAngles ? (int)in_lds : 0;
+    const bool far = in_lds > kAngles;
+    p.angles = far ? 0 : (int)in_lds;
     const int64_t kv = places * p.groups;
     if (kv + q_blocks >= (1ll << 31)) return UZIP_EINVAL;
     p.kv_grid = (int)kv;
     if (a->q.data && !p.Hq)
         if (const int rc = turn_in_place(a, cache->seqs, cache->dim, rope, s)) return rc;
     const dim3 grid((unsigned)(kv + q_blocks));
-    const size_t lds = (size_t)p.angles * sizeof(float2);
-    if (cache->dtype == UZIP_KV_I8) {
-        if (a->dtype == UZIP_KV_F16) k_append8<true, true><<<grid, kThreads, lds, s>>>(p);
-        else k_append8<false, true><<<grid, kThreads, lds, s>>>(p);
-    } else {
-        if (a->dtype == UZIP_KV_F16) k_append8<true, false><<<grid, kThreads, lds, s>>>(p);
-        else k_append8<false, false><<<grid, kThreads, lds, s>>>(p);
-    }
+    const bool f16 = a->dtype == UZIP_KV_F16, i8 = cache->dtype == UZIP_KV_I8;
+    if (!p.rot) launch_append8<kStill>(p, grid, f16, i8, s);
+    else if (far) launch_append8<kFar>(p, grid, f16, i8, s);
+    else if (!p.interleaved && p.rot % 16 == 0) launch_append8<kHalves>(p, grid, f16, i8, s);
+    else launch_append8<kAny>(p, grid, f16, i8, s);
     UZIP_KV_LAUNCH_CHECK("k_append8");
     return UZIP_OK;
 }
