@@ -40,6 +40,8 @@ namespace {
 constexpr int kWaves = 4;                     // per workgroup
 constexpr int kTileKeys = 32;
 
+enum { kParts, kRuns, kWalks };
+
 struct AttendParams {
     CacheView c;
     const char *q;
@@ -55,7 +57,7 @@ struct AttendParams {
     float2 *part_ml;                          // [row][split]: maximum (times c, less Rows::kLift), sum
     int T, G, R, D, heads, seqs;              // heads: key/value heads
     int *used;                                // parts of each sequence, when flat
-    int flat;                                 // Walk
+    int flat;                                 // Walk, even_part
     int nsplit, nrg, slots, min_steps, unit;  // unit: tiles that a workgroup takes in one step
     int wk;                                   // waves of a workgroup that share rows and split keys
     float c2;                                 // scale * log2(e)
@@ -70,6 +72,14 @@ __device__ inline int end_of(const AttendParams &p, int n, int nd)
 struct Place {
     int b, h, rg, split, n, nd, end, t0, t1;
     bool whole;                                   // all the tiles of b: the output is final
+
+    // A wave's lanes may leave a loop apart, so that the compiler takes what
+    // follows for different in each: says that it is the same.
+    __device__ inline void uniform()
+    {
+        const auto same = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+        b = same(b), split = same(split), n = same(n), nd = same(nd), end = same(end), t0 = same(t0), t1 = same(t1), whole = same(whole);
+    }
 };
 
 // Each sequence cut into p.nsplit parts or fewer, one workgroup each.
@@ -102,6 +112,23 @@ __device__ inline Place part_of_sequence(const AttendParams &p)
     return at;
 }
 
+// What a workgroup's number says. spread: workgroups go to the 8 dies in turn,
+// and those of all heads for the same keys, whose rows lie side by side, are on
+// one (16 sequences of up to 30000 FP8 keys of 64 in pages: 105 us, 87 so).
+struct Number {
+    int h, rg, k;
+
+    __device__ inline Number(const AttendParams &p, bool spread)
+    {
+        int id = (int)blockIdx.x, die = 0;
+        if (spread) die = id & 7, id >>= 3;
+        h = id % p.heads;
+        id /= p.heads;
+        rg = id % p.nrg;
+        k = spread ? id / p.nrg * 8 + die : id / p.nrg;
+    }
+};
+
 // The places of a workgroup of which there is one a CU, so that none may have
 // more to do than another: the steps (`unit` tiles) of all sequences lie in a
 // row, for each key/value head and group of rows, and each of p.slots
@@ -121,13 +148,10 @@ struct Walk {
         return steps(p, clamp_length(p.length, b, p.c.tokens), clamp_drafted(p.drafted, b, p.T));
     }
 
-    __device__ inline Walk(const AttendParams &p)
+    __device__ inline Walk(const AttendParams &p, bool spread = false)
     {
-        int id = (int)blockIdx.x;
-        h = id % p.heads;
-        id /= p.heads;
-        rg = id % p.nrg;
-        slot = id / p.nrg;
+        const Number num(p, spread);
+        h = num.h, rg = num.rg, slot = num.k;
         b = slot, start = s0 = 0, s1 = 1, chunk = 1, len = cnt = 0;
         if (p.nsplit == 1) return;
         const int lane = (int)(threadIdx.x & 63);
@@ -178,6 +202,12 @@ struct Walk {
         if (!found) s1 = 0;
     }
 
+    __device__ inline void uniform()
+    {
+        const auto same = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+        b = same(b), start = same(start), s0 = same(s0), s1 = same(s1), chunk = same(chunk);
+    }
+
     __device__ inline bool next(const AttendParams &p, Place &at)
     {
         at.h = h, at.rg = rg;
@@ -207,6 +237,67 @@ struct Walk {
         return false;
     }
 };
+
+// One place a workgroup, none longer than another's may be: each sequence is cut
+// into runs of `chunk` steps, as many as it has, and each workgroup finds the
+// sequence and run that its number falls into. p.used says of how many parts a
+// sequence is. (Cut into as many parts each, long sequences would end last.)
+__device__ inline bool even_part(const AttendParams &p, Place &at)
+{
+    const Number num(p, true);
+    at.h = num.h, at.rg = num.rg;
+    const int k = num.k, lane = (int)(threadIdx.x & 63);
+    at.b = at.split = at.n = at.nd = at.end = at.t0 = at.t1 = 0, at.whole = false;
+    if (p.nsplit == 1) {                          // a workgroup a sequence
+        if (k >= p.seqs) return false;
+        at.b = k;
+        at.n = clamp_length(p.length, k, p.c.tokens), at.nd = clamp_drafted(p.drafted, k, p.T);
+        at.end = end_of(p, at.n, at.nd);
+        at.t1 = (at.end + kTileKeys - 1) / kTileKeys, at.whole = true;
+        at.uniform();
+        return true;
+    }
+    int len = 0, cnt = 0, total = 0, most = 0;
+    for (int i = lane; i < p.seqs; i += 64) {
+        len = clamp_length(p.length, i, p.c.tokens), cnt = clamp_drafted(p.drafted, i, p.T);
+        const int st = Walk::steps(p, len, cnt);
+        total += st;
+        most = max(most, st);
+    }
+    for (int x = 1; x < 64; x <<= 1) total += __shfl_xor(total, x), most = max(most, __shfl_xor(most, x));
+    total = __builtin_amdgcn_readfirstlane(total);
+    most = __builtin_amdgcn_readfirstlane(most);
+    const int chunk = max(max(p.min_steps, (total + p.slots - 1) / p.slots), (most + p.nsplit - 1) / p.nsplit);
+    const bool tell = blockIdx.x == 0 && threadIdx.x < 64;
+    bool found = false;
+    for (int base = 0, before = 0; base < p.seqs && (!found || tell); base += 64) {
+        const int i = base + lane;
+        if (p.seqs > 64 && i < p.seqs) len = clamp_length(p.length, i, p.c.tokens), cnt = clamp_drafted(p.drafted, i, p.T);
+        const int parts = i < p.seqs ? max((Walk::steps(p, len, cnt) + chunk - 1) / chunk, 1) : 0;
+        int sum = parts;
+        for (int x = 1; x < 64; x <<= 1) {
+            const int v = __shfl_up(sum, x);
+            if (lane >= x) sum += v;
+        }
+        if (tell && i < p.seqs) p.used[i] = parts;
+        const uint64_t past = __builtin_amdgcn_ballot_w64(before + sum > k);
+        if (!found && past) {
+            const int l = __builtin_ctzll(past);
+            const int of = __builtin_amdgcn_readlane(parts, l);
+            at.b = base + l;
+            at.split = k - (before + __builtin_amdgcn_readlane(sum, l) - of);
+            at.n = __builtin_amdgcn_readlane(len, l), at.nd = __builtin_amdgcn_readlane(cnt, l);
+            at.end = end_of(p, at.n, at.nd);
+            const int tiles = (at.end + kTileKeys - 1) / kTileKeys;
+            at.t0 = at.split * chunk * p.unit, at.t1 = min(at.t0 + chunk * p.unit, tiles);
+            at.whole = of == 1;
+            found = true;
+        }
+        before += __builtin_amdgcn_readlane(sum, 63);
+    }
+    at.uniform();
+    return __builtin_amdgcn_readfirstlane(found);
+}
 
 // What a kernel is made for: the types of the cache and, where that has 8 bits,
 // of the queries. E4M3 and 8-bit integers have a scale for each block of tokens
@@ -298,6 +389,29 @@ __device__ inline uint32_t not_finite(uint32_t w)
     }
 }
 
+// Loaded elements are widened behind this and not before: the compiler would
+// carry them from one tile to the next in their wide form, which the registers
+// do not hold.
+template <typename V, int N, int M>
+__device__ inline void hold(V (&v)[N][M])
+{
+    constexpr int W = sizeof(V) / 4;
+    typedef uint32_t Words __attribute__((ext_vector_type(W)));
+#pragma unroll
+    for (int i = 0; i < N; i++)
+#pragma unroll
+        for (int j = 0; j < M; j++) {
+            Words u = __builtin_bit_cast(Words, v[i][j]);
+#pragma unroll
+            for (int k = 0; k < W; k++) {
+                uint32_t word = u[k];
+                asm volatile("" : "+v"(word));
+                u[k] = word;
+            }
+            v[i][j] = __builtin_bit_cast(V, u);
+        }
+}
+
 // A row's 16-byte fragments of Q for the matrix cores (8 dims at 32 ks + 8 g).
 template <int KS, bool PAD>
 __device__ inline void load_q(const AttendParams &p, const char *row, bool there, int g, u32x4 (&f)[KS])
@@ -359,10 +473,10 @@ struct TileFinder {
             t.k[x] = p.c.k + (t.there[x] ? ko + h * p.c.ks2 : 0);
             t.v[x] = p.c.v + (t.there[x] ? vo + h * p.c.vs2 : 0);
             if constexpr (SCALED) {           // by scalar loads; of a half tile that is not there, 0
-                const int64_t first = p.c.table ? (int64_t)__builtin_amdgcn_readlane(entry, 2 * (i & 31) + x) : (int64_t)b;
-                const int block = (p.c.table ? key & ((1 << p.c.shift) - 1) : key) >> p.scales.shift;
-                const int64_t ka = first * p.scales.k0 + block * p.scales.k1 + h * p.scales.k2;
-                const int64_t va = first * p.scales.v0 + block * p.scales.v1 + h * p.scales.v2;
+                const uint32_t from = p.c.table ? (uint32_t)__builtin_amdgcn_readlane(entry, 2 * (i & 31) + x) : (uint32_t)b;
+                const uint32_t block = (uint32_t)(p.c.table ? key & ((1 << p.c.shift) - 1) : key) >> p.scales.shift;
+                const uint32_t ka = from * p.scales.k0 + block * p.scales.k1 + (uint32_t)h * p.scales.k2;
+                const uint32_t va = from * p.scales.v0 + block * p.scales.v1 + (uint32_t)h * p.scales.v2;
                 const float ks = scalar_load(p.scales.k + (t.there[x] ? ka : 0)), vs = scalar_load(p.scales.v + (t.there[x] ? va : 0));
                 t.ks[x] = t.there[x] ? ks : 0.f;
                 t.vs[x] = t.there[x] ? vs : 0.f;
@@ -852,7 +966,7 @@ struct Rows {
 // were rounded, and by 2.22e-3 with one; in 14.9 us both. Not so the FP16
 // weights of BF16 queries, three bits finer than the output: 1.689e-3 and
 // 1.698e-3, in 130 and 120 us (2 x 4 tokens over 131072 FP8 keys).
-template <int CT, int DP, int RB, bool PAD>
+template <int CT, int DP, int RB, bool PAD, int SPLIT>
 __global__ __launch_bounds__(kWaves * 64, DP == 256 ? 1 : 2) void k_attend(AttendParams p)
 {
     using W = Rows<CT, DP, RB, PAD, CT != kE5M2BF>;
@@ -860,63 +974,112 @@ __global__ __launch_bounds__(kWaves * 64, DP == 256 ? 1 : 2) void k_attend(Atten
     __shared__ float smem[2 * RB * 16 * DP + W::join_words(kWaves)];
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int wkey = wave & (p.wk - 1), wrow = wave / p.wk;
-    const Place at = part_of_sequence(p);
-    if (at.split && at.t0 >= at.t1) return;
-    W w;
-    w.init(p, at.b, at.h, (at.rg * (kWaves / p.wk) + wrow) * RB * 16, at.n, at.end);
+    const auto work = [&](const Place &at) {
+        W w;
+        w.init(p, at.b, at.h, (at.rg * (kWaves / p.wk) + wrow) * RB * 16, at.n, at.end);
 
-    const int first = at.t0 + wkey, count = w.row0 < p.R ? (at.t1 - first + p.wk - 1) / p.wk : 0;
-    int i = 0;
-    if (count > 0) {
-        const uint32_t koff = (uint32_t)(w.x * p.c.ks1) + w.g * 8 * W::es;
-        TileFinder<is_scaled(CT)> finder;
-        Tile t = finder.at(p, at.b, at.h, 0, first, at.n, w.lim);
-        Raw<CT> kr[2][KS];
-        if (t.fast) load_keys<CT, KS, PAD, false>(p, t, w.lim, w.x, w.g, koff, kr);
-        while (t.fast) {
-            Tile nxt = t;
-            nxt.fast = false;
-            if (++i < count) {
-                const Tile f = finder.at(p, at.b, at.h, i, first, at.n, w.lim);
-                if (f.fast) nxt = f;
+        const int first = at.t0 + wkey, count = w.row0 < p.R ? (at.t1 - first + p.wk - 1) / p.wk : 0;
+        int i = 0;
+        if (count > 0) {
+            const uint32_t koff = (uint32_t)(w.x * p.c.ks1) + w.g * 8 * W::es;
+            Raw<CT> kr[2][KS];
+            const auto next_of = [&](TileFinder<is_scaled(CT)> &finder, const Tile &t) {
+                Tile nxt = t;
+                nxt.fast = false;
+                if (++i < count) {
+                    const Tile f = finder.at(p, at.b, at.h, i, first, at.n, w.lim);
+                    if (f.fast) nxt = f;
+                }
+                return nxt;
+            };
+            TileFinder<is_scaled(CT)> finder;
+            Tile t = finder.at(p, at.b, at.h, 0, first, at.n, w.lim);
+            if constexpr (is_scaled(CT)) {
+                // The elements of a tile are few enough registers for all of the
+                // next one to be under way: its keys once this one's are widened,
+                // its values once this one's are multiplied.
+                typename W::Values v[W::VC][8];
+                if (t.fast) {
+                    load_keys<CT, KS, PAD, false>(p, t, w.lim, w.x, w.g, koff, kr);
+                    w.template load_values<false>(p, t, v);
+                }
+                while (t.fast) {
+                    const Tile nxt = next_of(finder, t);
+                    u32x4 k[2][KS];
+                    hold(kr);
+#pragma unroll
+                    for (int hf = 0; hf < 2; hf++)
+#pragma unroll
+                        for (int ks = 0; ks < KS; ks++) k[hf][ks] = widen<CT>(kr[hf][ks]);
+                    // No branch between the products and the first use of the
+                    // scores: beside a short one the compiler counted a product's
+                    // wait states along the longer way only, and scores were read
+                    // too early.
+                    if (nxt.fast) load_keys<CT, KS, PAD, false>(p, nxt, w.lim, w.x, w.g, koff, kr);
+                    f32x4 s[RB][2];
+                    u32x4 pw[W::TERMS][RB];
+                    w.score(k, s);
+                    w.scaled(t.ks, s);
+                    w.raise(p.c2, s);
+                    w.weigh(p.c2, s, t.vs, pw);
+                    hold(v);
+                    w.add(v, pw);
+                    if (nxt.fast) w.template load_values<false>(p, nxt, v);
+                    t = nxt;
+                }
+            } else {
+                if (t.fast) load_keys<CT, KS, PAD, false>(p, t, w.lim, w.x, w.g, koff, kr);
+                while (t.fast) {
+                    const Tile nxt = next_of(finder, t);
+                    typename W::Values v[W::VC][8];
+                    w.template load_values<false>(p, t, v);
+                    u32x4 k[2][KS];
+#pragma unroll
+                    for (int hf = 0; hf < 2; hf++)
+#pragma unroll
+                        for (int ks = 0; ks < KS; ks++) k[hf][ks] = widen<CT>(kr[hf][ks]);
+                    f32x4 s[RB][2];
+                    u32x4 pw[W::TERMS][RB];
+                    w.score(k, s);
+                    if (nxt.fast) load_keys<CT, KS, PAD, false>(p, nxt, w.lim, w.x, w.g, koff, kr);
+                    w.raise(p.c2, s);
+                    w.weigh(p.c2, s, t.vs, pw);
+                    w.add(v, pw);
+                    t = nxt;
+                }
             }
-            typename W::Values v[W::VC][8];
-            w.template load_values<false>(p, t, v);
-            u32x4 k[2][KS];
-#pragma unroll
-            for (int hf = 0; hf < 2; hf++)
-#pragma unroll
-                for (int ks = 0; ks < KS; ks++) k[hf][ks] = widen<CT>(kr[hf][ks]);
-            f32x4 s[RB][2];
-            u32x4 pw[W::TERMS][RB];
-            // Beside scales the scores are read where they were made, in one
-            // block: with the short branch of the loads between, the compiler
-            // counted a product's wait states along the longer way only, and
-            // scores were read too early.
-            if (is_scaled(CT) && nxt.fast) load_keys<CT, KS, PAD, false>(p, nxt, w.lim, w.x, w.g, koff, kr);
-            w.score(k, s);
-            if (!is_scaled(CT) && nxt.fast) load_keys<CT, KS, PAD, false>(p, nxt, w.lim, w.x, w.g, koff, kr);
-            w.scaled(t.ks, s);
-            w.raise(p.c2, s);
-            w.weigh(p.c2, s, t.vs, pw);
-            w.add(v, pw);
-            t = nxt;
         }
-    }
-    TileFinder<is_scaled(CT)> finder;
-    for (; i < count; i++) {
-        const Tile t = finder.at(p, at.b, at.h, i, first, at.n, w.lim);
-        if (t.key >= w.lim) break;
-        w.masked_tile(p, t, at);
-    }
+        TileFinder<is_scaled(CT)> finder;
+        for (; i < count; i++) {
+            const Tile t = finder.at(p, at.b, at.h, i, first, at.n, w.lim);
+            if (t.key >= w.lim) break;
+            w.masked_tile(p, t, at);
+        }
 
-    w.close(p.c2);
-    if (p.wk > 1) {
-        w.join(kWaves, p.wk, wkey, wave - wkey, smem + 2 * RB * 16 * DP, smem + (p.wk == 4 ? 0 : wrow) * RB * 16 * DP);
-        if (wkey) return;
+        w.close(p.c2);
+        if (p.wk > 1) {
+            w.join(kWaves, p.wk, wkey, wave - wkey, smem + 2 * RB * 16 * DP, smem + (p.wk == 4 ? 0 : wrow) * RB * 16 * DP);
+            if (wkey) return;
+        }
+        w.store(p, at);
+        if (w.odd) w.poison(p, at);
+    };
+    if constexpr (SPLIT == kRuns) {
+        Place at;
+        if (even_part(p, at)) work(at);
+    } else if constexpr (SPLIT == kWalks) {
+        Walk walk(p, true);
+        walk.uniform();
+        Place at;
+        while (walk.next(p, at)) {
+            at.uniform();
+            work(at);
+        }
+    } else {
+        const Place at = part_of_sequence(p);
+        if (at.split && at.t0 >= at.t1) return;
+        work(at);
     }
-    w.store(p, at);
-    if (w.odd) w.poison(p, at);
 }
 
 // Many rows: bound by the matrix cores and the exponentials. Eight waves of 32
@@ -1052,8 +1215,9 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
                     in = key & ((1 << p.c.shift) - 1);
                     there = there && first < p.c.pages;
                 }
-                const float *from = lane & 4 ? p.scales.v + (int64_t)first * p.scales.v0 + (in >> p.scales.shift) * p.scales.v1 + at.h * p.scales.v2
-                                             : p.scales.k + (int64_t)first * p.scales.k0 + (in >> p.scales.shift) * p.scales.k1 + at.h * p.scales.k2;
+                const uint32_t block = (uint32_t)in >> p.scales.shift;
+                const float *from = lane & 4 ? p.scales.v + (first * p.scales.v0 + block * p.scales.v1 + (uint32_t)at.h * p.scales.v2)
+                                             : p.scales.k + (first * p.scales.k0 + block * p.scales.k1 + (uint32_t)at.h * p.scales.k2);
                 if (!there) from = reinterpret_cast<const float *>(kZeros);
                 if (lane < 8)
                     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
@@ -1417,12 +1581,12 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attend_weigh(AttendParams p)
 // ------------------------------------------------------------------- host --
 struct Plan {
     int DP, RB, wk, nrg, nsplit, slots, min_steps, unit;
-    bool shared, flat;                            // k_attend_shared, Walk
+    bool shared, flat, walks;                     // k_attend_shared, Walk or even_part, Walk without sharing keys
     uint64_t rows, grid, off_ml, off_used, off_lse, bytes;
 };
 
 // may_share: the cache's rows begin on 16 bytes and end on them.
-Plan make_plan(uint32_t seqs, uint32_t kv_heads, uint32_t dim, uint32_t cache_tokens, uint32_t T, uint32_t heads, bool may_share)
+Plan make_plan(uint32_t seqs, uint32_t kv_heads, uint32_t dim, uint32_t cache_tokens, uint32_t T, uint32_t heads, bool may_share, bool scaled)
 {
     Plan a;
     const uint32_t G = heads / kv_heads;
@@ -1461,12 +1625,25 @@ Plan make_plan(uint32_t seqs, uint32_t kv_heads, uint32_t dim, uint32_t cache_to
     // FP8 keys 39 and 34). 32 rows, 2 x 131072 FP8 keys: 120 us, with two 140,
     // with four 143; a head dim of 256, 16 rows, 9155 keys: 36 us, with two 38.
     // More sequences than that leaves for each head: a workgroup each.
-    const uint64_t want = !a.shared && a.RB == 1 && a.DP < 256 ? 8 * kCUs : kCUs, each = (uint64_t)kv_heads * a.nrg;
+    // Beside scales, where a wave has all of its next tile under way: two a CU
+    // (32 rows, 2 x 131072 keys 116 us, with one 168, with four 133; 16 rows, 4
+    // x 16384 keys 35 and, with eight, 45), and eight of heads of 64, whose
+    // tiles are half as long (105 and 87 us where Number says).
+    uint64_t want = !a.shared && a.RB == 1 && a.DP < 256 ? 8 * kCUs : kCUs;
+    if (scaled && !a.shared && a.DP > 64) want = 2 * kCUs;
+    const uint64_t each = (uint64_t)kv_heads * a.nrg;
     const uint64_t slots = want > each ? want / each : 1;
     const uint64_t steps = (tiles + a.unit - 1) / a.unit, most = (steps + a.min_steps - 1) / a.min_steps;
     a.slots = (int)slots;
     a.nsplit = 1;
-    a.flat = a.shared && most > 1 && seqs < 4 * slots && (slots > 1 || seqs > 1);
+    a.flat = (a.shared || scaled) && most > 1 && seqs < 4 * slots && (slots > 1 || seqs > 1);
+    // Runs in workgroups of their own end apart by as much as one is long; where
+    // that is more than 4096 keys, each workgroup takes its share of all
+    // sequences instead, one place after the other, though a place begins and
+    // ends in some 6 us: 32 rows of ragged sequences of up to 16384 keys 125 us
+    // and, in runs, 168; of up to 8192 85 and 106; of up to 4096 56 and 54; 64
+    // of up to 1024 38 and 29.
+    a.walks = a.flat && scaled && !a.shared && a.RB == 1 && a.DP == 128 && seqs > 1 && seqs * tiles >= 128 * slots;
     if (a.flat) {
         // parts of one sequence: up to four times what equal lengths give
         uint64_t n = seqs == 1 ? slots : 4 * ((slots + seqs - 1) / seqs) + 1;
@@ -1476,7 +1653,8 @@ Plan make_plan(uint32_t seqs, uint32_t kv_heads, uint32_t dim, uint32_t cache_to
         const uint64_t n = (slots + seqs - 1) / seqs;
         a.nsplit = (int)(n > most ? most : n);
     }
-    a.grid = each * (a.flat ? slots : (uint64_t)seqs * a.nsplit);
+    const uint64_t runs = !a.flat ? (uint64_t)seqs * a.nsplit : a.shared || a.walks ? slots : slots + seqs;
+    a.grid = each * (scaled && !a.shared ? (runs + 7) / 8 * 8 : runs);
     a.rows = (uint64_t)seqs * heads * T;
     const auto up = [](uint64_t v) { return (v + 255) & ~255ull; };
     a.off_ml = a.nsplit > 1 ? up(a.rows * a.nsplit * a.DP * 4) : 0;
@@ -1493,9 +1671,15 @@ bool valid_shapes(uint32_t seqs, uint32_t kv_heads, uint32_t dim, uint32_t cache
 }
 
 template <int CT, int DP, int RB, bool PAD>
-int launch(const AttendParams &p, uint64_t grid, hipStream_t s)
+int launch(const AttendParams &p, uint64_t grid, bool walks, hipStream_t s)
 {
-    k_attend<CT, DP, RB, PAD><<<(unsigned)grid, kWaves * 64, 0, s>>>(p);
+    if constexpr (is_scaled(CT) && RB == 1 && DP == 128)
+        if (walks) {
+            k_attend<CT, DP, RB, PAD, kWalks><<<(unsigned)grid, kWaves * 64, 0, s>>>(p);
+            UZIP_KV_LAUNCH_CHECK("k_attend");
+            return UZIP_OK;
+        }
+    k_attend<CT, DP, RB, PAD, is_scaled(CT) ? kRuns : kParts><<<(unsigned)grid, kWaves * 64, 0, s>>>(p);
     UZIP_KV_LAUNCH_CHECK("k_attend");
     return UZIP_OK;
 }
@@ -1512,8 +1696,8 @@ int run(const AttendParams &p, const Plan &plan, int half, hipStream_t s)
             UZIP_KV_LAUNCH_CHECK("k_attend_shared");
             rc = UZIP_OK;
         }
-    } else if (plan.RB == 1) rc = launch<CT, DP, 1, PAD>(p, grid, s);
-    else rc = launch<CT, DP, 2, PAD>(p, grid, s);
+    } else if (plan.RB == 1) rc = launch<CT, DP, 1, PAD>(p, grid, plan.walks, s);
+    else rc = launch<CT, DP, 2, PAD>(p, grid, false, s);
     if (rc) return rc;
     if (p.nsplit > 1) {
         if (p.nsplit <= 16 || (p.flat && p.nsplit <= 64)) k_attend_join_few<DP><<<(unsigned)((plan.rows + 15) / 16), 256, 0, s>>>(p, (int64_t)plan.rows, half);
@@ -1539,9 +1723,12 @@ int run_type(const AttendParams &p, const Plan &plan, int half, hipStream_t s)
 uint64_t workspace_bytes(uint32_t seqs, uint32_t kv_heads, uint32_t dim, uint32_t cache_tokens, uint32_t tokens, uint32_t heads)
 {
     if (!valid_shapes(seqs, kv_heads, dim, cache_tokens, tokens, heads)) return 0;
-    const uint64_t a = make_plan(seqs, kv_heads, dim, cache_tokens, tokens, heads, true).bytes;
-    const uint64_t b = make_plan(seqs, kv_heads, dim, cache_tokens, tokens, heads, false).bytes;
-    return a > b ? a : b;
+    uint64_t most = 0;
+    for (int i = 0; i < 4; i++) {
+        const uint64_t bytes = make_plan(seqs, kv_heads, dim, cache_tokens, tokens, heads, i & 1, i & 2).bytes;
+        if (bytes > most) most = bytes;
+    }
+    return most;
 }
 
 // SCALED: the cache is E4M3 or 8-bit integers with these scales
@@ -1562,7 +1749,7 @@ int attend(const uzip_kv_cache_t *cache, const uzip_kv_scales_t *scales, const u
     if (ws_bytes < workspace_bytes(cache->seqs, cache->heads, cache->dim, cache->tokens, a->tokens, a->heads)) return UZIP_ENOSPC;
     int64_t bits = cache->dim * elem_size((int)cache->dtype);
     for (int i = 0; i < 3; i++) bits |= (cache->k_stride[i] | cache->v_stride[i]) * elem_size((int)cache->dtype);
-    const Plan plan = make_plan(cache->seqs, cache->heads, cache->dim, cache->tokens, a->tokens, a->heads, (bits & 15) == 0);
+    const Plan plan = make_plan(cache->seqs, cache->heads, cache->dim, cache->tokens, a->tokens, a->heads, (bits & 15) == 0, SCALED);
     if (plan.grid >= (1ull << 31) || (uint64_t)cache->seqs * ((cache->tokens + 31) / 32) >= (1ull << 31) ||
         (uint64_t)cache->seqs * cache->heads * ((cache->tokens + 127) / 128) >= (1ull << 31)) return UZIP_EINVAL;
 
