@@ -412,6 +412,28 @@ __device__ inline void hold(V (&v)[N][M])
         }
 }
 
+// Byte e of each of eight dwords, a lane's values of one dim and eight keys, as
+// BF16.
+template <int CT>
+__device__ inline u32x4 turned_over(const uint32_t (&w)[8], int e)
+{
+    u32x4 a;
+    if constexpr (is_i8(CT)) {
+#pragma unroll
+        for (int k = 0; k < 4; k++) a[k] = cut2<false>(byte_to_f32(w[2 * k], e), byte_to_f32(w[2 * k + 1], e));
+    } else {                                  // 4 x 4 bytes turned over, then widened
+#pragma unroll
+        for (int k = 0; k < 8; k += 4) {
+            const uint32_t sel = e < 2 ? 0x05010400u : 0x07030602u;
+            const uint32_t low = __builtin_amdgcn_perm(w[k + 1], w[k], sel), high = __builtin_amdgcn_perm(w[k + 3], w[k + 2], sel);
+            const uint32_t four = __builtin_amdgcn_perm(high, low, e % 2 ? 0x07060302u : 0x05040100u);
+            a[k / 2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(four, 1.f, false));
+            a[k / 2 + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(four, 1.f, true));
+        }
+    }
+    return a;
+}
+
 // A row's 16-byte fragments of Q for the matrix cores (8 dims at 32 ks + 8 g).
 template <int KS, bool PAD>
 __device__ inline void load_q(const AttendParams &p, const char *row, bool there, int g, u32x4 (&f)[KS])
@@ -619,14 +641,16 @@ struct Rows {
         bool any = false;
 #pragma unroll
         for (int rb = 0; rb < RB; rb++) {
-            top[rb] = quad_max(fmaxf(fmaxf(fmaxf(s[rb][0][0], s[rb][0][1]), fmaxf(s[rb][0][2], s[rb][0][3])),
-                                     fmaxf(fmaxf(s[rb][1][0], s[rb][1][1]), fmaxf(s[rb][1][2], s[rb][1][3]))));
+            top[rb] = fmaxf(fmaxf(fmaxf(s[rb][0][0], s[rb][0][1]), fmaxf(s[rb][0][2], s[rb][0][3])),
+                            fmaxf(fmaxf(s[rb][1][0], s[rb][1][1]), fmaxf(s[rb][1][2], s[rb][1][3])));
+            if constexpr (!is_scaled(CT)) top[rb] = quad_max(top[rb]);
             any = any || (top[rb] - m[rb]) * c2 > kSlack;
         }
         if (__builtin_expect(__builtin_amdgcn_ballot_w64(any) != 0 || far, 0)) {
             far = false;
 #pragma unroll
             for (int rb = 0; rb < RB; rb++) {
+                if constexpr (is_scaled(CT)) top[rb] = quad_max(top[rb]);      // a row's lanes have to agree only here
                 const float up = fmaxf(top[rb], m[rb]);
                 const float a = __builtin_amdgcn_exp2f((m[rb] - (up == -INFINITY ? 0.f : up)) * c2);
                 m[rb] = up;
@@ -669,7 +693,8 @@ struct Rows {
                 if constexpr (FINE) {
                     pw[0][rb][i] = cut2<f16>(a, b);
                     const f32x2 had = unpack2<f16>(pw[0][rb][i]);
-                    pw[1][rb][i] = pack2<f16>(__builtin_amdgcn_fmed3f(a - had.x, kLeast, a), __builtin_amdgcn_fmed3f(b - had.y, kLeast, b));
+                    if constexpr (is_scaled(CT)) pw[1][rb][i] = pack2<f16>(a - had.x, b - had.y);      // no infinities there
+                    else pw[1][rb][i] = pack2<f16>(__builtin_amdgcn_fmed3f(a - had.x, kLeast, a), __builtin_amdgcn_fmed3f(b - had.y, kLeast, b));
                 } else {
                     pw[0][rb][i] = pack2<f16>(a, b);
                 }
@@ -681,23 +706,15 @@ struct Rows {
     __device__ inline static u32x4 fragment(const Values (&v)[VC][8], int c, int e)
     {
         u32x4 a;
-        if constexpr (is_scaled(CT) && !is_i8(CT)) {      // 4 x 4 bytes turned over, then widened
+        if constexpr (is_scaled(CT)) {
+            uint32_t w[8];
 #pragma unroll
-            for (int k = 0; k < 8; k += 4) {
-                const uint32_t sel = e % 4 < 2 ? 0x05010400u : 0x07030602u;
-                const uint32_t low = __builtin_amdgcn_perm(v[c][k + 1][e / 4], v[c][k][e / 4], sel);
-                const uint32_t high = __builtin_amdgcn_perm(v[c][k + 3][e / 4], v[c][k + 2][e / 4], sel);
-                const uint32_t four = __builtin_amdgcn_perm(high, low, e % 2 ? 0x07060302u : 0x05040100u);
-                a[k / 2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(four, 1.f, false));
-                a[k / 2 + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(four, 1.f, true));
-            }
-            return a;
+            for (int k = 0; k < 8; k++) w[k] = v[c][k][e / 4];
+            return turned_over<CT>(w, e % 4);
         }
 #pragma unroll
         for (int k = 0; k < 4; k++) {
-            if constexpr (is_i8(CT)) {
-                a[k] = cut2<false>(byte_to_f32(v[c][2 * k][e / 4], e % 4), byte_to_f32(v[c][2 * k + 1][e / 4], e % 4));
-            } else if constexpr (is_byte(CT)) {
+            if constexpr (is_byte(CT)) {
                 const uint32_t sel = ((4u + e % 4) << 24) | (0x0cu << 16) | ((uint32_t)(e % 4) << 8) | 0x0cu;
                 a[k] = __builtin_amdgcn_perm(v[c][2 * k + 1][e / 4], v[c][2 * k][e / 4], sel);
             } else {
@@ -736,34 +753,39 @@ struct Rows {
             }
     }
 
+    // Scores of keys that a row does not see become -inf.
+    __device__ inline void hide(const AttendParams &p, const Tile &t, const Place &at, f32x4 (&s)[RB][2])
+    {
+        const int n = at.n, nd = at.nd;
+        uint32_t seen[RB];
+#pragma unroll
+        for (int rb = 0; rb < RB; rb++) seen[rb] = 0;
+        if (p.tree && t.key + kTileKeys > n) {
+#pragma unroll
+            for (int rb = 0; rb < RB; rb++) seen[rb] = tree_bits(p, at.b, tok[rb], t.key + 4 * g - n, nd, at.end - n);
+        }
+#pragma unroll
+        for (int rb = 0; rb < RB; rb++) {
+            seen[rb] |= leading_bits((p.tree ? n : min(lim, n + tok[rb] + 1)) - t.key - 4 * g);
+            seen[rb] &= there_bits(t);
+#pragma unroll
+            for (int i = 0; i < 8; i++) s[rb][i >> 2][i & 3] = seen[rb] >> i & 1 ? s[rb][i >> 2][i & 3] : -INFINITY;
+        }
+    }
+
     // One tile. values() is called for the values when the scores are done.
     // Not `fast`: one that not every row sees whole (the drafted tokens' own,
     // the last one, one with an absent page).
     template <typename F>
     __device__ inline void tile(const AttendParams &p, const Tile &t, const Place &at, const u32x4 (&k)[2][KS], Values (&v)[VC][8], F values)
     {
-        const int n = at.n, nd = at.nd;
+        const int n = at.n;
         f32x4 s[RB][2];
         u32x4 pw[TERMS][RB];
         score(k, s);
         scaled(t.ks, s);
         values(v);
-        if (!t.fast) {
-            uint32_t seen[RB];
-#pragma unroll
-            for (int rb = 0; rb < RB; rb++) seen[rb] = 0;
-            if (p.tree && t.key + kTileKeys > n) {
-#pragma unroll
-                for (int rb = 0; rb < RB; rb++) seen[rb] = tree_bits(p, at.b, tok[rb], t.key + 4 * g - n, nd, at.end - n);
-            }
-#pragma unroll
-            for (int rb = 0; rb < RB; rb++) {
-                seen[rb] |= leading_bits((p.tree ? n : min(lim, n + tok[rb] + 1)) - t.key - 4 * g);
-                seen[rb] &= there_bits(t);
-#pragma unroll
-                for (int i = 0; i < 8; i++) s[rb][i >> 2][i & 3] = seen[rb] >> i & 1 ? s[rb][i >> 2][i & 3] : -INFINITY;
-            }
-        }
+        if (!t.fast) hide(p, t, at, s);
         raise(p.c2, s);
         weigh(p.c2, s, t.vs, pw);
         if (!is_i8(CT) && t.key + kTileKeys > n) {
@@ -1129,17 +1151,12 @@ template <int CT, int DP, bool PAD, bool PAGED>
 __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams p)
 {
     constexpr int RB = 2;
-    // one term of a weight; beside scales it is BF16, too coarse for an FP16 output
-    using W = Rows<CT, DP, RB, PAD, is_scaled(CT) && f16_queries(CT)>;
-    constexpr bool SCALED = is_scaled(CT);
+    using W = Rows<CT, DP, RB, PAD, false>;
     constexpr int KS = W::KS, es = W::es, ROW = DP * es, PIECES = ROW / 16;
     constexpr int LOADS = 2 * 64 * ROW / (kShared * 64 * 16);      // 16-byte pieces a thread loads a stage
     constexpr int STAGE = 2 * 64 * ROW, RING = ROW == 256 ? 4 : 8;
-    constexpr int WAITED = (RING - 3) * (LOADS + SCALED);          // loads of the stages behind the one waited for
     static_assert(RING * STAGE >= 4 * RB * 16 * DP * 4, "the waves' outputs are joined in the ring");
     __shared__ __attribute__((aligned(16))) char smem[RING * STAGE + W::join_words(kShared) * 4];
-    // each wave's scales of a stage's four half tiles, the keys' and the values'
-    __shared__ float lscale[SCALED ? RING * kShared * 8 : 1];
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int wkey = wave & (p.wk - 1), wrow = wave / p.wk;
     Walk walk(p);
@@ -1205,32 +1222,6 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
                 __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
                                                  (__attribute__((address_space(3))) void *)(to + j * kShared * 1024), 16, 0, 0);
             }
-            if constexpr (SCALED) {
-                const int lane = tid & 63, key = key0 + i * 64 + (lane & 3) * 16;
-                uint32_t first = (uint32_t)at.b;
-                int in = key;
-                bool there = key < at.end;
-                if constexpr (PAGED) {
-                    first = (uint32_t)__shfl(entry, (i & 15) * 4 + (lane & 3));
-                    in = key & ((1 << p.c.shift) - 1);
-                    there = there && first < p.c.pages;
-                }
-                const uint32_t block = (uint32_t)in >> p.scales.shift;
-                const float *from = lane & 4 ? p.scales.v + (first * p.scales.v0 + block * p.scales.v1 + (uint32_t)at.h * p.scales.v2)
-                                             : p.scales.k + (first * p.scales.k0 + block * p.scales.k1 + (uint32_t)at.h * p.scales.k2);
-                if (!there) from = reinterpret_cast<const float *>(kZeros);
-                if (lane < 8)
-                    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
-                                                     (__attribute__((address_space(3))) void *)(lscale + (i % RING * kShared + wave) * 8), 4, 0, 0);
-            }
-        };
-        // scales of a tile's halves
-        const auto scales_of = [&](int i, int tile, float (&ks)[2], float (&vs)[2]) {
-            if constexpr (SCALED) {
-                const float *from = lscale + (i % RING * kShared + wave) * 8 + tile * 2;
-#pragma unroll
-                for (int hf = 0; hf < 2; hf++) ks[hf] = from[hf], vs[hf] = from[4 + hf];
-            }
         };
         // The queries are waited for here: a wait for them inside the loop would be
         // one for every stage under way. The first stages arrive meanwhile.
@@ -1264,7 +1255,7 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
         // shorter. Behind the barrier all waves' are, and all are past the values
         // of stage i - 2, whose place is free.
         const auto enter = [&](int i) {
-            if (issued - i == RING - 2) __builtin_amdgcn_s_waitcnt(0x0f70 | (WAITED & 15) | (WAITED >> 4) << 14);
+            if (issued - i == RING - 2) __builtin_amdgcn_s_waitcnt(0x0f70 | ((RING - 3) * LOADS & 15) | ((RING - 3) * LOADS >> 4) << 14);
             else __builtin_amdgcn_s_waitcnt(0x0f70);
             asm volatile("" ::: "memory");
             __builtin_amdgcn_s_barrier();
@@ -1277,18 +1268,15 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
         const bool rows = w.row0 < p.R;               // else this wave only loads
         if (fast > 0) {
             f32x4 s[RB][2];
-            const auto step = [&](int i, const char *stage, int tile, int next_i, const char *next_stage, int next_tile) {
+            const auto step = [&](const char *stage, int tile, const char *next_stage, int next_tile) {
                 typename W::Values v[W::VC][8];
                 u32x4 k[2][KS], pw[W::TERMS][RB];
                 f32x4 next[RB][2];
-                float ks[2], vs[2], other[2];
-                scales_of(i, tile, other, vs);
-                scales_of(next_i, next_tile, ks, other);
+                const float none[2] = {1.f, 1.f};     // no scales
                 keys_of(next_stage, next_tile, k);
                 values_of(stage, tile, v);
-                w.weigh(p.c2, s, vs, pw);
+                w.weigh(p.c2, s, none, pw);
                 w.score(k, next);
-                w.scaled(ks, next);
                 w.add(v, pw);
     #pragma unroll
                 for (int rb = 0; rb < RB; rb++)
@@ -1299,19 +1287,16 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
             enter(0);
             if (rows) {
                 u32x4 k[2][KS];
-                float ks[2], vs[2];
                 keys_of(smem, p.wk == 1 ? 0 : wkey, k);
-                scales_of(0, p.wk == 1 ? 0 : wkey, ks, vs);
                 w.score(k, s);
-                w.scaled(ks, s);
                 w.raise(p.c2, s);
             }
             for (int i = 0; i < fast; i++) {
                 const char *stage = smem + i % RING * STAGE, *next = i + 1 < fast ? smem + (i + 1) % RING * STAGE : stage;
                 // after the last tile its own scores again, which change nothing
-                if (p.wk == 1 && rows) step(i, stage, 0, i, stage, 1);
+                if (p.wk == 1 && rows) step(stage, 0, stage, 1);
                 if (i + 1 < fast) enter(i + 1);
-                if (rows) step(i, stage, p.wk == 1 ? 1 : wkey, i + 1 < fast ? i + 1 : i, next, p.wk == 1 ? 0 : wkey);
+                if (rows) step(stage, p.wk == 1 ? 1 : wkey, next, p.wk == 1 ? 0 : wkey);
             }
         }
         for (int i = fast; i < stages; i++) {
@@ -1330,8 +1315,256 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
                 u32x4 k[2][KS];
                 typename W::Values v[W::VC][8];
                 keys_of(stage, tile, k);
-                scales_of(i, tile, t.ks, t.vs);
                 w.tile(p, t, at, k, v, [&](typename W::Values (&u)[W::VC][8]) { values_of(stage, tile, u); });
+            }
+        }
+        w.close(p.c2);
+        if (p.wk == 2) {
+            __syncthreads();                          // the ring's memory is free
+            w.join(kShared, 2, wkey, wave - wkey, reinterpret_cast<float *>(smem + RING * STAGE), reinterpret_cast<float *>(smem) + wrow * RB * 16 * DP);
+            if (wkey) continue;
+        }
+        w.store(p, at);
+        if (w.odd) w.poison(p, at);
+    }
+}
+
+// The same for 8 bits with scales, whose elements take longer to widen than to
+// multiply: a workgroup does it once for all its waves. Threads read the
+// elements of the stage after the next into registers, and write those of the
+// next one to LDS in 16 bits, keys in rows as above, values as the matrix cores
+// take them: for dim e of each lane's, the 16 bytes of all 64 lanes in order.
+// So a stage is read from one of three places while the next one fills another,
+// with one barrier a stage. Half the waves widen values, right behind it, half
+// keys, a tile later, so that the two waves of a SIMD are not at the same thing.
+// Trees of 64 tokens of 64 FP16 heads over 8 ragged sequences of up to 8205 E4M3
+// keys of 128: 212 us, with every wave widening for itself 277, with all of them
+// widening at once 221. The products, in two terms, are 43 us at the dense peak;
+// the vector units are busy for half the time, the matrix cores for a third.
+template <int CT, int DP, bool PAD, bool PAGED>
+__global__ __launch_bounds__(kShared * 64, 2) void k_attend_wide(AttendParams p)
+{
+    constexpr int RB = 2;
+    // one term of a weight; it is BF16 beside scales, too coarse for an FP16 output
+    using W = Rows<CT, DP, RB, PAD, f16_queries(CT)>;
+    constexpr int KS = W::KS, VE = W::VE, ROW = DP * 2, PIECES = ROW / 16;
+    constexpr int TILE = DP * 64, STAGE = 64 * ROW + 2 * TILE, RING = 3;      // a tile's values, and bytes of a stage
+    constexpr int UNITS = DP / 64;                // of 16 elements of keys, a thread
+    static_assert(RING * STAGE >= 4 * RB * 16 * DP * 4, "the waves' outputs are joined in the ring");
+    __shared__ __attribute__((aligned(16))) char smem[RING * STAGE + W::join_words(kShared) * 4];
+    __shared__ float lscale[RING * 8];            // of the four half tiles, the keys' and the values'
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int wkey = wave & (p.wk - 1), wrow = wave / p.wk;
+    Walk walk(p);
+    walk.uniform();
+    Place at;
+    while (walk.next(p, at)) {
+        at.uniform();
+        int tid = (int)threadIdx.x;
+        asm volatile("" : "+v"(tid));
+        __syncthreads();                              // the ring is free
+
+        // Stages of 64 keys, the first `fast` of them all cached tokens, which
+        // every row sees; in pages, up to the first that touches an absent one.
+        const int key0 = at.t0 * kTileKeys, stages = (at.t1 - at.t0 + 1) / 2;
+        int fast = min((at.t1 - at.t0) / 2, max(at.n - key0, 0) / 64);
+        if constexpr (PAGED) {
+            const int lane = tid & 63;
+            for (int i = 0; i < fast * 4; i += 64) {
+                const bool bad = i + lane < fast * 4 && (uint32_t)p.c.table[at.b * p.c.ts + ((key0 + (i + lane) * 16) >> p.c.shift)] >= p.c.pages;
+                const uint64_t any = __builtin_amdgcn_ballot_w64(bad);
+                if (any) fast = (i + __builtin_ctzll(any)) / 4;
+            }
+        }
+        // What a thread reads of a stage. Values: 4 dims of the eight keys of a
+        // lane; keys: 16 elements of a row, UNITS times. first[]: their keys'
+        // numbers in the stage, two of which may lie in different pages.
+        const bool val = wave < kShared / 2, some = !val || tid < 2 * DP;
+        const int quad = tid % (DP / 4), vg = tid / (DP / 4) & 3, vtile = tid / DP & 1;
+        int row[2];
+#pragma unroll
+        for (int j = 0; j < 2; j++) row[j] = val ? vtile * 32 + j * 16 + 4 * vg : ((tid & 255) + j * 256) / (DP / 16) & 63;
+        const int chunk = (tid & 255) % (DP / 16);
+        const bool pad = PAD && (val ? quad * 4 : chunk * 16) >= p.D;
+        const char *base = (val ? p.c.v + at.h * p.c.vs2 + quad * 4 : p.c.k + at.h * p.c.ks2 + chunk * 16) + (PAGED ? 0 : at.b * (val ? p.c.vs0 : p.c.ks0));
+        const int64_t step1 = val ? p.c.vs1 : p.c.ks1, step0 = val ? p.c.vs0 : p.c.ks0;
+        const int shalf = tid & 3;                    // threads 0 to 7: a half tile's scale, of values from 4 on
+        uint32_t raw[8], page[2] = {0, 0}, spage = 0;
+        float sraw = 0.f;
+        const auto look_up = [&](int i) {             // pages of a stage
+            if constexpr (PAGED) {
+#pragma unroll
+                for (int j = 0; j < 2; j++) {
+                    const int key = key0 + i * 64 + row[j];
+                    page[j] = key < at.end ? (uint32_t)p.c.table[at.b * p.c.ts + (key >> p.c.shift)] : ~0u;
+                }
+                if (tid < 8) {
+                    const int key = key0 + i * 64 + shalf * 16;
+                    spage = key < at.end ? (uint32_t)p.c.table[at.b * p.c.ts + (key >> p.c.shift)] : ~0u;
+                }
+            }
+        };
+        const auto fetch = [&](int i) {
+#pragma unroll
+            for (int r = 0; r < 8; r++) raw[r] = 0;
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const int key = key0 + i * 64 + row[j];
+                const bool there = some && !pad && (!PAGED || page[j] < p.c.pages);
+                const int64_t in = PAGED ? key & ((1 << p.c.shift) - 1) : key;
+                const char *from = base + (PAGED ? (int64_t)page[j] * step0 : 0) + in * step1;
+                if (val) {
+#pragma unroll
+                    for (int r = 0; r < 4; r++)
+                        if (there && key + r < at.end) raw[j * 4 + r] = *reinterpret_cast<const uint32_t *>(from + r * step1);
+                } else if (j < UNITS && there && key < at.end) {
+                    const u32x4 w = *reinterpret_cast<const u32x4 *>(from);
+#pragma unroll
+                    for (int r = 0; r < 4; r++) raw[j * 4 + r] = w[r];
+                }
+            }
+            if (tid < 8) {
+                const int key = key0 + i * 64 + shalf * 16;
+                const uint32_t from = PAGED ? spage : (uint32_t)at.b;
+                const uint32_t block = (uint32_t)(PAGED ? key & ((1 << p.c.shift) - 1) : key) >> p.scales.shift;
+                sraw = 0.f;
+                if (key < at.end && (!PAGED || spage < p.c.pages))
+                    sraw = tid & 4 ? p.scales.v[from * p.scales.v0 + block * p.scales.v1 + (uint32_t)at.h * p.scales.v2]
+                                   : p.scales.k[from * p.scales.k0 + block * p.scales.k1 + (uint32_t)at.h * p.scales.k2];
+            }
+            if (i + 1 < stages) look_up(i + 1);
+        };
+        const auto put = [&](int i) {
+            char *stage = smem + i % RING * STAGE;
+            if (val) {
+                if (some)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const int d = quad * 4 + e;
+                        *reinterpret_cast<u32x4 *>(stage + 64 * ROW + vtile * TILE + d % VE * 1024 + vg * 256 + d / VE * 16) = turned_over<CT>(raw, e);
+                    }
+            } else {
+#pragma unroll
+                for (int j = 0; j < UNITS; j++)
+#pragma unroll
+                    for (int k = 0; k < 2; k++)
+                        *reinterpret_cast<u32x4 *>(stage + row[j] * ROW + (((2 * chunk + k) ^ mixed<PIECES>(row[j])) << 4)) =
+                            widen<CT>(Raw<CT>{raw[j * 4 + 2 * k], raw[j * 4 + 2 * k + 1]});
+            }
+            if (tid < 8) lscale[i % RING * 8 + tid] = sraw;
+        };
+        look_up(0);
+        fetch(0);
+        W w;
+        w.init(p, at.b, at.h, (at.rg * (kShared / p.wk) + wrow) * RB * 16, at.n, at.end);
+        put(0);
+        if (stages > 1) fetch(1);
+        // Behind the barrier all waves have written stage i, and none reads stage
+        // i - 2 any more, whose place is that of i + 1.
+        const auto refill = [&](int i) {
+            if (i + 1 < stages) put(i + 1);
+            if (i + 2 < stages) fetch(i + 2);
+        };
+        const auto enter = [&](int i, bool whole) {
+            __syncthreads();
+            if (val || whole) refill(i);
+        };
+        const auto keys_of = [&](int i, int tile, u32x4 (&k)[2][KS], float (&ks)[2]) {
+            const char *kb = smem + i % RING * STAGE + (tile * 32 + w.x) * ROW;
+#pragma unroll
+            for (int hf = 0; hf < 2; hf++) {
+#pragma unroll
+                for (int kk = 0; kk < KS; kk++)
+                    k[hf][kk] = *reinterpret_cast<const u32x4 *>(kb + hf * 16 * ROW + (((kk * 4 + w.g) ^ mixed<PIECES>(w.x)) << 4));
+                ks[hf] = lscale[i % RING * 8 + tile * 2 + hf];
+            }
+        };
+        const auto scales_of = [&](int i, int tile, float (&vs)[2]) {
+#pragma unroll
+            for (int hf = 0; hf < 2; hf++) vs[hf] = lscale[i % RING * 8 + 4 + tile * 2 + hf];
+        };
+        // products with the values; CHECK: those that are not finite are left to poison()
+        const auto add = [&](int i, int tile, const u32x4 (&pw)[W::TERMS][RB], bool check) {
+            const char *vb = smem + i % RING * STAGE + 64 * ROW + tile * TILE + w.g * 256 + w.x * 16;
+            uint32_t any = 0;
+#pragma unroll
+            for (int e = 0; e < VE; e++) {
+                u32x4 a = *reinterpret_cast<const u32x4 *>(vb + e * 1024);
+                if (!is_i8(CT) && check)
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        const uint32_t bad = not_finite<kBF16>(a[k]);
+                        any |= bad;
+                        a[k] &= ~bad;
+                    }
+#pragma unroll
+                for (int t = 0; t < W::TERMS; t++)
+#pragma unroll
+                    for (int rb = 0; rb < RB; rb++) w.acc[rb][e] = mfma<false>(a, pw[t][rb], w.acc[rb][e]);
+            }
+            if (check) w.odd = w.odd || __builtin_amdgcn_ballot_w64(any != 0) != 0;
+        };
+        // One tile's weights and output beside the next tile's scores.
+        const bool rows = w.row0 < p.R;               // else this wave only widens
+        if (fast > 0) {
+            f32x4 s[RB][2];
+            const auto step = [&](int i, int tile, int next_i, int next_tile) {
+                u32x4 k[2][KS], pw[W::TERMS][RB];
+                f32x4 next[RB][2];
+                float ks[2], vs[2];
+                scales_of(i, tile, vs);
+                keys_of(next_i, next_tile, k, ks);
+                w.weigh(p.c2, s, vs, pw);
+                __builtin_amdgcn_s_setprio(1);
+                w.score(k, next);
+                w.scaled(ks, next);
+                add(i, tile, pw, false);
+                __builtin_amdgcn_s_setprio(0);
+#pragma unroll
+                for (int rb = 0; rb < RB; rb++)
+#pragma unroll
+                    for (int hf = 0; hf < 2; hf++) s[rb][hf] = next[rb][hf];
+                w.raise(p.c2, s);
+            };
+            enter(0, true);
+            if (rows) {
+                u32x4 k[2][KS];
+                float ks[2];
+                keys_of(0, p.wk == 1 ? 0 : wkey, k, ks);
+                w.score(k, s);
+                w.scaled(ks, s);
+                w.raise(p.c2, s);
+            }
+            for (int i = 0; i < fast; i++) {
+                // after the last tile its own scores again, which change nothing
+                if (p.wk == 1 && rows) step(i, 0, i, 1);
+                if (i + 1 < fast) enter(i + 1, false);
+                if (rows) step(i, p.wk == 1 ? 1 : wkey, i + 1 < fast ? i + 1 : i, i + 1 < fast ? p.wk == 1 ? 0 : wkey : p.wk == 1 ? 1 : wkey);
+                if (i + 1 < fast && !val) refill(i + 1);
+            }
+        }
+        for (int i = fast; i < stages; i++) {
+            enter(i, true);
+            for (int tile = wkey; tile < 2; tile += p.wk) {
+                Tile t;
+                t.key = key0 + i * 64 + tile * kTileKeys;
+                t.fast = false;
+                if (!rows || t.key >= w.lim) break;
+#pragma unroll
+                for (int hf = 0; hf < 2; hf++) {
+                    const int key = t.key + 16 * hf;
+                    t.there[hf] = key < at.end && (!PAGED || (uint32_t)p.c.table[at.b * p.c.ts + (key >> p.c.shift)] < p.c.pages);
+                }
+                u32x4 k[2][KS], pw[W::TERMS][RB];
+                f32x4 s[RB][2];
+                keys_of(i, tile, k, t.ks);
+                scales_of(i, tile, t.vs);
+                w.score(k, s);
+                w.scaled(t.ks, s);
+                w.hide(p, t, at, s);
+                w.raise(p.c2, s);
+                w.weigh(p.c2, s, t.vs, pw);
+                add(i, tile, pw, t.key + kTileKeys > at.n);
             }
         }
         w.close(p.c2);
@@ -1691,8 +1924,13 @@ int run(const AttendParams &p, const Plan &plan, int half, hipStream_t s)
     int rc = UZIP_EINVAL;
     if (plan.shared) {
         if constexpr (DP <= 128) {
-            if (p.c.table) k_attend_shared<CT, DP, PAD, true><<<(unsigned)grid, kShared * 64, 0, s>>>(p);
-            else k_attend_shared<CT, DP, PAD, false><<<(unsigned)grid, kShared * 64, 0, s>>>(p);
+            if constexpr (is_scaled(CT)) {
+                if (p.c.table) k_attend_wide<CT, DP, PAD, true><<<(unsigned)grid, kShared * 64, 0, s>>>(p);
+                else k_attend_wide<CT, DP, PAD, false><<<(unsigned)grid, kShared * 64, 0, s>>>(p);
+            } else {
+                if (p.c.table) k_attend_shared<CT, DP, PAD, true><<<(unsigned)grid, kShared * 64, 0, s>>>(p);
+                else k_attend_shared<CT, DP, PAD, false><<<(unsigned)grid, kShared * 64, 0, s>>>(p);
+            }
             UZIP_KV_LAUNCH_CHECK("k_attend_shared");
             rc = UZIP_OK;
         }
