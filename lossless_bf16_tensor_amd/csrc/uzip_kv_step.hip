@@ -31,7 +31,8 @@ constexpr int kNodes = 1024;                      // of a tree, at most
 struct Walked {
     int at, next, count, rejected;                // rejected: children of `at`, whose tokens are listed
     double c, mass;
-    int pending, pad;                             // mass has to become a sum before node `next` is tried
+    int pending;                                  // mass has to become a sum before node `next` is tried
+    int at_sums;                                  // which of the two places its sums are in
 };
 
 struct VerifyParams {
@@ -42,8 +43,9 @@ struct VerifyParams {
     const float *uniform;
     int32_t *path, *count, *token;
     int T, V, slices, segs;
-    double *sums;                                 // [sequence][segs]
-    Walked *state;                                // [sequence]
+    double *sums;                                 // [2][sequence][segs]
+    Walked *state;                                // [2][sequence]
+    int seqs, rounds;                             // launches of k_verify_more
     int32_t *rejected;                            // [sequence][T]
 };
 
@@ -191,6 +193,60 @@ __global__ __launch_bounds__(kVerifyThreads) void k_verify(VerifyParams p)
     }
 }
 
+// Sum over the workgroup of what its threads have, in one order; wave_sum: a word a wave.
+__device__ inline double whole_sum(double sum, double *wave_sum, int waves)
+{
+    for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
+    if ((threadIdx.x & 63) == 0) wave_sum[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    double total = 0.;
+    for (int i = 0; i < waves; i++) total += wave_sum[i];
+    __syncthreads();
+    return total;
+}
+
+// Walks that wait for a sum go on. What they wait for was written by the launch
+// before, and they write to the other place, since all of a sequence's
+// workgroups read it.
+template <int PT>
+__global__ __launch_bounds__(kVerifyThreads) void k_verify_more(VerifyParams p, int round)
+{
+    __shared__ int32_t list[kNodes];              // of rejected tokens: none with q
+    __shared__ Walked shared;
+    __shared__ double wave_sum[kVerifyWaves];
+    const int slice = (int)blockIdx.x % p.slices, b = (int)blockIdx.x / p.slices;
+    const int tid = (int)threadIdx.x, nd = clamp_drafted(p.drafted, b, p.T);
+    if (nd == 0) return;
+    const Walked was = p.state[(int64_t)(round & 1) * p.seqs + b];
+    Walked *out = p.state + (int64_t)(~round & 1) * p.seqs + b;
+    if (!was.pending) {
+        if (slice == 0 && tid == 0) *out = was;
+        return;
+    }
+    const double *sums = p.sums + ((int64_t)was.at_sums * p.seqs + b) * p.segs;
+    double sum = 0.;
+    for (int i = tid; i < p.segs; i += kVerifyThreads) sum += sums[i];
+    const double total = whole_sum(sum, wave_sum, kVerifyWaves);
+    if (tid < 64) {
+        Walked w = was;
+        w.mass = total;
+        walk<PT>(p, b, nd, w, list, slice == 0);
+        if (w.at != was.at || w.c != was.c) w.at_sums ^= 1;
+        if (tid == 0) {
+            shared = w;
+            if (slice == 0) *out = w;
+        }
+    }
+    __syncthreads();
+    const Walked w = shared;
+    if (w.at_sums == was.at_sums) return;         // the same sums
+    const char *pr = p.p + b * p.p0 + w.at * p.p1, *qr = p.q + b * p.q0 + w.at * p.q1;
+    for (int seg = slice * kVerifyWaves + (tid >> 6); seg < p.segs; seg += p.slices * kVerifyWaves) {
+        const double one = segment_sum<PT>(p, pr, qr, w, list, seg);
+        if ((tid & 63) == 0) p.sums[((int64_t)w.at_sums * p.seqs + b) * p.segs + seg] = one;
+    }
+}
+
 template <int PT>
 __global__ __launch_bounds__(kEndThreads) void k_verify_end(VerifyParams p)
 {
@@ -205,10 +261,10 @@ __global__ __launch_bounds__(kEndThreads) void k_verify_end(VerifyParams p)
         if (tid == 0) p.count[b] = 0, p.token[b] = -1;
         return;
     }
-    Walked w = p.state[b];
+    Walked w = p.state[(int64_t)(p.rounds & 1) * p.seqs + b];
     for (int i = tid; i < w.rejected; i += threads) list[i] = p.rejected[(int64_t)b * p.T + i];
     __syncthreads();
-    double *sums = p.sums + (int64_t)b * p.segs;
+    double *sums = p.sums + ((int64_t)w.at_sums * p.seqs + b) * p.segs;
     const char *pr, *qr;
     double total;
     bool plain = false;                           // nothing was left: from p itself
@@ -216,25 +272,20 @@ __global__ __launch_bounds__(kEndThreads) void k_verify_end(VerifyParams p)
         pr = p.p + b * p.p0 + w.at * p.p1, qr = p.q && !plain ? p.q + b * p.q0 + w.at * p.q1 : nullptr;
         double sum = 0.;
         for (int i = tid; i < p.segs; i += threads) sum += sums[i];
-        for (int x = 1; x < 64; x <<= 1) sum += __shfl_xor(sum, x);
-        if (lane == 0) wave_sum[wave] = sum;
-        __syncthreads();
-        total = 0.;
-        for (int i = 0; i < waves; i++) total += wave_sum[i];
-        __syncthreads();
+        total = whole_sum(sum, wave_sum, waves);
         if (w.pending) {
             if (wave == 0) {
                 const int at = w.at;
                 const double c = w.c;
                 w.mass = total;
                 walk<PT>(p, b, nd, w, list, true);
-                w.pad = w.at != at || w.c != c;   // other sums are needed
+                w.at_sums = w.at != at || w.c != c;       // other sums are needed
                 if (lane == 0) shared = w;
             }
             __syncthreads();
             w = shared;
             __syncthreads();
-            if (!w.pad) continue;                 // mass was 0, and c is what it was
+            if (!w.at_sums) continue;                 // mass was 0, and c is what it was
         } else if (!(total > 0.) && !plain) {
             plain = true;
             w.rejected = 0;
@@ -316,8 +367,8 @@ VerifyWs verify_ws(uint64_t seqs, uint64_t nodes, uint64_t vocab)
 {
     const auto up = [](uint64_t v) { return (v + 255) & ~255ull; };
     VerifyWs w;
-    w.off_state = up(seqs * ((vocab + kSeg - 1) / kSeg) * 8);
-    w.off_rejected = w.off_state + up(seqs * sizeof(Walked));
+    w.off_state = up(2 * seqs * ((vocab + kSeg - 1) / kSeg) * 8);
+    w.off_rejected = w.off_state + up(2 * seqs * sizeof(Walked));
     w.bytes = w.off_rejected + up(seqs * nodes * 4);
     return w;
 }
@@ -332,6 +383,10 @@ int run_verify(const VerifyParams &p, int seqs, hipStream_t s)
 {
     k_verify<PT><<<(unsigned)(seqs * p.slices), kVerifyThreads, 0, s>>>(p);
     UZIP_KV_LAUNCH_CHECK("k_verify");
+    for (int i = 0; i < p.rounds; i++) {
+        k_verify_more<PT><<<(unsigned)(seqs * p.slices), kVerifyThreads, 0, s>>>(p, i);
+        UZIP_KV_LAUNCH_CHECK("k_verify_more");
+    }
     // a walk that asks for sums has them made by the one workgroup: as wide as it can be
     k_verify_end<PT><<<(unsigned)seqs, p.q && p.parent ? kEndThreads : kVerifyThreads, 0, s>>>(p);
     UZIP_KV_LAUNCH_CHECK("k_verify_end");
@@ -764,6 +819,12 @@ int uzip_kv_verify(const uzip_kv_verify_args_t *a, void *d_ws, uint64_t ws_bytes
     // a segment a wave while there are workgroups to spare, four a CU
     const int64_t most = (p.segs + kVerifyWaves - 1) / kVerifyWaves, want = (4 * kCUs + a->seqs - 1) / a->seqs;
     p.slices = (int)(most < want ? most : want);
+    // Two launches that make one more sum, where rows are long and some of the
+    // sequences will ask for sums again and again: 16 trees of 32 nodes over
+    // 131072 tokens 41 us, without 60; but one tree 26 and 21, 64 over 50000 64
+    // and 60.
+    p.seqs = (int)a->seqs;
+    p.rounds = a->draft && a->parent && p.T > 2 && p.segs >= 64 && p.seqs >= 4 && p.seqs <= 32 ? 2 : 0;
     char *w = static_cast<char *>(d_ws);
     p.sums = reinterpret_cast<double *>(w);
     p.state = reinterpret_cast<Walked *>(w + ws.off_state);

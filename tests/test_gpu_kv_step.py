@@ -76,6 +76,20 @@ def test_every_child_is_rejected_and_tried_in_order():
     check(s)
 
 
+@pytest.mark.parametrize("B,near", [(3, 0.6), (4, 4.0), (9, 1.5), (32, 2.0)])
+def test_long_rows_of_some_trees(B, near):
+    """Sums made by launches of their own, as many as walks ask for and fewer."""
+    s = problem(B, 14, 66000, near=near, tree=True, seed=B)
+    drafted = [14] * B
+    drafted[0], drafted[1], drafted[-1] = 0, 2, 13
+    found = check(s, drafted)
+    assert len({n for _, n, _ in found}) > 1
+    s["draft"] = s["target"].clone()           # nothing is ever left
+    s["target"] = s["target"] * 0.5
+    s["uniform"][:, 1:] = 0.75
+    check(s)
+
+
 @pytest.mark.parametrize("tree", [False, True])
 def test_equal_probabilities_accept_all(tree):
     s = problem(3, 9, 700, tree=tree, seed=2, near=0.0)
