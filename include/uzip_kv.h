@@ -208,7 +208,7 @@ int uzip_kv_evict(const uzip_kv_cache_t *cache, const uzip_kv_cache_t *out, cons
  * needs none (d_ws may then be NULL) or the shapes are invalid. */
 uint64_t uzip_kv_evict_workspace_bytes(uint32_t seqs, uint32_t kv_heads, uint32_t cache_tokens);
 
-/* Scales of an 8-bit cache: `block` tokens (a power of two, at least 16, at
+/* Scales of an 8-bit cache: `block` tokens (a power of two from 16 to 65536, at
  * most the page) of a head share one for their keys and one for their values,
  * and an element stands for itself times it. That of token t of sequence b,
  * head h: k[b * k_stride[0] + t / block * k_stride[1] + h * k_stride[2]]; in

@@ -15,10 +15,11 @@ types: bfloat16, float16, or float8_e5m2 beside queries of either. The head dim
 is a multiple of 8 up to 256. No tensor is empty.
 
 Caches in 8 bits with scales (:func:`append` and :func:`attend` with k_scale and
-v_scale) are float8_e4m3fn or int8. A block of tokens of a head, a power of two,
-at least 16, shares a scale for its keys and one for its values: float32
+v_scale) are float8_e4m3fn or int8. A block of tokens of a head, a power of two
+from 16 to 65536, shares a scale for its keys and one for its values: float32
 [sequences, blocks, kv heads], or [pages, blocks of a page, kv heads], any
-strides; the number of blocks says how long they are.
+strides; the number of blocks says how long they are. Scales of blocks that are
+seen are positive, from 2^-100 to 2^100.
 
 Steps with drafted tokens go on with :func:`verify`, :func:`accept` and, where
 caches are in pages, :func:`fork`, :func:`compact` and :func:`copy_pages`.
@@ -228,24 +229,27 @@ def _cache(k: torch.Tensor, v: torch.Tensor, table, seqs: int, scaled: bool = Fa
                         seqs, heads, dim, tokens, second, first, 0), heads, dim, tokens)
 
 
-def _block(scale: torch.Tensor, tokens: int) -> int:
-    """Tokens that share a scale: the power of two, at least 16, of which a tensor of `tokens` has scale.shape[1]."""
+@functools.lru_cache(maxsize=4096)
+def _block(scales: tuple, cache: tuple) -> int:
+    """Tokens that share a scale: the power of two, at least 16, by which scales
+    of this shape are those of a cache of that; 0 where there is none."""
+    first, tokens, heads, _ = cache
     block = 16
-    while block < tokens and -(-tokens // block) > scale.shape[1]:
+    while block < tokens and len(scales) == 3 and -(-tokens // block) > scales[1]:
         block *= 2
-    return block if -(-tokens // block) == scale.shape[1] else 0
+    return block if block <= 65536 and scales == (first, -(-tokens // block), heads) else 0
 
 
 def _scales(k_scale, v_scale, cache: torch.Tensor):
     """Packed uzip_kv_scales_t."""
     if k_scale is None or v_scale is None:
         raise ValueError("k_scale and v_scale go together")
-    first, second, heads, _ = cache.shape
-    block = _block(k_scale, second) if k_scale.dim() == 3 else 0
-    for t in (k_scale, v_scale):
-        if not (t.dtype == torch.float32 and t.device == cache.device and block and t.shape == (first, -(-second // block), heads)):
-            raise ValueError(f"k_scale, v_scale: expected float32 [{first}, blocks, {heads}] on {cache.device}, blocks of a power of two "
-                             f"of tokens, at least 16, {second} tokens in all")
+    dev, shape = cache.device, cache.shape
+    block = _block(tuple(k_scale.shape), tuple(shape)) if len(shape) == 4 else 0
+    if not (block and v_scale.shape == k_scale.shape and k_scale.dtype == v_scale.dtype == torch.float32
+            and k_scale.device == dev and v_scale.device == dev):
+        raise ValueError(f"k_scale, v_scale: expected float32 [{shape[0]}, blocks, {shape[2]}] on {dev}, blocks of a power of two of tokens "
+                         f"from 16 to 65536, {shape[1]} tokens in all")
     return _SCALES.pack(k_scale.data_ptr(), v_scale.data_ptr(), *k_scale.stride(), *v_scale.stride(), block, 0)
 
 
@@ -602,6 +606,8 @@ def verify(tokens: torch.Tensor, target: torch.Tensor, uniform: torch.Tensor, *,
         if not (draft.shape == target.shape and draft.dtype == target.dtype and draft.device == dev):
             raise ValueError("draft differs from target in shape, type or device")
     at, tok = _ints(tokens, B, T, dev, "tokens")
+    if uniform.requires_grad:
+        _no_gradient()
     ua, us = _ints(uniform, B, T, dev, "uniform", torch.float32)
     pa = par = 0
     if parent is not None:

@@ -252,6 +252,34 @@ def test_work_enough_for_shared_keys(B, T, hq, H, D, S, qt, cache, block, layout
     assert ((w.double().sum((1, 2)).cpu() - total).abs() <= total * 2.0 ** -10)[fine & (length > 0)].all()
 
 
+@pytest.mark.parametrize("B,T,hq,H,D,S,cache,block,layout", [
+    (70, 1, 16, 8, 128, 4000, E4M3, 16, "shd"), (35, 3, 8, 4, 120, 9000, I8, 32, "paged64"), (130, 2, 8, 2, 128, 500, I8, 16, "paged16"),
+    (300, 1, 8, 8, 64, 100, E4M3, 64, "shd"), (9, 5, 16, 1, 64, 3000, I8, 16, "hsd"), (66, 1, 1, 1, 256, 2500, E4M3, 16, "shd"),
+    (700, 1, 8, 8, 128, 40, I8, 16, "shd"), (5, 20, 16, 8, 128, 5000, I8, 128, "shd"), (80, 9, 8, 2, 192, 300, E4M3, 16, "shd")])
+def test_many_sequences(B, T, hq, H, D, S, cache, block, layout):
+    """Ragged ones, some of nothing: runs of their own, shares of all sequences, a workgroup a sequence."""
+    q, k, v, ks, vs, table = make(B, T, hq, H, D, S, BF16, cache, block, layout, seed=B + S, dev=DEV)
+    g = torch.Generator().manual_seed(B)
+    G = hq // H
+    length = torch.randint(0, S - T + 1, (B,), generator=g).to(torch.int32)
+    length[::7], length[1::9] = 0, S - T
+    drafted = torch.randint(0, T + 1, (B,), generator=g).to(torch.int32)
+    drafted[B // 2], length[B // 2] = T, S - T
+    lse, w = torch.empty(B, T, hq, device=DEV), torch.zeros(B, H, k.shape[1] if table is None else table.shape[1] * k.shape[1], device=DEV)
+    out = kv.attend(q, put(k.cpu(), layout), put(v.cpu(), layout), length.to(DEV), table=table, drafted=drafted.to(DEV), lse=lse, score=w,
+                    k_scale=put(ks.cpu(), layout), v_scale=put(vs.cpu(), layout))
+    for b in sorted({0, 1, 2, 5 % B, B // 2, B - 1, 63 % B, 64 % B, 65 % B}):
+        for h in {0, H - 1}:
+            args = [t[:, :, h:h + 1] for t in (k, v, ks, vs)] if table is not None else [t[b:b + 1, :, h:h + 1] for t in (k, v, ks, vs)]
+            want = step_rows(q[b:b + 1, :, h * G:h * G + G].cpu(), [t.cpu() for t in args], block, length[b:b + 1],
+                             None if table is None else table[b:b + 1].cpu(), None, drafted[b:b + 1], range(T), False)
+            for i, (o, ob, l, lb) in want.items():
+                ref.within(out[b, i, h * G:h * G + G], o, ob, f"out {b} {i} {h}")
+                ref.within(lse[b, i, h * G:h * G + G], l, lb, f"lse {b} {i} {h}")
+    total = (drafted * hq).double()
+    assert ((w.double().sum((1, 2)).cpu() - total).abs() <= total * 2.0 ** -10).all()
+
+
 def step_rows(q, args, block, length, table, tree, drafted, rows, coarse):
     """Rows of one sequence and key/value head by the 64-bit form, with their bounds."""
     k, v, ks, vs = args
@@ -458,9 +486,10 @@ def test_append_turns(dtype, cache, D, rot, interleaved, T):
                     assert (part <= sb * MOST[cache] * (1 + 2.0 ** -20)).all() and (part > sb / 2 * MOST[cache] * (1 - 2.0 ** -20)).all()
 
 
-def test_many_angles_in_a_block():
-    """More than a workgroup holds: worked out where they are used, the same."""
-    D, block, T = 256, 128, 128
+@pytest.mark.parametrize("D", [256, 128, 120])
+def test_many_angles_in_a_block(D):
+    """More than a workgroup holds, worked out where they are used, and as many as it holds."""
+    block, T = 128, 128
     nk, nv = new_tokens(1, T, 1, D, BF16, 3)
     freq = kv.rope_freq(D, device=DEV)
     got = []

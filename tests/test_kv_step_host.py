@@ -171,9 +171,9 @@ def test_pools_as_runs():
 
 
 @pytest.mark.parametrize("tokens,blocks,block", [(16, 1, 16), (17, 2, 16), (17, 1, 32), (100, 7, 16), (100, 4, 32), (100, 2, 64), (100, 1, 128), (64, 4, 16),
-                                                 (1, 1, 16), (131072, 2048, 64), (100, 3, 0), (100, 8, 0), (100, 0, 0)])
+                                                 (1, 1, 16), (131072, 2048, 64), (100, 3, 0), (100, 8, 0), (100, 0, 0), (131072, 1, 0)])
 def test_block_by_the_number_of_scales(tokens, blocks, block):
-    assert kv._block(torch.zeros(1, blocks, 1), tokens) == block
+    assert kv._block((1, blocks, 1), (1, tokens, 1, 64)) == block
 
 
 def operands(dtype=E4M3):
@@ -200,7 +200,7 @@ def test_host_tensors_are_refused(call):
         CALLS[call](operands())
 
 
-@pytest.mark.parametrize("call,names", [("append", ("q", "new", "new_v", "ks", "vs")), ("attend", ("q", "ks", "vs")), ("verify", ("p", "d")),
+@pytest.mark.parametrize("call,names", [("append", ("q", "new", "new_v", "ks", "vs")), ("attend", ("q", "ks", "vs")), ("verify", ("p", "d", "u")),
                                         ("accept", ("k16", "v16")), ("copy", ("pool",))])
 def test_tensors_that_require_a_gradient(call, names):
     for name in names:
