@@ -249,7 +249,12 @@ __device__ inline void turn_queries(const Append8Params &p, float2 *cs)
 // One launch: workgroups for the keys and values of a block of tokens of some
 // heads, then those that turn queries. A wave (or, of long blocks, the four of
 // a workgroup) takes the keys or values of a head: turns the new tokens, finds
-// their largest magnitude, and rounds what it holds in registers.
+// their largest magnitude, and rounds what it holds in registers. Bound by
+// memory where there is much: 2 x 8192 decoded tokens of 8 heads of 128 into
+// integers in pages, blocks of 16, 28 us, 3.6 TB/s (a copy 5.1; every element is
+// read once, and a wave's loads, their maximum and the stores follow each
+// other). One token with 64 query heads 5.4 us: the trips to memory for the
+// length, the tokens and the scale, and the angles.
 template <bool F16, bool I8, int MODE>
 __global__ __launch_bounds__(kThreads, MODE == kStill ? 4 : 3) void k_append8(Append8Params p)
 {

@@ -165,6 +165,10 @@ __device__ inline double segment_sum(const VerifyParams &p, const char *pr, cons
     return sum;
 }
 
+// Bound by trips to memory that depend on each other: tokens, their
+// probabilities, the row where the walk ends, its sums, a segment again. A chain
+// of 5 nodes over 32000 tokens 5 us and, for k_verify_end, 7; 16 trees of 32
+// over 131072 9, twice 7, and 10.
 template <int PT>
 __global__ __launch_bounds__(kVerifyThreads) void k_verify(VerifyParams p)
 {
@@ -397,7 +401,8 @@ int run_verify(const VerifyParams &p, int seqs, hipStream_t s)
 // Token length + path[j] becomes token length + j. A way down a tree goes up
 // in its numbers, so path[j] >= j, and a row is read before or when it is
 // written if each thread, for its 8 elements, goes through the rows in order;
-// kMoved rows' loads are under way together.
+// kMoved rows' loads are under way together. Bound by the chain of trips: count,
+// path, page numbers, rows; 64 sequences of 64 nodes in pages 7 us, one 2.
 constexpr int kAcceptThreads = 256, kMoved = 8, kChunk = 64;
 
 struct AcceptParams {
@@ -451,6 +456,9 @@ __global__ __launch_bounds__(kAcceptThreads) void k_accept(AcceptParams p)
 // ------------------------------------------------------------------ pages --
 // What holds a page is read off the table itself, so there are no counts that
 // could go wrong: a word a page, the least of the marks that its holders make.
+// Marks, the plan and the table are launches of their own, since each needs all
+// of the one before: 256 sequences of up to 512 pages of 11000 in 2 + 5 + 6 + 4
+// us. The plan is one workgroup's, which looks at 8192 pages at a time.
 constexpr uint32_t kFree = 0xffffffffu;
 constexpr uint32_t kHeld = 0;                     // fork: full, or held outside; compact: held outside
 // fork: 1 + the first sequence that fills it on; compact: 1 of the table; then 2 + where it goes
@@ -678,7 +686,8 @@ __global__ __launch_bounds__(kPageThreads) void k_compact_fill(PageParams p, int
 }
 
 // Pages are copied as bytes, in units of U, kCopied of which a thread has under
-// way. Each workgroup takes a piece of one page of one pool.
+// way. Each workgroup takes a piece of one page of one pool. 4000 pages of 64 KB
+// in two pools: 207 us, the rate of a copy.
 constexpr int kPools = 8, kCopied = 4;
 struct Pool {
     char *data;
