@@ -237,11 +237,15 @@ int uzip_kv_append_scaled(const uzip_kv_cache_t *cache, const uzip_kv_scales_t *
                           const uzip_kv_rope_t *rope, hipStream_t s);
 
 /* async. uzip_kv_attend over a cache of E4M3 or I8, with queries of BF16 or
- * F16. The workspace is that of uzip_kv_attend. Weights times the values'
+ * F16. Weights times the values'
  * scales are multiplied with the values in two terms of BF16; in one, for BF16
  * queries, where more than 64 rows share keys over much work. */
 int uzip_kv_attend_scaled(const uzip_kv_cache_t *cache, const uzip_kv_scales_t *scales, const uzip_kv_attend_args_t *a,
                           void *d_ws, uint64_t ws_bytes, hipStream_t s);
+
+/* Workspace of uzip_kv_attend_scaled for these shapes; 0 when they are invalid. */
+uint64_t uzip_kv_attend_scaled_workspace_bytes(uint32_t seqs, uint32_t kv_heads, uint32_t dim, uint32_t cache_tokens,
+                                               uint32_t tokens, uint32_t heads);
 
 /* async. Which drafted tokens the target accepts. Each sequence has a tree of
  * nodes: node 0 is its last token, node i > 0 is a drafted token tokens[b, i]

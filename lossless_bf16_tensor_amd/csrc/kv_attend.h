@@ -1347,9 +1347,11 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
 // with one barrier a stage. Half the waves widen values, right behind it, half
 // keys, a tile later, so that the two waves of a SIMD are not at the same thing.
 // Trees of 64 tokens of 64 FP16 heads over 8 ragged sequences of up to 8205 E4M3
-// keys of 128: 212 us, with every wave widening for itself 277, with all of them
-// widening at once 221. The products, in two terms, are 43 us at the dense peak;
-// the vector units are busy for half the time, the matrix cores for a third.
+// keys of 128: 204 us, with every wave widening for itself 277, with all of them
+// widening at once 10 more, with values read from LDS where they are used 8 more
+// (keys read two fragments at a time, 3 more). The products, in two terms, are 43
+// us at the dense peak; the vector units are busy for 55 % of the time, the matrix
+// cores for 36.
 template <int CT, int DP, bool PAD, bool PAGED>
 __global__ __launch_bounds__(kShared * 64, 2) void k_attend_wide(AttendParams p)
 {
@@ -1492,24 +1494,40 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_wide(AttendParams p)
 #pragma unroll
             for (int hf = 0; hf < 2; hf++) vs[hf] = lscale[i % RING * 8 + 4 + tile * 2 + hf];
         };
-        // products with the values; CHECK: those that are not finite are left to poison()
-        const auto add = [&](int i, int tile, const u32x4 (&pw)[W::TERMS][RB], bool check) {
+        // Products with the values, two dims of a lane's at a time, the next two on
+        // their way from LDS meanwhile; the first two are read by ready(), before
+        // what else there is to do. check: those that are not finite are left to
+        // poison().
+        u32x4 two[2][2];
+        const auto read_two = [&](int i, int tile, int e) {
             const char *vb = smem + i % RING * STAGE + 64 * ROW + tile * TILE + w.g * 256 + w.x * 16;
+#pragma unroll
+            for (int k = 0; k < 2; k++) two[e / 2 & 1][k] = *reinterpret_cast<const u32x4 *>(vb + (e + k) * 1024);
+        };
+        const auto ready = [&](int i, int tile) { read_two(i, tile, 0); };
+        const auto add = [&](int i, int tile, const u32x4 (&pw)[W::TERMS][RB], bool check) {
             uint32_t any = 0;
 #pragma unroll
-            for (int e = 0; e < VE; e++) {
-                u32x4 a = *reinterpret_cast<const u32x4 *>(vb + e * 1024);
-                if (!is_i8(CT) && check)
+            for (int e = 0; e < VE; e += 2) {
+                if (e + 2 < VE) {
+                    read_two(i, tile, e + 2);
+                    __builtin_amdgcn_sched_barrier(0);        // not moved down to where they are used
+                }
 #pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        const uint32_t bad = not_finite<kBF16>(a[k]);
-                        any |= bad;
-                        a[k] &= ~bad;
-                    }
+                for (int j = 0; j < 2; j++) {
+                    u32x4 a = two[e / 2 & 1][j];
+                    if (!is_i8(CT) && check)
 #pragma unroll
-                for (int t = 0; t < W::TERMS; t++)
+                        for (int k = 0; k < 4; k++) {
+                            const uint32_t bad = not_finite<kBF16>(a[k]);
+                            any |= bad;
+                            a[k] &= ~bad;
+                        }
 #pragma unroll
-                    for (int rb = 0; rb < RB; rb++) w.acc[rb][e] = mfma<false>(a, pw[t][rb], w.acc[rb][e]);
+                    for (int t = 0; t < W::TERMS; t++)
+#pragma unroll
+                        for (int rb = 0; rb < RB; rb++) w.acc[rb][e + j] = mfma<false>(a, pw[t][rb], w.acc[rb][e + j]);
+                }
             }
             if (check) w.odd = w.odd || __builtin_amdgcn_ballot_w64(any != 0) != 0;
         };
@@ -1524,6 +1542,8 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_wide(AttendParams p)
                 scales_of(i, tile, vs);
                 keys_of(next_i, next_tile, k, ks);
                 w.weigh(p.c2, s, vs, pw);
+                ready(i, tile);
+                __builtin_amdgcn_sched_barrier(0);
                 __builtin_amdgcn_s_setprio(1);
                 w.score(k, next);
                 w.scaled(ks, next);
@@ -1573,6 +1593,7 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_wide(AttendParams p)
                 w.hide(p, t, at, s);
                 w.raise(p.c2, s);
                 w.weigh(p.c2, s, t.vs, pw);
+                ready(i, tile);
                 add(i, tile, pw, t.key + kTileKeys > at.n);
             }
         }
@@ -1967,15 +1988,12 @@ int run_type(const AttendParams &p, const Plan &plan, int half, hipStream_t s)
     return p.D == 256 ? run<CT, 256, false>(p, plan, half, s) : run<CT, 256, true>(p, plan, half, s);
 }
 
-uint64_t workspace_bytes(uint32_t seqs, uint32_t kv_heads, uint32_t dim, uint32_t cache_tokens, uint32_t tokens, uint32_t heads)
+uint64_t workspace_bytes(uint32_t seqs, uint32_t kv_heads, uint32_t dim, uint32_t cache_tokens, uint32_t tokens, uint32_t heads, bool scaled)
 {
     if (!valid_shapes(seqs, kv_heads, dim, cache_tokens, tokens, heads)) return 0;
-    uint64_t most = 0;
-    for (int i = 0; i < 4; i++) {
-        const uint64_t bytes = make_plan(seqs, kv_heads, dim, cache_tokens, tokens, heads, i & 1, i & 2).bytes;
-        if (bytes > most) most = bytes;
-    }
-    return most;
+    const uint64_t a = make_plan(seqs, kv_heads, dim, cache_tokens, tokens, heads, true, scaled).bytes;
+    const uint64_t b = make_plan(seqs, kv_heads, dim, cache_tokens, tokens, heads, false, scaled).bytes;
+    return a > b ? a : b;
 }
 
 // SCALED: the cache is E4M3 or 8-bit integers with these scales
@@ -1993,7 +2011,7 @@ int attend(const uzip_kv_cache_t *cache, const uzip_kv_scales_t *scales, const u
     if (a->reserved || (a->score && (a->score_stride[0] < 0 || a->score_stride[1] < 0 || a->score_tokens > cache->tokens))) return UZIP_EINVAL;
     if (a->tree && (a->tree_stride[0] < 0 || a->tree_stride[1] < 0)) return UZIP_EINVAL;
     if (!d_ws || !aligned(d_ws, 16)) return UZIP_EINVAL;
-    if (ws_bytes < workspace_bytes(cache->seqs, cache->heads, cache->dim, cache->tokens, a->tokens, a->heads)) return UZIP_ENOSPC;
+    if (ws_bytes < workspace_bytes(cache->seqs, cache->heads, cache->dim, cache->tokens, a->tokens, a->heads, SCALED)) return UZIP_ENOSPC;
     int64_t bits = cache->dim * elem_size((int)cache->dtype);
     for (int i = 0; i < 3; i++) bits |= (cache->k_stride[i] | cache->v_stride[i]) * elem_size((int)cache->dtype);
     const Plan plan = make_plan(cache->seqs, cache->heads, cache->dim, cache->tokens, a->tokens, a->heads, (bits & 15) == 0, SCALED);

@@ -7,7 +7,7 @@ extern "C" {
 uint64_t uzip_kv_attend_workspace_bytes(uint32_t seqs, uint32_t kv_heads, uint32_t dim, uint32_t cache_tokens,
                                         uint32_t tokens, uint32_t heads)
 {
-    return uzip_kv::workspace_bytes(seqs, kv_heads, dim, cache_tokens, tokens, heads);
+    return uzip_kv::workspace_bytes(seqs, kv_heads, dim, cache_tokens, tokens, heads, false);
 }
 
 int uzip_kv_attend(const uzip_kv_cache_t *cache, const uzip_kv_attend_args_t *a, void *d_ws, uint64_t ws_bytes,

@@ -51,7 +51,8 @@ from .uzip import UzipError, lib as _codec_lib
 
 # every symbol include/uzip_kv.h declares
 EXPORTS = ("uzip_kv_rope", "uzip_kv_append", "uzip_kv_attend", "uzip_kv_attend_workspace_bytes", "uzip_kv_evict",
-           "uzip_kv_evict_workspace_bytes", "uzip_kv_append_scaled", "uzip_kv_attend_scaled", "uzip_kv_verify",
+           "uzip_kv_evict_workspace_bytes", "uzip_kv_append_scaled", "uzip_kv_attend_scaled",
+           "uzip_kv_attend_scaled_workspace_bytes", "uzip_kv_verify",
            "uzip_kv_verify_workspace_bytes", "uzip_kv_accept", "uzip_kv_fork", "uzip_kv_compact", "uzip_kv_copy_pages",
            "uzip_kv_pages_workspace_bytes")
 
@@ -92,6 +93,7 @@ def lib():
             "uzip_kv_evict_workspace_bytes": (u64, [u32] * 3),
             "uzip_kv_append_scaled": (ctypes.c_int, [st, st, st, st, vp]),
             "uzip_kv_attend_scaled": (ctypes.c_int, [st, st, st, vp, u64, vp]),
+            "uzip_kv_attend_scaled_workspace_bytes": (u64, [u32] * 6),
             "uzip_kv_verify": (ctypes.c_int, [st, vp, u64, vp]),
             "uzip_kv_verify_workspace_bytes": (u64, [u32] * 3),
             "uzip_kv_accept": (ctypes.c_int, [st, st, vp]),
@@ -415,9 +417,10 @@ def append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, k_cache: to
 
 
 @functools.lru_cache(maxsize=4096)
-def attend_workspace_bytes(seqs: int, kv_heads: int, dim: int, cache_tokens: int, tokens: int, heads: int) -> int:
-    """Workspace that :func:`attend` needs for these shapes; 0 when they are invalid."""
-    return int(lib().uzip_kv_attend_workspace_bytes(seqs, kv_heads, dim, cache_tokens, tokens, heads))
+def attend_workspace_bytes(seqs: int, kv_heads: int, dim: int, cache_tokens: int, tokens: int, heads: int, scaled: bool = False) -> int:
+    """Workspace that :func:`attend` needs for these shapes, scaled: over a cache with scales; 0 when they are invalid."""
+    call = lib().uzip_kv_attend_scaled_workspace_bytes if scaled else lib().uzip_kv_attend_workspace_bytes
+    return int(call(seqs, kv_heads, dim, cache_tokens, tokens, heads))
 
 
 def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, length: torch.Tensor, *,
@@ -479,7 +482,7 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, length
                 raise ValueError("out differs from q in shape, type or device")
             _written(out, "out")
         if ws is None:
-            ws = torch.empty(attend_workspace_bytes(B, heads, D, tokens, T, hq), dtype=torch.uint8, device=dev)
+            ws = torch.empty(attend_workspace_bytes(B, heads, D, tokens, T, hq, scaled), dtype=torch.uint8, device=dev)
         else:
             if not (ws.dtype == torch.uint8 and ws.is_contiguous() and ws.device == dev):
                 raise ValueError(f"ws: expected contiguous uint8 on {dev} from a 16-byte boundary")

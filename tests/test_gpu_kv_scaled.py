@@ -326,7 +326,7 @@ def test_attend_in_a_graph_on_another_stream():
     torch.cuda.synchronize()
     assert torch.equal(got, want)
     out = torch.empty_like(dq)
-    ws = torch.empty(kv.attend_workspace_bytes(3, 2, 128, 15 * 64, 4, 16), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(kv.attend_workspace_bytes(3, 2, 128, 15 * 64, 4, 16, True), dtype=torch.uint8, device=DEV)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         kv.attend(dq, dk, dv, n, table=dt, k_scale=dks, v_scale=dvs, out=out, ws=ws)
@@ -514,7 +514,7 @@ def test_append_then_attend_in_a_graph():
     n = torch.tensor([190, 0, 77], dtype=torch.int32, device=DEV)
     dk, dv, dks, dvs, dt = (put(t) for t in (k, v, ks, vs, table))
     turned, out = torch.empty_like(q), torch.empty_like(q)
-    ws = torch.empty(kv.attend_workspace_bytes(B, H, D, 7 * 32, T, hq), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(kv.attend_workspace_bytes(B, H, D, 7 * 32, T, hq, True), dtype=torch.uint8, device=DEV)
 
     def run():
         kv.append(q, nk, nv, dk, dv, n, freq, table=dt, k_scale=dks, v_scale=dvs, out=turned)

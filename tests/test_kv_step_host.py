@@ -65,13 +65,24 @@ def test_other_refusals_of_caches_with_scales():
     assert kv.lib().uzip_kv_attend_scaled(cache(dtype=4), None, None, 1 << 25, 1 << 30, None) == EINVAL
     for bad in (dict(dtype=2), dict(T=0), dict(heads=6), dict(scale=0.0), dict(ws=0), dict(q=tensor(8)), dict(out=tensor(1 << 22))):
         assert attend(**bad) == EINVAL, bad
-    assert attend(ws_bytes=kv.attend_workspace_bytes(1, 4, 128, 64, 4, 8) - 1) == ENOSPC
+    assert attend(ws_bytes=kv.attend_workspace_bytes(1, 4, 128, 64, 4, 8, True) - 1) == ENOSPC
     for bad in (dict(dtype=2), dict(T=0), dict(heads=0), dict(length=0), dict(k=tensor(0)), dict(v=tensor(12)), dict(q=tensor(0)),
                 dict(out=tensor(1 << 22, (0, 2048, 128))), dict(out=tensor(1 << 23), k=tensor(1 << 23)), dict(f=scales(v=1 << 26)),
                 dict(c=cache(dtype=4, v=1 << 20))):
         assert append(**bad) == EINVAL, bad
     for bad in BAD_ROPES:
         assert append(rope=rope_args(**bad)) == EINVAL
+
+
+def test_workspace_of_attention_over_scales():
+    """Parts of split rows: within a few times the queries' own size in binary32, whatever the capacity; none for bad shapes."""
+    assert kv.attend_workspace_bytes(0, 4, 128, 64, 4, 8, True) == kv.attend_workspace_bytes(1, 4, 128, 64, 4, 6, True) == 0
+    for B in (1, 7, 64, 500):
+        for T in (1, 5, 64):
+            for S in (1, 100, 20000, 1 << 20):
+                rows = B * T * 64
+                parts = 1 + 4 * (2048 // B + 1)
+                assert kv.attend_workspace_bytes(B, 8, 128, S, T, 64, True) <= rows * parts * 128 * 5 + (1 << 16)
 
 
 def verify(target=1 << 20, draft=0, ps=(400, 100), qs=(400, 100), tokens=1 << 24, parent=0, drafted=0, uniform=1 << 24, tok=4, par=4, us=4,
