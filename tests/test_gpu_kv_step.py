@@ -459,3 +459,51 @@ def test_a_step_of_drafted_trees():
         chain = kv.attend(q[b:b + 1, way], k, v, length[b:b + 1], table=table[b:b + 1])
         assert torch.allclose(chain[0].float(), out[b, way].float(), atol=2.0 ** -6, rtol=2.0 ** -6)
     assert (token >= 0).all()
+
+
+def test_pages_and_accepted_tokens_in_a_graph_and_on_another_stream():
+    """A step's bookkeeping captured and replayed with other tables in the same memory, and on a stream of its own."""
+    page, pages, E, S, B, T = 16, 400, 9, 20, 30, 12
+    pool = torch.randn(pages, page, 2, 64, device=DEV).to(BF16)
+    other = torch.randn(pages, page, 2, 64, device=DEV).to(BF16)
+    sets = []
+    for seed in (1, 2):
+        table, length = tables(S, E, page, pages, seed)
+        rng = random.Random(seed)
+        parent = torch.tensor([rng.randrange(-1, S) for _ in range(B)], dtype=I32)
+        path = torch.tensor([[0] + sorted(rng.sample(range(1, T), 5)) + [-1] * (T - 6) for _ in range(B)], dtype=I32)
+        sets.append([put(x) for x in (table, length, parent, path, torch.randint(0, 7, (B,), generator=torch.Generator().manual_seed(seed)).to(I32))])
+    mine = [x.clone() for x in sets[0]]
+    a, b = pool.clone(), other.clone()
+    ws = torch.empty(kv.pages_workspace_bytes(pages, B, E), dtype=torch.uint8, device=DEV)
+
+    def run(k, v, table, length, parent, path, count, stream=None):
+        t, n, moves, left = kv.fork(table, length, parent, pages, page, room=T, ws=ws, stream=stream)
+        kv.copy_pages(moves, k, v, stream=stream)
+        kv.accept(k, v, n, path, count, table=t, stream=stream)
+        c, moved, used = kv.compact(t, n, pages, page, stream=stream)
+        kv.copy_pages(moved, k, v, stream=stream)
+        return t, n, moves, left, c, moved, used
+
+    want = []
+    for s in sets:
+        k, v = pool.clone(), other.clone()
+        want.append([x.clone() for x in (*run(k, v, *s), k, v)])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    k, v = pool.clone(), other.clone()
+    torch.cuda.synchronize()
+    got = run(k, v, *sets[0], stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip((*got, k, v), want[0]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(a, b, *mine)
+    for i in (0, 1, 0, 1):
+        for x, y in zip(mine, sets[i]):
+            x.copy_(y)
+        a.copy_(pool), b.copy_(other)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip((*got, a, b), want[i]))
