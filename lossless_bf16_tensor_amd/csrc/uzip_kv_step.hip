@@ -64,8 +64,8 @@ template <int PT>
 __device__ void walk(const VerifyParams &p, int b, int nd, Walked &w, int32_t *list, bool tell)
 {
     const int lane = (int)(threadIdx.x & 63);
-    bool whole = w.pending == 0;                  // mass is what it says
-    if (w.pending) whole = true, w.pending = 0;
+    bool whole = true;                            // mass is what it says
+    w.pending = 0;
     for (int base = w.next & ~63; base < nd; base += 64) {
         const int node = base + lane;
         const bool in = node >= 1 && node < nd;
