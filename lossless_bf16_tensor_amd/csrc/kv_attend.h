@@ -544,6 +544,20 @@ __device__ inline uint32_t tree_bits(const AttendParams &p, int b, int tok, int 
     return bits;
 }
 
+// Scores that can be read. A product's result is there after eight wait states,
+// which the hardware does not keep by itself; the compiler counts them, but
+// where a branch between the products and the first use leaves instructions out
+// it has counted those of the longer way (head dim 64: seven along the other).
+// Behind such a branch they are waited for here; its own ones, a few of the
+// thousands of cycles that a tile's memory takes, are then not needed.
+template <int N>
+__device__ inline void settle(f32x4 (&s)[N][2])
+{
+    static_assert(N <= 2, "every result is named");
+    if constexpr (N == 1) asm("s_nop 7" : "+v"(s[0][0]), "+v"(s[0][1]));
+    else asm("s_nop 7" : "+v"(s[0][0]), "+v"(s[0][1]), "+v"(s[1][0]), "+v"(s[1][1]));
+}
+
 // 8 dims (32 ks + 8 g ..) of key x in each half
 template <int CT, int KS, bool PAD, bool MASKED>
 __device__ inline void load_keys(const AttendParams &p, const Tile &t, int end, int x, int g, uint32_t off, Raw<CT> (&r)[2][KS])
@@ -790,6 +804,7 @@ struct Rows {
         score(k, s);
         scaled(t.ks, s);
         values(v);
+        if constexpr (!is_scaled(CT)) settle(s);          // the scaled ones have been read above
         if (!t.fast) hide(p, t, at, s);
         raise(p.c2, s);
         weigh(p.c2, s, t.vs, pw);
@@ -1042,10 +1057,8 @@ __global__ __launch_bounds__(kWaves * 64, DP == 256 ? 1 : 2) void k_attend(Atten
                     for (int hf = 0; hf < 2; hf++)
 #pragma unroll
                         for (int ks = 0; ks < KS; ks++) k[hf][ks] = widen<CT>(kr[hf][ks]);
-                    // No branch between the products and the first use of the
-                    // scores: beside a short one the compiler counted a product's
-                    // wait states along the longer way only, and scores were read
-                    // too early.
+                    // before the products: no branch between them and the first
+                    // use of the scores, and no wait of settle()
                     if (nxt.fast) load_keys<CT, KS, PAD, false>(p, nxt, w.lim, w.x, w.g, koff, kr);
                     f32x4 s[RB][2];
                     u32x4 pw[W::TERMS][RB];
@@ -1073,6 +1086,7 @@ __global__ __launch_bounds__(kWaves * 64, DP == 256 ? 1 : 2) void k_attend(Atten
                     u32x4 pw[W::TERMS][RB];
                     w.score(k, s);
                     if (nxt.fast) load_keys<CT, KS, PAD, false>(p, nxt, w.lim, w.x, w.g, koff, kr);
+                    settle(s);
                     w.raise(p.c2, s);
                     w.weigh(p.c2, s, t.vs, pw);
                     w.add(v, pw);
@@ -1802,7 +1816,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attend_weigh(AttendParams p)
             f32x4 sum[2] = {};
             for (int j = 0; j < blocks; j++) {
                 const float row = lrow[j * 16 + x];
-                f32x4 s[2];
+                f32x4 sc[1][2], (&s)[2] = sc[0];
 #pragma unroll
                 for (int ks = 0; ks < KS; ks++) {
                     const u32x4 q = lq[(j * KS + ks) * 64 + lane];
@@ -1817,6 +1831,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void k_attend_weigh(AttendParams p)
                     bits |= leading_bits((p.tree ? n : min(end, n + tok + 1)) - t.key - 4 * g);
                     seen &= bits & there_bits(t);
                 }
+                if constexpr (!is_scaled(CT)) settle(sc);
 #pragma unroll
                 for (int i8 = 0; i8 < 8; i8++) {
                     const float w = __builtin_amdgcn_exp2f(fmaf(s[i8 >> 2][i8 & 3], p.c2, -row));
