@@ -238,8 +238,7 @@ int uzip_kv_append_scaled(const uzip_kv_cache_t *cache, const uzip_kv_scales_t *
 
 /* async. uzip_kv_attend over a cache of E4M3 or I8, with queries of BF16 or
  * F16. Weights times the values' scales are multiplied with the values in two
- * terms of BF16; in one, for BF16 queries, where more than 64 rows share keys
- * over much work. */
+ * terms of BF16, whatever the shapes. */
 int uzip_kv_attend_scaled(const uzip_kv_cache_t *cache, const uzip_kv_scales_t *scales, const uzip_kv_attend_args_t *a,
                           void *d_ws, uint64_t ws_bytes, hipStream_t s);
 

@@ -1,0 +1,43 @@
+"""kv.append and kv.attend over caches with scales: weights' precision, ranges
+and the ways of cutting work that other tests do not reach."""
+import pytest
+import torch
+
+import kv_reference as ref
+from kv_step_reference import E4M3, I8
+from lossless_bf16_tensor_amd import kv
+from test_gpu_kv_scaled import BF16, DEV, F16, make, step_rows
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("q", [BF16, F16])
+@pytest.mark.parametrize("cache", [I8, E4M3])
+@pytest.mark.parametrize("B,T,hq,H,D,S", [(1, 4, 8, 2, 128, 300), (5, 70, 32, 8, 128, 2400), (5, 70, 32, 8, 64, 2400)])
+def test_weights_are_finer_than_the_output(q, cache, B, T, hq, H, D, S):
+    """All weights are one number, an equal share times a scale just above the
+    middle between two BF16 values, so a weight in one term of BF16 would be off by 2^-8 for all
+    keys alike: 1.625 (1 + 2^-7) instead of 1.625 (1 + 2^-8), which BF16 rounds
+    on to 1.6406, 9.2e-3 from 1.6314, where half its step is 3.9e-3."""
+    vs = torch.full((B, -(-S // 16), H), 1 + 2.0 ** -8 + 2.0 ** -14, device=DEV)
+    k, v = torch.zeros(B, S, H, D, device=DEV).to(cache), torch.full((B, S, H, D), 13.0 if cache == I8 else 1.625, device=DEV).to(cache)
+    vs /= 8.0 if cache == I8 else 1.0
+    n = torch.tensor([S - T - 17 * b for b in range(B)], dtype=torch.int32, device=DEV)
+    out = kv.attend(torch.zeros(B, T, hq, D, dtype=q, device=DEV), k, v, n, k_scale=torch.ones_like(vs), v_scale=vs)
+    want = 1.625 * (1 + 2.0 ** -8 + 2.0 ** -14)
+    # a rounding of the output, 2^-16 of two terms, and a rounding of a binary32 sum for each key
+    assert ((out.double() - want).abs() <= want * (ref.HALF[q] * (1 + 2.0 ** -7) + 2.0 ** -16 + S * 2.0 ** -24)).all()
+
+
+@pytest.mark.parametrize("B,T,hq,H,D,S,cache,layout", [(5, 24, 96, 32, 128, 1760, I8, "shd"), (5, 70, 32, 8, 64, 2400, E4M3, "paged32")])
+def test_many_rows_are_as_precise_as_few(B, T, hq, H, D, S, cache, layout):
+    q, k, v, ks, vs, table = make(B, T, hq, H, D, S, BF16, cache, 16, layout, seed=B + T, dev=DEV)
+    G = hq // H
+    length, drafted = torch.tensor([S - T - 31 * b for b in range(B)], dtype=torch.int32), torch.full((B,), T, dtype=torch.int32)
+    out = kv.attend(q, k, v, length.to(DEV), table=table, k_scale=ks, v_scale=vs)
+    for b in (0, B - 1):
+        args = [t[:, :, :1].cpu() for t in (k, v, ks, vs)] if table is not None else [t[b:b + 1, :, :1].cpu() for t in (k, v, ks, vs)]
+        want = step_rows(q[b:b + 1, :, :G].cpu(), args, 16, length[b:b + 1], None if table is None else table[b:b + 1].cpu(), None, drafted[b:b + 1],
+                         [0, T // 2, T - 1], False)
+        for i, (o, ob, _, _) in want.items():
+            ref.within(out[b, i, :G], o, ob, f"out {b} {i}")
