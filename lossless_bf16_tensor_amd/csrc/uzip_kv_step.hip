@@ -105,7 +105,10 @@ __device__ void walk(const VerifyParams &p, int b, int nd, Walked &w, int32_t *l
             } else if (!again) {
                 w.mass -= pk;
                 if (lane == 0) list[w.rejected] = xk;
+                // read by the wave's other lanes from here on
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
                 __builtin_amdgcn_wave_barrier();
+                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
                 w.rejected++;
             }
         }
