@@ -458,13 +458,14 @@ __global__ __launch_bounds__(kAcceptThreads) void k_accept(AcceptParams p)
 
 // ------------------------------------------------------------------ pages --
 // What holds a page is read off the table itself, so there are no counts that
-// could go wrong: a word a page, the least of the marks that its holders make.
+// could go wrong: a word a page, which its holders mark, and for a fork another,
+// the least of the sequences that have it as their partly filled last one.
 // Marks, the plan and the table are launches of their own, since each needs all
-// of the one before: 256 sequences of up to 512 pages of 11000 in 2 + 5 + 6 + 4
+// of the one before: 256 sequences of up to 512 pages of 11000 in 2 + 4 + 7 + 4
 // us. The plan is one workgroup's, which looks at 8192 pages at a time.
 constexpr uint32_t kFree = 0xffffffffu;
-constexpr uint32_t kHeld = 0;                     // fork: full, or held outside; compact: held outside
-// fork: 1 + the first sequence that fills it on; compact: 1 of the table; then 2 + where it goes
+constexpr uint32_t kHeld = 0;                     // fork: whole, or held outside; compact: held outside
+// compact: 1 of the table; then 2 + where it goes
 constexpr int kPageThreads = 256, kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
 
 struct PageParams {
@@ -473,6 +474,7 @@ struct PageParams {
     int64_t t0;
     int32_t *out_table, *out_length, *moves, *left;
     uint32_t *mark;                               // [pages]
+    uint32_t *first;                              // fork: [pages], 1 + the first sequence that fills it on
     int32_t *given;                               // pages handed out, in order
     int32_t *offset;                              // [seqs]: of a sequence's first one
     int rows, seqs, entries, pages, shift, room;  // rows: of table
@@ -501,7 +503,9 @@ struct Branch {
 __global__ __launch_bounds__(kPageThreads) void k_pages_clear(PageParams p)
 {
     const int i = (int)(blockIdx.x * kPageThreads + threadIdx.x);
-    if (i < p.pages) p.mark[i] = p.held && p.held[i] ? kHeld : kFree;
+    if (i >= p.pages) return;
+    p.mark[i] = p.held && p.held[i] ? kHeld : kFree;
+    if (p.first) p.first[i] = kFree;
 }
 
 __global__ __launch_bounds__(kPageThreads) void k_pages_mark(PageParams p, int parts)
@@ -511,13 +515,15 @@ __global__ __launch_bounds__(kPageThreads) void k_pages_mark(PageParams p, int p
     if (s.row < 0 || e >= s.full + s.part) return;
     const uint32_t x = s.page(p, e);
     if (x >= (uint32_t)p.pages) return;
-    // Stores of one value need no atomics, and whatever they meet there, the
-    // least mark is what a page ends with: 256 sequences of 270 pages 12 us with
-    // atomics for all, 4.5 so.
-    const uint32_t as = p.compact ? 1u : e < s.full ? kHeld : 1u + (uint32_t)b;
-    if (p.mark[x] <= as) return;
-    if (p.compact || e < s.full) p.mark[x] = as;
-    else atomicMin(p.mark + x, as);
+    // Stores of one value need no atomics; the words that a minimum is taken of
+    // are others, since dies would not see each other's stores before it. (256
+    // sequences of 270 pages 3.5 us; 12 with atomics for all or with atomic stores.)
+    if (p.compact || e < s.full) {
+        const uint32_t as = p.compact ? 1u : kHeld;
+        if (p.mark[x] > as) p.mark[x] = as;
+    } else {
+        atomicMin(p.first + x, 1u + (uint32_t)b);
+    }
 }
 
 // inclusive sum over the workgroup's threads, and of all; wsum: one word a wave
@@ -545,20 +551,30 @@ __device__ inline bool copied(const PageParams &p, const Branch &s, int b)
 {
     if (!s.part) return false;
     const uint32_t x = s.page(p, s.full);
-    return x < (uint32_t)p.pages && p.mark[x] != 1u + (uint32_t)b;
+    return x < (uint32_t)p.pages && (p.mark[x] == kHeld || p.first[x] != 1u + (uint32_t)b);
 }
 
 constexpr int kPlanPages = 8;                     // pages a thread looks at, at a time
 
+// a fork's are kHeld, kFree or a first sequence
+template <bool FORK>
 __device__ inline void load_marks(const PageParams &p, int first, uint32_t (&m)[kPlanPages])
 {
     if (first + kPlanPages <= p.pages) {
         const u32x4 a = *reinterpret_cast<const u32x4 *>(p.mark + first), c = *reinterpret_cast<const u32x4 *>(p.mark + first + 4);
 #pragma unroll
         for (int i = 0; i < 4; i++) m[i] = a[i], m[4 + i] = c[i];
+        if constexpr (FORK) {
+            const u32x4 d = *reinterpret_cast<const u32x4 *>(p.first + first), e = *reinterpret_cast<const u32x4 *>(p.first + first + 4);
+#pragma unroll
+            for (int i = 0; i < 4; i++) m[i] = min(m[i], d[i]), m[4 + i] = min(m[4 + i], e[i]);
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < kPlanPages; i++) m[i] = first + i < p.pages ? p.mark[first + i] : kHeld;
+        for (int i = 0; i < kPlanPages; i++) {
+            m[i] = first + i < p.pages ? p.mark[first + i] : kHeld;
+            if (FORK && first + i < p.pages) m[i] = min(m[i], p.first[first + i]);
+        }
     }
 }
 
@@ -582,7 +598,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_fork_plan(PageParams p)
     for (int base = 0; base < p.pages; base += kPlanThreads * kPlanPages) {
         const int first = base + tid * kPlanPages;
         uint32_t m[kPlanPages];
-        load_marks(p, first, m);
+        load_marks<true>(p, first, m);
         int mine = 0;
 #pragma unroll
         for (int i = 0; i < kPlanPages; i++) mine += m[i] == kFree;
@@ -630,7 +646,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_compact_plan(PageParams p)
     int used = 0, all;
     for (int base = 0; base < p.pages; base += kPlanThreads * kPlanPages) {
         uint32_t m[kPlanPages];
-        load_marks(p, base + tid * kPlanPages, m);
+        load_marks<false>(p, base + tid * kPlanPages, m);
         int mine = 0;
 #pragma unroll
         for (int i = 0; i < kPlanPages; i++) mine += base + tid * kPlanPages + i < p.pages && m[i] != kFree;
@@ -641,7 +657,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_compact_plan(PageParams p)
     for (int base = 0; base < used; base += kPlanThreads * kPlanPages) {
         const int first = base + tid * kPlanPages;
         uint32_t m[kPlanPages];
-        load_marks(p, first, m);
+        load_marks<false>(p, first, m);
         int mine = 0;
 #pragma unroll
         for (int i = 0; i < kPlanPages; i++) mine += first + i < used && m[i] == kFree;
@@ -656,7 +672,7 @@ __global__ __launch_bounds__(kPlanThreads) void k_compact_plan(PageParams p)
     for (int base = used / (kPlanThreads * kPlanPages) * (kPlanThreads * kPlanPages); base < p.pages; base += kPlanThreads * kPlanPages) {
         const int first = base + tid * kPlanPages;
         uint32_t m[kPlanPages];
-        load_marks(p, first, m);
+        load_marks<false>(p, first, m);
         int mine = 0;
 #pragma unroll
         for (int i = 0; i < kPlanPages; i++) mine += first + i >= used && m[i] == 1u;
@@ -734,14 +750,15 @@ __global__ __launch_bounds__(kPageThreads) void k_copy_pages(CopyParams p)
 }
 
 struct PagesWs {
-    uint64_t off_given, off_offset, bytes;
+    uint64_t off_first, off_given, off_offset, bytes;
 };
 
 PagesWs pages_ws(uint64_t pages, uint64_t seqs, uint64_t entries)
 {
     const auto up = [](uint64_t v) { return (v + 255) & ~255ull; };
     PagesWs w;
-    w.off_given = up(pages * 4);
+    w.off_first = up(pages * 4);
+    w.off_given = w.off_first + up(pages * 4);
     const uint64_t given = seqs * entries > pages ? seqs * entries : pages;
     w.off_offset = w.off_given + up(given * 4);
     w.bytes = w.off_offset + up(seqs * 4);
@@ -771,6 +788,7 @@ int plan_pages(const uzip_kv_pages_t *a, bool compact, void *d_ws, uint64_t ws_b
     p.out_table = a->out_table, p.out_length = a->out_length, p.moves = a->moves, p.left = a->left;
     char *w = static_cast<char *>(d_ws);
     p.mark = reinterpret_cast<uint32_t *>(w);
+    p.first = compact ? nullptr : reinterpret_cast<uint32_t *>(w + ws.off_first);
     p.given = reinterpret_cast<int32_t *>(w + ws.off_given);
     p.offset = reinterpret_cast<int32_t *>(w + ws.off_offset);
     p.rows = (int)a->rows, p.seqs = (int)a->seqs, p.entries = (int)a->entries, p.pages = (int)a->pages;

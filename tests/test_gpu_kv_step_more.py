@@ -2,7 +2,7 @@
 import pytest
 import torch
 
-from test_gpu_kv_step import I32, check
+from test_gpu_kv_step import I32, check, check_fork
 
 pytestmark = pytest.mark.gpu
 
@@ -21,3 +21,19 @@ def test_a_token_again_right_behind_its_rejection(dtype):
         tokens[b, 1:] = torch.randperm(V, generator=g)[:pairs].repeat_interleave(2).int()
     found = check(dict(tokens=tokens, target=p, uniform=u, draft=None, parent=torch.tensor([-1] + [0] * (2 * pairs), dtype=I32)))
     assert {n for _, n, _ in found} == {1}
+
+
+def test_pages_that_are_whole_for_some_and_partly_filled_for_others():
+    """The same pages marked from all over the chip, as whole ones and as last
+    ones: whole for any sequence, they are nobody's to fill on."""
+    S, E, page, pages = 900, 40, 16, 3000
+    g = torch.Generator().manual_seed(6)
+    prefix = torch.randperm(pages, generator=g)[:E].to(I32)
+    table = prefix.expand(S, E).contiguous()
+    length = torch.randint(1, E * page, (S,), generator=g).to(I32)
+    length[S // 2:] = (length[S // 2:] // page * page).clamp(min=page) - 3          # last pages partly filled, up to all of them
+    table[::7, -1] = torch.randperm(pages, generator=g)[:len(table[::7])].to(I32)
+    parent = torch.randint(0, S, (1500,), generator=g).to(I32)
+    for held in (None, torch.rand(pages, generator=g) < 0.05):
+        t, n, moves, left = check_fork(table, length, parent, pages, page, 20, held)
+        assert int((moves[:, 0] >= 0).sum()) > 1000
