@@ -772,9 +772,12 @@ struct Rows {
             }
     }
 
-    // Scores of keys that a row does not see become -inf.
-    __device__ inline void hide(const AttendParams &p, const Tile &t, const Place &at, f32x4 (&s)[RB][2])
+    // Scores of keys that a row does not see become -inf, and the values' scale
+    // of a half tile that no row sees 0: it may be anything, and a weight of
+    // zero times it NaN.
+    __device__ inline void hide(const AttendParams &p, const Tile &t, const Place &at, f32x4 (&s)[RB][2], float (&vs)[2])
     {
+        uint32_t any = 0;
         const int n = at.n, nd = at.nd;
         uint32_t seen[RB];
 #pragma unroll
@@ -787,9 +790,13 @@ struct Rows {
         for (int rb = 0; rb < RB; rb++) {
             seen[rb] |= leading_bits((p.tree ? n : min(lim, n + tok[rb] + 1)) - t.key - 4 * g);
             seen[rb] &= there_bits(t);
+            any |= seen[rb];
 #pragma unroll
             for (int i = 0; i < 8; i++) s[rb][i >> 2][i & 3] = seen[rb] >> i & 1 ? s[rb][i >> 2][i & 3] : -INFINITY;
         }
+        if constexpr (is_scaled(CT))
+#pragma unroll
+            for (int x = 0; x < 2; x++) vs[x] = __builtin_amdgcn_ballot_w64((any >> 4 * x & 15) != 0) != 0 ? vs[x] : 0.f;
     }
 
     // One tile. values() is called for the values when the scores are done.
@@ -805,9 +812,11 @@ struct Rows {
         scaled(t.ks, s);
         values(v);
         if constexpr (!is_scaled(CT)) settle(s);          // the scaled ones have been read above
-        if (!t.fast) hide(p, t, at, s);
+        float vs[2] = {1.f, 1.f};
+        if constexpr (is_scaled(CT)) vs[0] = t.vs[0], vs[1] = t.vs[1];
+        if (!t.fast) hide(p, t, at, s, vs);
         raise(p.c2, s);
-        weigh(p.c2, s, t.vs, pw);
+        weigh(p.c2, s, vs, pw);
         if (!is_i8(CT) && t.key + kTileKeys > n) {
             // A value that is not finite must reach only the rows that see its
             // key, and in a product it would reach all (0 * inf): poison() adds it.
@@ -1606,7 +1615,7 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_wide(AttendParams p)
                 scales_of(i, tile, t.vs);
                 w.score(k, s);
                 w.scaled(t.ks, s);
-                w.hide(p, t, at, s);
+                w.hide(p, t, at, s, t.vs);
                 w.raise(p.c2, s);
                 w.weigh(p.c2, s, t.vs, pw);
                 ready(i, tile);

@@ -1,12 +1,14 @@
 """kv.append and kv.attend over caches with scales: weights' precision, ranges
 and the ways of cutting work that other tests do not reach."""
+import math
+
 import pytest
 import torch
 
 import kv_reference as ref
 from kv_step_reference import E4M3, I8
 from lossless_bf16_tensor_amd import kv
-from test_gpu_kv_scaled import BF16, DEV, F16, make, step_rows
+from test_gpu_kv_scaled import BF16, DEV, F16, check, make, step_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +43,40 @@ def test_many_rows_are_as_precise_as_few(B, T, hq, H, D, S, cache, layout):
                          [0, T // 2, T - 1], False)
         for i, (o, ob, _, _) in want.items():
             ref.within(out[b, i, :G], o, ob, f"out {b} {i}")
+
+
+@pytest.mark.parametrize("cache", [I8, E4M3])
+@pytest.mark.parametrize("q", [BF16, F16])
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_scales_of_blocks_that_no_query_sees(cache, q, bad):
+    """Drafted tokens that the tree names for nobody have no effect, whatever their
+    elements and scales hold, in a cache and in pages, in few rows and in many."""
+    for B, T, hq, H, D, n, layout in ((1, 40, 4, 2, 64, 48, "shd"), (2, 40, 16, 2, 128, 64, "paged16")):
+        qq, k, v, ks, vs, table = make(B, T, hq, H, D, n + T, q, cache, 16, layout, seed=T)
+        tree = torch.ones(T, T, dtype=torch.bool).tril()
+        tree[:, 16:32] = False
+        for b in range(B):
+            at = (b, n // 16 + 1) if table is None else (int(table[b, n // 16 + 1]), 0)
+            ks[at], vs[at] = bad, bad
+        check(qq, k, v, ks, vs, table, [n] * B, tree=tree)
+
+
+@pytest.mark.parametrize("layout", ["shd", "paged32"])
+def test_scales_of_blocks_that_none_of_many_rows_sees(layout):
+    B, T, hq, H, D, S = 5, 70, 32, 8, 128, 2400
+    q, k, v, ks, vs, table = make(B, T, hq, H, D, S, F16, E4M3, 32, layout, seed=9, dev=DEV)
+    G, n = hq // H, 2304                                             # of whole blocks and pages
+    tree = torch.ones(T, T, dtype=torch.bool).tril()
+    tree[:, 32:64] = False
+    for b in range(B):
+        at = (b, n // 32 + 1) if table is None else (int(table[b, n // 32 + 1]), 0)
+        ks[at], vs[at] = math.nan, math.inf
+    length, drafted = torch.full((B,), n, dtype=torch.int32), torch.full((B,), T, dtype=torch.int32)
+    lse = torch.empty(B, T, hq, device=DEV)
+    out = kv.attend(q, k, v, length.to(DEV), table=table, tree=tree.to(DEV), lse=lse, k_scale=ks, v_scale=vs)
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    args = [t[:, :, :1].cpu() for t in (k, v, ks, vs)] if table is not None else [t[:1, :, :1].cpu() for t in (k, v, ks, vs)]
+    want = step_rows(q[:1, :, :G].cpu(), args, 32, length[:1], None if table is None else table[:1].cpu(), tree[None], drafted[:1], [0, 31, 40, T - 1], False)
+    for i, (o, ob, l, lb) in want.items():
+        ref.within(out[0, i, :G], o, ob, f"out {i}")
+        ref.within(lse[0, i, :G], l, lb, f"lse {i}")
