@@ -214,7 +214,8 @@ uint64_t uzip_kv_evict_workspace_bytes(uint32_t seqs, uint32_t kv_heads, uint32_
  * head h: k[b * k_stride[0] + t / block * k_stride[1] + h * k_stride[2]]; in
  * pages, of row r of page p: k[p * k_stride[0] + r / block * k_stride[1] + ...].
  * Strides are any that are not negative and lead to no element 2^30; 4-byte
- * aligned. Scales of blocks that are seen are positive, in [2^-100, 2^100]. */
+ * aligned. Scales of blocks that are seen are positive, in [2^-80, 2^80]: sums of
+ * 2^30 weights, each up to 2^8, times values then fit binary32. */
 typedef struct uzip_kv_scales {
     float   *k;
     float   *v;
@@ -232,7 +233,8 @@ typedef struct uzip_kv_scales {
  * tokens of the block are rounded to it, each element times old scale / new
  * scale. An element is x / scale rounded to nearest even in binary32; beyond
  * MAX it is MAX with its sign, and NaN is NaN in E4M3, 0 in I8. Of a block that
- * receives nothing nothing is written. */
+ * receives nothing nothing is written. A magnitude above 2^80 MAX gets the scale
+ * that holds it, beyond the range above: attention over it may be infinite. */
 int uzip_kv_append_scaled(const uzip_kv_cache_t *cache, const uzip_kv_scales_t *scales, const uzip_kv_append_args_t *a,
                           const uzip_kv_rope_t *rope, hipStream_t s);
 

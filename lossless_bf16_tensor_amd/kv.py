@@ -19,7 +19,9 @@ v_scale) are float8_e4m3fn or int8. A block of tokens of a head, a power of two
 from 16 to 65536, shares a scale for its keys and one for its values: float32
 [sequences, blocks, kv heads], or [pages, blocks of a page, kv heads], any
 strides; the number of blocks says how long they are. Scales of blocks that are
-seen are positive, from 2^-100 to 2^100.
+seen are positive, from 2^-80 to 2^80; :func:`append` makes larger ones for
+magnitudes above 2^80 times an element's largest, over which attention may be
+infinite.
 
 Steps with drafted tokens go on with :func:`verify`, :func:`accept` and, where
 caches are in pages, :func:`fork`, :func:`compact` and :func:`copy_pages`.

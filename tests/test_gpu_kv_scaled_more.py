@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import kv_reference as ref
-from kv_step_reference import E4M3, I8
+from kv_step_reference import E4M3, I8, MOST
 from lossless_bf16_tensor_amd import kv
 from test_gpu_kv_scaled import BF16, DEV, F16, check, make, step_rows
 
@@ -80,3 +80,31 @@ def test_scales_of_blocks_that_none_of_many_rows_sees(layout):
     for i, (o, ob, l, lb) in want.items():
         ref.within(out[0, i, :G], o, ob, f"out {i}")
         ref.within(lse[0, i, :G], l, lb, f"lse {i}")
+
+
+@pytest.mark.parametrize("cache", [I8, E4M3])
+@pytest.mark.parametrize("power", [80, -80])
+@pytest.mark.parametrize("B,T,hq,H,D,S", [(1, 1, 1, 1, 8, 1 << 22), (1, 4, 8, 2, 64, 1 << 18), (5, 70, 32, 8, 128, 2400)])
+def test_scales_at_the_ends_of_their_range(cache, power, B, T, hq, H, D, S):
+    """The largest values. First under weights that grow by just less than what has
+    the maximum raised, so that sums are of weights of 2^7.9; then all but one
+    under weights of 2^-20."""
+    k, v = torch.zeros(B, S, H, D, device=DEV).to(cache), torch.full((B, S, H, D), MOST[cache], device=DEV).to(cache)
+    ks, vs = torch.ones(B, -(-S // 16), H, device=DEV), torch.full((B, -(-S // 16), H), 2.0 ** power, device=DEV)
+    q = torch.zeros(B, T, hq, D, dtype=BF16, device=DEV)
+    q[..., 0] = 1.0
+    n = torch.full((B,), S - T, dtype=torch.int32, device=DEV)
+    k.view(torch.uint8)[:, S // 32:, :, 0] = torch.full((1,), 64.0, device=DEV).to(cache).view(torch.uint8)
+    ks.fill_(7.9 * math.log(2) * math.sqrt(D) / 64)
+    want = MOST[cache] * 2.0 ** power
+    out = kv.attend(q, k, v, n, k_scale=ks, v_scale=vs).double()
+    # the output's rounding; sums of each wave, and of the waves, of 2^12 roundings at most
+    assert ((out / want - 1).abs() <= 2.0 ** -8 * (1 + 2.0 ** -7) + 2.0 ** -11).all()
+    k.view(torch.uint8).zero_()
+    k.view(torch.uint8)[:, 5, :, 0] = torch.full((1,), 64.0, device=DEV).to(cache).view(torch.uint8)
+    v.view(torch.uint8)[:, 5] = 0
+    ks.fill_(20 * math.log(2) * math.sqrt(D) / 64)
+    out = kv.attend(q, k, v, n, k_scale=ks, v_scale=vs).double()
+    for i in range(T):
+        others = (S - T + i) * 2.0 ** -20
+        assert ((out[:, i] / (want * others / (1 + others)) - 1).abs() <= 2.0 ** -8 * (1 + 2.0 ** -7) + 2.0 ** -11).all()
