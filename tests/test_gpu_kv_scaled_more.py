@@ -108,3 +108,24 @@ def test_scales_at_the_ends_of_their_range(cache, power, B, T, hq, H, D, S):
     for i in range(T):
         others = (S - T + i) * 2.0 ** -20
         assert ((out[:, i] / (want * others / (1 + others)) - 1).abs() <= 2.0 ** -8 * (1 + 2.0 ** -7) + 2.0 ** -11).all()
+
+
+@pytest.mark.parametrize("cache", [I8, E4M3])
+def test_scales_of_the_farthest_strides(cache):
+    """Scales whose last one is element 2^30 - 1 of their memory: the same output and cache as with scales side by side."""
+    H, D, page, block = 2, 64, 32, 16
+    first = (2 ** 30 - 1 - 64 - 7) // 2
+    assert 2 * first + 64 + 7 == 2 ** 30 - 1
+    q, k, v, ks, vs, _ = make(1, 3, 4, H, D, 70, BF16, cache, block, "paged32", seed=3, dev=DEV)
+    k, v, ks, vs = k[:3].clone(), v[:3].clone(), ks[:3].contiguous(), vs[:3].contiguous()
+    table, n = torch.tensor([[2, 0, 1]], dtype=torch.int32, device=DEV), torch.tensor([70], dtype=torch.int32, device=DEV)
+    far = [torch.zeros(2 ** 30, device=DEV).as_strided((3, 2, H), (first, 64, 7)) for _ in "kv"]
+    for a, b in zip(far, (ks, vs)):
+        a.copy_(b)
+    new = (torch.randn(1, 3, H, D, device=DEV) * 40).to(BF16)
+    got = []
+    for s in ((ks, vs), far):
+        kk, vv = k.clone(), v.clone()
+        kv.append(None, new, new, kk, vv, n, table=table, k_scale=s[0], v_scale=s[1])
+        got.append([x.contiguous().view(torch.uint8) for x in (kv.attend(q, kk, vv, n, table=table, k_scale=s[0], v_scale=s[1]), kk, vv, *s)])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
