@@ -1959,6 +1959,13 @@ bool valid_shapes(uint32_t seqs, uint32_t kv_heads, uint32_t dim, uint32_t cache
            heads >= kv_heads && heads <= 65535 && heads % kv_heads == 0 && (uint64_t)seqs * T * heads < (1ull << 30);
 }
 
+// workgroups of k_attend_weigh
+uint64_t weigh_grid(uint32_t cache_tokens, uint64_t seqs, uint64_t heads, uint64_t weigh_tiles)
+{
+    const uint64_t each = kWaves * weigh_tiles, tiles = ((uint64_t)cache_tokens + kTileKeys - 1) / kTileKeys;
+    return (tiles + each - 1) / each * seqs * heads;
+}
+
 template <int CT, int DP, int RB, bool PAD>
 int launch(const AttendParams &p, uint64_t grid, bool walks, hipStream_t s)
 {
@@ -1999,8 +2006,7 @@ int run(const AttendParams &p, const Plan &plan, int half, hipStream_t s)
         UZIP_KV_LAUNCH_CHECK("k_attend_join");
     }
     if (p.score) {
-        const uint64_t each = (uint64_t)kWaves * p.weigh_tiles, tiles = ((uint64_t)p.c.tokens + kTileKeys - 1) / kTileKeys;
-        k_attend_weigh<CT, DP, PAD><<<(unsigned)((tiles + each - 1) / each * p.seqs * p.heads), kWaves * 64, 0, s>>>(p);
+        k_attend_weigh<CT, DP, PAD><<<(unsigned)weigh_grid(p.c.tokens, p.seqs, p.heads, p.weigh_tiles), kWaves * 64, 0, s>>>(p);
         UZIP_KV_LAUNCH_CHECK("k_attend_weigh");
     }
     return UZIP_OK;
@@ -2041,8 +2047,11 @@ int attend(const uzip_kv_cache_t *cache, const uzip_kv_scales_t *scales, const u
     int64_t bits = cache->dim * elem_size((int)cache->dtype);
     for (int i = 0; i < 3; i++) bits |= (cache->k_stride[i] | cache->v_stride[i]) * elem_size((int)cache->dtype);
     const Plan plan = make_plan(cache->seqs, cache->heads, cache->dim, cache->tokens, a->tokens, a->heads, (bits & 15) == 0, SCALED);
-    if (plan.grid >= (1ull << 31) || (uint64_t)cache->seqs * ((cache->tokens + 31) / 32) >= (1ull << 31) ||
-        (uint64_t)cache->seqs * cache->heads * ((cache->tokens + 127) / 128) >= (1ull << 31)) return UZIP_EINVAL;
+    if (plan.grid * (plan.shared ? kShared : kWaves) * 64 >= kLaunchThreads || (uint64_t)cache->seqs * ((cache->tokens + 31) / 32) >= (1ull << 31)) return UZIP_EINVAL;
+    // accumulated weights: enough workgroups to fill the chip four times, rows read once for up to eight tiles of a wave
+    const uint64_t waves = (uint64_t)cache->seqs * cache->heads * ((cache->tokens + kTileKeys - 1) / kTileKeys);
+    const uint64_t share = waves / (4 * kCUs * kWaves), weigh_tiles = share < 1 ? 1 : share > 8 ? 8 : share;
+    if (a->score && weigh_grid(cache->tokens, cache->seqs, cache->heads, weigh_tiles) * kWaves * 64 >= kLaunchThreads) return UZIP_EINVAL;
 
     AttendParams p;
     memset(&p, 0, sizeof p);
@@ -2075,10 +2084,7 @@ int attend(const uzip_kv_cache_t *cache, const uzip_kv_scales_t *scales, const u
     p.seqs = (int)cache->seqs;
     p.used = reinterpret_cast<int *>(ws + plan.off_used);
     p.flat = plan.flat;
-    // enough workgroups to fill the chip four times, rows read once for up to eight tiles of a wave
-    const uint64_t waves = (uint64_t)cache->seqs * cache->heads * ((cache->tokens + kTileKeys - 1) / kTileKeys);
-    const uint64_t share = waves / (4 * kCUs * kWaves);
-    p.weigh_tiles = (int)(share < 1 ? 1 : share > 8 ? 8 : share);
+    p.weigh_tiles = (int)weigh_tiles;
     p.wk = plan.wk;
     p.unit = plan.unit;
     p.c2 = a->scale * 1.4426950408889634f;

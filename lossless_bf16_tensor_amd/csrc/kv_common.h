@@ -24,6 +24,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kBF16 = (int)UZIP_KV_BF16, kF16 = (int)UZIP_KV_F16, kE5M2 = (int)UZIP_KV_E5M2;
 constexpr uint32_t kCUs = 256;                   // of the one GPU this library is for
+constexpr uint64_t kLaunchThreads = 1ull << 32;  // a launch has fewer
 constexpr int64_t kMaxTokenStride = 1ll << 26;   // elements: 16 rows' offsets fit 32 bits
 
 constexpr uint32_t elem_size(int dtype) { return dtype >= kE5M2 ? 1u : 2u; }

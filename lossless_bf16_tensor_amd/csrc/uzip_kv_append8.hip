@@ -466,7 +466,7 @@ extern "C" int uzip_kv_append_scaled(const uzip_kv_cache_t *cache, const uzip_kv
     const bool far = in_lds > kAngles;
     p.angles = far ? 0 : (int)in_lds;
     const int64_t kv = places * p.groups;
-    if (kv + q_blocks >= (1ll << 31)) return UZIP_EINVAL;
+    if ((uint64_t)(kv + q_blocks) * kThreads >= kLaunchThreads) return UZIP_EINVAL;
     p.kv_grid = (int)kv;
     if (a->q.data && !p.Hq)
         if (const int rc = turn_in_place(a, cache->seqs, cache->dim, rope, s)) return rc;

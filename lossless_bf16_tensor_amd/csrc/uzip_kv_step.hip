@@ -798,7 +798,6 @@ int plan_pages(const uzip_kv_pages_t *a, bool compact, void *d_ws, uint64_t ws_b
     p.most = (int)(cells < a->pages / 2 ? cells : a->pages / 2);
     const int parts = (p.entries + kPageThreads - 1) / kPageThreads;
     const unsigned grid = (unsigned)(p.seqs * parts);
-    if ((uint64_t)p.seqs * parts >= (1ull << 31)) return UZIP_EINVAL;
     k_pages_clear<<<(unsigned)((p.pages + kPageThreads - 1) / kPageThreads), kPageThreads, 0, s>>>(p);
     k_pages_mark<<<grid, kPageThreads, 0, s>>>(p, parts);
     if (compact) {
@@ -875,7 +874,7 @@ int uzip_kv_accept(const uzip_kv_cache_t *cache, const uzip_kv_accept_args_t *a,
     p.length = a->length, p.path = a->path, p.count = a->count, p.path0 = a->path_stride;
     p.T = (int)a->nodes, p.H = (int)cache->heads, p.per = (int)cache->dim / 8;
     p.parts = (2 * p.H * p.per + kAcceptThreads - 1) / kAcceptThreads;
-    if ((uint64_t)cache->seqs * p.parts >= (1ull << 31)) return UZIP_EINVAL;
+    if ((uint64_t)cache->seqs * p.parts * kAcceptThreads >= kLaunchThreads) return UZIP_EINVAL;
     const unsigned grid = (unsigned)(cache->seqs * p.parts);
     if (elem_size((int)cache->dtype) == 2) k_accept<u32x4><<<grid, kAcceptThreads, 0, s>>>(p);
     else k_accept<u32x2><<<grid, kAcceptThreads, 0, s>>>(p);
@@ -914,7 +913,6 @@ int uzip_kv_copy_pages(const int32_t *moves, uint32_t count, const uzip_kv_pool_
     const uint32_t unit = !(bits & 15) ? 16 : !(bits & 3) ? 4 : 1;
     CopyParams p;
     memset(&p, 0, sizeof p);
-    p.moves = moves;
     p.pages = pages;
     for (uint32_t i = 0; i < n; i++) {
         const uzip_kv_pool_t &q = pools[i];
@@ -927,12 +925,16 @@ int uzip_kv_copy_pages(const int32_t *moves, uint32_t count, const uzip_kv_pool_
         p.parts += o.parts;
     }
     p.pools = (int)n;
-    if ((uint64_t)count * p.parts >= (1ull << 31)) return UZIP_EINVAL;
-    const unsigned grid = (unsigned)(count * p.parts);
-    if (unit == 16) k_copy_pages<u32x4><<<grid, kPageThreads, 0, s>>>(p);
-    else if (unit == 4) k_copy_pages<uint32_t><<<grid, kPageThreads, 0, s>>>(p);
-    else k_copy_pages<uint8_t><<<grid, kPageThreads, 0, s>>>(p);
-    UZIP_KV_LAUNCH_CHECK("k_copy_pages");
+    // as many moves a launch as it can hold: at most 2^20 workgroups each of 8 pools
+    const uint32_t most = (uint32_t)((kLaunchThreads - 1) / kPageThreads / p.parts);
+    for (uint32_t first = 0; first < count; first += most) {
+        const unsigned grid = (count - first < most ? count - first : most) * p.parts;
+        p.moves = moves + 2 * (int64_t)first;
+        if (unit == 16) k_copy_pages<u32x4><<<grid, kPageThreads, 0, s>>>(p);
+        else if (unit == 4) k_copy_pages<uint32_t><<<grid, kPageThreads, 0, s>>>(p);
+        else k_copy_pages<uint8_t><<<grid, kPageThreads, 0, s>>>(p);
+        UZIP_KV_LAUNCH_CHECK("k_copy_pages");
+    }
     return UZIP_OK;
 }
 

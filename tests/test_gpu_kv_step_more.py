@@ -2,7 +2,8 @@
 import pytest
 import torch
 
-from test_gpu_kv_step import I32, check, check_fork
+from lossless_bf16_tensor_amd import kv
+from test_gpu_kv_step import DEV, I32, check, check_fork
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +38,17 @@ def test_pages_that_are_whole_for_some_and_partly_filled_for_others():
     for held in (None, torch.rand(pages, generator=g) < 0.05):
         t, n, moves, left = check_fork(table, length, parent, pages, page, 20, held)
         assert int((moves[:, 0] >= 0).sum()) > 1000
+
+
+def test_more_moves_than_a_launch_holds():
+    """A table of moves that is padded, as compact's is, beyond 2^24 workgroups: its first, middle and last ones are made."""
+    n = (1 << 24) + 3
+    moves = torch.full((n, 2), -1, dtype=I32, device=DEV)
+    real = {0: (1, 10), n // 2: (2, 11), (1 << 24) - 2: (3, 12), (1 << 24) - 1: (4, 13), 1 << 24: (5, 14), n - 1: (6, 15)}
+    pool = torch.arange(20 * 16 * 3, device=DEV).view(20, 16, 3).to(torch.int8)
+    want = pool.clone()
+    for i, (a, b) in real.items():
+        moves[i] = torch.tensor([a, b], dtype=I32)
+        want[b] = pool[a]
+    kv.copy_pages(moves, pool)
+    assert torch.equal(pool, want)

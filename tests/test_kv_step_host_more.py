@@ -1,5 +1,6 @@
 """More CPU tests of the host side of the operators over 8-bit caches and pages.
 Every call below returns before it touches the GPU."""
+from lossless_bf16_tensor_amd import kv
 from test_kv_host import EINVAL, ENOSPC, cache
 from test_kv_step_host import append, attend, scales
 
@@ -13,3 +14,20 @@ def test_scales_lead_to_no_element_2_to_the_30():
         assert attend(c, scales(**{name: near}), ws_bytes=0) == ENOSPC
         assert attend(c, scales(**{name: far}), ws_bytes=0) == EINVAL
         assert append(c, scales(**{name: far})) == EINVAL
+
+
+def test_more_workgroups_than_a_launch_holds():
+    """Refused before anything runs, not when a later kernel cannot be launched."""
+    many = dict(seqs=65535, heads=512, dim=8, ks=(4096, 4096, 8), vs=(4096, 4096, 8), tokens=1)
+    c = cache(dtype=4, **many)
+    assert attend(c, scales(ks=(512, 512, 1), vs=(512, 512, 1)), T=1, heads=512) == EINVAL
+    args = kv._ATTEND.pack(1 << 22, 4096, 4096, 8, 1 << 21, 4096, 4096, 8, 0, 0, 0, 0, 1 << 24, 0, 0, 0, 0, 0, 1, 512, 0.1, 0, 0)
+    assert kv.lib().uzip_kv_attend(cache(**many), args, 1 << 25, 1 << 40, None) == EINVAL
+    # ... for the accumulated weights
+    long = dict(seqs=4096, heads=2, dim=8, ks=(16, 16, 8), vs=(16, 16, 8), tokens=1 << 24)
+    args = kv._ATTEND.pack(1 << 22, 16, 16, 8, 1 << 21, 16, 16, 8, 0, 1 << 23, 0, 0, 1 << 24, 0, 0, 0, 0, 0, 1, 2, 0.1, 1 << 24, 0)
+    assert kv.lib().uzip_kv_attend(cache(**long), args, 1 << 25, 1 << 50, None) == EINVAL
+    one = dict(seqs=1, heads=1, dim=8, ks=(0, 8, 8), vs=(0, 8, 8), tokens=1 << 30)
+    assert append(cache(dtype=4, **one), scales(ks=(0, 1, 1), vs=(0, 1, 1)), T=(1 << 28) + 16, heads=1) == EINVAL
+    wide = dict(seqs=65535, heads=4096, dim=256, ks=(1 << 20, 1 << 20, 256), vs=(1 << 20, 1 << 20, 256), tokens=1)
+    assert kv.lib().uzip_kv_accept(cache(**wide), kv._ACCEPT.pack(1 << 24, 1 << 24, 4, 1 << 24, 4, 0), None) == EINVAL
