@@ -299,7 +299,7 @@ int launch_rope(RopeParams &p, const uzip_kv_rope_t *r, uint32_t seqs, bool f16,
     p.parts = (p.units + p.share - 1) / p.share;
     if (p.tokens > 1) p.parts = 1, p.share = p.units * p.tokens;
     const int64_t blocks = (p.count + p.tokens - 1) / p.tokens * p.parts;
-    if (blocks >= (1ll << 31)) return UZIP_EINVAL;
+    if ((uint64_t)blocks * kRopeThreads >= kLaunchThreads) return UZIP_EINVAL;
     const dim3 grid((unsigned)blocks);
 #define UZIP_KV_ROPE(F, C)                                                                    \
     do {                                                                                      \
@@ -898,7 +898,7 @@ int uzip_kv_evict(const uzip_kv_cache_t *cache, const uzip_kv_cache_t *out, cons
     p.found = reinterpret_cast<uint2 *>(static_cast<char *>(d_ws) + ws.off_found);
     p.slices = (int)ws.slices;
     const uint64_t each = 256 / (p.D / 8) * 4, groups = (a->keep + each - 1) / each;
-    if (rows * groups >= (1ull << 31) || rows * ws.slices >= (1ull << 31)) return UZIP_EINVAL;
+    if (rows * groups * 256 >= kLaunchThreads || rows * (ws.slices ? ws.slices : 1) * kSelThreads >= kLaunchThreads) return UZIP_EINVAL;
     return cache->dtype == UZIP_KV_E5M2 ? launch_evict<u32x2>(p, rows, s) : launch_evict<u32x4>(p, rows, s);
 }
 
