@@ -285,22 +285,19 @@ __global__ __launch_bounds__(kThreads, MODE == kStill ? 4 : 3) void k_append8(Ap
     const auto position = [&](int row) { return p.pos ? (int64_t)p.pos[b * p.pos_stride + t0 + row] : lo + row; };
     const int per = p.D / 8, units = rows * per;
     const int lanes = p.waves * 64, lane = p.waves == 1 ? tid & 63 : tid;
-    const int step = p.waves == 1 ? kAppendWaves : 1, end = min((group + 1) * p.items, 2 * p.H);
+    const int item = group * p.items + (p.waves == 1 ? wave : 0);      // of the wave, or of all four
     const auto row_of = [&](int u) { return per == 1 ? u : (int)__umulhi((uint32_t)u, p.per_magic); };
 
-    bool val;
-    const char *src;
-    char *dst;
-    float *scale, before;
-    int64_t ss, ds;
+    // where the item is, its scale and its first elements
+    const bool there = item < 2 * p.H, val = item >= p.H;
+    const int h = val ? item - p.H : item;
+    const char *src = val ? p.v + b * p.vs0 + t0 * p.vs1 + h * p.vs2 : p.k + b * p.ks0 + t0 * p.ks1 + h * p.ks2;
+    const int64_t ss = val ? p.vs1 : p.ks1, ds = val ? p.c.vs1 : p.c.ks1;
+    char *dst = val ? p.c.v + vo + h * p.c.vs2 : p.c.k + ko + h * p.c.ks2;
+    float *scale = val ? p.f.v + (first * p.f.v0 + block * p.f.v1 + h * p.f.v2) : p.f.k + (first * p.f.k0 + block * p.f.k1 + h * p.f.k2);
+    float before = 0.f;
     Eight raw[KEEP];
-    const auto fetch = [&](int item) {            // where an item is, its scale and its first elements
-        val = item >= p.H;
-        const int h = val ? item - p.H : item;
-        src = val ? p.v + b * p.vs0 + t0 * p.vs1 + h * p.vs2 : p.k + b * p.ks0 + t0 * p.ks1 + h * p.ks2;
-        ss = val ? p.vs1 : p.ks1, ds = val ? p.c.vs1 : p.c.ks1;
-        dst = val ? p.c.v + vo + h * p.c.vs2 : p.c.k + ko + h * p.c.ks2;
-        scale = val ? p.f.v + (first * p.f.v0 + block * p.f.v1 + h * p.f.v2) : p.f.k + (first * p.f.k0 + block * p.f.k1 + h * p.f.k2);
+    if (there) {
 #pragma unroll
         for (int r = 0; r < KEEP; r++) {
             if (r * lanes >= units) continue;
@@ -308,80 +305,74 @@ __global__ __launch_bounds__(kThreads, MODE == kStill ? 4 : 3) void k_append8(Ap
             raw[r] = load8<MODE>(p, src + row * ss, (u - row * per) * 8, !val);
         }
         before = *scale;
-    };
-    int item = group * p.items + (p.waves == 1 ? wave : 0);
-    if (item < end) fetch(item);
+    }
     if (MODE != kFar && MODE != kStill && group * p.items < p.H) {
         for (int i = tid; i < rows * half; i += kThreads) cs[i] = angle_of(p, position(i / half), i % half);
         __syncthreads();
     }
-    for (; item < end;) {
-        const auto elements = [&](const Eight &r, int u, float (&y)[8]) {
-            const int row = row_of(u);
-            turned8<F16, MODE>(p, r, (u - row * per) * 8, !val, cs + row * half, MODE == kFar && !val ? position(row) : 0, y);
-        };
-        const auto again = [&](int u) {
-            const int row = row_of(u);
-            return load8<MODE>(p, src + row * ss, (u - row * per) * 8, !val);
-        };
-        float top = 0.f;
-        const auto look = [&](const float (&y)[8]) {
+    if (!there) return;
+    const auto elements = [&](const Eight &r, int u, float (&y)[8]) {
+        const int row = row_of(u);
+        turned8<F16, MODE>(p, r, (u - row * per) * 8, !val, cs + row * half, MODE == kFar && !val ? position(row) : 0, y);
+    };
+    const auto again = [&](int u) {
+        const int row = row_of(u);
+        return load8<MODE>(p, src + row * ss, (u - row * per) * 8, !val);
+    };
+    float top = 0.f;
+    const auto look = [&](const float (&y)[8]) {
 #pragma unroll
-            for (int e = 0; e < 8; e++) top = fabsf(y[e]) < INFINITY ? fmaxf(top, fabsf(y[e])) : top;
-        };
-        float kept[KEEP][8];
+        for (int e = 0; e < 8; e++) top = fabsf(y[e]) < INFINITY ? fmaxf(top, fabsf(y[e])) : top;
+    };
+    float kept[KEEP][8];
 #pragma unroll
-        for (int r = 0; r < KEEP; r++) {
-            if (r * lanes >= units) continue;
-            elements(raw[r], min(r * lanes + lane, units - 1), kept[r]);
-            look(kept[r]);
-        }
-        for (int u = KEEP * lanes + lane; u < units; u += lanes) {
-            float y[8];
-            elements(again(u), u, y);
-            look(y);
-        }
-        for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
-        if (p.waves > 1) {
-            if ((tid & 63) == 0) wave_top[wave] = top;
-            __syncthreads();                      // and all waves have read the scale
-            top = fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3]));
-        }
-        const float now = skip && top <= before * E::kMost ? before : E::scale_for(top);
-        if (skip && now != before) {              // the earlier tokens in the new scale
-            const float ratio = before / now;
-            for (int u = lane; u < skip * per; u += lanes) {
-                const int row = row_of(u);
-                u32x2 *at = reinterpret_cast<u32x2 *>(dst + row * ds + (u - row * per) * 8);
-                const u32x2 w = *at;
-                float y[8];
-                E::unpack4(w.x, y, 0);
-                E::unpack4(w.y, y, 4);
-#pragma unroll
-                for (int e = 0; e < 8; e++) y[e] *= ratio;
-                *at = E::pack8(y);
-            }
-        }
-        const auto put = [&](int u, float (&y)[8]) {
-            const int row = row_of(u);
-            divide8(y, now);
-            *reinterpret_cast<u32x2 *>(dst + (skip + row) * ds + (u - row * per) * 8) = E::pack8(y);
-        };
-#pragma unroll
-        for (int r = 0; r < KEEP; r++) {
-            const int u = r * lanes + lane;
-            if (u < units) put(u, kept[r]);
-        }
-        for (int u = KEEP * lanes + lane; u < units; u += lanes) {
-            float y[8];
-            elements(again(u), u, y);
-            put(u, y);
-        }
-        if (lane == 0) *scale = now;
-        if (p.waves > 1) __syncthreads();         // wave_top is free
-        item += step;
-        if (item < end) fetch(item);
+    for (int r = 0; r < KEEP; r++) {
+        if (r * lanes >= units) continue;
+        elements(raw[r], min(r * lanes + lane, units - 1), kept[r]);
+        look(kept[r]);
     }
+    for (int u = KEEP * lanes + lane; u < units; u += lanes) {
+        float y[8];
+        elements(again(u), u, y);
+        look(y);
+    }
+    for (int x = 1; x < 64; x <<= 1) top = fmaxf(top, __shfl_xor(top, x));
+    if (p.waves > 1) {
+        if ((tid & 63) == 0) wave_top[wave] = top;
+        __syncthreads();                      // and all waves have read the scale
+        top = fmaxf(fmaxf(wave_top[0], wave_top[1]), fmaxf(wave_top[2], wave_top[3]));
+    }
+    const float now = skip && top <= before * E::kMost ? before : E::scale_for(top);
+    if (skip && now != before) {              // the earlier tokens in the new scale
+        const float ratio = before / now;
+        for (int u = lane; u < skip * per; u += lanes) {
+            const int row = row_of(u);
+            u32x2 *at = reinterpret_cast<u32x2 *>(dst + row * ds + (u - row * per) * 8);
+            const u32x2 w = *at;
+            float y[8];
+            E::unpack4(w.x, y, 0);
+            E::unpack4(w.y, y, 4);
+#pragma unroll
+            for (int e = 0; e < 8; e++) y[e] *= ratio;
+            *at = E::pack8(y);
+        }
+    }
+    const auto put = [&](int u, float (&y)[8]) {
+        const int row = row_of(u);
+        divide8(y, now);
+        *reinterpret_cast<u32x2 *>(dst + (skip + row) * ds + (u - row * per) * 8) = E::pack8(y);
+    };
+#pragma unroll
+    for (int r = 0; r < KEEP; r++) {
+        const int u = r * lanes + lane;
+        if (u < units) put(u, kept[r]);
+    }
+    for (int u = KEEP * lanes + lane; u < units; u += lanes) {
+        float y[8];
+        elements(again(u), u, y);
+        put(u, y);
+    }
+    if (lane == 0) *scale = now;
 }
 
 template <int MODE>
