@@ -8,7 +8,7 @@ import torch
 import kv_reference as ref
 from kv_step_reference import E4M3, I8, MOST
 from lossless_bf16_tensor_amd import kv
-from test_gpu_kv_scaled import BF16, DEV, F16, check, make, step_rows
+from test_gpu_kv_scaled import BF16, DEV, F16, bits, check, make, put, step_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -129,3 +129,56 @@ def test_scales_of_the_farthest_strides(cache):
         kv.append(None, new, new, kk, vv, n, table=table, k_scale=s[0], v_scale=s[1])
         got.append([x.contiguous().view(torch.uint8) for x in (kv.attend(q, kk, vv, n, table=table, k_scale=s[0], v_scale=s[1]), kk, vv, *s)])
     assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+# long ragged batches of few rows, where each workgroup takes its share of all sequences
+WALKS = [(32, 1, 16, 8, 128, 8200, BF16, E4M3, 16, "paged64", False), (20, 4, 32, 8, 128, 13200, BF16, I8, 32, "paged32", True),
+         (64, 3, 32, 16, 120, 4200, F16, I8, 64, "hsd", True), (7, 16, 32, 32, 72, 10000, F16, E4M3, 16, "paged16", False),
+         (100, 2, 32, 16, 128, 1400, BF16, I8, 128, "paged128", True), (16, 8, 16, 8, 128, 16400, F16, E4M3, 32, "shd", True)]
+
+
+@pytest.mark.parametrize("B,T,hq,H,D,S,qt,cache,block,layout,with_tree", WALKS)
+def test_shares_of_all_sequences(B, T, hq, H, D, S, qt, cache, block, layout, with_tree):
+    """Ragged and empty sequences, fewer drafted tokens than given, absent pages, a
+    value that is NaN in a drafted token of a sequence that many workgroups share."""
+    q, k, v, ks, vs, table = make(B, T, hq, H, D, S, qt, cache, block, layout, seed=B + T, dev=DEV)
+    g = torch.Generator().manual_seed(B)
+    G = hq // H
+    length = (torch.rand(B, generator=g) ** 3 * (S - T)).to(torch.int32)
+    drafted = torch.randint(1, T + 1, (B,), generator=g).to(torch.int32)
+    length[0], drafted[0] = S - T, T                  # the longest, in many parts
+    length[1], length[3], drafted[3], drafted[4] = 0, 0, 0, 0
+    length[B - 1], drafted[B - 1] = S - T - 1, T
+    tree = None
+    if with_tree:
+        tree = torch.rand(B, T, T, generator=g) < 0.5
+        tree[:, T - 1] = False
+    if table is not None:
+        page = k.shape[1]
+        table[0, 3] = -1
+        table[0, (S - T) // page - 1] = k.shape[0] + 7
+        table[B - 1, 0] = -1
+    if cache == E4M3:
+        n = S - T                                      # the first drafted token of sequence 0
+        at = (0, n) if table is None else (int(table[0, n // page]), n % page)
+        bits(v)[at][:, 5] = 0x7f
+        if with_tree:
+            tree[0, :, 0] = torch.arange(T) % 2 == 0
+    kk, vv, kks, vvs = (put(t.cpu(), layout) for t in (k, v, ks, vs))
+    got = []
+    for _ in range(2):
+        lse, w = torch.empty(B, T, hq, device=DEV), torch.zeros(B, H, S if table is None else table.shape[1] * page, device=DEV)
+        out = kv.attend(q, kk, vv, length.to(DEV), table=table, tree=put(tree), drafted=drafted.to(DEV), lse=lse, score=w, k_scale=kks, v_scale=vvs)
+        got.append((out, lse, w))
+    assert all(torch.equal(bits(x), bits(y)) for x, y in zip(*got))
+    for b in sorted({0, 1, 2, 3, 4, 5, B // 2, B - 2, B - 1}):
+        for h in sorted({0, H - 1}):
+            args = [t[:, :, h:h + 1].cpu() for t in (k, v, ks, vs)] if table is not None else [t[b:b + 1, :, h:h + 1].cpu() for t in (k, v, ks, vs)]
+            want = step_rows(q[b:b + 1, :, h * G:h * G + G].cpu(), args, block, length[b:b + 1], None if table is None else table[b:b + 1].cpu(),
+                             None if tree is None else tree[b:b + 1], drafted[b:b + 1], sorted({0, 1 % T, T - 1}), False)
+            for i, (o, ob, l, lb) in want.items():
+                ref.within(out[b, i, h * G:h * G + G], o, ob, f"out {b} {i} {h}")
+                ref.within(lse[b, i, h * G:h * G + G], l, lb, f"lse {b} {i} {h}")
+    assert torch.isnan(out[0, 0, :, 5]).all() == (cache == E4M3)
+    seeing = torch.isfinite(lse).sum((1, 2)).double().cpu()
+    assert ((w.double().sum((1, 2)).cpu() - seeing).abs() <= seeing * 2.0 ** -10).all()
