@@ -234,13 +234,16 @@ typedef struct uzip_kv_scales {
  * scale. An element is x / scale rounded to nearest even in binary32; beyond
  * MAX it is MAX with its sign, and NaN is NaN in E4M3, 0 in I8. Of a block that
  * receives nothing nothing is written. A magnitude above 2^80 MAX gets the scale
- * that holds it, beyond the range above: attention over it may be infinite. */
+ * that holds it, beyond the range above: attention over it may be infinite.
+ * Drafted tokens that are rejected later have had their part in a scale: it
+ * stays, and what rounding to it cost the block's earlier tokens too. */
 int uzip_kv_append_scaled(const uzip_kv_cache_t *cache, const uzip_kv_scales_t *scales, const uzip_kv_append_args_t *a,
                           const uzip_kv_rope_t *rope, hipStream_t s);
 
 /* async. uzip_kv_attend over a cache of E4M3 or I8, with queries of BF16 or
  * F16. Weights times the values' scales are multiplied with the values in two
- * terms of BF16, whatever the shapes. */
+ * terms of BF16, whatever the shapes. uzip_kv_evict and uzip_kv_accept take no
+ * such cache: a token that changes its block would have to be rounded again. */
 int uzip_kv_attend_scaled(const uzip_kv_cache_t *cache, const uzip_kv_scales_t *scales, const uzip_kv_attend_args_t *a,
                           void *d_ws, uint64_t ws_bytes, hipStream_t s);
 

@@ -1019,7 +1019,7 @@ struct Rows {
 // 1.698e-3, in 130 and 120 us (2 x 4 tokens over 131072 FP8 keys).
 // With scales: the same chain over 2 x 131072 tokens in 8-bit integers 105 us,
 // 5.1 TB/s, the rate of a copy; 32 ragged sequences of up to 16384 E4M3 tokens
-// in pages 118 us, 4.5 TB/s, where rows of a head are 128 bytes, 1 KB apart (side
+// in pages 116 us, 4.5 TB/s, where rows of a head are 128 bytes, 1 KB apart (side
 // by side 104); one over 2048 tokens 11 us.
 template <int CT, int DP, int RB, bool PAD, int SPLIT>
 __global__ __launch_bounds__(kWaves * 64, DP == 256 ? 1 : 2) void k_attend(AttendParams p)
@@ -1370,18 +1370,17 @@ __global__ __launch_bounds__(kShared * 64, 2) void k_attend_shared(AttendParams 
 // with one barrier a stage. Half the waves widen values, right behind it, half
 // keys, a tile later, so that the two waves of a SIMD are not at the same thing.
 // Trees of 64 tokens of 64 FP16 heads over 8 ragged sequences of up to 8205 E4M3
-// keys of 128: 204 us, with every wave widening for itself 277, with all of them
-// widening at once 10 more, with values read from LDS where they are used 8 more
-// (keys read two fragments at a time, 3 more). The products, in two terms, are 43
-// us at the dense peak; the vector units are busy for 55 % of the time, the matrix
-// cores for 36.
+// keys of 128: 199 us under the profiler, with every wave widening for itself 277,
+// with all of them widening at once 10 more, with values read from LDS where they
+// are used 8 more (keys read two fragments at a time, 3 more). The products, in
+// two terms, are 43 us at the dense peak; the vector units are busy for 57 % of
+// the time, the matrix cores for 38.
 template <int CT, int DP, bool PAD, bool PAGED>
 __global__ __launch_bounds__(kShared * 64, 2) void k_attend_wide(AttendParams p)
 {
     constexpr int RB = 2;
     // Two terms of a weight, as with few rows: it is BF16 beside scales, and one
-    // would be as coarse as a BF16 output. (For those queries the call above
-    // takes 192 us so, 184 with one term.)
+    // would be as coarse as a BF16 output and save 4 to 6 %
     using W = Rows<CT, DP, RB, PAD, true>;
     constexpr int KS = W::KS, VE = W::VE, ROW = DP * 2, PIECES = ROW / 16;
     constexpr int TILE = DP * 64, STAGE = 64 * ROW + 2 * TILE, RING = 3;      // a tile's values, and bytes of a stage
@@ -1917,7 +1916,10 @@ Plan make_plan(uint32_t seqs, uint32_t kv_heads, uint32_t dim, uint32_t cache_to
     // Beside scales, where a wave has all of its next tile under way: two a CU
     // (32 rows, 2 x 131072 keys 116 us, with one 168, with four 133; 16 rows, 4
     // x 16384 keys 35 and, with eight, 45), and eight of heads of 64, whose
-    // tiles are half as long (105 and 87 us where Number says).
+    // tiles are half as long (105 and 87 us where Number says). Heads of 256 too,
+    // though their registers hold one at a time: 32 ragged sequences of up to
+    // 16384 keys, 4 rows, 296 us and, with one, 327, 4 of them 51 and 68; but
+    // equal lengths, 2 x 131072 keys of 32 rows, 251 and 239.
     uint64_t want = !a.shared && a.RB == 1 && a.DP < 256 ? 8 * kCUs : kCUs;
     if (scaled && !a.shared && a.DP > 64) want = 2 * kCUs;
     const uint64_t each = (uint64_t)kv_heads * a.nrg;
@@ -1929,9 +1931,11 @@ Plan make_plan(uint32_t seqs, uint32_t kv_heads, uint32_t dim, uint32_t cache_to
     // Runs in workgroups of their own end apart by as much as one is long; where
     // that is more than 4096 keys, each workgroup takes its share of all
     // sequences instead, one place after the other, though a place begins and
-    // ends in some 6 us: 32 rows of ragged sequences of up to 16384 keys 125 us
-    // and, in runs, 168; of up to 8192 85 and 106; of up to 4096 56 and 54; 64
-    // of up to 1024 38 and 29.
+    // ends in some 6 us: 32 ragged sequences of up to 16384 keys, 4 rows, 124 us
+    // and, in runs, 169; of up to 8192 84 and 106; of up to 4096 58 both; 64 of up
+    // to 4096 76 and 91, of up to 1024 37 and 29; equal ones, 2 of 131072 keys, 104
+    // and 103. Made and measured for up to 16 rows of heads of 65 to 128; others
+    // take runs.
     a.walks = a.flat && scaled && !a.shared && a.RB == 1 && a.DP == 128 && seqs > 1 && seqs * tiles >= 128 * slots;
     if (a.flat) {
         // parts of one sequence: up to four times what equal lengths give

@@ -251,10 +251,16 @@ __device__ inline void turn_queries(const Append8Params &p, float2 *cs)
 // a workgroup) takes the keys or values of a head: turns the new tokens, finds
 // their largest magnitude, and rounds what it holds in registers. Bound by
 // memory where there is much: 2 x 8192 decoded tokens of 8 heads of 128 into
-// integers in pages, blocks of 16, 28 us, 3.6 TB/s (a copy 5.1; every element is
+// integers in pages, blocks of 16, 25 us, 3.9 TB/s (a copy 5.1; every element is
 // read once, and a wave's loads, their maximum and the stores follow each
-// other). One token with 64 query heads 5.4 us: the trips to memory for the
-// length, the tokens and the scale, and the angles.
+// other). One token with 64 query heads 4.7 us: the trips to memory for the
+// length, the tokens and the scale, and the angles. Long blocks are slow: one
+// workgroup takes a block of a head, 2 x 8192 tokens of 8 heads into E4M3 in
+// blocks of 64, 256 and 1024 22, 25 and 64 us; turned, by angles that LDS holds
+// for 128 tokens of 128 dims and that every head works out for itself beyond, 54,
+// 147 and 363. And where one token raises a block's scale, one wave rounds the
+// earlier ones again, a trip to memory after the other: 8 heads of 128, the last
+// token of blocks of 128, 1024 and 65536, 12, 71 and 6500 us a call.
 template <bool F16, bool I8, int MODE>
 __global__ __launch_bounds__(kThreads, MODE == kStill ? 4 : 3) void k_append8(Append8Params p)
 {

@@ -849,9 +849,10 @@ int uzip_kv_verify(const uzip_kv_verify_args_t *a, void *d_ws, uint64_t ws_bytes
     const int64_t most = (p.segs + kVerifyWaves - 1) / kVerifyWaves, want = (4 * kCUs + a->seqs - 1) / a->seqs;
     p.slices = (int)(most < want ? most : want);
     // Two launches that make one more sum, where rows are long and some of the
-    // sequences will ask for sums again and again: 16 trees of 32 nodes over
-    // 131072 tokens 41 us, without 60; but one tree 26 and 21, 64 over 50000 64
-    // and 60.
+    // sequences will ask for sums again and again. Trees of 32 nodes over 131072
+    // tokens, calls' means over 12 drawings and without: 4 of them 27 and 28 us, 16
+    // 38 and 55, 32 50 and 70; 16 over 70000 39 and 43. One tree (23 us) and 64
+    // over 50000 (57) do without.
     p.seqs = (int)a->seqs;
     p.rounds = a->draft && a->parent && p.T > 2 && p.segs >= 64 && p.seqs >= 4 && p.seqs <= 32 ? 2 : 0;
     char *w = static_cast<char *>(d_ws);

@@ -366,7 +366,9 @@ def append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, k_cache: to
     With k_scale and v_scale the cache is float8_e4m3fn or int8, and a block of a
     head that receives tokens gets a scale that holds them: its own, if it has
     earlier tokens and that does, else the smallest power of two that does, to
-    which its earlier tokens are rounded."""
+    which its earlier tokens are rounded. That stays when drafted tokens are
+    rejected later: what is in a block depends on all that was appended to it.
+    Blocks of up to 128 tokens are filled fastest."""
     scaled = k_scale is not None or v_scale is not None
     if (k.requires_grad or v.requires_grad or k_cache.requires_grad or v_cache.requires_grad or (q is not None and q.requires_grad)
             or (freq is not None and freq.requires_grad) or (out is not None and out.requires_grad)
@@ -446,7 +448,9 @@ def attend(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, length
     effect, whatever they hold. out does not overlap the inputs.
 
     With k_scale and v_scale the cache is float8_e4m3fn or int8, and an element
-    stands for itself times the scale of its block and head."""
+    stands for itself times the scale of its block and head. :func:`accept` and
+    :func:`evict` take no such cache: of a drafted tree, append what was accepted
+    again, from 16-bit keys and values, as a chain."""
     if (q.requires_grad or k_cache.requires_grad or v_cache.requires_grad or (score is not None and score.requires_grad)
             or (lse is not None and lse.requires_grad) or (out is not None and out.requires_grad)
             or (k_scale is not None and k_scale.requires_grad) or (v_scale is not None and v_scale.requires_grad)):
@@ -518,7 +522,7 @@ def evict(k_cache: torch.Tensor, v_cache: torch.Tensor, score: torch.Tensor, len
     keep, kv heads, dim] with the kept tokens in order and zeros behind them,
     ready for ``uzip.encode``; their scores [sequences, kv heads, keep]; min(length,
     keep); and where each came from, int32 [sequences, kv heads, keep], -1
-    behind the last. Keys keep the positions they were turned to. Launches are
+    behind the last. Caches with scales are not taken. Keys keep the positions they were turned to. Launches are
     sized by what score can hold, not by length: where caches are much larger
     than what is in them, pass slices that end behind the longest sequence."""
     if (k_cache.requires_grad or v_cache.requires_grad or score.requires_grad or (k_out is not None and k_out.requires_grad)
@@ -639,7 +643,7 @@ def accept(k_cache: torch.Tensor, v_cache: torch.Tensor, length: torch.Tensor, p
     appended as a chain. path [sequences, nodes] and count as :func:`verify`
     returns them. length is not changed: the tokens that the cache then has are
     length + count. Caches with scales are not taken: draft chains over them,
-    whose accepted tokens are in place."""
+    whose accepted tokens are in place, or append a tree's accepted ones again."""
     if k_cache.requires_grad or v_cache.requires_grad:
         _no_gradient()
     B = length.numel()

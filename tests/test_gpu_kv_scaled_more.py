@@ -6,9 +6,10 @@ import pytest
 import torch
 
 import kv_reference as ref
-from kv_step_reference import E4M3, I8, MOST
+import kv_step_reference as step
+from kv_step_reference import E4M3, F64, I8, MOST
 from lossless_bf16_tensor_amd import kv
-from test_gpu_kv_scaled import BF16, DEV, F16, bits, check, make, put, step_rows
+from test_gpu_kv_scaled import BF16, DEV, F16, bits, check, make, new_tokens, powers, put, step_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -182,3 +183,29 @@ def test_shares_of_all_sequences(B, T, hq, H, D, S, qt, cache, block, layout, wi
     assert torch.isnan(out[0, 0, :, 5]).all() == (cache == E4M3)
     seeing = torch.isfinite(lse).sum((1, 2)).double().cpu()
     assert ((w.double().sum((1, 2)).cpu() - seeing).abs() <= seeing * 2.0 ** -10).all()
+
+
+@pytest.mark.parametrize("cache", [I8, E4M3])
+@pytest.mark.parametrize("layout", ["shd", "paged32"])
+def test_accepted_tokens_of_a_tree_are_appended_again(cache, layout):
+    """Over caches with scales the accepted nodes' keys and values go in once more, as
+    a chain. Earlier tokens of a block keep the scale that a rejected one raised."""
+    B, T, H, D, S, block = 2, 12, 2, 64, 96, 16
+    _, k, v, ks, vs, table = make(B, 1, H, H, D, S, BF16, cache, block, layout, seed=4)
+    ks, vs = powers(ks), powers(vs)
+    nk, nv = new_tokens(B, T, H, D, BF16, 5)
+    nk[:, 5], nv[:, 6] = nk[:, 5] * 64, nv[:, 6] * 64                   # rejected, and far larger than the others
+    n = torch.tensor([40, 63], dtype=torch.int32)
+    path, count = torch.tensor([[0, 3, 7, 8], [0, 1, 11, 11]]), torch.tensor([4, 3], dtype=torch.int32)
+    dk, dv, dks, dvs = (t.to(DEV) for t in (k, v, ks, vs))
+    way = [torch.stack([x[b, path[b]] for b in range(B)]) for x in (nk, nv)]
+    kv.append(None, nk.to(DEV), nv.to(DEV), dk, dv, n.to(DEV), table=put(table), k_scale=dks, v_scale=dvs)
+    kv.append(None, way[0].to(DEV), way[1].to(DEV), dk, dv, n.to(DEV), table=put(table), drafted=count.to(DEV), k_scale=dks, v_scale=dvs)
+    for got, s, c, cs, x, y in ((dk, dks, k, ks, nk, way[0]), (dv, dvs, v, vs, nv, way[1])):
+        once, s1, _ = step.append8(c, cs, x.to(F64), n, None, table, block)
+        want, s2, _ = step.append8(once.to(cache), s1.float(), y.to(F64), n, count, table, block)
+        assert torch.equal(s.cpu().to(F64), s2) and (s2 > cs.to(F64) * 8).any()
+        for b in range(B):
+            for t in range(int(n[b] + count[b])):
+                at = step.place(c, table, b, t)
+                assert torch.equal(got[at].cpu().to(F64), want[at]), (b, t)
